@@ -21,6 +21,13 @@
  * before that layer's step 1).
  * Request leases with generation tags return a finished request's rows and
  * slot-table region to the cache.
+ * Several tokens of a request at once (a piece of a prompt, draft tokens to
+ * verify): qsa_append_chunk, qsa_chunk_index_score, qsa_chunk_select_topk and
+ * qsa_chunk_sparse_attn run the same steps for every token of a chunk, each
+ * with its own causal context and its own selection; qsa_request_truncate
+ * takes back tokens (rejected drafts).
+ * Pages of the cache: qsa_request_fork starts a request with the first tokens
+ * of another one, qsa_cache_compact closes the gaps of the pool.
  *
  * Sources.  The method is described on two pages:
  *  [offload digest] "Оффлоадинг KV-кэша Qwen3.8-Flash-Next в RAM через vLLM без
@@ -91,6 +98,8 @@ extern "C" {
 #define QSA_MAX_BUDGET_TOKENS 8192
 /* Largest hot_rows of a cache (see qsa_cache_config). */
 #define QSA_MAX_HOT_ROWS 65536
+/* Largest number of rows (token x layer) of one chunk call. */
+#define QSA_MAX_CHUNK_ROWS 65536
 
 typedef enum qsa_status_t {
   QSA_OK = 0,
@@ -209,6 +218,28 @@ typedef struct qsa_batch {
   int32_t reserved0;
   const qsa_handle* requests;   /* host [n_req] */
 } qsa_batch;
+
+/* A chunk: the newest n_tokens[i] tokens (0 <= n_tokens[i] <= ctx_len) of
+ * request i, at layers layer0 .. layer0+n_layers-1.  Token j of request i sits
+ * at position ctx_len_i - n_tokens[i] + j, and as a query it sees positions up
+ * to its own.  Per-row arrays hold layer after layer, request after request:
+ * with N = sum of n_tokens, row = i_layer * N + (n_tokens[0] + .. +
+ * n_tokens[i-1]) + j.  At most QSA_MAX_CHUNK_ROWS rows and QSA_MAX_UNITS
+ * (request, layer) pairs in one call; a call with no rows does nothing. */
+typedef struct qsa_chunk {
+  int32_t n_req;
+  int32_t layer0;
+  int32_t n_layers;
+  int32_t reserved0;            /* must be 0 */
+  const qsa_handle* requests;   /* host [n_req] */
+  const int32_t* n_tokens;      /* host [n_req] */
+} qsa_chunk;
+
+/* Type of the index queries of qsa_chunk_index_score. */
+typedef enum qsa_query_type {
+  QSA_QUERY_F32 = 0,
+  QSA_QUERY_BF16 = 1
+} qsa_query_type;
 
 typedef struct qsa_cache qsa_cache;
 
@@ -449,6 +480,109 @@ qsa_status_t qsa_sparse_decode_attn(qsa_cache* cache, const qsa_batch* batch,
                                     const int32_t* n_sel, int32_t budget_tokens,
                                     const void* gathered, float softmax_scale,
                                     float* out, float* lse, void* stream);
+
+/* ------------------------------------------------- several tokens at once */
+
+/* qsa_append_token for every token of a chunk (after one qsa_request_advance
+ * of n_tokens tokens per request, or right after qsa_request_begin for the
+ * first piece of a prompt): k_new device fp32 [rows][64], kv_new device
+ * [rows][2048], quantised and stored under the rules given there.  The slot
+ * tables end as n_tokens single appends would leave them: a ring request
+ * keeps its newest ring_tokens rows in the ring, every older token of the
+ * chunk is cold, and so is every token that lost its ring row.
+ * Both buffers 16-byte aligned.
+ * Errors: INVALID_ARG, STALE_HANDLE, NO_DEVICE, CUDA. */
+qsa_status_t qsa_append_chunk(qsa_cache* cache, const qsa_chunk* chunk, const float* k_new,
+                              const void* kv_new, void* stream);
+
+/* qsa_index_score for every query of a chunk.  Row x at position p (query i
+ * of the chunk) gets blk_scores[x * blk_stride + b] = max of S_t over the
+ * tokens t = 4b .. 4b+3 with t <= p, for b < ceil((p+1)/4); the other entries
+ * of the row are left as they were.
+ * q_idx: device [rows][8][64] of query_type (QSA_QUERY_F32 or QSA_QUERY_BF16;
+ * fp32 queries are carried to fp32's own precision); w: device fp32 [rows][8];
+ * blk_scores: device fp32 [rows][blk_stride], blk_stride >= ceil(ctx/4) of
+ * every request.  Scores must be finite.
+ * Errors: INVALID_ARG, STALE_HANDLE, NO_DEVICE, CUDA. */
+qsa_status_t qsa_chunk_index_score(qsa_cache* cache, const qsa_chunk* chunk, const void* q_idx,
+                                   int32_t query_type, const float* w, float* blk_scores,
+                                   int64_t blk_stride, void* stream);
+
+/* qsa_select_c4_topk for every query of a chunk: row x at position p keeps the
+ * K = min(budget_tokens/4, ceil((p+1)/4)) best of its ceil((p+1)/4) blocks
+ * under the same order, in ascending id order, in sel_blocks[x *
+ * (budget_tokens/4) + i]; n_sel[x] = K.  Entries past K are left as they were.
+ * Arguments and errors as there, [rows] in place of [units]. */
+qsa_status_t qsa_chunk_select_topk(qsa_cache* cache, const qsa_chunk* chunk,
+                                   const float* blk_scores, int64_t blk_stride,
+                                   int32_t budget_tokens, int32_t* sel_blocks, int32_t* n_sel,
+                                   void* stream);
+
+/* Bytes of workspace qsa_chunk_sparse_attn needs for this chunk, or -1 for a
+ * bad chunk (qsa_last_error_string() tells).  The size depends on the sizes
+ * of the chunk and of its requests alone; it never shrinks when a request
+ * grows, so one of the largest chunk serves smaller ones of as few requests. */
+int64_t qsa_chunk_attn_workspace_bytes(qsa_cache* cache, const qsa_chunk* chunk,
+                                       int32_t budget_tokens);
+
+/* qsa_sparse_decode_attn for every query of a chunk: row x at position p
+ * attends over the tokens t <= p of its selected blocks (distinct block ids,
+ * in any order; a block past p/4 is skipped and reported as BAD_BLOCK).  Rows
+ * are read through the slot table (pool rows from HBM, cold rows from the host
+ * history); no planned miss of qsa_hot_cache_plan may be pending.
+ * q: device bf16 bits [rows][16][128]; sel_blocks, n_sel: as written by
+ * qsa_chunk_select_topk; out: device bf16 bits [rows][16][128], rounded once
+ * from the fp32 sums; lse: device fp32 [rows][16] or NULL (-inf, and out = 0,
+ * for a row with no tokens).  A key or value that is not finite reaches only
+ * the queries that select its token.
+ * workspace: device, 16-byte aligned, qsa_chunk_attn_workspace_bytes bytes,
+ * used by one call at a time: calls that may overlap need one each.
+ * Errors: INVALID_ARG, STALE_HANDLE, NO_DEVICE, CUDA; bad blocks, counts and
+ * slots go to the device error word (BAD_BLOCK, BAD_SLOT). */
+qsa_status_t qsa_chunk_sparse_attn(qsa_cache* cache, const qsa_chunk* chunk, const uint16_t* q,
+                                   const int32_t* sel_blocks, const int32_t* n_sel,
+                                   int32_t budget_tokens, float softmax_scale, uint16_t* out,
+                                   float* lse, void* workspace, int64_t workspace_bytes,
+                                   void* stream);
+
+/* ------------------------------------------------------ pages of the cache */
+
+/* Take back the newest tokens of a request: ctx_len becomes new_ctx_len
+ * (1 <= new_ctx_len <= ctx_len).  Host bookkeeping only; work already
+ * enqueued must not use the tokens taken back afterwards.  Their positions
+ * can be advanced over and appended to again.  Tokens whose ring row the
+ * tokens taken back had been given stay cold (read from the host history).
+ * Errors: INVALID_ARG, STALE_HANDLE. */
+qsa_status_t qsa_request_truncate(qsa_cache* cache, qsa_handle request, int64_t new_ctx_len);
+
+/* Lease a new request (desc as for qsa_request_begin, with any placement)
+ * that starts with the first desc->ctx_len tokens of `parent`
+ * (1 <= desc->ctx_len <= its ctx_len): on `stream`, the tokens' index keys,
+ * scales and KV rows are copied at every layer, the rows read through the
+ * parent's slot tables and stored where the child's placement keeps them
+ * (region rows; host history; host history and tail ring).  Nothing is shared
+ * afterwards.  desc->host_rows must not overlap the parent's host history.
+ * The child's hot rows start free.  No planned miss of the parent
+ * (qsa_hot_cache_plan) may be pending.
+ * Errors: as qsa_request_begin, INVALID_ARG, STALE_HANDLE (parent); nothing is
+ * leased on error.  A bad slot of the parent goes to the device error word
+ * (BAD_SLOT), and its row is not copied. */
+qsa_status_t qsa_request_fork(qsa_cache* cache, qsa_handle parent, const qsa_request_desc* desc,
+                              void* stream, qsa_handle* out);
+
+/* Slide the pool regions of all live requests to the front of the pool (behind
+ * the staging rows, in their present order), so that the free rows form one
+ * range: enqueued on `stream`, rows are moved and every slot-table entry (and
+ * pending plan) that names a moved row is changed with it, whichever request
+ * it belongs to.  hbm_row_base and hot_row_base of the requests change;
+ * handles stay valid.  *moved_rows (may be NULL) receives the rows moved.
+ * Work on any request of the cache that is in flight on other streams must
+ * have finished, and later work must be ordered behind `stream`.  Graphs that
+ * captured calls of this library before must be captured again.  A stream
+ * that is being captured is refused.
+ * Errors: INVALID_ARG, CUDA (the contents of moved regions are then
+ * undefined). */
+qsa_status_t qsa_cache_compact(qsa_cache* cache, void* stream, int64_t* moved_rows);
 
 /* -------------------------------------------------- host history memory */
 

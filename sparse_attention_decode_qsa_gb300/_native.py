@@ -22,6 +22,9 @@ KV_FP8 = 1
 MAX_UNITS = 256
 MAX_BUDGET_TOKENS = 8192
 MAX_HOT_ROWS = 65536
+MAX_CHUNK_ROWS = 65536
+QUERY_F32 = 0
+QUERY_BF16 = 1
 STATIC_MAX_UNITS = 16
 STATIC_MAX_ROWS = 2048
 
@@ -85,6 +88,12 @@ class Batch(C.Structure):
                 ("reserved0", C.c_int32), ("requests", C.POINTER(Handle))]
 
 
+class Chunk(C.Structure):
+    _fields_ = [("n_req", C.c_int32), ("layer0", C.c_int32), ("n_layers", C.c_int32),
+                ("reserved0", C.c_int32), ("requests", C.POINTER(Handle)),
+                ("n_tokens", C.POINTER(C.c_int32))]
+
+
 # name -> (restype, argtypes); every entry point declared in include/qsa.h
 SIGNATURES = {
     "qsa_abi_version": (C.c_int32, []),
@@ -116,6 +125,19 @@ SIGNATURES = {
     "qsa_sparse_decode_attn": (C.c_int, [C.c_void_p, C.POINTER(Batch), C.c_void_p, C.c_void_p,
                                          C.c_void_p, C.c_int32, C.c_void_p, C.c_float,
                                          C.c_void_p, C.c_void_p, C.c_void_p]),
+    "qsa_append_chunk": (C.c_int, [C.c_void_p, C.POINTER(Chunk), C.c_void_p, C.c_void_p, C.c_void_p]),
+    "qsa_chunk_index_score": (C.c_int, [C.c_void_p, C.POINTER(Chunk), C.c_void_p, C.c_int32,
+                                        C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
+    "qsa_chunk_select_topk": (C.c_int, [C.c_void_p, C.POINTER(Chunk), C.c_void_p, C.c_int64,
+                                        C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "qsa_chunk_attn_workspace_bytes": (C.c_int64, [C.c_void_p, C.POINTER(Chunk), C.c_int32]),
+    "qsa_chunk_sparse_attn": (C.c_int, [C.c_void_p, C.POINTER(Chunk), C.c_void_p, C.c_void_p,
+                                        C.c_void_p, C.c_int32, C.c_float, C.c_void_p, C.c_void_p,
+                                        C.c_void_p, C.c_int64, C.c_void_p]),
+    "qsa_request_truncate": (C.c_int, [C.c_void_p, Handle, C.c_int64]),
+    "qsa_request_fork": (C.c_int, [C.c_void_p, Handle, C.POINTER(RequestDesc), C.c_void_p,
+                                   C.POINTER(Handle)]),
+    "qsa_cache_compact": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(C.c_int64)]),
     "qsa_host_alloc": (C.c_int, [C.c_int32, C.c_int32, C.c_int64, C.POINTER(C.c_void_p)]),
     "qsa_host_free": (C.c_int, [C.c_void_p]),
     "qsa_sparse_decode_attn_noalloc": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32,

@@ -36,6 +36,18 @@ def _batch(handles, layer0: int, n_layers: int):
     return b
 
 
+def _chunk(handles, n_tokens, layer0: int, n_layers: int):
+    n = len(handles)
+    if len(n_tokens) != n:
+        raise ValueError("one token count per request")
+    arr = (N.Handle * n)(*handles)
+    cnt = (C.c_int32 * n)(*n_tokens)
+    ch = N.Chunk(n, layer0, n_layers, 0, C.cast(arr, C.POINTER(N.Handle)),
+                 C.cast(cnt, C.POINTER(C.c_int32)))
+    ch._keep = (arr, cnt)
+    return ch
+
+
 class HostMemory:
     """Host memory from qsa_host_alloc: pages on a host NUMA node, mapped into
     the device's page tables and the host's at one address.  Pass
@@ -211,6 +223,33 @@ class Cache:
               "qsa_poll_error")
         return st.value, det.value
 
+    # -------------------------------------------------- pages of the cache
+    def truncate(self, handle: N.Handle, ctx_len: int):
+        """Take back the newest tokens: the request's context becomes ctx_len."""
+        check(self.L.qsa_request_truncate(self.h, handle, int(ctx_len)), "qsa_request_truncate")
+
+    def request_fork(self, parent: N.Handle, ctx_len: int, placement: int = N.KV_HBM, host_rows=None,
+                     stream=None, max_ctx: int = 0) -> N.Handle:
+        """Lease a request that starts with the first ctx_len tokens of
+        `parent` (copied: keys, rows), with the placement, host history and
+        growth that request_begin takes."""
+        d = N.RequestDesc(ctx_len, placement, max_ctx, None)
+        if host_rows is not None:
+            d.host_rows = host_rows.data_ptr() if isinstance(host_rows, torch.Tensor) else int(host_rows)
+        out = N.Handle()
+        check(self.L.qsa_request_fork(self.h, parent, C.byref(d), _stream(stream) if self.device else None,
+                                      C.byref(out)), "qsa_request_fork")
+        if isinstance(host_rows, torch.Tensor):
+            self._host[out.index] = host_rows
+        return out
+
+    def compact(self, stream=None) -> int:
+        """Close the gaps of the pool; returns the number of rows moved."""
+        moved = C.c_int64()
+        check(self.L.qsa_cache_compact(self.h, _stream(stream) if self.device else None, C.byref(moved)),
+              "qsa_cache_compact")
+        return moved.value
+
     # ------------------------------------------------------ producer side
     def append_token(self, handles, layer0, n_layers, k_new, kv_new, stream=None):
         """Store each unit's newest token: k_new fp32 [units][64] index keys,
@@ -260,3 +299,82 @@ class Cache:
                                             _ptr(sel_blocks), _ptr(n_sel), budget_tokens, g,
                                             float(softmax_scale), _ptr(out), _ptr(lse),
                                             _stream(stream)), "qsa_sparse_decode_attn")
+
+    def _rows(self, t, what, dtypes, shape):
+        """Pointer of a per-row tensor.  Its type, shape (None: any size), device
+        and layout are checked here, since the library sees a bare address."""
+        if t is None:
+            return None
+        if t.dtype not in dtypes:
+            raise ValueError(f"{what}: type {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+        if t.dim() != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
+            raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
+        if self.device is not None and t.device != self.pool.device:
+            raise ValueError(f"{what}: on {t.device}, the cache on {self.pool.device}")
+        return _ptr(t)
+
+    # ------------------------------------------------ several tokens at once
+    # handles: requests; n_tokens: how many of each request's newest tokens.
+    # Rows: layer after layer, request after request.
+    def append_chunk(self, handles, n_tokens, layer0, n_layers, k_new, kv_new, stream=None):
+        """Store the chunk's tokens: k_new fp32 [rows][64], kv_new uint8 [rows][2048]."""
+        ch = _chunk(handles, n_tokens, layer0, n_layers)
+        rows = n_layers * sum(n_tokens)
+        check(self.L.qsa_append_chunk(self.h, C.byref(ch),
+                                      self._rows(k_new, "k_new", (torch.float32,), (rows, N.INDEX_DIM)),
+                                      self._rows(kv_new, "kv_new", (torch.uint8,), (rows, N.ROW_BYTES)),
+                                      _stream(stream)), "qsa_append_chunk")
+
+    def chunk_index_score(self, handles, n_tokens, layer0, n_layers, q_idx, w, blk_scores, stream=None):
+        """Block scores of every query: q_idx fp32 or bf16 [rows][8][64], w fp32
+        [rows][8], blk_scores fp32 [rows][stride]."""
+        ch = _chunk(handles, n_tokens, layer0, n_layers)
+        rows = n_layers * sum(n_tokens)
+        check(self.L.qsa_chunk_index_score(
+            self.h, C.byref(ch),
+            self._rows(q_idx, "q_idx", (torch.float32, torch.bfloat16), (rows, N.INDEX_HEADS, N.INDEX_DIM)),
+            N.QUERY_BF16 if q_idx.dtype == torch.bfloat16 else N.QUERY_F32,
+            self._rows(w, "w", (torch.float32,), (rows, N.INDEX_HEADS)),
+            self._rows(blk_scores, "blk_scores", (torch.float32,), (rows, None)), blk_scores.shape[-1],
+            _stream(stream)), "qsa_chunk_index_score")
+
+    def chunk_select_topk(self, handles, n_tokens, layer0, n_layers, blk_scores, budget_tokens,
+                          sel_blocks, n_sel, stream=None):
+        """Best blocks of every query: sel_blocks int32 [rows][budget/4], n_sel int32 [rows]."""
+        ch = _chunk(handles, n_tokens, layer0, n_layers)
+        rows = n_layers * sum(n_tokens)
+        check(self.L.qsa_chunk_select_topk(
+            self.h, C.byref(ch), self._rows(blk_scores, "blk_scores", (torch.float32,), (rows, None)),
+            blk_scores.shape[-1], budget_tokens,
+            self._rows(sel_blocks, "sel_blocks", (torch.int32,), (rows, budget_tokens // 4)),
+            self._rows(n_sel, "n_sel", (torch.int32,), (rows,)), _stream(stream)), "qsa_chunk_select_topk")
+
+    def chunk_attn_workspace_bytes(self, handles, n_tokens, layer0, n_layers, budget_tokens) -> int:
+        ch = _chunk(handles, n_tokens, layer0, n_layers)
+        n = self.L.qsa_chunk_attn_workspace_bytes(self.h, C.byref(ch), budget_tokens)
+        if n < 0:
+            raise QsaError(N.ERR_INVALID_ARG, "qsa_chunk_attn_workspace_bytes",
+                           self.L.qsa_last_error_string().decode(errors="replace"))
+        return n
+
+    def chunk_sparse_attn(self, handles, n_tokens, layer0, n_layers, q, sel_blocks, n_sel, budget_tokens,
+                          softmax_scale, out, lse=None, workspace=None, stream=None):
+        """Attention of every query over its own blocks: q and out bf16
+        [rows][16][128], lse fp32 [rows][16].  workspace: uint8 of
+        chunk_attn_workspace_bytes bytes; allocated for the call when None."""
+        ch = _chunk(handles, n_tokens, layer0, n_layers)
+        rows = n_layers * sum(n_tokens)
+        if workspace is None:
+            need = self.chunk_attn_workspace_bytes(handles, n_tokens, layer0, n_layers, budget_tokens)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            if isinstance(stream, torch.cuda.Stream):
+                workspace.record_stream(stream)
+        heads = (rows, N.Q_HEADS, N.HEAD_DIM)
+        check(self.L.qsa_chunk_sparse_attn(
+            self.h, C.byref(ch), self._rows(q, "q", (torch.bfloat16,), heads),
+            self._rows(sel_blocks, "sel_blocks", (torch.int32,), (rows, budget_tokens // 4)),
+            self._rows(n_sel, "n_sel", (torch.int32,), (rows,)), budget_tokens, float(softmax_scale),
+            self._rows(out, "out", (torch.bfloat16,), heads),
+            self._rows(lse, "lse", (torch.float32,), (rows, N.Q_HEADS)),
+            self._rows(workspace, "workspace", (torch.uint8,), (None,)), workspace.numel(),
+            _stream(stream)), "qsa_chunk_sparse_attn")

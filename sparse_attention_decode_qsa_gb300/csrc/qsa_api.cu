@@ -14,6 +14,7 @@
 // the index-score work counters of every request x layer).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -222,6 +223,27 @@ struct qsa_cache {
     return QSA_OK;
   }
 
+  // Validate a chunk and describe its units and rows for the kernels.
+  qsa_status_t build_chunk(const qsa_chunk* ch, ChunkDesc* d) const {
+    if (!ch) return fail(QSA_ERR_INVALID_ARG, "null chunk");
+    if (ch->reserved0 != 0) return fail(QSA_ERR_INVALID_ARG, "chunk.reserved0 must be 0");
+    const qsa_batch b = {ch->n_req, ch->layer0, ch->n_layers, 0, ch->requests};
+    if (qsa_status_t st = build_batch(&b, &d->b)) return st;
+    if (!ch->n_tokens) return fail(QSA_ERR_INVALID_ARG, "null n_tokens");
+    int64_t x = 0;
+    for (int u = 0; u < d->b.n_units; ++u) {
+      const int32_t n = ch->n_tokens[u % ch->n_req];
+      if (n < 0 || n > d->b.u[u].n)
+        return fail(QSA_ERR_INVALID_ARG, "n_tokens %d outside [0, %lld]", n, (long long)d->b.u[u].n);
+      d->row0[u] = (int32_t)x;
+      x += n;
+      if (x > QSA_MAX_CHUNK_ROWS)
+        return fail(QSA_ERR_INVALID_ARG, "chunk has more than %d rows", QSA_MAX_CHUNK_ROWS);
+    }
+    d->row0[d->b.n_units] = (int32_t)x;
+    return QSA_OK;
+  }
+
   // Validate a batch and describe its units for the kernels.
   qsa_status_t build_batch(const qsa_batch* b, BatchDesc* d) const {
     if (!has_device) return fail(QSA_ERR_NO_DEVICE, "cache has no device storage");
@@ -276,6 +298,53 @@ struct qsa_cache {
     return QSA_OK;
   }
 };
+
+namespace {
+
+qsa_status_t check_budget(const qsa_cache* c, int32_t budget_tokens) {
+  if (budget_tokens < 4 || budget_tokens % 4 || budget_tokens > c->cfg.budget_tokens)
+    return fail(QSA_ERR_INVALID_ARG, "budget_tokens %d must be a multiple of 4 in [4, %d]", budget_tokens,
+                c->cfg.budget_tokens);
+  return QSA_OK;
+}
+
+qsa_status_t check_stride(const ChunkDesc& d, int64_t blk_stride) {
+  for (int u = 0; u < d.b.n_units; ++u)
+    if (d.unit_tokens(u) > 0 && blk_stride < (d.b.u[u].n + 3) / 4)
+      return fail(QSA_ERR_INVALID_ARG, "blk_stride %lld < %lld blocks of unit %d", (long long)blk_stride,
+                  (long long)((d.b.u[u].n + 3) / 4), u);
+  return QSA_OK;
+}
+
+// Change every slot (and pending row) of every live request that names a
+// moved row.  Moves are ascending and go down, so a row's new place is never
+// inside the old place of a later move: they can be applied in pieces.
+cudaError_t remap_slots(const qsa_cache* c, const std::vector<RowMove>& moves, cudaStream_t s) {
+  const bool hot = c->cfg.hot_rows > 0;
+  const WorkspaceLayout w = workspace_layout(c->cfg);
+  for (size_t m0 = 0; m0 < moves.size(); m0 += kMaxMoves) {
+    RemapParams p{};
+    p.n_layers = c->cfg.n_layers;
+    p.ctx_cap = c->cfg.ctx_capacity;
+    p.slot_table = c->cfg.slot_table;
+    p.pend_stride = hot ? c->cfg.budget_tokens : 0;
+    p.hot_pend = hot ? c->ws_at<int32_t>(w.hot_pend) : nullptr;
+    for (size_t m = m0; m < moves.size() && p.n_moves < kMaxMoves; ++m) p.moves[p.n_moves++] = moves[m];
+    for (size_t i = 0; i < c->leases.size(); ++i) {
+      if (c->leases[i].active) {
+        p.req[p.n_req] = (int32_t)i;
+        p.ctx[p.n_req++] = (int32_t)c->leases[i].ctx_len;
+      }
+      if (p.n_req == kMaxRemaps || (p.n_req > 0 && i + 1 == c->leases.size())) {
+        if (const cudaError_t e = launch_remap(p, s)) return e;
+        p.n_req = 0;
+      }
+    }
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -726,6 +795,226 @@ qsa_status_t qsa_sparse_decode_attn(qsa_cache* c, const qsa_batch* batch, const 
                                      static_cast<const uint8_t*>(gathered), softmax_scale, out,
                                      lse, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+  return ok();
+}
+
+qsa_status_t qsa_append_chunk(qsa_cache* c, const qsa_chunk* chunk, const float* k_new,
+                              const void* kv_new, void* stream) {
+  if (!c) return fail(QSA_ERR_INVALID_ARG, "null cache");
+  DeviceGuard guard(c->device);
+  if (qsa_status_t st = c->check_stream(stream, guard)) return st;
+  ChunkDesc d;
+  if (qsa_status_t st = c->build_chunk(chunk, &d)) return st;
+  if (d.rows() == 0) return ok();
+  if (!k_new || !kv_new) return fail(QSA_ERR_INVALID_ARG, "null k_new or kv_new");
+  if (reinterpret_cast<uintptr_t>(k_new) % 16 || reinterpret_cast<uintptr_t>(kv_new) % 16)
+    return fail(QSA_ERR_INVALID_ARG, "k_new and kv_new must be 16-byte aligned");
+  ChunkTargets tg;
+  for (int u = 0; u < d.b.n_units; ++u) {
+    const Lease& l = c->leases[d.b.u[u].req];
+    tg.row_base[u] = l.placement == QSA_KV_HOST ? -1 : l.row_base + (int64_t)d.b.u[u].layer * l.layer_rows;
+    tg.ring[u] = l.placement == QSA_KV_HOST_RING ? l.layer_rows : 0;
+  }
+  cudaError_t e = launch_append_chunk(d, tg, k_new, static_cast<const uint8_t*>(kv_new),
+                                      static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "chunk append launch");
+  return ok();
+}
+
+qsa_status_t qsa_chunk_index_score(qsa_cache* c, const qsa_chunk* chunk, const void* q_idx,
+                                   int32_t query_type, const float* w, float* blk_scores,
+                                   int64_t blk_stride, void* stream) {
+  if (!c) return fail(QSA_ERR_INVALID_ARG, "null cache");
+  DeviceGuard guard(c->device);
+  if (qsa_status_t st = c->check_stream(stream, guard)) return st;
+  ChunkDesc d;
+  if (qsa_status_t st = c->build_chunk(chunk, &d)) return st;
+  if (query_type != QSA_QUERY_F32 && query_type != QSA_QUERY_BF16)
+    return fail(QSA_ERR_INVALID_ARG, "unknown query_type %d", query_type);
+  if (d.rows() == 0) return ok();
+  if (!q_idx || !w || !blk_scores) return fail(QSA_ERR_INVALID_ARG, "null q_idx, w or blk_scores");
+  if (reinterpret_cast<uintptr_t>(q_idx) % 16 || reinterpret_cast<uintptr_t>(w) % 16 ||
+      reinterpret_cast<uintptr_t>(blk_scores) % 16)
+    return fail(QSA_ERR_INVALID_ARG, "q_idx, w and blk_scores must be 16-byte aligned");
+  if (qsa_status_t st = check_stride(d, blk_stride)) return st;
+  cudaError_t e = launch_chunk_score(d, q_idx, query_type == QSA_QUERY_BF16, w, blk_scores, blk_stride,
+                                     static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "chunk score launch");
+  return ok();
+}
+
+qsa_status_t qsa_chunk_select_topk(qsa_cache* c, const qsa_chunk* chunk, const float* blk_scores,
+                                   int64_t blk_stride, int32_t budget_tokens, int32_t* sel_blocks,
+                                   int32_t* n_sel, void* stream) {
+  if (!c) return fail(QSA_ERR_INVALID_ARG, "null cache");
+  DeviceGuard guard(c->device);
+  if (qsa_status_t st = c->check_stream(stream, guard)) return st;
+  ChunkDesc d;
+  if (qsa_status_t st = c->build_chunk(chunk, &d)) return st;
+  if (qsa_status_t st = check_budget(c, budget_tokens)) return st;
+  if (d.rows() == 0) return ok();
+  if (!blk_scores || !sel_blocks || !n_sel) return fail(QSA_ERR_INVALID_ARG, "null array");
+  if (reinterpret_cast<uintptr_t>(blk_scores) % 16 || reinterpret_cast<uintptr_t>(sel_blocks) % 16 ||
+      reinterpret_cast<uintptr_t>(n_sel) % 16)
+    return fail(QSA_ERR_INVALID_ARG, "blk_scores, sel_blocks and n_sel must be 16-byte aligned");
+  if (qsa_status_t st = check_stride(d, blk_stride)) return st;
+  cudaError_t e = launch_chunk_topk(d, blk_scores, blk_stride, budget_tokens / 4, sel_blocks, n_sel,
+                                    static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "chunk top-k launch");
+  return ok();
+}
+
+int64_t qsa_chunk_attn_workspace_bytes(qsa_cache* c, const qsa_chunk* chunk, int32_t budget_tokens) {
+  if (!c) { fail(QSA_ERR_INVALID_ARG, "null cache"); return -1; }
+  DeviceGuard guard(c->device);
+  if (guard.status() != cudaSuccess) { cuda_fail(guard.status(), "making the cache's device current"); return -1; }
+  ChunkDesc d;
+  if (c->build_chunk(chunk, &d) != QSA_OK || check_budget(c, budget_tokens) != QSA_OK) return -1;
+  const int64_t bytes = chunk_attn_workspace(d, budget_tokens);
+  ok();
+  return bytes;
+}
+
+qsa_status_t qsa_chunk_sparse_attn(qsa_cache* c, const qsa_chunk* chunk, const uint16_t* q,
+                                   const int32_t* sel_blocks, const int32_t* n_sel,
+                                   int32_t budget_tokens, float softmax_scale, uint16_t* out,
+                                   float* lse, void* workspace, int64_t workspace_bytes,
+                                   void* stream) {
+  if (!c) return fail(QSA_ERR_INVALID_ARG, "null cache");
+  DeviceGuard guard(c->device);
+  if (qsa_status_t st = c->check_stream(stream, guard)) return st;
+  ChunkDesc d;
+  if (qsa_status_t st = c->build_chunk(chunk, &d)) return st;
+  if (qsa_status_t st = check_budget(c, budget_tokens)) return st;
+  if (!(softmax_scale == softmax_scale)) return fail(QSA_ERR_INVALID_ARG, "softmax_scale is NaN");
+  if (d.rows() == 0) return ok();
+  if (!q || !sel_blocks || !n_sel || !out || !workspace) return fail(QSA_ERR_INVALID_ARG, "null array");
+  if (reinterpret_cast<uintptr_t>(q) % 16 || reinterpret_cast<uintptr_t>(out) % 16 ||
+      reinterpret_cast<uintptr_t>(workspace) % 16 || reinterpret_cast<uintptr_t>(lse) % 16 ||
+      reinterpret_cast<uintptr_t>(sel_blocks) % 16 || reinterpret_cast<uintptr_t>(n_sel) % 16)
+    return fail(QSA_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+  const int64_t need = chunk_attn_workspace(d, budget_tokens);
+  if (workspace_bytes < need)
+    return fail(QSA_ERR_INVALID_ARG, "workspace has %lld bytes, needs %lld", (long long)workspace_bytes,
+                (long long)need);
+  cudaError_t e = launch_chunk_attn(d, q, sel_blocks, n_sel, budget_tokens, softmax_scale, out, lse,
+                                    workspace, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+  return ok();
+}
+
+qsa_status_t qsa_request_truncate(qsa_cache* c, qsa_handle h, int64_t new_ctx_len) {
+  if (!c) return fail(QSA_ERR_INVALID_ARG, "null cache");
+  const Lease* cl;
+  if (qsa_status_t st = c->check_handle(h, &cl)) return st;
+  if (new_ctx_len < 1 || new_ctx_len > cl->ctx_len)
+    return fail(QSA_ERR_INVALID_ARG, "new_ctx_len %lld outside [1, %lld]", (long long)new_ctx_len,
+                (long long)cl->ctx_len);
+  c->leases[h.index].ctx_len = new_ctx_len;
+  return ok();
+}
+
+qsa_status_t qsa_request_fork(qsa_cache* c, qsa_handle parent, const qsa_request_desc* desc, void* stream,
+                              qsa_handle* out) {
+  if (!c || !desc || !out) return fail(QSA_ERR_INVALID_ARG, "null argument");
+  const Lease* pl;
+  if (qsa_status_t st = c->check_handle(parent, &pl)) return st;
+  if (desc->ctx_len < 1 || desc->ctx_len > pl->ctx_len)
+    return fail(QSA_ERR_INVALID_ARG, "ctx_len %lld outside [1, %lld], the parent's tokens",
+                (long long)desc->ctx_len, (long long)pl->ctx_len);
+  qsa_handle child;
+  if (qsa_status_t st = qsa_request_begin(c, desc, stream, &child)) return st;
+  const Lease& l = c->leases[child.index];
+  const int64_t R = c->row_bytes();
+  if (pl->host_rows && l.host_rows) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(pl->host_rows), b = reinterpret_cast<uintptr_t>(l.host_rows);
+    if (a < b + (uint64_t)(c->cfg.n_layers * l.max_ctx * R) && b < a + (uint64_t)(c->cfg.n_layers * pl->max_ctx * R)) {
+      qsa_request_end(c, child);
+      return fail(QSA_ERR_INVALID_ARG, "host_rows overlaps the parent's host history");
+    }
+  }
+  if (c->has_device) {
+    DeviceGuard guard(c->device);
+    ForkParams p{};
+    p.src_req = (int32_t)parent.index;
+    p.dst_req = (int32_t)child.index;
+    p.n_layers = c->cfg.n_layers;
+    p.n_tokens = l.ctx_len;
+    p.ctx_cap = c->cfg.ctx_capacity;
+    p.pool_rows = c->cfg.hbm_pool_rows;
+    p.index_keys = c->cfg.index_keys;
+    p.index_scales = c->cfg.index_scales;
+    p.slot_table = c->cfg.slot_table;
+    p.pool = static_cast<uint8_t*>(c->cfg.hbm_pool);
+    p.row_bytes = (int32_t)R;
+    p.src_host = pl->host_rows;
+    p.src_stride = pl->max_ctx;
+    p.dst_host = const_cast<uint8_t*>(l.host_rows);
+    p.dst_stride = l.max_ctx;
+    p.dst_base = l.row_base;
+    p.dst_layer_rows = l.layer_rows;
+    p.dst_ring = l.placement == QSA_KV_HOST_RING;
+    p.err = c->err();
+    cudaError_t e = guard.status();
+    if (e == cudaSuccess) e = launch_fork(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) {
+      qsa_request_end(c, child);
+      return cuda_fail(e, "fork launch");
+    }
+  }
+  *out = child;
+  return ok();
+}
+
+qsa_status_t qsa_cache_compact(qsa_cache* c, void* stream, int64_t* moved_rows) {
+  if (!c) return fail(QSA_ERR_INVALID_ARG, "null cache");
+  DeviceGuard guard(c->device);
+  if (qsa_status_t st = c->check_stream(stream, guard)) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (c->has_device) {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    const cudaError_t e = cudaStreamIsCapturing(s, &cs);
+    if (e != cudaSuccess) return cuda_fail(e, "querying the stream's capture status");
+    if (cs != cudaStreamCaptureStatusNone)
+      return fail(QSA_ERR_INVALID_ARG, "the pool's layout cannot change in a captured graph");
+  }
+  try {
+    std::vector<Lease*> held;      // leases with pool rows, ascending
+    for (Lease& l : c->leases)
+      if (l.active && l.rows > 0) held.push_back(&l);
+    std::sort(held.begin(), held.end(), [](const Lease* a, const Lease* b) { return a->row_base < b->row_base; });
+    std::vector<RowMove> moves;
+    int64_t at = c->staging_total, moved = 0;
+    for (const Lease* l : held) {
+      if (l->row_base > at) {
+        moves.push_back({l->row_base, l->rows, l->row_base - at});
+        moved += l->rows;
+      }
+      at += l->rows;
+    }
+    std::map<int64_t, int64_t> free_rows;
+    if (at < c->cfg.hbm_pool_rows) free_rows[at] = c->cfg.hbm_pool_rows - at;
+    if (c->has_device) {
+      cudaError_t e = cudaSuccess;
+      for (const RowMove& m : moves) {
+        if (e == cudaSuccess)
+          e = launch_move_rows(static_cast<uint8_t*>(c->cfg.hbm_pool), c->row_bytes(), m.from, m.from - m.down,
+                               m.rows, s);
+      }
+      if (e == cudaSuccess && !moves.empty()) e = remap_slots(c, moves, s);
+      if (e != cudaSuccess) return cuda_fail(e, "compaction launch");
+    }
+    at = c->staging_total;
+    for (Lease* l : held) {
+      if (l->hot_base >= 0) l->hot_base -= l->row_base - at;
+      l->row_base = at;
+      at += l->rows;
+    }
+    c->free_rows.swap(free_rows);
+    if (moved_rows) *moved_rows = moved;
+  } catch (const std::bad_alloc&) {
+    return fail(QSA_ERR_INVALID_ARG, "out of host memory");
+  }
   return ok();
 }
 

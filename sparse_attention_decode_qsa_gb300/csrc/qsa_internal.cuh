@@ -52,6 +52,11 @@ enum KernelId : int32_t {
   kKernSlotSet = 6,
   kKernAppend = 7,
   kKernHot = 8,
+  kKernChunkAppend = 9,
+  kKernChunkScore = 10,
+  kKernChunkTopk = 11,
+  kKernChunkAttn = 12,
+  kKernFork = 13,
 };
 
 // One decode unit (request slot, layer) of a call.
@@ -98,6 +103,27 @@ struct BatchDesc {
   }
   __host__ __device__ int64_t unit_state(int u_) const {
     return (int64_t)u[u_].req * n_layers + u[u_].layer;
+  }
+};
+
+// A chunk: unit u holds the rows row0[u] .. row0[u+1]-1 of the call, the newest
+// tokens of its request in ascending order.
+struct ChunkDesc {
+  BatchDesc b;
+  int32_t row0[kMaxUnits + 1];
+
+  __host__ __device__ int rows() const { return row0[b.n_units]; }
+  __host__ __device__ int unit_tokens(int u_) const { return row0[u_ + 1] - row0[u_]; }
+  // Position of row x of unit u_ in its request's context.
+  __host__ __device__ int64_t position(int u_, int x) const { return b.u[u_].n - row0[u_ + 1] + x; }
+  // Unit of row x (units without rows are passed over).
+  __device__ int unit_of_row(int x) const {
+    int lo = 0, hi = b.n_units - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (row0[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
   }
 };
 
@@ -316,6 +342,76 @@ cudaError_t launch_append_token(const BatchDesc& b, const AppendTargets& tg, con
 // misses from host memory and writes them into their hot rows.
 cudaError_t launch_hot_fetch(const BatchDesc& b, const int32_t* sel_blocks, const int32_t* n_sel,
                              int32_t budget_tokens, bool copy_rows, cudaStream_t s);
+
+// Chunk forms: as the launchers above for every row of a chunk.  row_base: the
+// first pool row of each unit's region at its layer (-1: none), ring: its ring
+// length (0: a resident region, token t in region row t).
+struct ChunkTargets {
+  int64_t row_base[kMaxUnits];
+  int32_t ring[kMaxUnits];
+};
+
+cudaError_t launch_append_chunk(const ChunkDesc& c, const ChunkTargets& tg, const float* k_new,
+                                const uint8_t* kv_new, cudaStream_t s);
+
+cudaError_t launch_chunk_score(const ChunkDesc& c, const void* q_idx, bool q_bf16, const float* w,
+                               float* blk_scores, int64_t blk_stride, cudaStream_t s);
+
+cudaError_t launch_chunk_topk(const ChunkDesc& c, const float* blk_scores, int64_t blk_stride,
+                              int32_t k_max, int32_t* sel_blocks, int32_t* n_sel, cudaStream_t s);
+
+int64_t chunk_attn_workspace(const ChunkDesc& c, int32_t budget_tokens);
+
+cudaError_t launch_chunk_attn(const ChunkDesc& c, const uint16_t* q, const int32_t* sel_blocks,
+                              const int32_t* n_sel, int32_t budget_tokens, float softmax_scale,
+                              uint16_t* out, float* lse, void* workspace, cudaStream_t s);
+
+// Pages: copy the first n_tokens tokens of a request (all layers) to another.
+struct ForkParams {
+  int32_t src_req, dst_req;      // request slots
+  int32_t n_layers;
+  int64_t n_tokens;
+  int64_t ctx_cap, pool_rows;
+  uint8_t* index_keys;
+  uint16_t* index_scales;
+  const int32_t* slot_table;
+  uint8_t* pool;
+  int32_t row_bytes;
+  const uint8_t* src_host;       // parent's host history or nullptr
+  int64_t src_stride;            // its rows per layer
+  uint8_t* dst_host;             // child's host history or nullptr
+  int64_t dst_stride;
+  int64_t dst_base;              // child's pool region
+  int32_t dst_layer_rows;        // its rows per layer (0: none)
+  int32_t dst_ring;              // 1: the region is a tail ring
+  ErrorWord* err;
+};
+
+cudaError_t launch_fork(const ForkParams& p, cudaStream_t s);
+
+// Move `rows` rows from pool row `from` to the lower row `to` (they may overlap).
+cudaError_t launch_move_rows(uint8_t* pool, int64_t row_bytes, int64_t from, int64_t to, int64_t rows,
+                             cudaStream_t s);
+
+// Rows [from, from + rows) of the pool have moved down by `down` rows.
+struct RowMove {
+  int64_t from, rows, down;
+};
+constexpr int kMaxMoves = 128;      // of one launch_remap
+constexpr int kMaxRemaps = 128;     // requests of one launch_remap
+struct RemapParams {
+  int32_t n_moves;                  // ascending by `from`
+  int32_t n_req;
+  int32_t n_layers;
+  int32_t pend_stride;              // entries of a pending map (0: no hot cache)
+  int64_t ctx_cap;
+  int32_t* slot_table;
+  int32_t* hot_pend;
+  RowMove moves[kMaxMoves];
+  int32_t req[kMaxRemaps];          // request slot
+  int32_t ctx[kMaxRemaps];          // its tokens
+};
+cudaError_t launch_remap(const RemapParams& p, cudaStream_t s);
 
 // Slot-table maintenance.
 cudaError_t launch_slot_fill(int32_t* rows, int32_t n_layers, int64_t ctx_cap, int64_t ctx_len,
