@@ -7,30 +7,32 @@
 // section "Механизм гибридного разреженного оффлоадинга").
 //
 // 1024 flops per (query, token): a dense contraction keys[tokens][64] x
-// q^T[64][queries x 8 heads], on the tensor cores (tcgen05, kind::f16, bf16
-// operands, fp32 accumulators).  An e4m3 code is exact in bf16; an fp32 query
-// goes in as three bf16 pieces (q = p0 + p1 + p2, each the round-to-nearest
-// bf16 of what is left: 24 bits), accumulated in the same tile, a bf16 query
-// as itself.  So products are exact and sums are fp32.
+// q^T[64][queries x 8 heads], on the tensor cores (tcgen05, kind::f16, fp32
+// accumulators) with f16 operands.  An e4m3 code is exact in f16, one
+// conversion instruction for two.  A query row (one head) is scaled by a power
+// of two until its largest element is in [1/2, 1); there f16 holds a bf16
+// element exactly down to 2^-17 of the largest and to 2^-25 of it below; an
+// fp32 query goes in as two pieces (the round-to-nearest f16, and that of what
+// is left), which together are off by at most 2^-25 of the row's largest
+// element.  Products are exact and sums are fp32.
 //
-// Tiling.  A group of queries (64 bf16 ones, 32 fp32 ones: what three pieces
-// leave room for) stays in shared memory as the B operand, up to 256 columns
-// (32 queries x 8 heads) per tile, while the keys stream past.  A step is 512
-// tokens = 128 blocks in four phases: phase k multiplies the tokens 4b + k, so
-// that a tensor-memory lane is a block, and the thread that owns the lane
-// takes the maximum over the block's four tokens in its registers, with no
-// exchange between threads, and stores 32 neighbouring blocks per warp.
-// The codes are turned into bf16 on the way from global to shared memory:
-// exponent and mantissa bits move into place and one multiplication by 2^120
-// corrects the bias (subnormal codes included).
+// Tiling.  A group of 64 queries stays in shared memory as the B operand, four
+// tiles of up to 128 columns (16 queries x 8 heads), while the keys stream
+// past.  A step is 512 tokens = 128 blocks in four phases: phase k multiplies
+// the tokens 4b + k, so that a tensor-memory lane is a block, and the thread
+// that owns the lane takes the maximum over the block's four tokens in its
+// registers, with no exchange between threads, and stores 32 neighbouring
+// blocks per warp.
 //
-// Warp roles (one CTA per SM, all of tensor memory: two accumulators of 256
-// columns): 8 epilogue warps (relu, head weights, scale, maximum), 4 converter
-// warps (a step's codes in flight in registers), one MMA warp.  All waits are
-// bounded.  The steps of all groups form one list, cut into equal runs, one
-// per CTA; a run that crosses into another group rebuilds B.
+// Warp roles (one CTA per SM, all of tensor memory: four accumulators of
+// 128 columns): 2 converter warps, one MMA warp, and 4 epilogue warps per
+// accumulator (relu, head weights, scale, maximum), so that an accumulator's
+// MMAs run while the others' are read.
+// All waits are bounded.  The steps of all groups form one list, cut into
+// equal runs, one per CTA; a run that crosses into another group rebuilds B.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include "tc_common.cuh"
 
@@ -39,27 +41,31 @@ namespace {
 
 using namespace tc;
 
-constexpr int kEpiWarps = 8, kConvWarps = 4;
-constexpr int kThreads = 32 * (kEpiWarps + kConvWarps + 1);     // 416
-constexpr int kRoleConv = kEpiWarps, kRoleMma = kEpiWarps + kConvWarps;
-constexpr int kTileQueries = 32;                  // queries per B tile: 256 columns
+constexpr int kAccs = 4;                          // tiles, each with its accumulator
+constexpr int kAccCols = 512 / kAccs;
+constexpr int kTileQueries = kAccCols / kIndexHeads;             // at most, per tile: 16
+constexpr int kGroup = kAccs * kTileQueries;      // queries per group: 64
+constexpr int kEpiWarps = 4;                      // epilogue warps per accumulator
+constexpr int kConvWarps = 2;
+constexpr int kConvLoads = 512 / (32 * kConvWarps);              // 16-byte loads per lane and phase
+// 19 warps: five on a scheduler at most, which leaves 96 registers per thread
+constexpr int kThreads = 32 * (kAccs * kEpiWarps + kConvWarps + 1);
+constexpr int kRoleConv = kAccs * kEpiWarps, kRoleMma = kRoleConv + kConvWarps;
 constexpr int kStepTokens = 512;                  // tokens per step: 128 blocks of 4
-constexpr int kABytes = 128 * kIndexDim * 2;      // one phase: 128 tokens of 64 bf16
-constexpr int kBTile = 8 * kTileQueries * kIndexDim * 2;        // 32 KiB
+constexpr int kABytes = 128 * kIndexDim * 2;      // one phase: 128 tokens of 64 f16
+constexpr int kBTile = kAccCols * kIndexDim * 2;  // 16 KiB
 constexpr uint32_t kTmemCols = 512;
 
-// Shared memory: the ring of phases (16 KiB each; a step's four stay until
-// both tiles have read them), B, head weights, barriers.
+// Shared memory: the ring of phases (16 KiB each), B (piece by piece, tile by
+// tile), head weights, barriers.
 template <bool kBf16>
 struct Layout {
-  static constexpr int kGroup = kBf16 ? 64 : 32;                 // queries per group
-  static constexpr int kQTiles = kGroup / kTileQueries;          // accumulators per phase
-  static constexpr int kPieces = kBf16 ? 1 : 3;
-  static constexpr int kStages = kBf16 ? 8 : 6;
+  static constexpr int kPieces = kBf16 ? 1 : 2;
+  static constexpr int kStages = kBf16 ? 6 : 5;
   static constexpr int kOffB = kStages * kABytes;
-  static constexpr int kOffW = kOffB + kQTiles * kPieces * kBTile;
+  static constexpr int kOffW = kOffB + kAccs * kPieces * kBTile;
   static constexpr int kOffBar = kOffW + kGroup * kIndexHeads * 4;
-  static constexpr int kNumBars = 2 * kStages + 4 + 1;           // a_full, a_empty, d_full, d_empty, done
+  static constexpr int kNumBars = 2 * kStages + 2 * kAccs + 1;   // a_full, a_empty, d_full, d_empty, done
   static constexpr int kOffSlot = kOffBar + 8 * kNumBars;
   static constexpr int kSmemBytes = kOffSlot + 16 + 1024;        // + alignment to 1024
   static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
@@ -79,41 +85,52 @@ struct ChunkScoreParams {
 // 1) / 512 + 1 of them.  With R = 512 / G and A = (first + G - 1) / G that is
 // (A + i) / R + 1, so the sum is closed.  (The unit's last group may hold
 // fewer queries and fewer steps; the callers cap it.)
-template <int G>
 __host__ __device__ __forceinline__ int64_t steps_before(int64_t first, int64_t j) {
-  constexpr int64_t R = kStepTokens / G;
+  constexpr int64_t G = kGroup, R = kStepTokens / G;
   const int64_t A = (first + G - 1) / G;
   auto S = [](int64_t m) { const int64_t q = m / R; return R * q * (q - 1) / 2 + (m % R) * q; };
   return S(A + j) - S(A) + j;
 }
-template <int G>
 __host__ __device__ __forceinline__ int64_t unit_steps(int64_t n, int64_t tokens) {
   if (tokens == 0) return 0;
-  const int64_t groups = (tokens + G - 1) / G;
-  return steps_before<G>(n - tokens, groups - 1) + (n - 1) / kStepTokens + 1;
+  const int64_t groups = (tokens + kGroup - 1) / kGroup;
+  return steps_before(n - tokens, groups - 1) + (n - 1) / kStepTokens + 1;
 }
 
-// Two bf16 from two e4m3 codes placed at bits 7-0 and 23-16 of x.
-__device__ __forceinline__ uint32_t to_bf16x2(uint32_t magnitude_at_4, uint32_t sign_at_15) {
-  const uint32_t raw = magnitude_at_4 | sign_at_15;
-  uint32_t out;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(out) : "r"(raw), "r"(0x7B807B80u));   // 2^120 twice
-  return out;
-}
-// Codes c0..c3 of a word as bf16 in the order c0, c2, c1, c3 (B has the same).
+// Four codes as f16.
 __device__ __forceinline__ uint2 convert4(uint32_t w) {
-  return make_uint2(to_bf16x2((w & 0x007F007Fu) << 4, (w & 0x00800080u) << 8),
-                    to_bf16x2((w & 0x7F007F00u) >> 4, w & 0x80008000u));
+  const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
+  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+  return make_uint2((uint32_t)a.x | ((uint32_t)a.y << 16), (uint32_t)b.x | ((uint32_t)b.y << 16));
 }
-__device__ __forceinline__ int dim_of(int place) {
-  const int r = place & 3;
-  return (place & ~3) | (r == 1 ? 2 : r == 2 ? 1 : r);
+
+// relu(x) * 2^-15 of dot products |x| <= 2^15 (64 elements below 1 by codes up
+// to 448), two as a pair: a saturating multiplication, which runs on the
+// multiply-add pipe; the one that takes maxima is half as wide.  Products and
+// multiply-adds of pairs.
+__device__ __forceinline__ uint64_t relu2(uint32_t a, uint32_t b) {
+  uint64_t d;
+  asm("{\n .reg .f32 x, y;\n mul.sat.f32 x, %1, 0f38000000;\n mul.sat.f32 y, %2, 0f38000000;\n"
+      " mov.b64 %0, {x, y};\n}\n"
+      : "=l"(d)
+      : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
 }
 
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_constant__ ChunkScoreParams p) {
   using L = Layout<kBf16>;
-  constexpr int G = L::kGroup, kQTiles = L::kQTiles, kPieces = L::kPieces, kStages = L::kStages;
+  constexpr int kPieces = L::kPieces, kStages = L::kStages;
   constexpr int kOffB = L::kOffB, kOffW = L::kOffW, kOffBar = L::kOffBar, kOffSlot = L::kOffSlot;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -123,8 +140,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
   auto a_full = [&](int i) { return bars + 8u * (uint32_t)i; };
   auto a_empty = [&](int i) { return bars + 8u * (uint32_t)(kStages + i); };
   auto d_full = [&](int i) { return bars + 8u * (uint32_t)(2 * kStages + i); };
-  auto d_empty = [&](int i) { return bars + 8u * (uint32_t)(2 * kStages + 2 + i); };
-  const uint32_t done = bars + 8u * (uint32_t)(2 * kStages + 4);
+  auto d_empty = [&](int i) { return bars + 8u * (uint32_t)(2 * kStages + kAccs + i); };
+  const uint32_t done = bars + 8u * (uint32_t)(2 * kStages + 2 * kAccs);
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kOffSlot);
   __shared__ int s_fail;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -134,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
     tmem_alloc<kTmemCols>(slot);
     if (lane == 0) {
       for (int i = 0; i < kStages; ++i) { mbar_init(a_full(i), 32 * kConvWarps); mbar_init(a_empty(i), 1); }
-      for (int i = 0; i < 2; ++i) { mbar_init(d_full(i), 1); mbar_init(d_empty(i), 32 * kEpiWarps); }
+      for (int i = 0; i < kAccs; ++i) { mbar_init(d_full(i), 1); mbar_init(d_empty(i), 32 * kEpiWarps); }
       mbar_init(done, 1);
       mbar_fence_init();
       s_fail = 0;
@@ -150,7 +167,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
   int64_t at = total * blockIdx.x / gridDim.x;
   const int64_t end = total * (blockIdx.x + 1) / gridDim.x;
   int phase = 0;      // phases streamed by this CTA (ring position)
-  int job = 0;        // accumulators filled
+  int fills = 0;      // epilogue: times its accumulator was filled
+  uint32_t used = 0, turn = 0;   // MMA warp, a bit per accumulator: filled before, parity of the next wait
   while (at < end) {
     // ---- the group and its part of the run
     int u = 0;
@@ -167,82 +185,88 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
     const int64_t first = n - tokens, local = at - p.step0[u];
     int grp = 0;
     {
-      int lo = 0, hi = (tokens + G - 1) / G - 1;
+      int lo = 0, hi = (tokens + kGroup - 1) / kGroup - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (steps_before<G>(first, mid) <= local) lo = mid; else hi = mid - 1;
+        if (steps_before(first, mid) <= local) lo = mid; else hi = mid - 1;
       }
       grp = lo;
     }
-    const int nq = tokens - grp * G < G ? tokens - grp * G : G;
-    const int64_t pos0 = first + (int64_t)grp * G;             // position of the group's first query
-    const int x0 = p.c.row0[u] + grp * G;
-    const int64_t s0 = local - steps_before<G>(first, grp);
+    const int nq = tokens - grp * kGroup < kGroup ? tokens - grp * kGroup : kGroup;
+    const int64_t pos0 = first + (int64_t)grp * kGroup;             // position of the group's first query
+    const int x0 = p.c.row0[u] + grp * kGroup;
+    const int64_t s0 = local - steps_before(first, grp);
     const int64_t s_all = (pos0 + nq - 1) / kStepTokens + 1;
     const int64_t s1 = s_all - s0 < end - at ? s_all : s0 + (end - at);
     at += s1 - s0;
     const int64_t row0 = p.c.b.unit_row(u);
-    // columns of each tile: 8 per query, in multiples of 16
-    auto tile_cols = [&](int t) {
-      const int q = nq - t * kTileQueries;
-      return q <= 0 ? 0 : (q >= kTileQueries ? 256 : (8 * q + 15) / 16 * 16);
-    };
+    // queries per tile (a multiple of 4: 32 columns) and tiles with queries
+    const int qt = ((nq + kAccs - 1) / kAccs + 3) / 4 * 4;
+    const int tiles = (nq + qt - 1) / qt;
 
     // ---- B and the head weights (all threads; the previous run is complete).
-    // Row r of a tile is head r & 7 of query r >> 3; rows past the group are 0.
-    for (int i = tid; i < G * kIndexHeads * (kIndexDim / 8); i += kThreads) {
-      const int c = i & 7, r = i >> 3;                         // chunk of 8 places, row over both tiles
+    // Row r of a tile is head r & 7 of the tile's query r >> 3, scaled by 2^-k
+    // (its largest element is in [2^(k-1), 2^k)); its head weight takes the
+    // inverse, and the 2^15 of relu2.  Rows past the group are 0.
+    for (int i = tid; i < tiles * qt * kIndexHeads * (kIndexDim / 8); i += kThreads) {
+      const int c = i & 7, r = i >> 3;                         // chunk of 8 places, row over all tiles
       const int q = r >> 3;
-      float v[8];
+      float v[8], top = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         v[e] = 0.f;
         if (q < nq) {
-          const int64_t src = ((int64_t)x0 * kIndexHeads + r) * kIndexDim + dim_of(8 * c + e);
+          const int64_t src = ((int64_t)x0 * kIndexHeads + r) * kIndexDim + 8 * c + e;
           v[e] = kBf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.q_idx)[src])
                        : reinterpret_cast<const float*>(p.q_idx)[src];
         }
+        top = fmaxf(top, fabsf(v[e]));
       }
-      const int tile = r >> 8, tr = r & 255;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));   // the row's 8 lanes
+      int k = 0;
+      if (top > 0.f) frexpf(top, &k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], -k);
+      if (c == 0) sw[r] = q < nq ? ldexpf(p.w[(int64_t)x0 * kIndexHeads + r], k + 15) : 0.f;
+      const int tile = q / qt, tr = r - tile * qt * kIndexHeads;
       uint8_t* dst = smem + kOffB + tile * kBTile + tr * 128 + ((c ^ (tr & 7)) << 4);
 #pragma unroll
       for (int pc = 0; pc < kPieces; ++pc) {
         uint32_t o[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+          const __half2 b = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
           o[e] = *reinterpret_cast<const uint32_t*>(&b);
           v[2 * e] -= __low2float(b);                          // exact
           v[2 * e + 1] -= __high2float(b);
         }
-        *reinterpret_cast<uint4*>(dst + pc * kBTile) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + pc * kAccs * kBTile) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
-    for (int i = tid; i < G * kIndexHeads; i += kThreads)
-      sw[i] = i < nq * kIndexHeads ? p.w[(int64_t)x0 * kIndexHeads + i] : 0.f;
     fence_async_smem();
     __syncthreads();
 
     const int steps = (int)(s1 - s0);
-    const int tiles = kQTiles == 2 && nq > kTileQueries ? 2 : 1;
     bool ok = true;
     if (warp >= kRoleConv && warp < kRoleMma) {
       // ---- converters: 16 codes per lane and load; lanes 4i .. 4i+3 hold one
-      // token, a warp 32 blocks in four loads per phase, the next phase's
-      // loads in flight.  A negative scale turns the code's sign.
+      // token, a load of a warp 8 blocks, the next phase's loads in flight.  A
+      // negative scale turns the code's sign.
       const int wc = warp - kRoleConv, sub = lane >> 2, part = lane & 3;
       const uint8_t* keys = p.c.b.index_keys + row0 * kIndexDim + part * 16;
       const uint16_t* scales = p.c.b.index_scales + row0;
-      uint4 v[2][4];
-      uint16_t sc[2][4];
+      uint4 v[2][kConvLoads];
+      uint32_t negative[2];                                    // bit j: load j's scale is negative
       auto load = [&](int e, int i) {                          // phase i of the run
-        const int64_t t0 = (s0 + (i >> 2)) * kStepTokens + 4 * (wc * 32 + sub) + (i & 3);
+        const int64_t t0 = (s0 + (i >> 2)) * kStepTokens + 4 * (wc * 8 * kConvLoads + sub) + (i & 3);
+        negative[e] = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kConvLoads; ++j) {
           const int64_t t = t0 + 32 * j;
           const bool in = i < 4 * steps && t < n;
           v[e][j] = in ? __ldg(reinterpret_cast<const uint4*>(keys + t * kIndexDim)) : make_uint4(0, 0, 0, 0);
-          sc[e][j] = in ? __ldg(scales + t) : (uint16_t)0;
+          negative[e] |= in ? (uint32_t)(__ldg(scales + t) >> 15) << j : 0u;
         }
       };
       load(0, 0);
@@ -256,9 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
           if (!ok) break;
           uint8_t* A = smem + st * kABytes;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int r = wc * 32 + j * 8 + sub;
-            const uint32_t flip = (sc[e][j] & 0x8000u) ? 0x80808080u : 0u;
+          for (int j = 0; j < kConvLoads; ++j) {
+            const int r = (wc * kConvLoads + j) * 8 + sub;
+            const uint32_t flip = (negative[e] >> j) & 1u ? 0x80808080u : 0u;
             const uint2 a = convert4(v[e][j].x ^ flip), b = convert4(v[e][j].y ^ flip);
             const uint2 c = convert4(v[e][j].z ^ flip), d = convert4(v[e][j].w ^ flip);
             *reinterpret_cast<uint4*>(A + r * 128 + (((2 * part) ^ (r & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
@@ -271,41 +295,44 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
         }
       }
     } else if (warp == kRoleMma) {
-      if (lane == 0) {
-        int jb = job;
+      const uint32_t idesc = idesc_f16((uint32_t)(8 * qt));
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      int st = phase % kStages;
+      uint32_t lap = (uint32_t)(phase / kStages) & 1u;
 #pragma unroll 1
-        for (int s = 0; s < steps && ok; ++s) {
+      for (int i = 0; i < 4 * steps && ok; ++i) {
+        ok = mbar_wait_warp(a_full(st), lap, err, kKernChunkScore);
 #pragma unroll 1
-          for (int i = 0; i < 4 * tiles && ok; ++i, ++jb) {
-            const int t = i >> 2, ph = phase + 4 * s + (i & 3), st = ph % kStages, buf = jb & 1;
-            if (t == 0) ok = mbar_wait(a_full(st), (uint32_t)(ph / kStages) & 1u, err, kKernChunkScore);
-            if (ok && jb >= 2) ok = mbar_wait(d_empty(buf), (uint32_t)(jb / 2 - 1) & 1u, err, kKernChunkScore);
-            if (!ok) break;
-            fence_after();
-            const uint32_t d = tmem + 256u * (uint32_t)buf;
-            const uint32_t idesc = idesc_bf16((uint32_t)tile_cols(t), false);
-            const uint32_t a = sb + st * kABytes;
+        for (int t = 0; t < tiles && ok; ++t) {
+          if ((used >> t) & 1u) ok = mbar_wait_warp(d_empty(t), (turn >> t) & 1u, err, kKernChunkScore);
+          if (!ok) break;
+          turn ^= ((used >> t) & 1u) << t;
+          used |= 1u << t;
+          fence_after();
+          if (elect_one()) {
+            const uint32_t d = tm + (uint32_t)(kAccCols * t), a = sb + st * kABytes;
+            const uint64_t a0 = desc_sw128(a, 16), b0 = desc_sw128(sb + kOffB + t * kBTile, 16);
 #pragma unroll
-            for (int pc = 0; pc < kPieces; ++pc) {
-              const uint32_t b = sb + kOffB + (t + pc) * kBTile;
+            for (int pc = 0; pc < kPieces; ++pc)
 #pragma unroll
               for (int ks = 0; ks < kIndexDim / 16; ++ks)
-                mma_ss(d, desc_sw128(a + 32 * ks, 16), desc_sw128(b + 32 * ks, 16), idesc, (pc | ks) != 0);
-            }
-            commit(d_full(buf));
+                mma_ss(d, a0 + 2 * ks, b0 + (uint64_t)(pc * kAccs * kBTile / 16 + 2 * ks), idesc, (pc | ks) != 0);
+            commit(d_full(t));
             if (t == tiles - 1) commit(a_empty(st));
           }
+          __syncwarp();
         }
+        if (++st == kStages) { st = 0; lap ^= 1u; }
       }
-      __syncwarp();
-    } else {
-      // ---- epilogue: thread = block (tensor-memory lane); warps 0-3 take
-      // queries 0-15 of a tile, warps 4-7 queries 16-31.  The loops over
-      // phases and tiles stay rolled: unrolled, the warp roles' code no longer
-      // fits the instruction cache (1573 us against 2048 x 131072 tokens).
-      const int half = warp >> 2, row = (warp & 3) * 32 + lane;
-      const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128u * (uint32_t)half;
+    } else if (warp / kEpiWarps < tiles) {
+      // ---- epilogue of one tile: thread = block (tensor-memory lane).  The
+      // loops over steps and phases stay rolled: with all phases unrolled the
+      // roles' code outgrew the instruction cache.
+      const int tile = warp / kEpiWarps, row = (warp & 3) * 32 + lane;
+      const int q0 = tile * qt, mine = nq - q0 < qt ? nq - q0 : qt;      // the tile's queries
+      const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(kAccCols * tile);
       const uint16_t* scales = p.c.b.index_scales + row0;
+      const ulonglong2* wq = reinterpret_cast<const ulonglong2*>(sw + q0 * kIndexHeads);
       uint16_t next[4];
       auto load_scales = [&](int64_t s) {
 #pragma unroll
@@ -315,7 +342,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
         }
       };
       load_scales(s0);
-      int jb = job;
 #pragma unroll 1
       for (int s = 0; s < steps && ok; ++s) {
         const int64_t b0 = (s0 + s) * (kStepTokens / 4);
@@ -326,56 +352,58 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
         if (s + 1 < steps) load_scales(s0 + s + 1);
         // every token of the step within every query's context?
         const bool whole = (s0 + s + 1) * kStepTokens - 1 <= pos0;
+        float best[kTileQueries];
+#pragma unroll
+        for (int i = 0; i < kTileQueries; ++i) best[i] = -INFINITY;
 #pragma unroll 1
-        for (int t = 0; t < tiles && ok; ++t) {
-          const int q0 = t * kTileQueries + 16 * half;         // this warp's first query
-          const float4* wq = reinterpret_cast<const float4*>(sw + q0 * kIndexHeads);
-          float best[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) best[i] = -INFINITY;
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            const int buf = jb & 1;
-            ok = mbar_wait(d_full(buf), (uint32_t)(jb / 2) & 1u, err, kKernChunkScore);
-            ++jb;
-            if (!ok) break;
-            fence_after();
-            const float m = k < 2 ? (k == 0 ? mag[0] : mag[1]) : (k == 2 ? mag[2] : mag[3]);
-            const uint32_t dcol = lane_base + 256u * (uint32_t)buf;
-            // queries before `from` do not see this token
-            const int64_t from = t0 + k - pos0 - q0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {                      // four queries: 32 columns
-              if (q0 + 4 * c >= nq) break;
-              uint32_t v[32];
-              ld32(dcol + 32 * c, v);
-              wait_ld();
-              reg_fence(v);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float4 wa = wq[2 * (4 * c + i)], wb = wq[2 * (4 * c + i) + 1];
-                const float wh[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-                float y = 0.f;
-#pragma unroll
-                for (int h = 0; h < 8; ++h) y = fmaf(wh[h], fmaxf(__uint_as_float(v[8 * i + h]), 0.f), y);
-                y *= m;
-                if (!whole && 4 * c + i < from) y = -INFINITY;
-                best[4 * c + i] = fmaxf(best[4 * c + i], y);
-              }
-            }
-            fence_before();
-            mbar_arrive(d_empty(buf));
-          }
+        for (int k = 0; k < 4; ++k) {
+          const float m = k < 2 ? (k == 0 ? mag[0] : mag[1]) : (k == 2 ? mag[2] : mag[3]);
+          ok = mbar_wait(d_full(tile), (uint32_t)fills & 1u, err, kKernChunkScore);
+          ++fills;
           if (!ok) break;
-          float* o = p.blk + (int64_t)(x0 + q0) * p.blk_stride + b0 + row;
+          fence_after();
+          // the tile's queries before `from` do not see this token
+          const int64_t from = t0 + k - pos0 - q0;
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (q0 + i < nq && t0 <= pos0 + q0 + i) o[i * p.blk_stride] = best[i];
+          for (int c = 0; c < kTileQueries / 4; ++c) {         // four queries: 32 columns
+            if (4 * c >= mine) break;
+            uint32_t v[32];
+            ld32(lane_base + 32u * (uint32_t)c, v);
+            wait_ld();
+            reg_fence(v);
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t* x = &v[8 * i];
+              const ulonglong2 wa = wq[2 * (4 * c + i)], wb = wq[2 * (4 * c + i) + 1];
+              uint64_t sum = mul2(wa.x, relu2(x[0], x[1]));
+              sum = fma2(wa.y, relu2(x[2], x[3]), sum);
+              sum = fma2(wb.x, relu2(x[4], x[5]), sum);
+              sum = fma2(wb.y, relu2(x[6], x[7]), sum);
+              y[i] = (__uint_as_float((uint32_t)sum) + __uint_as_float((uint32_t)(sum >> 32))) * m;
+            }
+            if (!whole) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (4 * c + i < from) y[i] = -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) best[4 * c + i] = fmaxf(best[4 * c + i], y[i]);
+          }
+          fence_before();
+          mbar_arrive(d_empty(tile));
+        }
+        if (!ok) break;
+        float* o = p.blk + (int64_t)(x0 + q0) * p.blk_stride + b0 + row;
+#pragma unroll
+        for (int i = 0; i < kTileQueries; ++i) {
+          if (i >= mine) break;
+          if (whole || t0 <= pos0 + q0 + i) *o = best[i];
+          o += p.blk_stride;
         }
       }
     }
     phase += 4 * steps;
-    job += 4 * steps * tiles;
     if (!ok) s_fail = 1;
     fence_before();
     __syncthreads();
@@ -395,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
 
 template <bool kBf16>
 cudaError_t launch(ChunkScoreParams& p, cudaStream_t s) {
-  constexpr int G = Layout<kBf16>::kGroup, kSmemBytes = Layout<kBf16>::kSmemBytes;
+  constexpr int kSmemBytes = Layout<kBf16>::kSmemBytes;
   static PerDeviceOnce setup;
   cudaError_t e = setup.run([] { return prefer_max_shared(chunk_score_kernel<kBf16>, kSmemBytes); });
   int sms = 0;
@@ -404,7 +432,7 @@ cudaError_t launch(ChunkScoreParams& p, cudaStream_t s) {
   int64_t total = 0;
   for (int u = 0; u < p.c.b.n_units; ++u) {
     p.step0[u] = (int32_t)total;
-    total += unit_steps<G>(p.c.b.u[u].n, p.c.unit_tokens(u));
+    total += unit_steps(p.c.b.u[u].n, p.c.unit_tokens(u));
     if (total > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   }
   p.step0[p.c.b.n_units] = (int32_t)total;

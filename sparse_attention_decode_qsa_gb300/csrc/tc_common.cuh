@@ -1,4 +1,4 @@
-// Tensor-core and barrier primitives shared by the chunk kernels: bf16
+// Tensor-core and barrier primitives shared by the chunk kernels: 16-bit
 // operands (kind::f16) in shared memory under the 128-byte swizzle, fp32
 // accumulators in tensor memory, bounded mbarrier waits.
 #pragma once
@@ -9,6 +9,7 @@ namespace qsa {
 namespace tc {
 
 constexpr uint32_t kWaitPolls = 1u << 20;   // bounded waits
+constexpr uint32_t kSuspendNs = 2000;       // a poll may sleep this long: polling warps take issue slots
 
 __device__ __forceinline__ uint32_t smem_u32(const void* ptr) { return (uint32_t)__cvta_generic_to_shared(ptr); }
 
@@ -22,10 +23,10 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
       " selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(kSuspendNs)
       : "memory");
   return ok != 0;
 }
@@ -38,6 +39,20 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, ErrorWo
     }
   }
   return true;
+}
+
+// Whole warp: the wait of every lane, its outcome the same for all.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, ErrorWord* err, int32_t kernel) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, err, kernel));
+}
+
+// One lane of a converged warp.  The MMA warps run their loops with all lanes
+// and elect one to issue: descriptors and barriers then stay in uniform
+// registers, where tcgen05 wants them.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
 }
 
 // Shared-memory writes of this thread become visible to the tensor core.
@@ -71,10 +86,13 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t leading)
          (1ull << 46) | (2ull << 61);
 }
 
-// kind::f16 instruction descriptor: D f32, A = B = bf16, M = 128, N (a multiple
-// of 16), A K-major, B K-major or MN-major.
+// kind::f16 instruction descriptor: D f32, A = B = f16 or bf16, M = 128, N (a
+// multiple of 16), A K-major, B K-major or MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t n) {
+  return (1u << 4) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
 __host__ __device__ constexpr uint32_t idesc_bf16(uint32_t n, bool b_mn_major) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn_major ? 1u << 16 : 0u) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+  return idesc_f16(n) | (1u << 7) | (1u << 10) | (b_mn_major ? 1u << 16 : 0u);
 }
 
 // D (tensor memory) [+]= A (shared) . B (shared)^T
@@ -98,7 +116,7 @@ __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// This thread's tensor-memory lane, 32 consecutive 32-bit columns.  Loaded
+// This thread's tensor-memory lane, 32 or 16 consecutive 32-bit columns.  Loaded
 // registers are valid after wait_ld(); reg_fence() keeps the compiler from
 // reading them earlier.
 __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -109,6 +127,14 @@ __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 }
