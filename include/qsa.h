@@ -518,10 +518,9 @@ qsa_status_t qsa_chunk_select_topk(qsa_cache* cache, const qsa_chunk* chunk,
                                    int32_t budget_tokens, int32_t* sel_blocks, int32_t* n_sel,
                                    void* stream);
 
-/* Bytes of workspace qsa_chunk_sparse_attn needs for this chunk, or -1 for a
- * bad chunk (qsa_last_error_string() tells).  The size depends on the sizes
- * of the chunk and of its requests alone; it never shrinks when a request
- * grows, so one of the largest chunk serves smaller ones of as few requests. */
+/* Bytes of workspace qsa_chunk_sparse_attn needs for this chunk (its requests'
+ * present lengths, n_tokens, n_layers and the budget), or -1 for a bad chunk
+ * (qsa_last_error_string() tells).  Ask again when any of them changes. */
 int64_t qsa_chunk_attn_workspace_bytes(qsa_cache* cache, const qsa_chunk* chunk,
                                        int32_t budget_tokens);
 

@@ -3,34 +3,134 @@
 //     logits_t = scale * q[x][h] . K_t[g],  t in the selected blocks, t <= p
 //     out[x][h] = sum_t softmax(logits)_t V_t[g],  lse = log sum_t exp(logits_t)
 // with the rows read through the slot table, as sparse_attn.cu does for one
-// query per request.
+// query per request ("Оффлоадинг KV-кэша Qwen3.8-Flash-Next в RAM через vLLM без
+// потери скорости декодирования", section "Механизм гибридного разреженного
+// оффлоадинга": attention reads only the selected rows).
+//
+// Neighbouring queries select mostly the same blocks.  So 64 queries form a
+// tile, the union of their blocks is attended densely on the tensor cores, and
+// a bit per (query, block) masks the probabilities: a row is read once per tile
+// and KV head instead of once per query that selects it (2048 queries over
+// 2048 rows of 2 KiB each would read 8.6 GB).  Three kernels:
+//  * plan: per tile the ascending list of blocks that any query selects, with
+//    a 64-bit mask of the queries that do (bitmaps in shared memory);
+//  * split: one CTA per (tile, KV head, split of the list), flash attention
+//    over 128 tokens (32 blocks) at a time;
+//  * join (when the list is split, so that few tiles still fill the device):
+//    log-sum-exp merge of the splits.
+//
+// Split kernel.  The tile's 64 queries x 4 heads of the group are 256 rows, two
+// halves of 128 = the tensor core's M: row = head * 32 + query, so a warp is a
+// head and a lane a query.  Per half and 128 tokens: S = Q K^T (8 MMAs of
+// K = 16, both operands in shared memory under the 128-byte swizzle), softmax
+// by the half's 4 warps (thread = row), P (bf16) over S's own columns of tensor
+// memory, O += P V (8 MMAs, P from tensor memory, V as an MN-major operand, so
+// that rows lie in shared memory as they come).  While one half is in softmax
+// the other's MMAs run.  Tensor memory: O and S of two halves, 4 x 128 columns.
+// Warps: 8 softmax, 4 loaders (cp.async of K[g], V[g] of each row, two stages
+// of 128 tokens; FP8 rows are turned into bf16 on the way, exactly, their
+// scales going to the logits and the probabilities), 1 MMA.  All waits are
+// bounded.
+//
+// The running maximum is taken over all tokens of the union (masking it would
+// cost a select per logit): any value serves that is not far below the
+// largest selected logit, and not so far above it that exponentials vanish.  A
+// row for which they do (sum below 2^-100), and a row whose output is not
+// finite (a value that is not finite times a masked probability of 0), is
+// computed again over its own tokens alone, by one warp in plain fp32
+// (attend_row): so a token reaches only the queries that select it.
+//
+// Rounding: P to bf16 (at most 2^-9 of each term; the tensor core takes no wider
+// type beside bf16 rows), and the output to bf16; the sum l is taken from the
+// unrounded probabilities, S, O, m and l are fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include "qsa_internal.cuh"
+#include "tc_common.cuh"
 
 namespace qsa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+using namespace tc;
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+constexpr int kTileQueries = 64;                  // two halves of 32
+constexpr int kStepBlocks = 32, kStepTokens = 4 * kStepBlocks;
+constexpr int kSoftWarps = 8, kLoadWarps = 4;
+constexpr int kThreads = 32 * (kSoftWarps + kLoadWarps + 1);     // 416
+constexpr int kRoleLoad = kSoftWarps, kRoleMma = kSoftWarps + kLoadWarps;
+constexpr int kStages = 2;
+constexpr int kPanel = 128 * 128;                 // 128 rows of 64 bf16
+constexpr int kQBytes = 2 * 2 * kPanel;           // two halves, two panels of 64 dims
+constexpr int kKvBytes = 2 * kPanel;              // K (or V) of a stage: two panels
+constexpr int kStageBytes = 2 * kKvBytes;
+
+// What the softmax of a step needs beside S.
+struct StepMeta {
+  uint32_t mine[2][32];         // [half][query]: bit b, the query selects block b of the step
+  uint32_t valid[4];            // bit per token of the step: its row exists
+  int32_t block[kStepBlocks];   // block ids
+  int32_t special[4];           // per loader warp: a row is missing, or a block reaches past the first query
+};
+struct Scales {                 // FP8 rows
+  float k[kStepTokens];         // K scale (times softmax scale and log2 e)
+  float v[kStepTokens];
+};
+constexpr int kOffKv = kQBytes;
+constexpr int kOffMeta = kOffKv + kStages * kStageBytes;
+constexpr int kOffScales = kOffMeta + kStages * (int)sizeof(StepMeta);
+constexpr int kOffBar = kOffScales + kStages * (int)sizeof(Scales);
+// kv_full[2], kv_empty[2], s_full[2], p_full[2], o_full[2]
+constexpr int kNumBars = 2 * kStages + 6;
+constexpr int kOffSlot = kOffBar + 8 * kNumBars;
+constexpr int kSmemBytes = kOffSlot + 16 + 1024;
+static_assert(kSmemBytes <= 227 * 1024 && sizeof(StepMeta) % 16 == 0, "one CTA's shared memory");
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 0, kColS = 256;        // + 128 per half
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWindow = 24576;                // blocks of one bitmap window (192 KiB)
+constexpr int kRowFloats = kHeadDim + 2;          // partial of a row: O, m, l
+
 struct ChunkAttnParams {
   ChunkDesc c;
-  const uint16_t* q;        // [rows][16][128] bf16 bits
-  const int32_t* sel;       // [rows][k_max]
-  const int32_t* n_sel;     // [rows]
+  int32_t tile0[kMaxUnits + 1];  // prefix sums of the tiles per unit
+  const uint16_t* q;             // [rows][16][128] bf16 bits
+  const int32_t* sel;            // [rows][k_max]
+  const int32_t* n_sel;          // [rows]
   int32_t k_max;
-  float scale_log2;         // softmax_scale * log2(e)
-  uint16_t* out;            // [rows][16][128] bf16 bits
-  float* lse;               // [rows][16] or nullptr
+  int32_t splits;
+  float scale_log2;              // |softmax_scale| * log2(e)
+  float sign;                    // the scale's sign (goes into Q)
+  uint16_t* out;                 // [rows][16][128] bf16 bits
+  float* lse;                    // [rows][16] or nullptr
+  int32_t cap;                   // list entries per tile (a multiple of 32)
+  int32_t* count;                // [tiles]
+  int32_t* block;                // [tiles][cap]
+  uint32_t* mask;                // [tiles][2][cap]
+  float* part;                   // [tiles][4][splits][256][kRowFloats]
+
+  __device__ int unit_of_tile(int t) const {
+    int lo = 0, hi = c.b.n_units - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (tile0[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  }
 };
 
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// ------------------------------------------------------- one row, plain fp32
 
 // Four values at dims 4 lane .. 4 lane + 3 of head vector hv (K heads 0-3,
 // then V heads 0-3) of a row.
@@ -48,27 +148,22 @@ __device__ __forceinline__ float4 row_values(const uint8_t* row, int hv, int lan
 }
 
 // One warp, one query row x and head h: online softmax over the row's own
-// selected tokens, in fp32.
-__device__ void attend_row(const ChunkAttnParams& p, int u, int x, int h) {
+// selected tokens.  (Bad blocks and slots have been reported by the plan and
+// the loaders.)
+__device__ __noinline__ void attend_row(const ChunkAttnParams& p, int u, int x, int h) {
   const int lane = threadIdx.x & 31, g = h / kGroup;
   const bool fp8 = p.c.b.row_bytes == kRowBytesFp8;
   const int64_t pos = p.c.position(u, x);
+  const float f = p.sign * p.scale_log2;
   const uint2 qv = reinterpret_cast<const uint2*>(p.q + ((int64_t)x * kQHeads + h) * kHeadDim)[lane];
-  const float q[4] = {bf16_lo(qv.x) * p.scale_log2, bf16_hi(qv.x) * p.scale_log2, bf16_lo(qv.y) * p.scale_log2,
-                      bf16_hi(qv.y) * p.scale_log2};
+  const float q[4] = {bf16_lo(qv.x) * f, bf16_hi(qv.x) * f, bf16_lo(qv.y) * f, bf16_hi(qv.y) * f};
   int nsel = p.n_sel[x];
-  if (nsel < 0 || nsel > p.k_max) {
-    if (lane == 0 && h == 0) report_error(p.c.b.err, QSA_ERR_BAD_BLOCK, kKernChunkAttn, nsel);
-    nsel = 0;
-  }
+  if (nsel < 0 || nsel > p.k_max) nsel = 0;
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j = 0; j < nsel; ++j) {
     const int64_t b = p.sel[(int64_t)x * p.k_max + j];
-    if (b < 0 || 4 * b > pos) {
-      if (lane == 0 && h == 0) report_error(p.c.b.err, QSA_ERR_BAD_BLOCK, kKernChunkAttn, b);
-      continue;
-    }
+    if (b < 0 || 4 * b > pos) continue;
     for (int i = 0; i < 4 && 4 * b + i <= pos; ++i) {
       const uint8_t* row = row_source(p.c.b, u, 4 * b + i, kKernChunkAttn);
       if (!row) continue;
@@ -86,38 +181,610 @@ __device__ void attend_row(const ChunkAttnParams& p, int u, int x, int h) {
     }
   }
   const float r = l == 0.f ? 0.f : 1.f / l;      // no tokens: zeros; NaN stays
-  __nv_bfloat162 o[2] = {__floats2bfloat162_rn(acc.x * r, acc.y * r), __floats2bfloat162_rn(acc.z * r, acc.w * r)};
-  reinterpret_cast<uint2*>(p.out + ((int64_t)x * kQHeads + h) * kHeadDim)[lane] = *reinterpret_cast<uint2*>(o);
+  reinterpret_cast<uint2*>(p.out + ((int64_t)x * kQHeads + h) * kHeadDim)[lane] =
+      make_uint2(pack_bf16(acc.x * r, acc.y * r), pack_bf16(acc.z * r, acc.w * r));
   if (p.lse && lane == 0) p.lse[(int64_t)x * kQHeads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-__global__ void __launch_bounds__(kThreads) chunk_attn_kernel(const __grid_constant__ ChunkAttnParams p) {
-  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+// ------------------------------------------------------------------- plan
+
+// One CTA per tile.  In windows of kPlanWindow blocks: a 64-bit query mask per
+// block in shared memory, set from the tile's selections, then compacted in
+// block order.  (A warp's lanes read consecutive entries of one query.)
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkAttnParams p,
+                                                                   int window) {
+  extern __shared__ __align__(16) uint32_t bits[];     // [window][2]
+  __shared__ uint32_t s_warp[kPlanThreads / 32];
+  const int tile = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int u = p.unit_of_tile(tile);
+  const int i0 = (tile - p.tile0[u]) * kTileQueries;
+  const int tokens = p.c.unit_tokens(u);
+  const int nq = tokens - i0 < kTileQueries ? tokens - i0 : kTileQueries;
+  const int x0 = p.c.row0[u] + i0;
+  const int64_t last = p.c.position(u, x0 + nq - 1) / 4;      // the tile's last block
+  int32_t* block = p.block + (int64_t)tile * p.cap;
+  uint32_t* mask0 = p.mask + (int64_t)tile * 2 * p.cap;
+  uint32_t* mask1 = mask0 + p.cap;
   grid_dependency_wait();
-  const int x = (int)(w / kQHeads);
+  int at = 0;
+  for (int64_t w0 = 0; w0 <= last; w0 += window) {
+    const int size = last + 1 - w0 < window ? (int)(last + 1 - w0) : window;
+    for (int i = tid; i < (size + 1) / 2; i += kPlanThreads)
+      reinterpret_cast<uint4*>(bits)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    for (int q = warp; q < nq; q += kPlanThreads / 32) {
+      const int64_t lim = p.c.position(u, x0 + q) / 4;
+      int nsel = p.n_sel[x0 + q];
+      if (nsel < 0 || nsel > p.k_max) {
+        if (w0 == 0 && lane == 0) report_error(p.c.b.err, QSA_ERR_BAD_BLOCK, kKernChunkAttn, nsel);
+        nsel = 0;
+      }
+      const int32_t* sel = p.sel + (int64_t)(x0 + q) * p.k_max;
+#pragma unroll 4
+      for (int j = lane; j < nsel; j += 32) {
+        const int64_t b = sel[j];
+        if (b < 0 || b > lim) {
+          if (w0 == 0) report_error(p.c.b.err, QSA_ERR_BAD_BLOCK, kKernChunkAttn, b);
+        } else if (b >= w0 && b < w0 + size) {
+          atomicOr(&bits[2 * (b - w0) + (q >> 5)], 1u << (q & 31));
+        }
+      }
+    }
+    __syncthreads();
+    // thread t: blocks t * per .. + per - 1
+    const int per = (size + kPlanThreads - 1) / kPlanThreads;
+    const int b0 = tid * per, b1 = b0 + per < size ? b0 + per : size;
+    uint32_t n = 0;
+    for (int b = b0; b < b1; ++b) n += (bits[2 * b] | bits[2 * b + 1]) != 0;
+    uint32_t v = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += y;
+    }
+    if (lane == 31) s_warp[warp] = v;
+    __syncthreads();
+    uint32_t w = s_warp[lane], before = 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+      if (lane >= o) w += y;
+    }
+    const uint32_t total = __shfl_sync(0xFFFFFFFFu, w, 31);
+    before = __shfl_sync(0xFFFFFFFFu, w, warp > 0 ? warp - 1 : 0);
+    int o = at + (int)((warp > 0 ? before : 0) + v - n);
+    for (int b = b0; b < b1; ++b) {
+      const uint32_t m0 = bits[2 * b], m1 = bits[2 * b + 1];
+      if (m0 | m1) {
+        block[o] = (int32_t)(w0 + b);
+        mask0[o] = m0;
+        mask1[o] = m1;
+        ++o;
+      }
+    }
+    at += (int)total;
+    __syncthreads();
+  }
+  if (tid == 0) p.count[tile] = at;
+}
+
+// ------------------------------------------------------------------ split
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Eight e4m3 codes as bf16, exactly: exponent and mantissa move into place,
+// and a multiplication by 2^120 corrects the bias (subnormal codes included).
+__device__ __forceinline__ uint32_t codes2_bf16(uint32_t w, uint32_t sel) {
+  const uint32_t u = __byte_perm(w, 0, sel);     // two codes, each in the upper byte of a half
+  const uint32_t raw = ((u & 0x7F007F00u) >> 4) | (u & 0x80008000u);
+  uint32_t o;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(raw), "r"(0x7B807B80u));
+  return o;
+}
+__device__ __forceinline__ uint4 codes8_bf16(uint2 w) {
+  return make_uint4(codes2_bf16(w.x, 0x1404), codes2_bf16(w.x, 0x3424), codes2_bf16(w.y, 0x1404),
+                    codes2_bf16(w.y, 0x3424));
+}
+
+template <bool kFp8>
+__global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_constant__ ChunkAttnParams p) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sb = smem_u32(smem);
+  StepMeta* meta = reinterpret_cast<StepMeta*>(smem + kOffMeta);
+  Scales* scales = reinterpret_cast<Scales*>(smem + kOffScales);
+  const uint32_t bars = sb + kOffBar;
+  auto kv_full = [&](int i) { return bars + 8u * (uint32_t)i; };
+  auto kv_empty = [&](int i) { return bars + 8u * (uint32_t)(kStages + i); };
+  auto s_full = [&](int h) { return bars + 8u * (uint32_t)(2 * kStages + h); };
+  auto p_full = [&](int h) { return bars + 8u * (uint32_t)(2 * kStages + 2 + h); };
+  auto o_full = [&](int h) { return bars + 8u * (uint32_t)(2 * kStages + 4 + h); };
+  uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kOffSlot);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  ErrorWord* err = p.c.b.err;
+
+  // grid: (tile, split) x KV head
+  const int g = blockIdx.y, tile = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
+  const int u = p.unit_of_tile(tile);
+  const int i0 = (tile - p.tile0[u]) * kTileQueries;
+  const int tokens = p.c.unit_tokens(u);
+  const int nq = tokens - i0 < kTileQueries ? tokens - i0 : kTileQueries;
+  const int x0 = p.c.row0[u] + i0;
+  const int halves = nq > 32 ? 2 : 1;
+  const int64_t pos0 = p.c.position(u, x0);
+
+  if (warp == kRoleMma) {
+    tmem_alloc<kTmemCols>(slot);
+    if (lane == 0) {
+      for (int i = 0; i < kStages; ++i) { mbar_init(kv_full(i), 32 * kLoadWarps); mbar_init(kv_empty(i), 1); }
+      for (int h = 0; h < 2; ++h) { mbar_init(s_full(h), 1); mbar_init(p_full(h), 128); mbar_init(o_full(h), 1); }
+      mbar_fence_init();
+    }
+  }
+  grid_dependency_wait();
+  // ---- Q: row head * 32 + query of each half, two panels of 64 dims
+  for (int i = tid; i < halves * 128 * 16; i += kThreads) {
+    const int c = i & 15, r = (i >> 4) & 127, h = i >> 11;
+    const int q = h * 32 + (r & 31), head = g * kGroup + (r >> 5);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (q < nq) v = reinterpret_cast<const uint4*>(p.q + ((int64_t)(x0 + q) * kQHeads + head) * kHeadDim)[c];
+    const uint32_t flip = p.sign < 0.f ? 0x80008000u : 0u;
+    v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
+    *reinterpret_cast<uint4*>(smem + (h * 2 + (c >> 3)) * kPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+  }
+  fence_async_smem();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *slot;
+
+  const int count = p.count[tile];
+  const int all = (count + kStepBlocks - 1) / kStepBlocks;
+  const int j0 = (int)((int64_t)all * split / p.splits), steps = (int)((int64_t)all * (split + 1) / p.splits) - j0;
+  bool ok = true;
+
+  if (warp >= kRoleLoad && warp < kRoleMma) {
+    // ---- loaders: warp w brings tokens 32 w .. 32 w + 31 of a step, lane = token
+    const int w = warp - kRoleLoad;
+    const int32_t* block = p.block + (int64_t)tile * p.cap;
+    const uint32_t* mask = p.mask + (int64_t)tile * 2 * p.cap;
+    const int32_t* slots = p.c.b.slot_table + p.c.b.unit_row(u);
+    const int64_t n = p.c.b.u[u].n;
+    const uint8_t* src = nullptr;
+    int32_t id = -1;
+    auto resolve = [&](int j) {
+      const int e = (j0 + j) * kStepBlocks + 8 * w + (lane >> 2);
+      src = nullptr;
+      id = -1;
+      if (j >= steps || e >= count) return;
+      id = block[e];
+      const int64_t t = 4 * (int64_t)id + (lane & 3);
+      if (t >= n) return;
+      const int32_t s = slots[t];
+      if (s >= 0 && (int64_t)s < p.c.b.pool_rows) src = p.c.b.pool + (int64_t)s * p.c.b.row_bytes;
+      else if (s == -1 && p.c.b.u[u].host_rows) src = p.c.b.u[u].host_rows + t * p.c.b.row_bytes;
+      else report_error(err, QSA_ERR_BAD_SLOT, kKernChunkAttn, ((int64_t)u << 40) | (t & 0xFFFFFFFFFFll));
+    };
+    resolve(0);
+    for (int j = 0; j < steps && ok; ++j) {
+      const int st = j % kStages;
+      if (j >= kStages) ok = mbar_wait_warp(kv_empty(st), (uint32_t)(j / kStages - 1) & 1u, err, kKernChunkAttn);
+      if (!ok) break;
+      StepMeta& m = meta[st];
+      const uint32_t there = __ballot_sync(0xFFFFFFFFu, src != nullptr);
+      const bool past = id >= 0 && 4 * (int64_t)id + 3 > pos0;
+      const bool special = __any_sync(0xFFFFFFFFu, past || (id >= 0 && src == nullptr));
+      if (lane == 0) {
+        m.valid[w] = there;
+        m.special[w] = special;
+      }
+      if ((lane & 3) == 0) m.block[8 * w + (lane >> 2)] = id;
+      if (w < halves) {
+        // transpose the step's 32 block masks: lane q gets query q's bits
+        const int e = (j0 + j) * kStepBlocks + lane;
+        const uint32_t bm = e < count ? mask[(int64_t)w * p.cap + e] : 0u;
+        uint32_t mine = 0;
+#pragma unroll
+        for (int q = 0; q < 32; ++q) {
+          const uint32_t b = __ballot_sync(0xFFFFFFFFu, (bm >> q) & 1u);
+          if (lane == q) mine = b;
+        }
+        m.mine[w][lane] = mine;
+      }
+      // lanes 0-15 copy K[g] (256 bytes of bf16), lanes 16-31 V[g]
+      const uint32_t dst0 = sb + kOffKv + st * kStageBytes + (lane < 16 ? 0 : kKvBytes) + ((lane & 15) >> 3) * kPanel;
+      const uint32_t c = lane & 7;
+      if (!kFp8) {
+        const int off = (lane < 16 ? 0 : kKvHeads * kHeadDim * 2) + g * kHeadDim * 2 + (lane & 15) * 16;
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) {
+          const uint8_t* s = reinterpret_cast<const uint8_t*>(
+              __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uintptr_t>(src), i));
+          const uint32_t r = 32 * w + i;
+          cp_async16(dst0 + r * 128 + ((c ^ (r & 7)) << 4), s ? s + off : p.c.b.pool, s ? 16u : 0u);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        resolve(j + 1);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      } else {
+        float ks = 0.f, vs = 0.f;
+        if (src) {
+          const uint16_t* sc = reinterpret_cast<const uint16_t*>(src + 2 * kKvHeads * kHeadDim);
+          ks = __half2float(__ushort_as_half(sc[g]));
+          vs = __half2float(__ushort_as_half(sc[kKvHeads + g]));
+        }
+        const int off = (lane < 16 ? 0 : kKvHeads * kHeadDim) + g * kHeadDim + (lane & 15) * 8;
+#pragma unroll 1
+        for (int i8 = 0; i8 < 32; i8 += 8) {
+          uint2 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint8_t* s = reinterpret_cast<const uint8_t*>(
+                __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uintptr_t>(src), i8 + i));
+            v[i] = s ? *reinterpret_cast<const uint2*>(s + off) : make_uint2(0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t r = 32 * w + i8 + i;
+            *reinterpret_cast<uint4*>(smem + (dst0 - sb) + r * 128 + ((c ^ (r & 7)) << 4)) = codes8_bf16(v[i]);
+          }
+        }
+        scales[st].k[32 * w + lane] = ks * p.scale_log2;
+        scales[st].v[32 * w + lane] = vs;
+        resolve(j + 1);
+      }
+      fence_async_smem();
+      mbar_arrive(kv_full(st));
+    }
+  } else if (warp == kRoleMma) {
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    const uint32_t is = idesc_bf16(kStepTokens, false), io = idesc_bf16(kHeadDim, true);
+    auto issue_s = [&](int h, int st) {
+      if (elect_one()) {
+        const uint64_t a = desc_sw128(sb + h * 2 * kPanel, 16), b = desc_sw128(sb + kOffKv + st * kStageBytes, 16);
+#pragma unroll
+        for (int k = 0; k < kHeadDim / 16; ++k) {
+          const uint64_t o = (uint64_t)(((k >> 2) * kPanel + (k & 3) * 32) >> 4);
+          mma_ss(tm + kColS + 128u * (uint32_t)h, a + o, b + o, is, k != 0);
+        }
+        commit(s_full(h));
+      }
+      __syncwarp();
+    };
+    if (steps > 0) {
+      ok = mbar_wait_warp(kv_full(0), 0, err, kKernChunkAttn);
+      if (ok) {
+        fence_after();
+        for (int h = 0; h < halves; ++h) issue_s(h, 0);
+      }
+    }
+    for (int j = 0; j < steps && ok; ++j) {
+      const int st = j % kStages;
+      for (int h = 0; h < halves && ok; ++h) {
+        ok = mbar_wait_warp(p_full(h), (uint32_t)j & 1u, err, kKernChunkAttn);
+        if (!ok) break;
+        fence_after();
+        if (elect_one()) {
+          const uint64_t b = desc_sw128(sb + kOffKv + st * kStageBytes + kKvBytes, kPanel);
+#pragma unroll
+          for (int k = 0; k < kStepTokens / 16; ++k)
+            mma_ts(tm + kColO + 128u * (uint32_t)h, tm + kColS + 128u * (uint32_t)h + 8u * k, b + (uint64_t)(k * 2048 >> 4),
+                   io, j > 0 || k > 0);
+          commit(o_full(h));
+          if (h == halves - 1) commit(kv_empty(st));
+        }
+        __syncwarp();
+        if (j + 1 < steps) {
+          // the next S goes over this step's P: after its products are complete
+          if (h == 0) ok = mbar_wait_warp(kv_full((j + 1) % kStages), (uint32_t)((j + 1) / kStages) & 1u, err, kKernChunkAttn);
+          if (ok) ok = mbar_wait_warp(o_full(h), (uint32_t)j & 1u, err, kKernChunkAttn);
+          if (!ok) break;
+          fence_after();
+          issue_s(h, (j + 1) % kStages);
+        }
+      }
+    }
+    // every product is complete before tensor memory is given back
+    if (ok && steps > 0)
+      for (int h = 0; h < halves; ++h) mbar_wait_warp(o_full(h), (uint32_t)(steps - 1) & 1u, err, kKernChunkAttn);
+  } else if (warp / 4 < halves) {
+    // ---- softmax: thread = row (head warp & 3, query lane) of half h
+    const int h = warp >> 2, head = g * kGroup + (warp & 3), q = 32 * h + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t colS = lane_base + kColS + 128u * (uint32_t)h, colO = lane_base + kColO + 128u * (uint32_t)h;
+    const int64_t pos = pos0 + q;
+    const float f = kFp8 ? 1.f : p.scale_log2;       // FP8: the K scales hold it
+    float m = -INFINITY, l = 0.f;                    // in units of log2
+    for (int j = 0; j < steps; ++j) {
+      const int st = j % kStages;
+      ok = mbar_wait_warp(s_full(h), (uint32_t)j & 1u, err, kKernChunkAttn);
+      // (long complete; orders the loaders' writes of the meta before its reads)
+      if (ok) ok = mbar_wait_warp(kv_full(st), (uint32_t)(j / kStages) & 1u, err, kKernChunkAttn);
+      if (!ok) break;
+      fence_after();
+      const StepMeta& sm = meta[st];
+      const uint32_t mine = sm.mine[h][lane];
+      const bool special = (sm.special[0] | sm.special[1] | sm.special[2] | sm.special[3]) != 0;
+      // ---- maximum over the step's tokens
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32];
+        ld32(colS + 32u * c, v);
+        wait_ld();
+        reg_fence(v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float s = __uint_as_float(v[i]);
+          if (kFp8) s *= scales[st].k[32 * c + i];
+          mx = fmaxf(mx, s);
+        }
+      }
+      mx *= f;
+      // the reference goes up only when the maximum has left it 2^8 behind
+      const bool up = mx > m + 8.f;                  // true for the first step
+      if (__any_sync(0xFFFFFFFFu, up)) {
+        const float mn = fmaxf(m, mx);
+        const float a = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
+        m = mn;
+        l *= a;
+        if (j > 0) {                                 // the products of step j - 1 are complete
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            ld32(colO + 32u * c, v);
+            wait_ld();
+            reg_fence(v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
+            st32(colO + 32u * c, v);
+          }
+          wait_st();
+        }
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+      // ---- probabilities, masked, over S's columns
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32], o[16];
+        ld32(colS + 32u * c, v);
+        wait_ld();
+        reg_fence(v);
+        uint32_t bits = mine >> (8 * c);
+        uint32_t tok = 0xFFFFFFFFu;                  // per token: its row exists and q sees it
+        if (special) {
+          tok = sm.valid[c];
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            const int64_t left = pos - 4 * (int64_t)sm.block[8 * c + b];   // tokens of the block that q sees, - 1
+            const uint32_t seen = left >= 3 ? 0xFu : (left < 0 ? 0u : (2u << (int)left) - 1u);
+            tok &= ~(0xFu << (4 * b)) | (seen << (4 * b));
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          const uint32_t on = (uint32_t)((int32_t)(bits << (31 - b)) >> 31);
+          float e[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float s = __uint_as_float(v[4 * b + i]);
+            if (kFp8) s *= scales[st].k[32 * c + 4 * b + i];
+            e[i] = __uint_as_float(__float_as_uint(exp2_fast(fmaf(s, f, -ref))) & on);
+          }
+          if (special) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!((tok >> (4 * b + i)) & 1u)) e[i] = 0.f;
+          }
+          l += (e[0] + e[1]) + (e[2] + e[3]);
+          if (kFp8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] *= scales[st].v[32 * c + 4 * b + i];
+          }
+          o[2 * b] = pack_bf16(e[0], e[1]);
+          o[2 * b + 1] = pack_bf16(e[2], e[3]);
+        }
+        st16(colS + 16u * c, o);
+      }
+      wait_st();
+      fence_before();
+      mbar_arrive(p_full(h));
+    }
+    // ---- the row's result
+    if (ok && steps > 0) ok = mbar_wait_warp(o_full(h), (uint32_t)(steps - 1) & 1u, err, kKernChunkAttn);
+    fence_after();
+    const int x = x0 + q;
+    const bool mine = ok && q < nq;
+    if (p.splits > 1) {
+      float* part = p.part + ((((int64_t)tile * kKvHeads + g) * p.splits + split) * 256 + h * 128 + (warp & 3) * 32 + lane) * kRowFloats;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32];
+        if (steps > 0) {
+          ld32(colO + 32u * c, v);
+          wait_ld();
+          reg_fence(v);
+        }
+        if (mine) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            *reinterpret_cast<float2*>(part + 32 * c + i) =
+                steps > 0 ? make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])) : make_float2(0.f, 0.f);
+        }
+      }
+      if (mine) *reinterpret_cast<float2*>(part + kHeadDim) = make_float2(m, l);
+    } else {
+      const float r = 1.f / l;
+      bool good = l > 0x1p-100f;                     // false for NaN
+      uint16_t* out = p.out + ((int64_t)x * kQHeads + head) * kHeadDim;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32];
+        if (steps > 0) {
+          ld32(colO + 32u * c, v);
+          wait_ld();
+          reg_fence(v);
+        }
+        if (mine && steps > 0) {
+          float far = 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) far = fmaxf(far, isfinite(__uint_as_float(v[i])) ? 0.f : 1.f);
+          good = good && far == 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            uint4 o;
+            o.x = pack_bf16(__uint_as_float(v[i]) * r, __uint_as_float(v[i + 1]) * r);
+            o.y = pack_bf16(__uint_as_float(v[i + 2]) * r, __uint_as_float(v[i + 3]) * r);
+            o.z = pack_bf16(__uint_as_float(v[i + 4]) * r, __uint_as_float(v[i + 5]) * r);
+            o.w = pack_bf16(__uint_as_float(v[i + 6]) * r, __uint_as_float(v[i + 7]) * r);
+            *reinterpret_cast<uint4*>(out + 32 * c + i) = o;
+          }
+        }
+      }
+      if (mine && good && p.lse) p.lse[(int64_t)x * kQHeads + head] = (m + log2f(l)) * kLn2;
+      for (uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && !good); again; again &= again - 1) {
+        __syncwarp();
+        attend_row(p, u, x0 + 32 * h + __ffs(again) - 1, head);
+      }
+    }
+  }
+
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == kRoleMma) tmem_free<kTmemCols>(tmem);
+}
+
+// ------------------------------------------------------------------- join
+
+// One warp per (row, head): lane l holds dims 4 l .. 4 l + 3.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ ChunkAttnParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  const int x = (int)(w / kQHeads), head = (int)(w % kQHeads);
+  grid_dependency_wait();
   if (x >= p.c.rows()) return;
-  attend_row(p, p.c.unit_of_row(x), x, (int)(w % kQHeads));
+  const int u = p.c.unit_of_row(x), i = x - p.c.row0[u], tile = p.tile0[u] + i / kTileQueries;
+  const int q = i % kTileQueries, row = (q >> 5) * 128 + (head % kGroup) * 32 + (q & 31);
+  const float* part = p.part + (((int64_t)tile * kKvHeads + head / kGroup) * p.splits * 256 + row) * kRowFloats;
+  const int64_t stride = 256 * kRowFloats;
+  float m = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, part[s * stride + kHeadDim]);
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < p.splits; ++s) {
+    const float ms = part[s * stride + kHeadDim], ls = part[s * stride + kHeadDim + 1];
+    if (ls == 0.f) continue;                         // nothing selected there
+    const float a = exp2f(ms - m);
+    const float2 o0 = *reinterpret_cast<const float2*>(part + s * stride + 4 * lane);
+    const float2 o1 = *reinterpret_cast<const float2*>(part + s * stride + 4 * lane + 2);
+    l = fmaf(ls, a, l);
+    acc = make_float4(fmaf(o0.x, a, acc.x), fmaf(o0.y, a, acc.y), fmaf(o1.x, a, acc.z), fmaf(o1.y, a, acc.w));
+  }
+  const bool fine = l > 0x1p-100f && isfinite(acc.x) && isfinite(acc.y) && isfinite(acc.z) && isfinite(acc.w);
+  if (!__all_sync(0xFFFFFFFFu, fine)) {
+    attend_row(p, u, x, head);
+    return;
+  }
+  const float r = 1.f / l;
+  reinterpret_cast<uint2*>(p.out + ((int64_t)x * kQHeads + head) * kHeadDim)[lane] =
+      make_uint2(pack_bf16(acc.x * r, acc.y * r), pack_bf16(acc.z * r, acc.w * r));
+  if (p.lse && lane == 0) p.lse[(int64_t)x * kQHeads + head] = (m + log2f(l)) * kLn2;
+}
+
+// ------------------------------------------------------------------- host
+
+struct AttnPlan {
+  int64_t tiles = 0, cap = 0, nb = 0;
+  int splits = 1;
+  int64_t off_block = 0, off_mask = 0, off_part = 0, bytes = 0;
+};
+
+AttnPlan make_plan(const ChunkDesc& c, int32_t budget_tokens, int sms, int32_t* tile0) {
+  AttnPlan a;
+  for (int u = 0; u < c.b.n_units; ++u) {
+    if (tile0) tile0[u] = (int32_t)a.tiles;
+    if (c.unit_tokens(u) == 0) continue;
+    a.tiles += (c.unit_tokens(u) + kTileQueries - 1) / kTileQueries;
+    const int64_t nb = (c.b.u[u].n + 3) / 4, most = (int64_t)(c.unit_tokens(u) < kTileQueries ? c.unit_tokens(u) : kTileQueries) * (budget_tokens / 4);
+    if (nb > a.nb) a.nb = nb;
+    const int64_t cap = nb < most ? nb : most;
+    if (cap > a.cap) a.cap = cap;
+  }
+  if (tile0) tile0[c.b.n_units] = (int32_t)a.tiles;
+  a.cap = (a.cap + kStepBlocks - 1) / kStepBlocks * kStepBlocks;
+  // fewer CTAs than SMs: split the lists, down to four steps each
+  const int64_t ctas = a.tiles * kKvHeads, steps = a.cap / kStepBlocks;
+  int64_t s = ctas > 0 ? sms / ctas : 1;
+  if (s > (steps + 3) / 4) s = (steps + 3) / 4;
+  a.splits = (int)(s < 1 ? 1 : s);
+  auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
+  a.off_block = up(4 * a.tiles);
+  a.off_mask = a.off_block + up(4 * a.tiles * a.cap);
+  a.off_part = a.off_mask + up(8 * a.tiles * a.cap);
+  a.bytes = a.off_part + (a.splits > 1 ? up(a.tiles * kKvHeads * a.splits * 256 * kRowFloats * 4) : 0);
+  return a;
 }
 
 }  // namespace
 
-int64_t chunk_attn_workspace(const ChunkDesc&, int32_t) { return 256; }
+int64_t chunk_attn_workspace(const ChunkDesc& c, int32_t budget_tokens) {
+  int sms = 0;
+  if (current_sm_count(&sms) != cudaSuccess) return -1;
+  const int64_t b = make_plan(c, budget_tokens, sms, nullptr).bytes;
+  return b > 256 ? b : 256;
+}
 
 cudaError_t launch_chunk_attn(const ChunkDesc& c, const uint16_t* q, const int32_t* sel_blocks,
                               const int32_t* n_sel, int32_t budget_tokens, float softmax_scale,
-                              uint16_t* out, float* lse, void*, cudaStream_t s) {
+                              uint16_t* out, float* lse, void* workspace, cudaStream_t s) {
+  static PerDeviceOnce setup;
+  cudaError_t e = setup.run([] {
+    cudaError_t r = prefer_max_shared(chunk_split_kernel<false>, kSmemBytes);
+    if (r == cudaSuccess) r = prefer_max_shared(chunk_split_kernel<true>, kSmemBytes);
+    if (r == cudaSuccess) r = prefer_max_shared(chunk_plan_kernel, kPlanWindow * 8);
+    return r;
+  });
+  int sms = 0;
+  if (e == cudaSuccess) e = current_sm_count(&sms);
+  if (e != cudaSuccess) return e;
   ChunkAttnParams p;
+  const AttnPlan a = make_plan(c, budget_tokens, sms, p.tile0);
   p.c = c;
   p.q = q;
   p.sel = sel_blocks;
   p.n_sel = n_sel;
   p.k_max = budget_tokens / 4;
-  p.scale_log2 = softmax_scale * kLog2e;
+  p.splits = a.splits;
+  p.scale_log2 = fabsf(softmax_scale) * kLog2e;
+  p.sign = softmax_scale < 0.f ? -1.f : 1.f;
   p.out = out;
   p.lse = lse;
+  p.cap = (int32_t)a.cap;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.count = reinterpret_cast<int32_t*>(ws);
+  p.block = reinterpret_cast<int32_t*>(ws + a.off_block);
+  p.mask = reinterpret_cast<uint32_t*>(ws + a.off_mask);
+  p.part = reinterpret_cast<float*>(ws + a.off_part);
+  const int window = (int)(a.nb < kPlanWindow ? (a.nb + 1) / 2 * 2 : kPlanWindow);
+  e = launch_kernel(chunk_plan_kernel, dim3((unsigned)a.tiles), dim3(kPlanThreads), (size_t)window * 8, s, 0, dim3(1),
+                    p, window);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)(a.tiles * a.splits), kKvHeads);
+  e = c.b.row_bytes == kRowBytesFp8
+          ? launch_kernel(chunk_split_kernel<true>, grid, dim3(kThreads), kSmemBytes, s, 0, dim3(1), p)
+          : launch_kernel(chunk_split_kernel<false>, grid, dim3(kThreads), kSmemBytes, s, 0, dim3(1), p);
+  if (e != cudaSuccess || a.splits == 1) return e;
   const int64_t warps = (int64_t)c.rows() * kQHeads;
-  return launch_kernel(chunk_attn_kernel, dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kThreads), 0, s, 0,
-                       dim3(1), p);
+  return launch_kernel(chunk_join_kernel, dim3((unsigned)((warps + 7) / 8)), dim3(kJoinThreads), 0, s, 0, dim3(1), p);
 }
 
 }  // namespace qsa
