@@ -81,10 +81,14 @@ struct Scales {                 // FP8 rows
 };
 constexpr int kOffKv = kQBytes;
 constexpr int kOffMeta = kOffKv + kStages * kStageBytes;
-constexpr int kOffScales = kOffMeta + kStages * (int)sizeof(StepMeta);
-constexpr int kOffBar = kOffScales + kStages * (int)sizeof(Scales);
-// kv_full[2], kv_empty[2], s_full[2], p_full[2], o_full[2]
-constexpr int kNumBars = 2 * kStages + 6;
+// Metas outlive their K stage (the softmax of step j reads meta j while K of
+// step j + 2 comes in), but not by three steps: K of step j + 3 comes after the
+// S of step j + 1, that after the P of step j.
+constexpr int kMetas = 4;
+constexpr int kOffScales = kOffMeta + kMetas * (int)sizeof(StepMeta);
+constexpr int kOffBar = kOffScales + kMetas * (int)sizeof(Scales);
+// k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2]
+constexpr int kNumBars = 4 * kStages + 6;
 constexpr int kOffSlot = kOffBar + 8 * kNumBars;
 constexpr int kSmemBytes = kOffSlot + 16 + 1024;
 static_assert(kSmemBytes <= 227 * 1024 && sizeof(StepMeta) % 16 == 0, "one CTA's shared memory");
@@ -189,12 +193,15 @@ __device__ __noinline__ void attend_row(const ChunkAttnParams& p, int u, int x, 
 // ------------------------------------------------------------------- plan
 
 // One CTA per tile.  In windows of kPlanWindow blocks: a 64-bit query mask per
-// block in shared memory, set from the tile's selections, then compacted in
-// block order.  (A warp's lanes read consecutive entries of one query.)
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkAttnParams p,
+// block in shared memory, set from the tile's selections (a warp's lanes read
+// consecutive entries of one query), then compacted in block order: warp w owns
+// a run of blocks, 32 at a time.
+constexpr int kPlanWarps = kPlanThreads / 32;
+__global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const __grid_constant__ ChunkAttnParams p,
                                                                    int window) {
-  extern __shared__ __align__(16) uint32_t bits[];     // [window][2]
-  __shared__ uint32_t s_warp[kPlanThreads / 32];
+  extern __shared__ __align__(16) uint32_t bits0[];    // [window] queries 0-31, then [window] queries 32-63
+  uint32_t* bits1 = bits0 + window;
+  __shared__ uint32_t s_warp[kPlanWarps];
   const int tile = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int u = p.unit_of_tile(tile);
   const int i0 = (tile - p.tile0[u]) * kTileQueries;
@@ -205,68 +212,66 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
   int32_t* block = p.block + (int64_t)tile * p.cap;
   uint32_t* mask0 = p.mask + (int64_t)tile * 2 * p.cap;
   uint32_t* mask1 = mask0 + p.cap;
-  grid_dependency_wait();
   int at = 0;
   for (int64_t w0 = 0; w0 <= last; w0 += window) {
     const int size = last + 1 - w0 < window ? (int)(last + 1 - w0) : window;
-    for (int i = tid; i < (size + 1) / 2; i += kPlanThreads)
-      reinterpret_cast<uint4*>(bits)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < (size + 3) / 4; i += kPlanThreads) {
+      reinterpret_cast<uint4*>(bits0)[i] = make_uint4(0, 0, 0, 0);
+      reinterpret_cast<uint4*>(bits1)[i] = make_uint4(0, 0, 0, 0);
+    }
     __syncthreads();
-    for (int q = warp; q < nq; q += kPlanThreads / 32) {
-      const int64_t lim = p.c.position(u, x0 + q) / 4;
-      int nsel = p.n_sel[x0 + q];
-      if (nsel < 0 || nsel > p.k_max) {
-        if (w0 == 0 && lane == 0) report_error(p.c.b.err, QSA_ERR_BAD_BLOCK, kKernChunkAttn, nsel);
-        nsel = 0;
-      }
-      const int32_t* sel = p.sel + (int64_t)(x0 + q) * p.k_max;
+    if (w0 == 0) grid_dependency_wait();               // the selection is read from here on
+    // entries of all queries, 32 of one query per warp and turn
+    const int turns = (p.k_max + 31) / 32;
 #pragma unroll 4
-      for (int j = lane; j < nsel; j += 32) {
-        const int64_t b = sel[j];
-        if (b < 0 || b > lim) {
-          if (w0 == 0) report_error(p.c.b.err, QSA_ERR_BAD_BLOCK, kKernChunkAttn, b);
-        } else if (b >= w0 && b < w0 + size) {
-          atomicOr(&bits[2 * (b - w0) + (q >> 5)], 1u << (q & 31));
-        }
+    for (int i = warp; i < nq * turns; i += kPlanWarps) {
+      const int q = i / turns, j = (i % turns) * 32 + lane;
+      const int nsel = p.n_sel[x0 + q];
+      if (nsel < 0 || nsel > p.k_max) {
+        if (w0 == 0 && j == 0) report_error(p.c.b.err, QSA_ERR_BAD_BLOCK, kKernChunkAttn, nsel);
+        continue;
+      }
+      if (j >= nsel) continue;
+      const int64_t b = p.sel[(int64_t)(x0 + q) * p.k_max + j];
+      if (b < 0 || b > p.c.position(u, x0 + q) / 4) {
+        if (w0 == 0) report_error(p.c.b.err, QSA_ERR_BAD_BLOCK, kKernChunkAttn, b);
+      } else if (b >= w0 && b < w0 + size) {
+        atomicOr((q < 32 ? bits0 : bits1) + (b - w0), 1u << (q & 31));
       }
     }
     __syncthreads();
-    // thread t: blocks t * per .. + per - 1
-    const int per = (size + kPlanThreads - 1) / kPlanThreads;
-    const int b0 = tid * per, b1 = b0 + per < size ? b0 + per : size;
+    const int run = ((size + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
+    const int b0 = warp * run, b1 = b0 + run < size ? b0 + run : size;
     uint32_t n = 0;
-    for (int b = b0; b < b1; ++b) n += (bits[2 * b] | bits[2 * b + 1]) != 0;
-    uint32_t v = n;
+    for (int b = b0; b < b1; b += 32)
+      n += __popc(__ballot_sync(0xFFFFFFFFu, b + lane < b1 && (bits0[b + lane] | bits1[b + lane])));
+    if (lane == 0) s_warp[warp] = n;
+    __syncthreads();
+    uint32_t v = s_warp[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, v, o);
       if (lane >= o) v += y;
     }
-    if (lane == 31) s_warp[warp] = v;
-    __syncthreads();
-    uint32_t w = s_warp[lane], before = 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, w, o);
-      if (lane >= o) w += y;
-    }
-    const uint32_t total = __shfl_sync(0xFFFFFFFFu, w, 31);
-    before = __shfl_sync(0xFFFFFFFFu, w, warp > 0 ? warp - 1 : 0);
-    int o = at + (int)((warp > 0 ? before : 0) + v - n);
-    for (int b = b0; b < b1; ++b) {
-      const uint32_t m0 = bits[2 * b], m1 = bits[2 * b + 1];
+    int o = at + (int)(__shfl_sync(0xFFFFFFFFu, v, warp) - n);
+    for (int b = b0; b < b1; b += 32) {
+      uint32_t m0 = 0, m1 = 0;
+      if (b + lane < b1) { m0 = bits0[b + lane]; m1 = bits1[b + lane]; }
+      const uint32_t some = __ballot_sync(0xFFFFFFFFu, (m0 | m1) != 0);
       if (m0 | m1) {
-        block[o] = (int32_t)(w0 + b);
-        mask0[o] = m0;
-        mask1[o] = m1;
-        ++o;
+        const int i = o + __popc(some & ((1u << lane) - 1u));
+        block[i] = (int32_t)(w0 + b + lane);
+        mask0[i] = m0;
+        mask1[i] = m1;
       }
+      o += __popc(some);
     }
-    at += (int)total;
+    at += (int)__shfl_sync(0xFFFFFFFFu, v, 31);
     __syncthreads();
   }
   if (tid == 0) p.count[tile] = at;
 }
+static_assert(kPlanWarps == 32, "one lane per warp in the scan");
 
 // ------------------------------------------------------------------ split
 
@@ -301,11 +306,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
   StepMeta* meta = reinterpret_cast<StepMeta*>(smem + kOffMeta);
   Scales* scales = reinterpret_cast<Scales*>(smem + kOffScales);
   const uint32_t bars = sb + kOffBar;
-  auto kv_full = [&](int i) { return bars + 8u * (uint32_t)i; };
-  auto kv_empty = [&](int i) { return bars + 8u * (uint32_t)(kStages + i); };
-  auto s_full = [&](int h) { return bars + 8u * (uint32_t)(2 * kStages + h); };
-  auto p_full = [&](int h) { return bars + 8u * (uint32_t)(2 * kStages + 2 + h); };
-  auto o_full = [&](int h) { return bars + 8u * (uint32_t)(2 * kStages + 4 + h); };
+  auto k_full = [&](int i) { return bars + 8u * (uint32_t)i; };
+  auto k_empty = [&](int i) { return bars + 8u * (uint32_t)(kStages + i); };
+  auto v_full = [&](int i) { return bars + 8u * (uint32_t)(2 * kStages + i); };
+  auto v_empty = [&](int i) { return bars + 8u * (uint32_t)(3 * kStages + i); };
+  auto s_full = [&](int h) { return bars + 8u * (uint32_t)(4 * kStages + h); };
+  auto p_full = [&](int h) { return bars + 8u * (uint32_t)(4 * kStages + 2 + h); };
+  auto o_full = [&](int h) { return bars + 8u * (uint32_t)(4 * kStages + 4 + h); };
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kOffSlot);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   ErrorWord* err = p.c.b.err;
@@ -323,8 +330,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
   if (warp == kRoleMma) {
     tmem_alloc<kTmemCols>(slot);
     if (lane == 0) {
-      for (int i = 0; i < kStages; ++i) { mbar_init(kv_full(i), 32 * kLoadWarps); mbar_init(kv_empty(i), 1); }
-      for (int h = 0; h < 2; ++h) { mbar_init(s_full(h), 1); mbar_init(p_full(h), 128); mbar_init(o_full(h), 1); }
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(k_full(i), 32 * kLoadWarps);
+        mbar_init(k_empty(i), 1);
+        mbar_init(v_full(i), 32 * kLoadWarps);
+        mbar_init(v_empty(i), 1);
+      }
+      for (int h = 0; h < 2; ++h) { mbar_init(s_full(h), 2); mbar_init(p_full(h), 128); mbar_init(o_full(h), 1); }
       mbar_fence_init();
     }
   }
@@ -357,92 +369,137 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
     const uint32_t* mask = p.mask + (int64_t)tile * 2 * p.cap;
     const int32_t* slots = p.c.b.slot_table + p.c.b.unit_row(u);
     const int64_t n = p.c.b.u[u].n;
-    const uint8_t* src = nullptr;
-    int32_t id = -1;
-    auto resolve = [&](int j) {
-      const int e = (j0 + j) * kStepBlocks + 8 * w + (lane >> 2);
-      src = nullptr;
-      id = -1;
-      if (j >= steps || e >= count) return;
-      id = block[e];
-      const int64_t t = 4 * (int64_t)id + (lane & 3);
-      if (t >= n) return;
-      const int32_t s = slots[t];
-      if (s >= 0 && (int64_t)s < p.c.b.pool_rows) src = p.c.b.pool + (int64_t)s * p.c.b.row_bytes;
-      else if (s == -1 && p.c.b.u[u].host_rows) src = p.c.b.u[u].host_rows + t * p.c.b.row_bytes;
-      else report_error(err, QSA_ERR_BAD_SLOT, kKernChunkAttn, ((int64_t)u << 40) | (t & 0xFFFFFFFFFFll));
+    // Block id (step j + 1), slot and mask word (step j) are fetched a step
+    // ahead of their use.  Lane = token: block lane / 4 of the warp's eight.
+    const int first = j0 * kStepBlocks + 8 * w + (lane >> 2), stop = (j0 + steps) * kStepBlocks;
+    auto block_id = [&](int j) {
+      const int e = first + j * kStepBlocks;
+      return e < stop && e < count ? block[e] : -1;
     };
-    resolve(0);
+    auto slot_of = [&](int32_t id) {                 // -2: no such token
+      const int64_t t = 4 * (int64_t)id + (lane & 3);
+      return id >= 0 && t < n ? slots[t] : -2;
+    };
+    auto mask_word = [&](int j) {                    // lane = block of the step, half w
+      const int e = (j0 + j) * kStepBlocks + lane;
+      return w < halves && j < steps && e < count ? mask[(int64_t)w * p.cap + e] : 0u;
+    };
+    int32_t id = block_id(0), id_next = block_id(1);
+    int32_t slot_now = slot_of(id);
+    uint32_t word = mask_word(0);
     for (int j = 0; j < steps && ok; ++j) {
       const int st = j % kStages;
-      if (j >= kStages) ok = mbar_wait_warp(kv_empty(st), (uint32_t)(j / kStages - 1) & 1u, err, kKernChunkAttn);
+      const uint32_t turn = (uint32_t)(j / kStages - 1) & 1u;
+      const int64_t t = 4 * (int64_t)id + (lane & 3);
+      const uint8_t* src = nullptr;
+      if (slot_now >= 0 && (int64_t)slot_now < p.c.b.pool_rows) {
+        src = p.c.b.pool + (int64_t)slot_now * p.c.b.row_bytes;
+      } else if (slot_now == -1 && p.c.b.u[u].host_rows) {
+        src = p.c.b.u[u].host_rows + t * p.c.b.row_bytes;
+      } else if (id >= 0 && t < n) {
+        report_error(err, QSA_ERR_BAD_SLOT, kKernChunkAttn, ((int64_t)u << 40) | (t & 0xFFFFFFFFFFll));
+      }
+      const int32_t slot_next = slot_of(id_next), id_after = block_id(j + 2);
+      const uint32_t word_next = mask_word(j + 1);
+      if (j >= kStages) ok = mbar_wait_warp(k_empty(st), turn, err, kKernChunkAttn);
       if (!ok) break;
-      StepMeta& m = meta[st];
-      const uint32_t there = __ballot_sync(0xFFFFFFFFu, src != nullptr);
-      const bool past = id >= 0 && 4 * (int64_t)id + 3 > pos0;
-      const bool special = __any_sync(0xFFFFFFFFu, past || (id >= 0 && src == nullptr));
-      if (lane == 0) {
-        m.valid[w] = there;
-        m.special[w] = special;
-      }
-      if ((lane & 3) == 0) m.block[8 * w + (lane >> 2)] = id;
-      if (w < halves) {
-        // transpose the step's 32 block masks: lane q gets query q's bits
-        const int e = (j0 + j) * kStepBlocks + lane;
-        const uint32_t bm = e < count ? mask[(int64_t)w * p.cap + e] : 0u;
-        uint32_t mine = 0;
+      const uint32_t kdst = kOffKv + st * kStageBytes + 32 * w * 128, vdst = kdst + kKvBytes;
+      const uintptr_t from = reinterpret_cast<uintptr_t>(src);
+      StepMeta& m = meta[j % kMetas];
+      auto write_meta = [&]() {
+        const uint32_t there = __ballot_sync(0xFFFFFFFFu, src != nullptr);
+        const bool past = id >= 0 && 4 * (int64_t)id + 3 > pos0;
+        const bool special = __any_sync(0xFFFFFFFFu, past || (id >= 0 && src == nullptr));
+        if (lane == 0) {
+          m.valid[w] = there;
+          m.special[w] = special;
+        }
+        if ((lane & 3) == 0) m.block[8 * w + (lane >> 2)] = id;
+        if (w < halves) {                            // transposed: lane q gets query q's bits of the 32 blocks
+          uint32_t mine = 0;
 #pragma unroll
-        for (int q = 0; q < 32; ++q) {
-          const uint32_t b = __ballot_sync(0xFFFFFFFFu, (bm >> q) & 1u);
-          if (lane == q) mine = b;
+          for (int q = 0; q < 32; ++q) {
+            const uint32_t b = __ballot_sync(0xFFFFFFFFu, (word >> q) & 1u);
+            if (lane == q) mine = b;
+          }
+          m.mine[w][lane] = mine;
         }
-        m.mine[w][lane] = mine;
-      }
-      // lanes 0-15 copy K[g] (256 bytes of bf16), lanes 16-31 V[g]
-      const uint32_t dst0 = sb + kOffKv + st * kStageBytes + (lane < 16 ? 0 : kKvBytes) + ((lane & 15) >> 3) * kPanel;
-      const uint32_t c = lane & 7;
+      };
       if (!kFp8) {
-        const int off = (lane < 16 ? 0 : kKvHeads * kHeadDim * 2) + g * kHeadDim * 2 + (lane & 15) * 16;
+        // 16 lanes copy the 256 bytes of a token's K[g] (or V[g]); two tokens per turn
+        const uint32_t c = lane & 15, hi = lane >> 4;
+        auto copy = [&](uint32_t dst, int off) {
 #pragma unroll 8
-        for (int i = 0; i < 32; ++i) {
-          const uint8_t* s = reinterpret_cast<const uint8_t*>(
-              __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uintptr_t>(src), i));
-          const uint32_t r = 32 * w + i;
-          cp_async16(dst0 + r * 128 + ((c ^ (r & 7)) << 4), s ? s + off : p.c.b.pool, s ? 16u : 0u);
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t r = 2 * i + hi;
+            const uint8_t* s = reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, from, (int)r));
+            cp_async16(sb + dst + (c >> 3) * kPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4), s ? s + off + c * 16 : p.c.b.pool,
+                       s ? 16u : 0u);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        copy(kdst, g * kHeadDim * 2);
+        write_meta();
+        if (j > 0) {                                 // V of step j - 1 has landed
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          fence_async_smem();
+          mbar_arrive(v_full((j - 1) % kStages));
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        resolve(j + 1);
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (j >= kStages) ok = mbar_wait_warp(v_empty(st), turn, err, kKernChunkAttn);
+        if (!ok) break;
+        copy(vdst, (kKvHeads + g) * kHeadDim * 2);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        fence_async_smem();
+        mbar_arrive(k_full(st));
+        if (j + 1 == steps) {
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+          fence_async_smem();
+          mbar_arrive(v_full(st));
+        }
       } else {
+        // 8 lanes read the 128 codes of a token's K[g] (or V[g]); four tokens per turn
+        const uint32_t c = lane & 7, four = lane >> 3;
+        uint4 kv[8], vv[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint8_t* s = reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, from, (int)(4 * i + four)));
+          kv[i] = s ? *reinterpret_cast<const uint4*>(s + g * kHeadDim + c * 16) : make_uint4(0, 0, 0, 0);
+          vv[i] = s ? *reinterpret_cast<const uint4*>(s + (kKvHeads + g) * kHeadDim + c * 16) : make_uint4(0, 0, 0, 0);
+        }
         float ks = 0.f, vs = 0.f;
         if (src) {
           const uint16_t* sc = reinterpret_cast<const uint16_t*>(src + 2 * kKvHeads * kHeadDim);
           ks = __half2float(__ushort_as_half(sc[g]));
           vs = __half2float(__ushort_as_half(sc[kKvHeads + g]));
         }
-        const int off = (lane < 16 ? 0 : kKvHeads * kHeadDim) + g * kHeadDim + (lane & 15) * 8;
-#pragma unroll 1
-        for (int i8 = 0; i8 < 32; i8 += 8) {
-          uint2 v[8];
+        write_meta();
+        scales[j % kMetas].k[32 * w + lane] = ks * p.scale_log2;
+        scales[j % kMetas].v[32 * w + lane] = vs;
+        // codes 16 c .. +15 are chunks 2 c, 2 c + 1 of the row's 16
+        auto store = [&](uint32_t dst, const uint4 (&x)[8]) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint8_t* s = reinterpret_cast<const uint8_t*>(
-                __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uintptr_t>(src), i8 + i));
-            v[i] = s ? *reinterpret_cast<const uint2*>(s + off) : make_uint2(0, 0);
+            const uint32_t r = 4 * i + four;
+            uint8_t* row = smem + dst + (c >> 2) * kPanel + r * 128;
+            const uint32_t c0 = (2 * c) & 7;
+            *reinterpret_cast<uint4*>(row + ((c0 ^ (r & 7)) << 4)) = codes8_bf16(make_uint2(x[i].x, x[i].y));
+            *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (r & 7)) << 4)) = codes8_bf16(make_uint2(x[i].z, x[i].w));
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t r = 32 * w + i8 + i;
-            *reinterpret_cast<uint4*>(smem + (dst0 - sb) + r * 128 + ((c ^ (r & 7)) << 4)) = codes8_bf16(v[i]);
-          }
-        }
-        scales[st].k[32 * w + lane] = ks * p.scale_log2;
-        scales[st].v[32 * w + lane] = vs;
-        resolve(j + 1);
+          fence_async_smem();
+        };
+        store(kdst, kv);
+        mbar_arrive(k_full(st));
+        if (j >= kStages) ok = mbar_wait_warp(v_empty(st), turn, err, kKernChunkAttn);
+        if (!ok) break;
+        store(vdst, vv);
+        mbar_arrive(v_full(st));
       }
-      fence_async_smem();
-      mbar_arrive(kv_full(st));
+      id = id_next;
+      id_next = id_after;
+      slot_now = slot_next;
+      word = word_next;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp == kRoleMma) {
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     const uint32_t is = idesc_bf16(kStepTokens, false), io = idesc_bf16(kHeadDim, true);
@@ -454,21 +511,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
           const uint64_t o = (uint64_t)(((k >> 2) * kPanel + (k & 3) * 32) >> 4);
           mma_ss(tm + kColS + 128u * (uint32_t)h, a + o, b + o, is, k != 0);
         }
+        mbar_arrive(s_full(h));      // passes on the loaders' writes of the meta (waited for with K)
         commit(s_full(h));
+        if (h == halves - 1) commit(k_empty(st));
       }
       __syncwarp();
     };
     if (steps > 0) {
-      ok = mbar_wait_warp(kv_full(0), 0, err, kKernChunkAttn);
+      ok = mbar_wait_warp(k_full(0), 0, err, kKernChunkAttn);
       if (ok) {
         fence_after();
         for (int h = 0; h < halves; ++h) issue_s(h, 0);
       }
     }
     for (int j = 0; j < steps && ok; ++j) {
-      const int st = j % kStages;
+      const int st = j % kStages, sn = (j + 1) % kStages;
       for (int h = 0; h < halves && ok; ++h) {
-        ok = mbar_wait_warp(p_full(h), (uint32_t)j & 1u, err, kKernChunkAttn);
+        if (h == 0) ok = mbar_wait_warp(v_full(st), (uint32_t)(j / kStages) & 1u, err, kKernChunkAttn);
+        if (ok) ok = mbar_wait_warp(p_full(h), (uint32_t)j & 1u, err, kKernChunkAttn);
         if (!ok) break;
         fence_after();
         if (elect_one()) {
@@ -478,16 +538,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
             mma_ts(tm + kColO + 128u * (uint32_t)h, tm + kColS + 128u * (uint32_t)h + 8u * k, b + (uint64_t)(k * 2048 >> 4),
                    io, j > 0 || k > 0);
           commit(o_full(h));
-          if (h == halves - 1) commit(kv_empty(st));
+          if (h == halves - 1) commit(v_empty(st));
         }
         __syncwarp();
         if (j + 1 < steps) {
           // the next S goes over this step's P: after its products are complete
-          if (h == 0) ok = mbar_wait_warp(kv_full((j + 1) % kStages), (uint32_t)((j + 1) / kStages) & 1u, err, kKernChunkAttn);
+          if (h == 0) ok = mbar_wait_warp(k_full(sn), (uint32_t)((j + 1) / kStages) & 1u, err, kKernChunkAttn);
           if (ok) ok = mbar_wait_warp(o_full(h), (uint32_t)j & 1u, err, kKernChunkAttn);
           if (!ok) break;
           fence_after();
-          issue_s(h, (j + 1) % kStages);
+          issue_s(h, sn);
         }
       }
     }
@@ -503,13 +563,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
     const float f = kFp8 ? 1.f : p.scale_log2;       // FP8: the K scales hold it
     float m = -INFINITY, l = 0.f;                    // in units of log2
     for (int j = 0; j < steps; ++j) {
-      const int st = j % kStages;
       ok = mbar_wait_warp(s_full(h), (uint32_t)j & 1u, err, kKernChunkAttn);
-      // (long complete; orders the loaders' writes of the meta before its reads)
-      if (ok) ok = mbar_wait_warp(kv_full(st), (uint32_t)(j / kStages) & 1u, err, kKernChunkAttn);
       if (!ok) break;
       fence_after();
-      const StepMeta& sm = meta[st];
+      const StepMeta& sm = meta[j % kMetas];
+      const Scales& sc = scales[j % kMetas];
       const uint32_t mine = sm.mine[h][lane];
       const bool special = (sm.special[0] | sm.special[1] | sm.special[2] | sm.special[3]) != 0;
       // ---- maximum over the step's tokens
@@ -523,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           float s = __uint_as_float(v[i]);
-          if (kFp8) s *= scales[st].k[32 * c + i];
+          if (kFp8) s *= sc.k[32 * c + i];
           mx = fmaxf(mx, s);
         }
       }
@@ -575,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float s = __uint_as_float(v[4 * b + i]);
-            if (kFp8) s *= scales[st].k[32 * c + 4 * b + i];
+            if (kFp8) s *= sc.k[32 * c + 4 * b + i];
             e[i] = __uint_as_float(__float_as_uint(exp2_fast(fmaf(s, f, -ref))) & on);
           }
           if (special) {
@@ -586,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
           l += (e[0] + e[1]) + (e[2] + e[3]);
           if (kFp8) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] *= scales[st].v[32 * c + 4 * b + i];
+            for (int i = 0; i < 4; ++i) e[i] *= sc.v[32 * c + 4 * b + i];
           }
           o[2 * b] = pack_bf16(e[0], e[1]);
           o[2 * b + 1] = pack_bf16(e[2], e[3]);
@@ -774,7 +832,7 @@ cudaError_t launch_chunk_attn(const ChunkDesc& c, const uint16_t* q, const int32
   p.block = reinterpret_cast<int32_t*>(ws + a.off_block);
   p.mask = reinterpret_cast<uint32_t*>(ws + a.off_mask);
   p.part = reinterpret_cast<float*>(ws + a.off_part);
-  const int window = (int)(a.nb < kPlanWindow ? (a.nb + 1) / 2 * 2 : kPlanWindow);
+  const int window = (int)(a.nb < kPlanWindow ? (a.nb + 3) / 4 * 4 : kPlanWindow);
   e = launch_kernel(chunk_plan_kernel, dim3((unsigned)a.tiles), dim3(kPlanThreads), (size_t)window * 8, s, 0, dim3(1),
                     p, window);
   if (e != cudaSuccess) return e;
