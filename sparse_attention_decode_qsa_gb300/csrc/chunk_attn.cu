@@ -21,15 +21,16 @@
 //
 // Split kernel.  The tile's 64 queries x 4 heads of the group are 256 rows, two
 // halves of 128 = the tensor core's M: row = head * 32 + query, so a warp is a
-// head and a lane a query.  Per half and 128 tokens: S = Q K^T (8 MMAs of
+// head and a lane a query.  Per half and 64 tokens: S = Q K^T (8 MMAs of
 // K = 16, both operands in shared memory under the 128-byte swizzle), softmax
 // by the half's 4 warps (thread = row), P (bf16) over S's own columns of tensor
-// memory, O += P V (8 MMAs, P from tensor memory, V as an MN-major operand, so
-// that rows lie in shared memory as they come).  While one half is in softmax
-// the other's MMAs run.  Tensor memory: O and S of two halves, 4 x 128 columns.
+// memory, O += P V (4 MMAs, P from tensor memory, V as an MN-major operand, so
+// that rows lie in shared memory as they come).  Each half has two S tiles in
+// turn: while one is in softmax, the other's P V and next S run.  Tensor
+// memory: per half O (128 columns) and two S (64 each).
 // Warps: 8 softmax, 4 loaders (cp.async of K[g], V[g] of each row, two stages
 // of 128 tokens; FP8 rows are turned into bf16 on the way, exactly, their
-// scales going to the logits and the probabilities), 1 MMA.  All waits are
+// scales going to the logits and the probabilities), 2 MMA (one per half).  All waits are
 // bounded.
 //
 // The running maximum is taken over all tokens of the union (masking it would
@@ -59,8 +60,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 constexpr int kTileQueries = 64;                  // two halves of 32
 constexpr int kStepBlocks = 32, kStepTokens = 4 * kStepBlocks;
+constexpr int kSubTokens = kStepTokens / 2;       // tokens of one S tile
 constexpr int kSoftWarps = 8, kLoadWarps = 4;
-constexpr int kThreads = 32 * (kSoftWarps + kLoadWarps + 1);     // 416
+constexpr int kMmaWarps = 2;                      // one per half
+constexpr int kThreads = 32 * (kSoftWarps + kLoadWarps + kMmaWarps);     // 448
 constexpr int kRoleLoad = kSoftWarps, kRoleMma = kSoftWarps + kLoadWarps;
 constexpr int kStages = 2;
 constexpr int kPanel = 128 * 128;                 // 128 rows of 64 bf16
@@ -87,8 +90,9 @@ constexpr int kOffMeta = kOffKv + kStages * kStageBytes;
 constexpr int kMetas = 4;
 constexpr int kOffScales = kOffMeta + kMetas * (int)sizeof(StepMeta);
 constexpr int kOffBar = kOffScales + kMetas * (int)sizeof(Scales);
-// k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2]
-constexpr int kNumBars = 4 * kStages + 6;
+// k_full[2], k_empty[2], v_full[2], v_empty[2], then per (half, 64 tokens)
+// s_full[4], p_full[4], o_full[4]
+constexpr int kNumBars = 4 * kStages + 12;
 constexpr int kOffSlot = kOffBar + 8 * kNumBars;
 constexpr int kSmemBytes = kOffSlot + 16 + 1024;
 static_assert(kSmemBytes <= 227 * 1024 && sizeof(StepMeta) % 16 == 0, "one CTA's shared memory");
@@ -221,22 +225,31 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const __gri
     }
     __syncthreads();
     if (w0 == 0) grid_dependency_wait();               // the selection is read from here on
-    // entries of all queries, 32 of one query per warp and turn
-    const int turns = (p.k_max + 31) / 32;
-#pragma unroll 4
+    // a warp takes 256 entries of one query at a time, all loads in flight
+    const int turns = (p.k_max + 255) / 256;
     for (int i = warp; i < nq * turns; i += kPlanWarps) {
-      const int q = i / turns, j = (i % turns) * 32 + lane;
+      const int q = i / turns, j0 = (i % turns) * 256 + lane;
+      const int32_t* sel = p.sel + (int64_t)(x0 + q) * p.k_max;
       const int nsel = p.n_sel[x0 + q];
-      if (nsel < 0 || nsel > p.k_max) {
-        if (w0 == 0 && j == 0) report_error(p.c.b.err, QSA_ERR_BAD_BLOCK, kKernChunkAttn, nsel);
+      const bool bad = nsel < 0 || nsel > p.k_max;
+      int32_t id[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) id[e] = j0 + 32 * e < p.k_max ? sel[j0 + 32 * e] : 0;
+      if (bad) {
+        if (w0 == 0 && lane == 0) report_error(p.c.b.err, QSA_ERR_BAD_BLOCK, kKernChunkAttn, nsel);
         continue;
       }
-      if (j >= nsel) continue;
-      const int64_t b = p.sel[(int64_t)(x0 + q) * p.k_max + j];
-      if (b < 0 || b > p.c.position(u, x0 + q) / 4) {
-        if (w0 == 0) report_error(p.c.b.err, QSA_ERR_BAD_BLOCK, kKernChunkAttn, b);
-      } else if (b >= w0 && b < w0 + size) {
-        atomicOr((q < 32 ? bits0 : bits1) + (b - w0), 1u << (q & 31));
+      const int64_t lim = p.c.position(u, x0 + q) / 4;
+      uint32_t* bits = q < 32 ? bits0 : bits1;
+      const uint32_t bit = 1u << (q & 31);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (j0 + 32 * e >= nsel) continue;
+        if (id[e] < 0 || id[e] > lim) {
+          if (w0 == 0) report_error(p.c.b.err, QSA_ERR_BAD_BLOCK, kKernChunkAttn, id[e]);
+        } else if (id[e] >= w0 && id[e] < w0 + size) {
+          atomicOr(bits + (id[e] - w0), bit);
+        }
       }
     }
     __syncthreads();
@@ -310,9 +323,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
   auto k_empty = [&](int i) { return bars + 8u * (uint32_t)(kStages + i); };
   auto v_full = [&](int i) { return bars + 8u * (uint32_t)(2 * kStages + i); };
   auto v_empty = [&](int i) { return bars + 8u * (uint32_t)(3 * kStages + i); };
-  auto s_full = [&](int h) { return bars + 8u * (uint32_t)(4 * kStages + h); };
-  auto p_full = [&](int h) { return bars + 8u * (uint32_t)(4 * kStages + 2 + h); };
-  auto o_full = [&](int h) { return bars + 8u * (uint32_t)(4 * kStages + 4 + h); };
+  auto s_full = [&](int h, int c) { return bars + 8u * (uint32_t)(4 * kStages + 2 * h + c); };
+  auto p_full = [&](int h, int c) { return bars + 8u * (uint32_t)(4 * kStages + 4 + 2 * h + c); };
+  auto o_full = [&](int h, int c) { return bars + 8u * (uint32_t)(4 * kStages + 8 + 2 * h + c); };
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kOffSlot);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   ErrorWord* err = p.c.b.err;
@@ -332,11 +345,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
     if (lane == 0) {
       for (int i = 0; i < kStages; ++i) {
         mbar_init(k_full(i), 32 * kLoadWarps);
-        mbar_init(k_empty(i), 1);
+        mbar_init(k_empty(i), (uint32_t)halves);
         mbar_init(v_full(i), 32 * kLoadWarps);
-        mbar_init(v_empty(i), 1);
+        mbar_init(v_empty(i), (uint32_t)halves);
       }
-      for (int h = 0; h < 2; ++h) { mbar_init(s_full(h), 2); mbar_init(p_full(h), 128); mbar_init(o_full(h), 1); }
+      for (int i = 0; i < 4; ++i) {
+        mbar_init(s_full(i >> 1, i & 1), 2);
+        mbar_init(p_full(i >> 1, i & 1), 128);
+        mbar_init(o_full(i >> 1, i & 1), 1);
+      }
       mbar_fence_init();
     }
   }
@@ -500,20 +517,25 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
       word = word_next;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-  } else if (warp == kRoleMma) {
+  } else if (warp >= kRoleMma && warp - kRoleMma < halves) {
+    // ---- MMA warp of half h
+    const int h = warp - kRoleMma;
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-    const uint32_t is = idesc_bf16(kStepTokens, false), io = idesc_bf16(kHeadDim, true);
-    auto issue_s = [&](int h, int st) {
+    const uint32_t colO = tm + kColO + 128u * (uint32_t)h, colS = tm + kColS + 128u * (uint32_t)h;
+    const uint32_t is = idesc_bf16(kSubTokens, false), io = idesc_bf16(kHeadDim, true);
+    const uint64_t qd = desc_sw128(sb + h * 2 * kPanel, 16);
+    // S of tokens 64 c .. of the step in K stage st
+    auto issue_s = [&](int c, int st) {
       if (elect_one()) {
-        const uint64_t a = desc_sw128(sb + h * 2 * kPanel, 16), b = desc_sw128(sb + kOffKv + st * kStageBytes, 16);
+        const uint64_t b = desc_sw128(sb + kOffKv + st * kStageBytes + c * kSubTokens * 128, 16);
 #pragma unroll
         for (int k = 0; k < kHeadDim / 16; ++k) {
           const uint64_t o = (uint64_t)(((k >> 2) * kPanel + (k & 3) * 32) >> 4);
-          mma_ss(tm + kColS + 128u * (uint32_t)h, a + o, b + o, is, k != 0);
+          mma_ss(colS + 64u * (uint32_t)c, qd + o, b + o, is, k != 0);
         }
-        mbar_arrive(s_full(h));      // passes on the loaders' writes of the meta (waited for with K)
-        commit(s_full(h));
-        if (h == halves - 1) commit(k_empty(st));
+        mbar_arrive(s_full(h, c));   // passes on the loaders' writes of the meta (waited for with K)
+        commit(s_full(h, c));
+        if (c == 1) commit(k_empty(st));
       }
       __syncwarp();
     };
@@ -521,88 +543,98 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
       ok = mbar_wait_warp(k_full(0), 0, err, kKernChunkAttn);
       if (ok) {
         fence_after();
-        for (int h = 0; h < halves; ++h) issue_s(h, 0);
+        issue_s(0, 0);
+        issue_s(1, 0);
       }
     }
+#pragma unroll 1
     for (int j = 0; j < steps && ok; ++j) {
       const int st = j % kStages, sn = (j + 1) % kStages;
-      for (int h = 0; h < halves && ok; ++h) {
-        if (h == 0) ok = mbar_wait_warp(v_full(st), (uint32_t)(j / kStages) & 1u, err, kKernChunkAttn);
-        if (ok) ok = mbar_wait_warp(p_full(h), (uint32_t)j & 1u, err, kKernChunkAttn);
+      ok = mbar_wait_warp(v_full(st), (uint32_t)(j / kStages) & 1u, err, kKernChunkAttn);
+#pragma unroll 1
+      for (int c = 0; c < 2 && ok; ++c) {
+        ok = mbar_wait_warp(p_full(h, c), (uint32_t)j & 1u, err, kKernChunkAttn);
         if (!ok) break;
         fence_after();
         if (elect_one()) {
-          const uint64_t b = desc_sw128(sb + kOffKv + st * kStageBytes + kKvBytes, kPanel);
+          const uint64_t b = desc_sw128(sb + kOffKv + st * kStageBytes + kKvBytes + c * kSubTokens * 128, kPanel);
 #pragma unroll
-          for (int k = 0; k < kStepTokens / 16; ++k)
-            mma_ts(tm + kColO + 128u * (uint32_t)h, tm + kColS + 128u * (uint32_t)h + 8u * k, b + (uint64_t)(k * 2048 >> 4),
-                   io, j > 0 || k > 0);
-          commit(o_full(h));
-          if (h == halves - 1) commit(v_empty(st));
+          for (int k = 0; k < kSubTokens / 16; ++k)
+            mma_ts(colO, colS + 64u * (uint32_t)c + 8u * k, b + (uint64_t)(k * 2048 >> 4), io, j > 0 || c > 0 || k > 0);
+          commit(o_full(h, c));
+          if (c == 1) commit(v_empty(st));
         }
         __syncwarp();
         if (j + 1 < steps) {
-          // the next S goes over this step's P: after its products are complete
-          if (h == 0) ok = mbar_wait_warp(k_full(sn), (uint32_t)((j + 1) / kStages) & 1u, err, kKernChunkAttn);
-          if (ok) ok = mbar_wait_warp(o_full(h), (uint32_t)j & 1u, err, kKernChunkAttn);
+          // the next S goes over this P: after its products are complete
+          if (c == 0) ok = mbar_wait_warp(k_full(sn), (uint32_t)((j + 1) / kStages) & 1u, err, kKernChunkAttn);
+          if (ok) ok = mbar_wait_warp(o_full(h, c), (uint32_t)j & 1u, err, kKernChunkAttn);
           if (!ok) break;
           fence_after();
-          issue_s(h, sn);
+          issue_s(c, sn);
         }
       }
     }
     // every product is complete before tensor memory is given back
-    if (ok && steps > 0)
-      for (int h = 0; h < halves; ++h) mbar_wait_warp(o_full(h), (uint32_t)(steps - 1) & 1u, err, kKernChunkAttn);
+    if (ok && steps > 0) mbar_wait_warp(o_full(h, 1), (uint32_t)(steps - 1) & 1u, err, kKernChunkAttn);
   } else if (warp / 4 < halves) {
     // ---- softmax: thread = row (head warp & 3, query lane) of half h
     const int h = warp >> 2, head = g * kGroup + (warp & 3), q = 32 * h + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t colS = lane_base + kColS + 128u * (uint32_t)h, colO = lane_base + kColO + 128u * (uint32_t)h;
+    const uint32_t colO = lane_base + kColO + 128u * (uint32_t)h;
     const int64_t pos = pos0 + q;
     const float f = kFp8 ? 1.f : p.scale_log2;       // FP8: the K scales hold it
     float m = -INFINITY, l = 0.f;                    // in units of log2
-    for (int j = 0; j < steps; ++j) {
-      ok = mbar_wait_warp(s_full(h), (uint32_t)j & 1u, err, kKernChunkAttn);
+#pragma unroll 1
+    for (int jc = 0; jc < 2 * steps; ++jc) {
+      const int j = jc >> 1, c = jc & 1;             // tokens 64 c .. of step j
+      const uint32_t colS = lane_base + kColS + 128u * (uint32_t)h + 64u * (uint32_t)c;
+      ok = mbar_wait_warp(s_full(h, c), (uint32_t)j & 1u, err, kKernChunkAttn);
       if (!ok) break;
       fence_after();
+      uint32_t v[2][32];
+      ld32(colS, v[0]);
+      ld32(colS + 32u, v[1]);
       const StepMeta& sm = meta[j % kMetas];
       const Scales& sc = scales[j % kMetas];
-      const uint32_t mine = sm.mine[h][lane];
+      const uint32_t mine = sm.mine[h][lane] >> (16 * c);
       const bool special = (sm.special[0] | sm.special[1] | sm.special[2] | sm.special[3]) != 0;
-      // ---- maximum over the step's tokens
+      wait_ld();
+      reg_fence(v[0]);
+      reg_fence(v[1]);
+      // ---- maximum over the tokens
       float mx = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32];
-        ld32(colS + 32u * c, v);
-        wait_ld();
-        reg_fence(v);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float s = __uint_as_float(v[i]);
-          if (kFp8) s *= sc.k[32 * c + i];
-          mx = fmaxf(mx, s);
+      for (int i = 0; i < kSubTokens; ++i) {
+        float s = __uint_as_float(v[i >> 5][i & 31]);
+        if (kFp8) {
+          s *= sc.k[kSubTokens * c + i];
+          v[i >> 5][i & 31] = __float_as_uint(s);
         }
+        mx = fmaxf(mx, s);
       }
       mx *= f;
       // the reference goes up only when the maximum has left it 2^8 behind
-      const bool up = mx > m + 8.f;                  // true for the first step
+      const bool up = mx > m + 8.f;                  // true for the first tokens
       if (__any_sync(0xFFFFFFFFu, up)) {
         const float mn = fmaxf(m, mx);
         const float a = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
         m = mn;
         l *= a;
-        if (j > 0) {                                 // the products of step j - 1 are complete
+        if (jc > 0) {
+          // all products so far have to be complete
+          ok = mbar_wait_warp(o_full(h, c ^ 1), (uint32_t)((jc - 1) >> 1) & 1u, err, kKernChunkAttn);
+          if (!ok) break;
+          fence_after();
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            ld32(colO + 32u * c, v);
+          for (int i = 0; i < kHeadDim; i += 16) {
+            uint32_t o[16];
+            ld16(colO + (uint32_t)i, o);
             wait_ld();
-            reg_fence(v);
+            reg_fence(o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * a);
-            st32(colO + 32u * c, v);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+            st16(colO + (uint32_t)i, o);
           }
           wait_st();
         }
@@ -610,30 +642,25 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
       const float ref = m == -INFINITY ? 0.f : m;
       // ---- probabilities, masked, over S's columns
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32], o[16];
-        ld32(colS + 32u * c, v);
-        wait_ld();
-        reg_fence(v);
-        uint32_t bits = mine >> (8 * c);
+      for (int w = 0; w < 2; ++w) {                  // 32 tokens
+        uint32_t o[16];
         uint32_t tok = 0xFFFFFFFFu;                  // per token: its row exists and q sees it
         if (special) {
-          tok = sm.valid[c];
-#pragma unroll
+          tok = sm.valid[2 * c + w];
+#pragma unroll 1
           for (int b = 0; b < 8; ++b) {
-            const int64_t left = pos - 4 * (int64_t)sm.block[8 * c + b];   // tokens of the block that q sees, - 1
+            const int64_t left = pos - 4 * (int64_t)sm.block[16 * c + 8 * w + b];   // tokens of the block that q sees, - 1
             const uint32_t seen = left >= 3 ? 0xFu : (left < 0 ? 0u : (2u << (int)left) - 1u);
             tok &= ~(0xFu << (4 * b)) | (seen << (4 * b));
           }
         }
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
-          const uint32_t on = (uint32_t)((int32_t)(bits << (31 - b)) >> 31);
+          const uint32_t on = (uint32_t)((int32_t)(mine << (31 - 8 * w - b)) >> 31);
           float e[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float s = __uint_as_float(v[4 * b + i]);
-            if (kFp8) s *= sc.k[32 * c + 4 * b + i];
+            const float s = __uint_as_float(v[w][4 * b + i]);
             e[i] = __uint_as_float(__float_as_uint(exp2_fast(fmaf(s, f, -ref))) & on);
           }
           if (special) {
@@ -644,19 +671,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
           l += (e[0] + e[1]) + (e[2] + e[3]);
           if (kFp8) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] *= sc.v[32 * c + 4 * b + i];
+            for (int i = 0; i < 4; ++i) e[i] *= sc.v[kSubTokens * c + 32 * w + 4 * b + i];
           }
           o[2 * b] = pack_bf16(e[0], e[1]);
           o[2 * b + 1] = pack_bf16(e[2], e[3]);
         }
-        st16(colS + 16u * c, o);
+        st16(colS + 16u * w, o);
       }
       wait_st();
       fence_before();
-      mbar_arrive(p_full(h));
+      mbar_arrive(p_full(h, c));
     }
     // ---- the row's result
-    if (ok && steps > 0) ok = mbar_wait_warp(o_full(h), (uint32_t)(steps - 1) & 1u, err, kKernChunkAttn);
+    if (ok && steps > 0) ok = mbar_wait_warp(o_full(h, 1), (uint32_t)(steps - 1) & 1u, err, kKernChunkAttn);
     fence_after();
     const int x = x0 + q;
     const bool mine = ok && q < nq;
