@@ -2,21 +2,24 @@
 // of its nb = ceil((p+1)/4) blocks under (score descending, block id
 // ascending), in ascending id order, as select_topk.cu selects for one query.
 //
-// One CTA per row.  A sample of kSample keys (groups of 8 neighbours, spread
-// evenly) gives a pivot that a little more than K keys reach, with a margin of
-// several standard deviations; one pass over the row collects the keys at or
-// above it, with their ids, in shared memory (and their places in a bitmap);
-// the rest works on those alone: radix select (11, 11, 10 bits) for the K-th
-// best key T and how many keys equal to T are kept, two bitmaps (above T, equal
-// to T) walked in id order, which gives the ascending output and the tie rule
-// (lowest ids first).  So a row is read once: the kernel is bound by that
-// (and not by a histogram of the whole row, whose few crowded bins serialise
-// their atomic additions: 222 us for 2048 rows of 32768 scores).
+// One CTA per row.  A sample of the row's keys gives a pivot that a little more
+// than K keys reach, with a margin of several standard deviations; one pass over
+// the row marks the keys at or above it in a bitmap (a ballot per 32 keys); the
+// marked ones, a few thousand at most, are fetched again in id order and the
+// rest works on those alone: one histogram over their own range and a ranking
+// of the few in the K-th key's bin find the K-th best key T and how many keys
+// equal to T are kept, and a scan over the candidates writes the ids, which come
+// out ascending, lowest ids first among the keys equal to T.  So a row is read
+// once, and no histogram sees the whole row, whose few crowded bins would
+// serialise their atomic additions (222 us for 2048 rows of 32768 scores;
+// collecting the keys themselves during the pass took 153; 100 as it is, two
+// fifths of the copy rate: what is left are the short steps after the pass, each
+// a few thousand cycles of latency, three rows to an SM).
 //
 // Where the pivot catches fewer than K or more than kCand keys (long runs of
 // equal scores), or the row is longer than the bitmaps (kWindow blocks), the
-// general path does the radix select on the row itself and walks it in
-// windows.
+// general path does the radix select on the row itself and walks it, window by
+// window, with two bitmaps (above T, equal to T).
 #include "qsa_internal.cuh"
 
 namespace qsa {
@@ -26,8 +29,8 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kWindow = 262144;      // blocks per window: two bitmaps of 32 KiB
-constexpr int kSample = 2048;        // keys of the sample: 4 per thread
 constexpr int kCand = 4096;          // candidates in shared memory
+constexpr int kLongRow = 32768;      // rows beyond this many blocks take 512 samples, not 256
 
 struct ChunkTopkParams {
   ChunkDesc c;
@@ -89,42 +92,37 @@ __device__ __forceinline__ void find_bin(const uint32_t* hist, uint32_t krem, ui
   __syncthreads();
 }
 
-// Ascending ids of the keys above T and the first krem (lowest ids) of those
-// equal to T, from bitmaps of blocks w0 .. w0 + 32 words - 1; out_at and eq_at
-// count what earlier windows gave.
-__device__ __forceinline__ void write_window(const uint32_t* above, const uint32_t* equal, int words, int64_t w0,
-                                             uint32_t krem, int K, int32_t* sel, uint32_t& out_at, uint32_t& eq_at,
-                                             uint32_t* s_warp) {
-  const int per = (words + kThreads - 1) / kThreads;
-  const int j0 = threadIdx.x * per, j1 = j0 + per < words ? j0 + per : words;
-  uint32_t na = 0, ne = 0;
-  for (int j = j0; j < j1; ++j) { na += __popc(above[j]); ne += __popc(equal[j]); }
-  uint32_t ta, te;
-  uint32_t a_before = out_at + scan(na, &ta, s_warp), e_before = eq_at + scan(ne, &te, s_warp);
-  for (int j = j0; j < j1; ++j) {
-    const uint32_t a = above[j], e = equal[j];
-    for (uint32_t m = a | e; m; m &= m - 1) {
-      const int bit = __ffs(m) - 1;
-      const uint32_t at = a_before + min(e_before, krem);
-      if ((a >> bit) & 1u) {
-        if (at < (uint32_t)K) sel[at] = (int32_t)(w0 + 32 * j + bit);
-        ++a_before;
-      } else {
-        if (e_before < krem && at < (uint32_t)K) sel[at] = (int32_t)(w0 + 32 * j + bit);
-        ++e_before;
-      }
-    }
-  }
-  out_at += ta;
-  eq_at += te;
+constexpr uint32_t kLeastKey = 0x007FFFFFu;      // of -infinity
+
+__device__ __forceinline__ float order_value(uint32_t key) {      // of order_key
+  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-__global__ void __launch_bounds__(kThreads) chunk_topk_kernel(const __grid_constant__ ChunkTopkParams p) {
+// The r-th largest (r >= 1) of kSamples keys in shared memory, the smallest key
+// with fewer than r above it: every key is compared with all others, kThreads /
+// kSamples threads per key.  *pivot starts at the largest key value.
+template <int kSamples>
+__device__ __forceinline__ void find_pivot(const uint32_t* sample, uint32_t r, uint32_t* pivot) {
+  constexpr int kShare = kThreads / kSamples;
+  const int part = threadIdx.x % kShare;
+  const uint32_t key = sample[threadIdx.x / kShare];
+  uint32_t above = 0;
+#pragma unroll 8
+  for (int j = part * 4; j < kSamples; j += 4 * kShare) {
+    const uint4 o = *reinterpret_cast<const uint4*>(sample + j);
+    above += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
+  }
+#pragma unroll
+  for (int o = kShare / 2; o > 0; o >>= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, o);
+  if (part == 0 && above < r) atomicMin(pivot, key);
+}
+
+__global__ void __launch_bounds__(kThreads, 3) chunk_topk_kernel(const __grid_constant__ ChunkTopkParams p) {
   extern __shared__ __align__(16) uint32_t bits[];     // two bitmaps of a window
   __shared__ __align__(16) uint32_t hist[kBins];
-  __shared__ uint32_t cand_key[kCand];
+  __shared__ __align__(16) uint32_t cand_key[kCand];
   __shared__ int32_t cand_id[kCand];
-  __shared__ uint32_t s_warp[kWarps], s_bin, s_rank, s_count;
+  __shared__ uint32_t s_warp[kWarps], s_bin, s_rank, s_pivot, s_max, s_list, s_key[32];
   const int x = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
   const int u = p.c.unit_of_row(x);
   const int64_t nb = p.c.position(u, x) / 4 + 1;
@@ -138,124 +136,165 @@ __global__ void __launch_bounds__(kThreads) chunk_topk_kernel(const __grid_const
     return;
   }
   const int words_max = (int)((nb < kWindow ? nb : kWindow) + 31) / 32;
-  uint32_t* above = bits;
-  uint32_t* equal = bits + words_max;
 
-  // ---- the usual path
-  uint32_t found = 0;
+  // ---- the usual path: candidates in id order
+  uint32_t found = 0, pivot = kLeastKey;
   if (nb <= kWindow && K < kCand / 2) {
     const int n = (int)nb;
-    if (tid == 0) s_count = 0;
-    for (int i = tid; i < words_max; i += kThreads) above[i] = equal[i] = 0;
-    // pivot: the key of rank r in the sample.  The number of sample keys among
-    // the row's K best has mean K kSample / n = e and a standard deviation
-    // below sqrt(e): r = e + 6 sqrt(e) + 8.  A row no longer than the candidate
-    // list needs none.
-    uint32_t pivot = 0;
+    if (tid == 0) { s_max = 0; s_list = 0; s_pivot = n > kCand ? 0xFFFFFFFFu : kLeastKey; }
+    for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+    // The number of sample keys among the row's K best has mean e = K samples /
+    // n and a standard deviation below sqrt(e): rank r = e + 4 sqrt(e) + 4.  A
+    // row no longer than the candidate list needs no pivot.
     if (n > kCand) {
-      const float e = (float)K * kSample / (float)n;
-      uint32_t krem = (uint32_t)(e + 6.f * sqrtf(e)) + 8u;
-      uint32_t k[kSample / kThreads];
-      const int group = tid >> 1, groups = kSample / 8;
-      const int64_t at = (int64_t)group * (n - 8) / (groups - 1) + 4 * (tid & 1);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) k[i] = order_key(s[at + i]);
-      uint32_t mask = 0;
-#pragma unroll 1
-      for (int shift = 21; shift >= 10; shift -= 11) {     // 22 bits are fine enough
-        for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if ((k[i] & mask) == pivot) atomicAdd(&hist[(k[i] >> shift) & 2047u], 1u);
-        __syncthreads();
-        find_bin(hist, krem, s_warp, &s_bin, &s_rank);
-        pivot |= s_bin << shift;
-        mask |= 2047u << shift;
-        krem = s_rank;
-        __syncthreads();
-      }
-    } else {
+      const int samples = n > kLongRow ? kThreads : kThreads / 2;
+      const float e = (float)K * samples / (float)n;
+      const uint32_t r = (uint32_t)(e + 4.f * sqrtf(e)) + 4u;        // below samples: K < kCand / 2 < n / 2
+      // spread evenly: neighbouring blocks' scores go together
+      if (tid < samples) cand_key[tid] = order_key(s[(int64_t)tid * (n - 1) / (samples - 1)]);
       __syncthreads();
+      if (samples == kThreads) find_pivot<kThreads>(cand_key, r, &s_pivot);
+      else find_pivot<kThreads / 2>(cand_key, r, &s_pivot);
     }
-    // one pass over the row
-    auto take = [&](uint32_t key, int id) {
-      if (key >= pivot) {
-        const uint32_t c = atomicAdd(&s_count, 1u);
-        if (c < (uint32_t)kCand) { cand_key[c] = key; cand_id[c] = id; }
-      }
-    };
-    const int head = (int)((16 - (reinterpret_cast<uintptr_t>(s) & 15)) & 15) / 4;   // to 16-byte loads
-    if (tid < head && tid < n) take(order_key(s[tid]), tid);
-    const int quads = (n - head) / 4;
-    const float4* s4 = reinterpret_cast<const float4*>(s + head);
+    __syncthreads();
+    pivot = s_pivot;
+    // one pass over the row: a warp takes 256 neighbouring keys at a time, one
+    // bitmap word per 32
+    // (the keys' order is the values' own: scores are not NaN)
     constexpr int kBatch = 8;
-    for (int q0 = tid; q0 < quads; q0 += kThreads * kBatch) {
-      float4 v[kBatch];
+    const int warp = tid >> 5;
+    const float least = order_value(pivot);
+    float v[kBatch];
+    auto load = [&](int b) {
+      if (b + 32 * kBatch <= n) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int q = q0 + i * kThreads;
-        v[i] = q < quads ? __ldcs(s4 + q) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      }
+        for (int i = 0; i < kBatch; ++i) v[i] = __ldg(s + b + 32 * i + lane);
+      } else {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int q = q0 + i * kThreads;
-        if (q >= quads) break;
-        const uint32_t k0 = order_key(v[i].x), k1 = order_key(v[i].y), k2 = order_key(v[i].z), k3 = order_key(v[i].w);
-        if (max(max(k0, k1), max(k2, k3)) >= pivot) {
-          const int id = head + 4 * q;
-          take(k0, id);
-          take(k1, id + 1);
-          take(k2, id + 2);
-          take(k3, id + 3);
+        for (int i = 0; i < kBatch; ++i) {
+          const int id = b + 32 * i + lane;
+          v[i] = id < n ? __ldg(s + id) : __uint_as_float(0x7FFFFFFFu);       // NaN: below everything
         }
       }
+    };
+    load(warp * 32 * kBatch);
+    for (int b = warp * 32 * kBatch; b < n; b += kThreads * kBatch) {
+      uint32_t word = 0;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, v[i] >= least);
+        if (lane == i) word = m;
+      }
+      load(b + kThreads * kBatch);       // the next ones, in flight
+      if (lane < kBatch && b / 32 + lane < words_max) bits[b / 32 + lane] = word;
     }
-    for (int i = head + 4 * quads + tid; i < n; i += kThreads) take(order_key(s[i]), i);
     __syncthreads();
-    found = s_count;
+    // the marked keys, in id order: thread t takes words t per .. t per + per - 1
+    const int per = (words_max + kThreads - 1) / kThreads;
+    const int j0 = tid * per, j1 = j0 + per < words_max ? j0 + per : words_max;
+    uint32_t c = 0;
+    for (int j = j0; j < j1; ++j) c += __popc(bits[j]);
+    uint32_t at = scan(c, &found, s_warp);
+    if (found <= (uint32_t)kCand) {
+      for (int j = j0; j < j1; ++j) {
+        for (uint32_t m = bits[j]; m; m &= m - 1) cand_id[at++] = 32 * j + __ffs(m) - 1;
+      }
+      __syncthreads();
+      uint32_t top = 0;
+      for (uint32_t i = tid; i < found; i += kThreads) {
+        const uint32_t k = order_key(__ldg(s + cand_id[i]));
+        cand_key[i] = k;
+        top = max(top, k);
+      }
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      if (lane == 0) atomicMax(&s_max, top);
+    }
     __syncthreads();
   }
 
   // ---- T: the K-th best key, krem: how many keys equal to T are kept
   const bool usual = found >= (uint32_t)K && found <= (uint32_t)kCand;
-  uint32_t T = 0, mask = 0, krem = (uint32_t)K;
-  for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift - 10) {
-    const uint32_t digits = shift == 0 ? 1024u : 2048u;
-    for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
-    __syncthreads();
-    if (usual) {
-      for (uint32_t i = tid; i < found; i += kThreads) {
-        const uint32_t k = cand_key[i];
-        if ((k & mask) == T) atomicAdd(&hist[(k >> shift) & (digits - 1)], 1u);
-      }
-    } else {
-      for (int64_t i = tid; i < nb; i += kThreads) {
-        const uint32_t k = order_key(s[i]);
-        if ((k & mask) == T) atomicAdd(&hist[(k >> shift) & (digits - 1)], 1u);
-      }
-    }
+  uint32_t T = 0, krem = (uint32_t)K;
+  bool exact = false;
+  if (usual) {
+    const uint32_t span = s_max - pivot;
+    const int shift = span < 2048u ? 0 : 21 - __clz(span);         // span >> shift < 2048
+    for (uint32_t i = tid; i < found; i += kThreads) atomicAdd(&hist[(cand_key[i] - pivot) >> shift], 1u);
     __syncthreads();
     find_bin(hist, krem, s_warp, &s_bin, &s_rank);
-    T |= s_bin << shift;
-    mask |= (digits - 1) << shift;
+    const uint32_t bin = s_bin, in_bin = hist[bin];
     krem = s_rank;
+    if (shift == 0) {
+      T = pivot + bin;
+      exact = true;
+    } else if (in_bin <= 32u) {
+      for (uint32_t i = tid; i < found; i += kThreads) {
+        const uint32_t k = cand_key[i];
+        if ((k - pivot) >> shift == bin) s_key[atomicAdd(&s_list, 1u)] = k;
+      }
+      __syncthreads();
+      // every warp ranks them: T is the value with fewer than krem above it and
+      // at least krem above or equal
+      const uint32_t v = (uint32_t)lane < in_bin ? s_key[lane] : 0u;
+      uint32_t gt = 0, eq = 0;
+      for (uint32_t j = 0; j < in_bin; ++j) {
+        const uint32_t o = __shfl_sync(0xFFFFFFFFu, v, (int)j);
+        gt += o > v;
+        eq += o == v;
+      }
+      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, (uint32_t)lane < in_bin && gt < krem && krem <= gt + eq);
+      const int src = hit ? __ffs(hit) - 1 : 0;
+      T = __shfl_sync(0xFFFFFFFFu, v, src);
+      krem -= __shfl_sync(0xFFFFFFFFu, gt, src);
+      exact = true;
+    }
+  }
+  if (!exact) {                          // radix select on the candidates, or on the row
+    uint32_t mask = 0;
+    T = 0;
+    krem = (uint32_t)K;
     __syncthreads();
+#pragma unroll 1
+    for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift - 10) {
+      const uint32_t digits = shift == 0 ? 1024u : 2048u;
+      for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+      __syncthreads();
+      const int64_t m = usual ? (int64_t)found : nb;
+      for (int64_t i = tid; i < m; i += kThreads) {
+        const uint32_t k = usual ? cand_key[i] : order_key(s[i]);
+        if ((k & mask) == T) atomicAdd(&hist[(k >> shift) & (digits - 1)], 1u);
+      }
+      __syncthreads();
+      find_bin(hist, krem, s_warp, &s_bin, &s_rank);
+      T |= s_bin << shift;
+      mask |= (digits - 1) << shift;
+      krem = s_rank;
+      __syncthreads();
+    }
   }
 
+  // ---- ids in ascending order
   uint32_t out_at = 0, eq_at = 0;
   if (usual) {
-    for (uint32_t i = tid; i < found; i += kThreads) {
+    const int per = ((int)found + kThreads - 1) / kThreads;          // at most 8
+    const int i0 = tid * per, i1 = i0 + per < (int)found ? i0 + per : (int)found;
+    uint32_t n = 0;                      // keys above T, and (upper half) equal to T
+    for (int i = i0; i < i1; ++i) n += (cand_key[i] > T ? 1u : 0u) + (cand_key[i] == T ? 0x10000u : 0u);
+    uint32_t total;
+    const uint32_t before = scan(n, &total, s_warp);
+    uint32_t a = before & 0xFFFFu, e = before >> 16;
+    for (int i = i0; i < i1; ++i) {
       const uint32_t k = cand_key[i];
-      const int id = cand_id[i];
-      if (k > T) atomicOr(&above[id >> 5], 1u << (id & 31));
-      else if (k == T) atomicOr(&equal[id >> 5], 1u << (id & 31));
+      const uint32_t at = a + min(e, krem);
+      if ((k > T || (k == T && e < krem)) && at < (uint32_t)K) sel[at] = cand_id[i];
+      a += k > T;
+      e += k == T;
     }
-    __syncthreads();
-    write_window(above, equal, words_max, 0, krem, K, sel, out_at, eq_at, s_warp);
     return;
   }
-  // ---- the general path: the row again, window by window
+  // the general path: the row again, window by window
+  uint32_t* above = bits;
+  uint32_t* equal = bits + words_max;
   for (int64_t w0 = 0; w0 < nb; w0 += kWindow) {
     const int count = nb - w0 < kWindow ? (int)(nb - w0) : kWindow;
     const int words = (count + 31) / 32;
@@ -266,7 +305,28 @@ __global__ void __launch_bounds__(kThreads) chunk_topk_kernel(const __grid_const
       if (lane == 0) { above[i / 32] = a; equal[i / 32] = e; }
     }
     __syncthreads();
-    write_window(above, equal, words, w0, krem, K, sel, out_at, eq_at, s_warp);
+    const int per = (words + kThreads - 1) / kThreads;
+    const int j0 = tid * per, j1 = j0 + per < words ? j0 + per : words;
+    uint32_t na = 0, ne = 0;
+    for (int j = j0; j < j1; ++j) { na += __popc(above[j]); ne += __popc(equal[j]); }
+    uint32_t ta, te;
+    uint32_t a_before = out_at + scan(na, &ta, s_warp), e_before = eq_at + scan(ne, &te, s_warp);
+    for (int j = j0; j < j1; ++j) {
+      const uint32_t a = above[j], e = equal[j];
+      for (uint32_t m = a | e; m; m &= m - 1) {
+        const int bit = __ffs(m) - 1;
+        const uint32_t at = a_before + min(e_before, krem);
+        if ((a >> bit) & 1u) {
+          if (at < (uint32_t)K) sel[at] = (int32_t)(w0 + 32 * j + bit);
+          ++a_before;
+        } else {
+          if (e_before < krem && at < (uint32_t)K) sel[at] = (int32_t)(w0 + 32 * j + bit);
+          ++e_before;
+        }
+      }
+    }
+    out_at += ta;
+    eq_at += te;
     __syncthreads();
   }
 }
