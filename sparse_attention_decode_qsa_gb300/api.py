@@ -40,12 +40,8 @@ def _chunk(handles, n_tokens, layer0: int, n_layers: int):
     n = len(handles)
     if len(n_tokens) != n:
         raise ValueError("one token count per request")
-    arr = (N.Handle * n)(*handles)
-    cnt = (C.c_int32 * n)(*n_tokens)
-    ch = N.Chunk(n, layer0, n_layers, 0, C.cast(arr, C.POINTER(N.Handle)),
-                 C.cast(cnt, C.POINTER(C.c_int32)))
-    ch._keep = (arr, cnt)
-    return ch
+    # (assigned arrays are kept alive by the structure)
+    return N.Chunk(n, layer0, n_layers, 0, (N.Handle * n)(*handles), (C.c_int32 * n)(*n_tokens))
 
 
 class HostMemory:
@@ -301,17 +297,23 @@ class Cache:
                                             _stream(stream)), "qsa_sparse_decode_attn")
 
     def _rows(self, t, what, dtypes, shape):
-        """Pointer of a per-row tensor.  Its type, shape (None: any size), device
-        and layout are checked here, since the library sees a bare address."""
+        """Address of a per-row tensor (None: a null pointer).  Its type, shape,
+        device and layout are checked here, since the library sees an address."""
         if t is None:
             return None
         if t.dtype not in dtypes:
             raise ValueError(f"{what}: type {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-        if t.dim() != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape)):
+        if t.shape != shape:
             raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
         if self.device is not None and t.device != self.pool.device:
             raise ValueError(f"{what}: on {t.device}, the cache on {self.pool.device}")
         return _ptr(t)
+
+    def _current(self, stream):
+        """The stream given, else the current one of the cache's device."""
+        if stream is None and self.device is not None:
+            return torch.cuda.current_stream(self.pool.device).cuda_stream
+        return _stream(stream)
 
     # ------------------------------------------------ several tokens at once
     # handles: requests; n_tokens: how many of each request's newest tokens.
@@ -323,7 +325,7 @@ class Cache:
         check(self.L.qsa_append_chunk(self.h, C.byref(ch),
                                       self._rows(k_new, "k_new", (torch.float32,), (rows, N.INDEX_DIM)),
                                       self._rows(kv_new, "kv_new", (torch.uint8,), (rows, N.ROW_BYTES)),
-                                      _stream(stream)), "qsa_append_chunk")
+                                      self._current(stream)), "qsa_append_chunk")
 
     def chunk_index_score(self, handles, n_tokens, layer0, n_layers, q_idx, w, blk_scores, stream=None):
         """Block scores of every query: q_idx fp32 or bf16 [rows][8][64], w fp32
@@ -335,8 +337,8 @@ class Cache:
             self._rows(q_idx, "q_idx", (torch.float32, torch.bfloat16), (rows, N.INDEX_HEADS, N.INDEX_DIM)),
             N.QUERY_BF16 if q_idx.dtype == torch.bfloat16 else N.QUERY_F32,
             self._rows(w, "w", (torch.float32,), (rows, N.INDEX_HEADS)),
-            self._rows(blk_scores, "blk_scores", (torch.float32,), (rows, None)), blk_scores.shape[-1],
-            _stream(stream)), "qsa_chunk_index_score")
+            self._rows(blk_scores, "blk_scores", (torch.float32,), (rows, blk_scores.shape[-1])), blk_scores.shape[-1],
+            self._current(stream)), "qsa_chunk_index_score")
 
     def chunk_select_topk(self, handles, n_tokens, layer0, n_layers, blk_scores, budget_tokens,
                           sel_blocks, n_sel, stream=None):
@@ -344,10 +346,10 @@ class Cache:
         ch = _chunk(handles, n_tokens, layer0, n_layers)
         rows = n_layers * sum(n_tokens)
         check(self.L.qsa_chunk_select_topk(
-            self.h, C.byref(ch), self._rows(blk_scores, "blk_scores", (torch.float32,), (rows, None)),
+            self.h, C.byref(ch), self._rows(blk_scores, "blk_scores", (torch.float32,), (rows, blk_scores.shape[-1])),
             blk_scores.shape[-1], budget_tokens,
             self._rows(sel_blocks, "sel_blocks", (torch.int32,), (rows, budget_tokens // 4)),
-            self._rows(n_sel, "n_sel", (torch.int32,), (rows,)), _stream(stream)), "qsa_chunk_select_topk")
+            self._rows(n_sel, "n_sel", (torch.int32,), (rows,)), self._current(stream)), "qsa_chunk_select_topk")
 
     def chunk_attn_workspace_bytes(self, handles, n_tokens, layer0, n_layers, budget_tokens) -> int:
         ch = _chunk(handles, n_tokens, layer0, n_layers)
@@ -376,5 +378,5 @@ class Cache:
             self._rows(n_sel, "n_sel", (torch.int32,), (rows,)), budget_tokens, float(softmax_scale),
             self._rows(out, "out", (torch.bfloat16,), heads),
             self._rows(lse, "lse", (torch.float32,), (rows, N.Q_HEADS)),
-            self._rows(workspace, "workspace", (torch.uint8,), (None,)), workspace.numel(),
-            _stream(stream)), "qsa_chunk_sparse_attn")
+            self._rows(workspace, "workspace", (torch.uint8,), (workspace.numel(),)), workspace.numel(),
+            self._current(stream)), "qsa_chunk_sparse_attn")
