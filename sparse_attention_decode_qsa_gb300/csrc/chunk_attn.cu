@@ -29,8 +29,8 @@
 // turn: while one is in softmax, the other's P V and next S run.  Tensor
 // memory: per half O (128 columns) and two S (64 each).
 // Warps: 8 softmax, 4 loaders (cp.async of K[g], V[g] of each row, two stages
-// of 128 tokens; FP8 rows are turned into bf16 on the way, exactly, their
-// scales going to the logits and the probabilities), 2 MMA (one per half).  All waits are
+// of 128 tokens; FP8 rows are turned into f16 (K) and bf16 (V) on the way,
+// exactly, their scales going to the logits and the probabilities), 2 MMA (one per half).  All waits are
 // bounded.
 //
 // The running maximum is taken over all tokens of the union (masking it would
@@ -327,6 +327,15 @@ __device__ __forceinline__ uint4 codes8_bf16(uint2 w) {
                     codes2_bf16(w.y, 0x3424));
 }
 
+// Eight e4m3 codes as f16, exactly.
+__device__ __forceinline__ uint32_t codes2_f16(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+__device__ __forceinline__ uint4 codes8_f16(uint2 w) {
+  return make_uint4(codes2_f16(w.x & 0xFFFFu), codes2_f16(w.x >> 16), codes2_f16(w.y & 0xFFFFu), codes2_f16(w.y >> 16));
+}
+
 template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_constant__ ChunkAttnParams p) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -343,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
   auto p_full = [&](int h, int c) { return bars + 8u * (uint32_t)(4 * kStages + 4 + 2 * h + c); };
   auto o_full = [&](int h, int c) { return bars + 8u * (uint32_t)(4 * kStages + 8 + 2 * h + c); };
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kOffSlot);
+  __shared__ float row_factor[kFp8 ? 256 : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   ErrorWord* err = p.c.b.err;
 
@@ -374,14 +384,34 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
     }
   }
   grid_dependency_wait();
-  // ---- Q: row head * 32 + query of each half, two panels of 64 dims
-  for (int i = tid; i < halves * 128 * 16; i += kThreads) {
+  // ---- Q: row head * 32 + query of each half, two panels of 64 dims.  Against
+  // FP8 rows it goes in as f16, beside the K codes, which f16 holds exactly: a
+  // row scaled by the power of two that puts its largest element into [1/2, 1),
+  // where f16 holds a bf16 element exactly down to 2^-17 of the largest and to
+  // 2^-25 of it below; the inverse goes to the logits (row_factor).
+  for (int i = tid; i < halves * 128 * 16; i += kThreads) {      // (whole warps)
     const int c = i & 15, r = (i >> 4) & 127, h = i >> 11;
     const int q = h * 32 + (r & 31), head = g * kGroup + (r >> 5);
     uint4 v = make_uint4(0, 0, 0, 0);
     if (q < nq) v = reinterpret_cast<const uint4*>(p.q + ((int64_t)(x0 + q) * kQHeads + head) * kHeadDim)[c];
     const uint32_t flip = p.sign < 0.f ? 0x80008000u : 0u;
     v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
+    if (kFp8) {
+      uint32_t* w[4] = {&v.x, &v.y, &v.z, &v.w};
+      float top = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(bf16_lo(*w[k])), fabsf(bf16_hi(*w[k]))));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));   // the row's 16 lanes
+      int e = 0;
+      if (top > 0.f && top < INFINITY) frexpf(top, &e);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const __half2 o = __floats2half2_rn(ldexpf(bf16_lo(*w[k]), -e), ldexpf(bf16_hi(*w[k]), -e));
+        *w[k] = *reinterpret_cast<const uint32_t*>(&o);
+      }
+      if (c == 0) row_factor[h * 128 + r] = ldexpf(1.f, e);
+    }
     *reinterpret_cast<uint4*>(smem + (h * 2 + (c >> 3)) * kPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
   }
   fence_async_smem();
@@ -512,22 +542,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
         scales[j % kMetas].k[32 * w + lane] = ks * p.scale_log2;
         scales[j % kMetas].v[32 * w + lane] = vs;
         // codes 16 c .. +15 are chunks 2 c, 2 c + 1 of the row's 16
-        auto store = [&](uint32_t dst, const uint4 (&x)[8]) {
+        auto store = [&](uint32_t dst, const uint4 (&x)[8], auto convert) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t r = 4 * i + four;
             uint8_t* row = smem + dst + (c >> 2) * kPanel + r * 128;
             const uint32_t c0 = (2 * c) & 7;
-            *reinterpret_cast<uint4*>(row + ((c0 ^ (r & 7)) << 4)) = codes8_bf16(make_uint2(x[i].x, x[i].y));
-            *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (r & 7)) << 4)) = codes8_bf16(make_uint2(x[i].z, x[i].w));
+            *reinterpret_cast<uint4*>(row + ((c0 ^ (r & 7)) << 4)) = convert(make_uint2(x[i].x, x[i].y));
+            *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (r & 7)) << 4)) = convert(make_uint2(x[i].z, x[i].w));
           }
           fence_async_smem();
         };
-        store(kdst, kv);
+        store(kdst, kv, [](uint2 w) { return codes8_f16(w); });
         mbar_arrive(k_full(st));
         if (j >= kStages) ok = mbar_wait_warp(v_empty(st), turn, err, kKernChunkAttn);
         if (!ok) break;
-        store(vdst, vv);
+        store(vdst, vv, [](uint2 w) { return codes8_bf16(w); });
         mbar_arrive(v_full(st));
       }
       // FP8 rows are loaded into registers, with no copies in flight: the next
@@ -549,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
     const int h = warp - kRoleMma;
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     const uint32_t colO = tm + kColO + 128u * (uint32_t)h, colS = tm + kColS + 128u * (uint32_t)h;
-    const uint32_t is = idesc_bf16(kSubTokens, false), io = idesc_bf16(kHeadDim, true);
+    const uint32_t is = kFp8 ? idesc_f16(kSubTokens) : idesc_bf16(kSubTokens, false), io = idesc_bf16(kHeadDim, true);
     const uint64_t qd = desc_sw128(sb + h * 2 * kPanel, 16);
     // S of tokens 64 c .. of the step in K stage st
     auto issue_s = [&](int c, int st) {
@@ -610,7 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t colO = lane_base + kColO + 128u * (uint32_t)h;
     const int64_t pos = pos0 + q;
-    const float f = kFp8 ? 1.f : p.scale_log2;       // FP8: the K scales hold it
+    // FP8: the K scales hold the softmax scale
+    const float f = kFp8 ? row_factor[128 * h + (warp & 3) * 32 + lane] : p.scale_log2;
     const uint64_t f2 = pair(f, f);
     float m = -INFINITY, l = 0.f;                    // in units of log2
 #pragma unroll 1
