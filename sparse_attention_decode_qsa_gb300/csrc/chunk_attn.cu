@@ -29,9 +29,9 @@
 // turn: while one is in softmax, the other's P V and next S run.  Tensor
 // memory: per half O (128 columns) and two S (64 each).
 // Warps: 8 softmax, 4 loaders (cp.async of K[g], V[g] of each row, two stages
-// of 128 tokens; FP8 rows are turned into f16 (K) and bf16 (V) on the way,
-// exactly, their scales going to the logits and the probabilities), 2 MMA (one per half).  All waits are
-// bounded.
+// of 128 tokens; FP8 codes are turned into f16 on the way, exactly, their scales
+// going to the logits and the probabilities), 2 MMA (one per half).  All waits
+// are bounded.
 //
 // The running maximum is taken over all tokens of the union (masking it would
 // cost a select per logit): any value serves that is not far below the
@@ -41,9 +41,9 @@
 // computed again over its own tokens alone, by one warp in plain fp32
 // (attend_row): so a token reaches only the queries that select it.
 //
-// Rounding: P to bf16 (at most 2^-9 of each term; the tensor core takes no wider
-// type beside bf16 rows), and the output to bf16; the sum l is taken from the
-// unrounded probabilities, S, O, m and l are fp32.
+// Rounding: P to bf16 (at most 2^-8 of each term; the tensor core takes no wider
+// type beside bf16 rows; P to f16 with FP8 rows, 2^-11), and the output to bf16;
+// the sum l is taken from the unrounded probabilities, S, O, m and l are fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -78,7 +78,7 @@ struct StepMeta {
   int32_t block[kStepBlocks];   // block ids
   int32_t special[4];           // per loader warp: a row is missing, or a block reaches past the first query
 };
-struct Scales {                 // FP8 rows
+struct __align__(16) Scales {   // FP8 rows
   float k[kStepTokens];         // K scale (times softmax scale and log2 e)
   float v[kStepTokens];
 };
@@ -135,6 +135,11 @@ __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x 
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 b = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
@@ -307,24 +312,15 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
-__device__ __forceinline__ uint64_t add2_(uint64_t a, uint64_t b) {
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
-}
-
-// Eight e4m3 codes as bf16, exactly: exponent and mantissa move into place,
-// and a multiplication by 2^120 corrects the bias (subnormal codes included).
-__device__ __forceinline__ uint32_t codes2_bf16(uint32_t w, uint32_t sel) {
-  const uint32_t u = __byte_perm(w, 0, sel);     // two codes, each in the upper byte of a half
-  const uint32_t raw = ((u & 0x7F007F00u) >> 4) | (u & 0x80008000u);
-  uint32_t o;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(raw), "r"(0x7B807B80u));
-  return o;
-}
-__device__ __forceinline__ uint4 codes8_bf16(uint2 w) {
-  return make_uint4(codes2_bf16(w.x, 0x1404), codes2_bf16(w.x, 0x3424), codes2_bf16(w.y, 0x1404),
-                    codes2_bf16(w.y, 0x3424));
 }
 
 // Eight e4m3 codes as f16, exactly.
@@ -353,6 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
   auto o_full = [&](int h, int c) { return bars + 8u * (uint32_t)(4 * kStages + 8 + 2 * h + c); };
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kOffSlot);
   __shared__ float row_factor[kFp8 ? 256 : 1];
+  __shared__ uint32_t v_most;      // FP8: bits of the first step's largest V scale
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   ErrorWord* err = p.c.b.err;
 
@@ -369,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
   if (warp == kRoleMma) {
     tmem_alloc<kTmemCols>(slot);
     if (lane == 0) {
+      v_most = 0;
       for (int i = 0; i < kStages; ++i) {
         mbar_init(k_full(i), 32 * kLoadWarps);
         mbar_init(k_empty(i), (uint32_t)halves);
@@ -532,32 +530,37 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
           kv[i] = s ? *reinterpret_cast<const uint4*>(s + g * kHeadDim + c * 16) : make_uint4(0, 0, 0, 0);
           vv[i] = s ? *reinterpret_cast<const uint4*>(s + (kKvHeads + g) * kHeadDim + c * 16) : make_uint4(0, 0, 0, 0);
         }
-        float ks = 0.f, vs = 0.f;
+        uint16_t kraw = 0, vraw = 0;   // (converted when used: a conversion here would wait for the loads)
         if (src) {
           const uint16_t* sc = reinterpret_cast<const uint16_t*>(src + 2 * kKvHeads * kHeadDim);
-          ks = __half2float(__ushort_as_half(sc[g]));
-          vs = __half2float(__ushort_as_half(sc[kKvHeads + g]));
+          kraw = sc[g];
+          vraw = sc[kKvHeads + g];
         }
         write_meta();
+        const float ks = __half2float(__ushort_as_half(kraw)), vs = __half2float(__ushort_as_half(vraw));
         scales[j % kMetas].k[32 * w + lane] = ks * p.scale_log2;
         scales[j % kMetas].v[32 * w + lane] = vs;
+        if (j == 0) {
+          const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(vs)));
+          if (lane == 0) atomicMax(&v_most, most);
+        }
         // codes 16 c .. +15 are chunks 2 c, 2 c + 1 of the row's 16
-        auto store = [&](uint32_t dst, const uint4 (&x)[8], auto convert) {
+        auto store = [&](uint32_t dst, const uint4 (&x)[8]) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t r = 4 * i + four;
             uint8_t* row = smem + dst + (c >> 2) * kPanel + r * 128;
             const uint32_t c0 = (2 * c) & 7;
-            *reinterpret_cast<uint4*>(row + ((c0 ^ (r & 7)) << 4)) = convert(make_uint2(x[i].x, x[i].y));
-            *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (r & 7)) << 4)) = convert(make_uint2(x[i].z, x[i].w));
+            *reinterpret_cast<uint4*>(row + ((c0 ^ (r & 7)) << 4)) = codes8_f16(make_uint2(x[i].x, x[i].y));
+            *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (r & 7)) << 4)) = codes8_f16(make_uint2(x[i].z, x[i].w));
           }
           fence_async_smem();
         };
-        store(kdst, kv, [](uint2 w) { return codes8_f16(w); });
+        store(kdst, kv);
         mbar_arrive(k_full(st));
         if (j >= kStages) ok = mbar_wait_warp(v_empty(st), turn, err, kKernChunkAttn);
         if (!ok) break;
-        store(vdst, vv, [](uint2 w) { return codes8_bf16(w); });
+        store(vdst, vv);
         mbar_arrive(v_full(st));
       }
       // FP8 rows are loaded into registers, with no copies in flight: the next
@@ -579,7 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
     const int h = warp - kRoleMma;
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     const uint32_t colO = tm + kColO + 128u * (uint32_t)h, colS = tm + kColS + 128u * (uint32_t)h;
-    const uint32_t is = kFp8 ? idesc_f16(kSubTokens) : idesc_bf16(kSubTokens, false), io = idesc_bf16(kHeadDim, true);
+    const uint32_t is = kFp8 ? idesc_f16(kSubTokens, false) : idesc_bf16(kSubTokens, false);
+    const uint32_t io = kFp8 ? idesc_f16(kHeadDim, true) : idesc_bf16(kHeadDim, true);
     const uint64_t qd = desc_sw128(sb + h * 2 * kPanel, 16);
     // S of tokens 64 c .. of the step in K stage st
     auto issue_s = [&](int c, int st) {
@@ -643,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
     // FP8: the K scales hold the softmax scale
     const float f = kFp8 ? row_factor[128 * h + (warp & 3) * 32 + lane] : p.scale_log2;
     const uint64_t f2 = pair(f, f);
-    float m = -INFINITY, l = 0.f;                    // in units of log2
+    float m = -INFINITY, l = 0.f, ve = 0.f;          // in units of log2
 #pragma unroll 1
     for (int jc = 0; jc < 2 * steps; ++jc) {
       const int j = jc >> 1, c = jc & 1;             // tokens 64 c .. of step j
@@ -664,8 +668,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
       // ---- maximum over the tokens
       if (kFp8) {
 #pragma unroll
-        for (int i = 0; i < kSubTokens; ++i)
-          v[i >> 5][i & 31] = __float_as_uint(__uint_as_float(v[i >> 5][i & 31]) * sc.k[kSubTokens * c + i]);
+        for (int i = 0; i < kSubTokens; i += 4) {
+          const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(&sc.k[kSubTokens * c + i]);
+          uint32_t* x = &v[i >> 5][i & 31];
+          const uint64_t a = mul2(pair(x[0], x[1]), k4.x), b = mul2(pair(x[2], x[3]), k4.y);
+          x[0] = (uint32_t)a;
+          x[1] = (uint32_t)(a >> 32);
+          x[2] = (uint32_t)b;
+          x[3] = (uint32_t)(b >> 32);
+        }
       }
       auto at = [&](int i) { return __uint_as_float(v[i >> 5][i & 31]); };
       float mx4[4] = {at(0), at(1), at(2), at(3)};   // four chains of three-way maxima
@@ -700,7 +711,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
           wait_st();
         }
       }
-      const float ref = m == -INFINITY ? 0.f : m;
+      // FP8: probabilities times V scales go in as f16.  The reference holds the
+      // binary exponent of the first step's largest V scale too, so that these
+      // products stay below 2^9 there (they overflow only where a V scale is 64
+      // times that one; the row is then computed again).
+      if (kFp8 && jc == 0) {
+        int e = 0;
+        const float most = __uint_as_float(v_most);
+        if (most > 0.f && most < INFINITY) frexpf(most, &e);
+        ve = (float)e;
+      }
+      const float ref = (m == -INFINITY ? 0.f : m) + ve;
       uint64_t l2 = pair(l, 0.f);
       // ---- probabilities, masked, over S's columns
 #pragma unroll
@@ -721,23 +742,27 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
           // a block that the query does not select: exp2(s f - inf) = 0 (NaN
           // where the logit is not finite: the row is computed again)
           const float add = (mine >> (8 * w + b)) & 1u ? -ref : -INFINITY;
-          const uint64_t add2 = pair(add, add);
-          const uint64_t x01 = fma2(pair(v[w][4 * b], v[w][4 * b + 1]), f2, add2);
-          const uint64_t x23 = fma2(pair(v[w][4 * b + 2], v[w][4 * b + 3]), f2, add2);
+          const uint64_t addend = pair(add, add);
+          const uint64_t x01 = fma2(pair(v[w][4 * b], v[w][4 * b + 1]), f2, addend);
+          const uint64_t x23 = fma2(pair(v[w][4 * b + 2], v[w][4 * b + 3]), f2, addend);
           float e[4] = {exp2_fast(lo_of(x01)), exp2_fast(hi_of(x01)), exp2_fast(lo_of(x23)), exp2_fast(hi_of(x23))};
           if (special) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if (!((tok >> (4 * b + i)) & 1u)) e[i] = 0.f;
           }
-          l2 = add2_(l2, pair(e[0], e[1]));
-          l2 = add2_(l2, pair(e[2], e[3]));
+          l2 = add2(l2, pair(e[0], e[1]));
+          l2 = add2(l2, pair(e[2], e[3]));
           if (kFp8) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] *= sc.v[kSubTokens * c + 32 * w + 4 * b + i];
+            const ulonglong2 v4 = *reinterpret_cast<const ulonglong2*>(&sc.v[kSubTokens * c + 32 * w + 4 * b]);
+            const uint64_t a = mul2(pair(e[0], e[1]), v4.x), d = mul2(pair(e[2], e[3]), v4.y);
+            e[0] = lo_of(a);
+            e[1] = hi_of(a);
+            e[2] = lo_of(d);
+            e[3] = hi_of(d);
           }
-          o[2 * b] = pack_bf16(e[0], e[1]);
-          o[2 * b + 1] = pack_bf16(e[2], e[3]);
+          o[2 * b] = kFp8 ? pack_f16(e[0], e[1]) : pack_bf16(e[0], e[1]);
+          o[2 * b + 1] = kFp8 ? pack_f16(e[2], e[3]) : pack_bf16(e[2], e[3]);
         }
         st16(colS + 16u * w, o);
       }
@@ -746,6 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
       fence_before();
       mbar_arrive(p_full(h, c));
     }
+    m += ve;                                         // l and O are in units of 2^m
     // ---- the row's result
     if (ok && steps > 0) ok = mbar_wait_warp(o_full(h, 1), (uint32_t)(steps - 1) & 1u, err, kKernChunkAttn);
     fence_after();

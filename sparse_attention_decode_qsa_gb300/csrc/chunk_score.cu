@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
         }
       }
     } else if (warp == kRoleMma) {
-      const uint32_t idesc = idesc_f16((uint32_t)(8 * qt));
+      const uint32_t idesc = idesc_f16((uint32_t)(8 * qt), false);
       const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
       int st = phase % kStages;
       uint32_t lap = (uint32_t)(phase / kStages) & 1u;

@@ -88,11 +88,11 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t leading)
 
 // kind::f16 instruction descriptor: D f32, A = B = f16 or bf16, M = 128, N (a
 // multiple of 16), A K-major, B K-major or MN-major.
-__host__ __device__ constexpr uint32_t idesc_f16(uint32_t n) {
-  return (1u << 4) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t n, bool b_mn_major) {
+  return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 __host__ __device__ constexpr uint32_t idesc_bf16(uint32_t n, bool b_mn_major) {
-  return idesc_f16(n) | (1u << 7) | (1u << 10) | (b_mn_major ? 1u << 16 : 0u);
+  return idesc_f16(n, b_mn_major) | (1u << 7) | (1u << 10);
 }
 
 // D (tensor memory) [+]= A (shared) . B (shared)^T
