@@ -438,9 +438,12 @@ qsa_status_t qsa_cache_destroy(qsa_cache* cache) {
   return ok();
 }
 
-qsa_status_t qsa_request_begin(qsa_cache* c, const qsa_request_desc* desc, void* stream,
-                               qsa_handle* out) {
-  if (!c || !desc || !out) return fail(QSA_ERR_INVALID_ARG, "null argument");
+namespace {
+
+// Lease a request (qsa_request_begin); fill_slots: enqueue the fill of its
+// slot-table rows (qsa_request_fork writes them itself).
+qsa_status_t begin_lease(qsa_cache* c, const qsa_request_desc* desc, void* stream, bool fill_slots,
+                         qsa_handle* out) {
   if (desc->ctx_len < 1) return fail(QSA_ERR_INVALID_ARG, "ctx_len must be >= 1");
   if (desc->ctx_len > c->cfg.ctx_capacity)
     return fail(QSA_ERR_CAPACITY, "ctx_len %lld exceeds capacity %lld", (long long)desc->ctx_len,
@@ -504,9 +507,10 @@ qsa_status_t qsa_request_begin(qsa_cache* c, const qsa_request_desc* desc, void*
 
   if (c->has_device) {
     int32_t* st = c->cfg.slot_table + (int64_t)slot * c->cfg.n_layers * c->cfg.ctx_capacity;
-    cudaError_t e = launch_slot_fill(st, c->cfg.n_layers, c->cfg.ctx_capacity, desc->ctx_len,
-                                     desc->placement, base, layer_rows,
-                                     static_cast<cudaStream_t>(stream));
+    cudaError_t e = cudaSuccess;
+    if (fill_slots)
+      e = launch_slot_fill(st, c->cfg.n_layers, c->cfg.ctx_capacity, desc->ctx_len, desc->placement, base,
+                           layer_rows, static_cast<cudaStream_t>(stream));
     if (e == cudaSuccess && hot) {
       // every hot row of the request free, cursors at row 0
       const WorkspaceLayout w = workspace_layout(c->cfg);
@@ -541,6 +545,14 @@ qsa_status_t qsa_request_begin(qsa_cache* c, const qsa_request_desc* desc, void*
   out->index = (uint32_t)slot;
   out->generation = l.generation;
   return ok();
+}
+
+}  // namespace
+
+qsa_status_t qsa_request_begin(qsa_cache* c, const qsa_request_desc* desc, void* stream,
+                               qsa_handle* out) {
+  if (!c || !desc || !out) return fail(QSA_ERR_INVALID_ARG, "null argument");
+  return begin_lease(c, desc, stream, true, out);
 }
 
 qsa_status_t qsa_request_end(qsa_cache* c, qsa_handle h) {
@@ -923,7 +935,7 @@ qsa_status_t qsa_request_fork(qsa_cache* c, qsa_handle parent, const qsa_request
     return fail(QSA_ERR_INVALID_ARG, "ctx_len %lld outside [1, %lld], the parent's tokens",
                 (long long)desc->ctx_len, (long long)pl->ctx_len);
   qsa_handle child;
-  if (qsa_status_t st = qsa_request_begin(c, desc, stream, &child)) return st;
+  if (qsa_status_t st = begin_lease(c, desc, stream, false, &child)) return st;
   const Lease& l = c->leases[child.index];
   const int64_t R = c->row_bytes();
   if (pl->host_rows && l.host_rows) {

@@ -366,7 +366,8 @@ cudaError_t launch_chunk_attn(const ChunkDesc& c, const uint16_t* q, const int32
                               const int32_t* n_sel, int32_t budget_tokens, float softmax_scale,
                               uint16_t* out, float* lse, void* workspace, cudaStream_t s);
 
-// Pages: copy the first n_tokens tokens of a request (all layers) to another.
+// Pages: copy the first n_tokens tokens of a request (all layers) to another,
+// and write the latter's slot-table rows.
 struct ForkParams {
   int32_t src_req, dst_req;      // request slots
   int32_t n_layers;
@@ -374,7 +375,7 @@ struct ForkParams {
   int64_t ctx_cap, pool_rows;
   uint8_t* index_keys;
   uint16_t* index_scales;
-  const int32_t* slot_table;
+  int32_t* slot_table;
   uint8_t* pool;
   int32_t row_bytes;
   const uint8_t* src_host;       // parent's host history or nullptr

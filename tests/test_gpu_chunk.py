@@ -490,6 +490,47 @@ def test_large_logits_and_far_apart_rows():
         f.close()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_far_below_other_queries_tokens_keep_their_own(fp8):
+    """Keys of half the blocks point along one direction with logits in the
+    hundreds for every query; queries of odd rows select only the others."""
+    f = Filled([1024], seed=9, budget=512, fp8=fp8)
+    try:
+        c = f.c
+        rows = c.slot_table[f.hs[0].index, 0, :1024].long()
+        kv = f.kv[0][0].numpy()
+        K, V = f.values(0, 0, list(range(1024)))
+        hot = [t for t in range(1024) if (t // 4) % 2 == 0]
+        d = torch.randn(128, generator=torch.Generator().manual_seed(4)).bfloat16()
+        raw = torch.from_numpy(kv).clone()
+        if fp8:
+            k = d.float().repeat(4, 1)
+            v = torch.zeros(1, 8, 128)
+            v[0, :4] = k
+            new = synth.fp8_kv_rows(v.bfloat16().view(1, 1024).view(torch.uint8).view(1, 2048))[0]
+            raw[hot, :512] = new[:512]
+            raw[hot, 1024:1032] = new[1024:1032]
+        else:
+            raw[hot, :1024] = d.repeat(4).view(torch.uint8)
+        f.kv[0] = raw[None]
+        c.pool[rows] = raw.to(f.dev)
+        q = (25.0 * d.float() + torch.randn(70, 16, 128, generator=torch.Generator().manual_seed(5))).bfloat16().to(f.dev)
+        pos = [p for _, p in f.positions([70])]
+        rng = np.random.RandomState(2)
+        sel, t = [], torch.full((70, 128), -1, dtype=torch.int32)
+        for x in range(70):
+            ids = np.arange(pos[x] // 4 + 1)
+            ids = ids[ids % 2 == 1] if x % 2 else ids
+            sel.append(np.sort(rng.choice(ids, 100, replace=False)))
+            t[x, :100] = torch.as_tensor(sel[x], dtype=torch.int32)
+        n = torch.full((70,), 100, dtype=torch.int32)
+        out, lse = _run_attention(f, [70], q, t, n, 512)
+        _clean(c)
+        _check_attention(f, [70], q, sel, [100] * 70, out, lse)
+    finally:
+        f.close()
+
+
 def test_bad_blocks_counts_and_slots_are_reported_and_skipped():
     f = Filled([300], seed=10, budget=64)
     try:

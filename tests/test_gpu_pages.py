@@ -147,6 +147,30 @@ def test_compaction_keeps_every_row(fp8, holes):
         f.close()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("gap,rows", [(45000, 70001), (45000, 30000)])
+def test_compaction_of_long_regions(fp8, gap, rows):
+    """Gaps wide enough for the form that moves chains side by side, with a
+    region longer than the gap (overlapping move) and one shorter.  Every row
+    carries its number."""
+    c = Q.Cache(n_layers=1, max_requests=2, ctx_capacity=max(gap, rows), hbm_pool_rows=gap + rows, budget_tokens=64,
+                staging_rows=0, kv_format=Q.KV_FP8 if fp8 else Q.KV_BF16)
+    a, b = c.request_begin(gap), c.request_begin(rows)
+    base = c.request_info(b).hbm_row_base
+    words = c.pool.view(torch.int32)
+    want = (torch.arange(rows, device=c.pool.device, dtype=torch.int32)[:, None] * 1024 +
+            torch.arange(words.shape[1], device=c.pool.device, dtype=torch.int32))
+    words[base:base + rows] = want
+    c.request_end(a)
+    assert c.compact() == rows
+    torch.cuda.synchronize()
+    _clean(c)
+    assert c.request_info(b).hbm_row_base == base - gap
+    assert torch.equal(words[base - gap:base - gap + rows], want)
+    assert torch.equal(c.slot_table[b.index, 0, :rows].long(), base - gap + torch.arange(rows, device=c.pool.device))
+    c.close()
+
+
 def test_compaction_follows_slots_that_name_other_requests_rows():
     f = Filled([30, 40, 50], seed=7, budget=64)
     try:
