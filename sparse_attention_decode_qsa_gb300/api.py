@@ -368,9 +368,12 @@ class Cache:
         rows = n_layers * sum(n_tokens)
         if workspace is None:
             need = self.chunk_attn_workspace_bytes(handles, n_tokens, layer0, n_layers, budget_tokens)
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            if isinstance(stream, torch.cuda.Stream):
-                workspace.record_stream(stream)
+            # allocated in the order of the stream that uses it: memory of the
+            # current stream may still be at work there
+            if stream is not None and not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=self.pool.device)
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=self.pool.device)
         heads = (rows, N.Q_HEADS, N.HEAD_DIM)
         check(self.L.qsa_chunk_sparse_attn(
             self.h, C.byref(ch), self._rows(q, "q", (torch.bfloat16,), heads),

@@ -883,6 +883,7 @@ int64_t qsa_chunk_attn_workspace_bytes(qsa_cache* c, const qsa_chunk* chunk, int
   ChunkDesc d;
   if (c->build_chunk(chunk, &d) != QSA_OK || check_budget(c, budget_tokens) != QSA_OK) return -1;
   const int64_t bytes = chunk_attn_workspace(d, budget_tokens);
+  if (bytes < 0) { fail(QSA_ERR_CUDA, "the device's SM count is unknown"); return -1; }
   ok();
   return bytes;
 }
@@ -906,6 +907,7 @@ qsa_status_t qsa_chunk_sparse_attn(qsa_cache* c, const qsa_chunk* chunk, const u
       reinterpret_cast<uintptr_t>(sel_blocks) % 16 || reinterpret_cast<uintptr_t>(n_sel) % 16)
     return fail(QSA_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
   const int64_t need = chunk_attn_workspace(d, budget_tokens);
+  if (need < 0) return fail(QSA_ERR_CUDA, "the device's SM count is unknown");
   if (workspace_bytes < need)
     return fail(QSA_ERR_INVALID_ARG, "workspace has %lld bytes, needs %lld", (long long)workspace_bytes,
                 (long long)need);

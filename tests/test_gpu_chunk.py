@@ -805,3 +805,32 @@ def test_captured_steps_replay_and_streams_keep_apart():
         _clean(c)
     finally:
         f.close()
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_workspace_allocated_for_another_stream_is_that_streams_own(raw):
+    """Memory freed on the current stream, which still writes to it, is not
+    taken as the workspace of a call on another stream."""
+    f = Filled([2500], seed=12, budget=512)
+    try:
+        nt = [40]
+        q = _queries(40, 9, f.dev)
+        _, _, t, n = _random_selection(f, nt, 512, seed=4)
+        t, n = t.to(f.dev), n.to(f.dev)
+        want, ls = _run_attention(f, nt, q, t, n, 512)
+        out, lse = torch.zeros_like(want), torch.zeros_like(ls)
+        need = f.c.chunk_attn_workspace_bytes(f.hs, nt, 0, 1, 512)
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            busy = torch.empty(need, dtype=torch.uint8, device=f.dev)
+            for _ in range(400):
+                busy.zero_()
+            del busy
+            f.c.chunk_sparse_attn(f.hs, nt, 0, 1, q, t, n, 512, SCALE, out, lse,
+                                  stream=side.cuda_stream if raw else side)
+            torch.cuda.synchronize()
+            assert torch.equal(out, want) and torch.equal(lse, ls)
+        _clean(f.c)
+    finally:
+        f.close()
