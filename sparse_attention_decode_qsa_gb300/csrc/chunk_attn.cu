@@ -431,8 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
     const uint32_t* mask = p.mask + (int64_t)tile * 2 * p.cap;
     const int32_t* slots = p.c.b.slot_table + p.c.b.unit_row(u);
     const int64_t n = p.c.b.u[u].n;
-    // Block id (step j + 1), slot and mask word (step j) are fetched a step
-    // ahead of their use.  Lane = token: block lane / 4 of the warp's eight.
+    // At step j the block id of step j + 3, the slot of step j + 2 and the mask
+    // word of step j + 1 are fetched.  Lane = token: block lane / 4 of the
+    // warp's eight.
     const int first = j0 * kStepBlocks + 8 * w + (lane >> 2), stop = (j0 + steps) * kStepBlocks;
     auto block_id = [&](int j) {
       const int e = first + j * kStepBlocks;
@@ -449,8 +450,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
       const int e = (j0 + j) * kStepBlocks + lane;
       return mh >= 0 && mh < halves && j < steps && e < count ? mask[(int64_t)mh * p.cap + e] : 0u;
     };
-    int32_t id = block_id(0), id_next = block_id(1);
-    int32_t slot_now = slot_of(id);
+    // FP8 rows are loaded into registers, with no copies in flight: rows two
+    // steps ahead are on their way from HBM meanwhile (290 -> 282 us at 2048
+    // queries; cp.async rows gain nothing from it, 179 -> 186 us)
+    auto prefetch = [&](int32_t slot) {
+      if (!kFp8 || slot < 0 || (int64_t)slot >= p.c.b.pool_rows) return;
+      const uint8_t* r = p.c.b.pool + (int64_t)slot * p.c.b.row_bytes + g * kHeadDim;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(r));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(r + kKvHeads * kHeadDim));
+    };
+    int32_t id = block_id(0), id_next = block_id(1), id_two = block_id(2);
+    int32_t slot_now = slot_of(id), slot_next = slot_of(id_next);
+    prefetch(slot_next);
     uint32_t word = mask_word(0);
     for (int j = 0; j < steps && ok; ++j) {
       const int st = j % kStages;
@@ -464,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
       } else if (id >= 0 && t < n) {
         report_error(err, QSA_ERR_BAD_SLOT, kKernChunkAttn, ((int64_t)u << 40) | (t & 0xFFFFFFFFFFll));
       }
-      const int32_t slot_next = slot_of(id_next), id_after = block_id(j + 2);
+      const int32_t slot_two = slot_of(id_two), id_three = block_id(j + 3);
       const uint32_t word_next = mask_word(j + 1);
       if (j >= kStages) ok = mbar_wait_warp(k_empty(st), turn, err, kKernChunkAttn);
       if (!ok) break;
@@ -564,17 +575,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
         store(vdst, vv);
         mbar_arrive(v_full(st));
       }
-      // FP8 rows are loaded into registers, with no copies in flight: the next
-      // step's are on their way from HBM meanwhile (45.9 -> 43.9 us for 32 draft
-      // queries; cp.async rows gain nothing from it, 179 -> 186 us at 2048)
-      if (kFp8 && slot_next >= 0 && (int64_t)slot_next < p.c.b.pool_rows) {
-        const uint8_t* r = p.c.b.pool + (int64_t)slot_next * p.c.b.row_bytes + g * kHeadDim;
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(r));
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(r + kKvHeads * kHeadDim));
-      }
+      prefetch(slot_two);
       id = id_next;
-      id_next = id_after;
+      id_next = id_two;
+      id_two = id_three;
       slot_now = slot_next;
+      slot_next = slot_two;
       word = word_next;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -853,19 +859,33 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
   const int q = i % kTileQueries, row = (q >> 5) * 128 + (head % kGroup) * 32 + (q & 31);
   const float* part = p.part + (((int64_t)tile * kKvHeads + head / kGroup) * p.splits * 256 + row) * kRowFloats;
   const int64_t stride = 256 * kRowFloats;
+  // a lane takes one split's maximum and sum; the splits' O follow, their loads
+  // in flight together
   float m = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, part[s * stride + kHeadDim]);
+  for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, part[s * stride + kHeadDim]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   float l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < p.splits; ++s) {
-    const float ms = part[s * stride + kHeadDim], ls = part[s * stride + kHeadDim + 1];
-    if (ls == 0.f) continue;                         // nothing selected there
-    const float a = exp2f(ms - m);
-    const float2 o0 = *reinterpret_cast<const float2*>(part + s * stride + 4 * lane);
-    const float2 o1 = *reinterpret_cast<const float2*>(part + s * stride + 4 * lane + 2);
-    l = fmaf(ls, a, l);
-    acc = make_float4(fmaf(o0.x, a, acc.x), fmaf(o0.y, a, acc.y), fmaf(o1.x, a, acc.z), fmaf(o1.y, a, acc.w));
+  for (int s0 = 0; s0 < p.splits; s0 += 32) {
+    float a = 0.f;                                   // 0: nothing selected there
+    if (s0 + lane < p.splits) {
+      const float2 ml = *reinterpret_cast<const float2*>(part + (s0 + lane) * stride + kHeadDim);
+      if (ml.y != 0.f) a = exp2f(ml.x - m);
+      l = fmaf(ml.y, a, l);
+    }
+    const int n = p.splits - s0 < 32 ? p.splits - s0 : 32;
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float w = __shfl_sync(0xFFFFFFFFu, a, s);
+      const float* o = part + (s0 + s) * stride + 4 * lane;
+      const float2 o0 = *reinterpret_cast<const float2*>(o), o1 = *reinterpret_cast<const float2*>(o + 2);
+      if (w != 0.f)
+        acc = make_float4(fmaf(o0.x, w, acc.x), fmaf(o0.y, w, acc.y), fmaf(o1.x, w, acc.z), fmaf(o1.y, w, acc.w));
+    }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
   const bool fine = l > 0x1p-100f && isfinite(acc.x) && isfinite(acc.y) && isfinite(acc.z) && isfinite(acc.w);
   if (!__all_sync(0xFFFFFFFFu, fine)) {
     attend_row(p, u, x, head);
