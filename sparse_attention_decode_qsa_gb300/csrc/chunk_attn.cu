@@ -92,9 +92,9 @@ constexpr int kMetas = 4;
 constexpr int kOffScales = kOffMeta + kMetas * (int)sizeof(StepMeta);
 constexpr int kOffBar = kOffScales + kMetas * (int)sizeof(Scales);
 // k_full[2], k_empty[2], v_full[2], v_empty[2], then per (half, 64 tokens)
-// s_full[4], p_full[4], o_full[4]
-constexpr int kNumBars = 4 * kStages + 12;
-constexpr int kOffSlot = kOffBar + 8 * kNumBars;
+// s_full[4], p_full[4], o_full[4], q_full
+constexpr int kNumBars = 4 * kStages + 13;
+constexpr int kOffSlot = (kOffBar + 8 * kNumBars + 15) / 16 * 16;
 constexpr int kSmemBytes = kOffSlot + 16 + 1024;
 static_assert(kSmemBytes <= 227 * 1024 && sizeof(StepMeta) % 16 == 0, "one CTA's shared memory");
 constexpr uint32_t kTmemCols = 512;
@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
   auto s_full = [&](int h, int c) { return bars + 8u * (uint32_t)(4 * kStages + 2 * h + c); };
   auto p_full = [&](int h, int c) { return bars + 8u * (uint32_t)(4 * kStages + 4 + 2 * h + c); };
   auto o_full = [&](int h, int c) { return bars + 8u * (uint32_t)(4 * kStages + 8 + 2 * h + c); };
+  const uint32_t q_full = bars + 8u * (uint32_t)(4 * kStages + 12);
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kOffSlot);
   __shared__ float row_factor[kFp8 ? 256 : 1];
   __shared__ uint32_t v_most;      // FP8: bits of the first step's largest V scale
@@ -379,45 +380,62 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
         mbar_init(p_full(i >> 1, i & 1), 128);
         mbar_init(o_full(i >> 1, i & 1), 1);
       }
+      mbar_init(q_full, 32 * kSoftWarps);
       mbar_fence_init();
     }
   }
-  grid_dependency_wait();
-  // ---- Q: row head * 32 + query of each half, two panels of 64 dims.  Against
-  // FP8 rows it goes in as f16, beside the K codes, which f16 holds exactly: a
-  // row scaled by the power of two that puts its largest element into [1/2, 1),
-  // where f16 holds a bf16 element exactly down to 2^-17 of the largest and to
-  // 2^-25 of it below; the inverse goes to the logits (row_factor).
-  for (int i = tid; i < halves * 128 * 16; i += kThreads) {      // (whole warps)
-    const int c = i & 15, r = (i >> 4) & 127, h = i >> 11;
-    const int q = h * 32 + (r & 31), head = g * kGroup + (r >> 5);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (q < nq) v = reinterpret_cast<const uint4*>(p.q + ((int64_t)(x0 + q) * kQHeads + head) * kHeadDim)[c];
-    const uint32_t flip = p.sign < 0.f ? 0x80008000u : 0u;
-    v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
-    if (kFp8) {
-      uint32_t* w[4] = {&v.x, &v.y, &v.z, &v.w};
-      float top = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(bf16_lo(*w[k])), fabsf(bf16_hi(*w[k]))));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));   // the row's 16 lanes
-      int e = 0;
-      if (top > 0.f && top < INFINITY) frexpf(top, &e);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const __half2 o = __floats2half2_rn(ldexpf(bf16_lo(*w[k]), -e), ldexpf(bf16_hi(*w[k]), -e));
-        *w[k] = *reinterpret_cast<const uint32_t*>(&o);
-      }
-      if (c == 0) row_factor[h * 128 + r] = ldexpf(1.f, e);
-    }
-    *reinterpret_cast<uint4*>(smem + (h * 2 + (c >> 3)) * kPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
-  }
-  fence_async_smem();
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = *slot;
+  grid_dependency_wait();
+
+  // The softmax warps bring Q in, while the loaders begin on K.
+  if (warp < kSoftWarps) {
+    // ---- Q: row head * 32 + query of each half, two panels of 64 dims.  Against
+    // FP8 rows it goes in as f16, beside the K codes, which f16 holds exactly: a
+    // row scaled by the power of two that puts its largest element into [1/2, 1),
+    // where f16 holds a bf16 element exactly down to 2^-17 of the largest and to
+    // 2^-25 of it below; the inverse goes to the logits (row_factor).
+    constexpr int kBatch = 4;                        // loads in flight
+    for (int i0 = tid; i0 < halves * 128 * 16; i0 += kBatch * 32 * kSoftWarps) {      // (whole warps)
+      uint4 in[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int i = i0 + b * 32 * kSoftWarps, c = i & 15, r = (i >> 4) & 127, q = (i >> 11) * 32 + (r & 31);
+        in[b] = make_uint4(0, 0, 0, 0);
+        if (q < nq)
+          in[b] = reinterpret_cast<const uint4*>(p.q + ((int64_t)(x0 + q) * kQHeads + g * kGroup + (r >> 5)) * kHeadDim)[c];
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int i = i0 + b * 32 * kSoftWarps, c = i & 15, r = (i >> 4) & 127, h = i >> 11;
+        uint4 v = in[b];
+        const uint32_t flip = p.sign < 0.f ? 0x80008000u : 0u;
+        v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
+        if (kFp8) {
+          uint32_t* w[4] = {&v.x, &v.y, &v.z, &v.w};
+          float top = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(bf16_lo(*w[k])), fabsf(bf16_hi(*w[k]))));
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));   // the row's 16 lanes
+          int e = 0;
+          if (top > 0.f && top < INFINITY) frexpf(top, &e);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const __half2 o = __floats2half2_rn(ldexpf(bf16_lo(*w[k]), -e), ldexpf(bf16_hi(*w[k]), -e));
+            *w[k] = *reinterpret_cast<const uint32_t*>(&o);
+          }
+          if (c == 0) row_factor[h * 128 + r] = ldexpf(1.f, e);
+        }
+        *reinterpret_cast<uint4*>(smem + (h * 2 + (c >> 3)) * kPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+      }
+    }
+    fence_async_smem();
+    mbar_arrive(q_full);
+    if (kFp8) asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory");      // row_factor
+  }
 
   const int count = p.count[tile];
   const int all = (count + kStepBlocks - 1) / kStepBlocks;
@@ -608,7 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
       __syncwarp();
     };
     if (steps > 0) {
-      ok = mbar_wait_warp(k_full(0), 0, err, kKernChunkAttn);
+      ok = mbar_wait_warp(q_full, 0, err, kKernChunkAttn);
+      if (ok) ok = mbar_wait_warp(k_full(0), 0, err, kKernChunkAttn);
       if (ok) {
         fence_after();
         issue_s(0, 0);
