@@ -38,6 +38,28 @@ __device__ __forceinline__ uint32_t code_of(float x, float f) {
   return (uint32_t)(uint8_t)__nv_cvt_float_to_fp8(fminf(fmaxf(x / f, -448.0f), 448.0f), __NV_SATFINITE, __NV_E4M3);
 }
 
+// The codes of eight elements under scale f > 0, whose quotients x / f are the
+// correctly rounded ones: q = x r with r = 1 / f correctly rounded, then one
+// step q - r (q f - x) with an exact remainder (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990).  Where the
+// remainder is inexact the quotient is far below the smallest code.  x may be
+// NaN (code of -448, as clamping gives), not infinite.
+__device__ __forceinline__ uint2 codes_of(const float (&x)[8], float f, float r) {
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 q;
+    q.x = x[2 * i] * r;
+    q.y = x[2 * i + 1] * r;
+    q.x = fmaf(-fmaf(q.x, f, -x[2 * i]), r, q.x);    // (these signs keep a zero's own)
+    q.y = fmaf(-fmaf(q.y, f, -x[2 * i + 1]), r, q.y);
+    q.x = fmaxf(q.x, -448.0f);                       // the conversion takes the upper end
+    q.y = fmaxf(q.y, -448.0f);
+    c[i] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
 __global__ void __launch_bounds__(kThreads) append_chunk_kernel(const __grid_constant__ ChunkAppendParams p) {
   const int lane = threadIdx.x & 31;
   const int x = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -115,11 +137,18 @@ __global__ void __launch_bounds__(kThreads) append_chunk_kernel(const __grid_con
     const __half vs = scale_of(va);
     const float vf = __half2float(vs);
     uint2 c8 = make_uint2(0u, 0u);
-    if (vf > 0.f) {
+    if (vf > 0.f && va < INFINITY) {
+      c8 = codes_of(e, vf, 1.0f / vf);
+    } else if (vf > 0.f) {
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        float x = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c8.x |= code_of(e[i], vf) << (8 * i);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c8.y |= code_of(e[4 + i], vf) << (8 * i);
+        for (int k = 0; k < 8; ++k) x = i == k ? e[k] : x;
+        const uint32_t c = code_of(x, vf) << (8 * (i & 3));
+        if (i < 4) c8.x |= c;
+        else c8.y |= c;
+      }
     }
     const int hv = 2 * j + (lane >> 4);
 #pragma unroll

@@ -834,3 +834,35 @@ def test_a_workspace_allocated_for_another_stream_is_that_streams_own(raw):
         _clean(f.c)
     finally:
         f.close()
+
+
+def test_fp8_codes_of_a_chunk_are_the_quotients_of_single_appends():
+    """Every bf16 value, infinities and NaN among them, in head vectors of
+    neighbouring values, of values far apart, and beside a largest element."""
+    g = torch.Generator().manual_seed(3)
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    near, far = x, x[torch.randperm(65536, generator=g)]
+    top = x.view(-1, 128).clone()
+    top[:, 0] = (0x4000 + torch.arange(512) % 128).to(torch.int16)        # 2 .. 3.98
+    small = torch.where(x.view(torch.bfloat16).float().view(-1, 128).abs() < 4, top, torch.zeros_like(top))
+    kv = torch.cat([near, far, small.flatten()]).view(-1, 1024).contiguous().view(torch.uint8)
+    n = kv.shape[0]
+    Q.lib()
+    c = Q.Cache(n_layers=1, max_requests=2, ctx_capacity=n + 1, hbm_pool_rows=2 * n + 2, budget_tokens=64,
+                ring_tokens=64, staging_rows=0, kv_format=Q.KV_FP8)
+    try:
+        dev = c.pool.device
+        kv, k = kv.to(dev), torch.randn(n, 64, generator=g).to(dev)
+        a = c.request_begin(1, max_ctx=n + 1)
+        c.advance(a, n)
+        c.append_chunk([a], [n], 0, 1, k, kv)
+        b = c.request_begin(1, max_ctx=n + 1)
+        for i in range(n):
+            c.advance(b)
+            c.append_token([b], 0, 1, k[i:i + 1], kv[i:i + 1])
+        torch.cuda.synchronize()
+        rows = [c.pool[c.slot_table[h.index, 0, 1:n + 1].long()] for h in (a, b)]
+        assert torch.equal(rows[0], rows[1])
+        _clean(c)
+    finally:
+        c.close()
