@@ -33,17 +33,25 @@ struct ChunkAppendParams {
 // fp16 scale of absmax a (round to nearest even of a / 448, saturating).
 __device__ __forceinline__ __half scale_of(float a) { return __float2half_rn(fminf(a / 448.0f, 65504.0f)); }
 
+__device__ __forceinline__ float reciprocal(float f) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(f));
+  return r;
+}
+
 // e4m3 code of x under scale f > 0.
 __device__ __forceinline__ uint32_t code_of(float x, float f) {
   return (uint32_t)(uint8_t)__nv_cvt_float_to_fp8(fminf(fmaxf(x / f, -448.0f), 448.0f), __NV_SATFINITE, __NV_E4M3);
 }
 
-// The codes of eight elements under scale f > 0, whose quotients x / f are the
-// correctly rounded ones: q = x r with r = 1 / f correctly rounded, then one
-// step q - r (q f - x) with an exact remainder (Markstein, "Computation of
-// elementary functions on the IBM RISC System/6000 processor", 1990).  Where the
-// remainder is inexact the quotient is far below the smallest code.  x may be
-// NaN (code of -448, as clamping gives), not infinite.
+// The codes of eight bf16 elements under an fp16 scale f > 0, as their correctly
+// rounded quotients x / f would give them.  With r = 1 / f to an ulp or two, q =
+// x r and one correction q - r (q f - x), whose remainder is exact, the quotient
+// is off by 2^-22 at most, and by nothing where it is a midpoint m of two codes:
+// then q f - x = m f d for a d of at most 2^-21, and the correction leaves m (1 -
+// d 2^-22), which rounds to m.  Every other quotient is far enough from the
+// midpoints: x has 8 bits and m f 16, so x / f differs from m by 2^-16 of it at
+// least.  x may be NaN (code of -448, as clamping gives), not infinite.
 __device__ __forceinline__ uint2 codes_of(const float (&x)[8], float f, float r) {
   uint32_t c[4];
 #pragma unroll
@@ -138,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) append_chunk_kernel(const __grid_con
     const float vf = __half2float(vs);
     uint2 c8 = make_uint2(0u, 0u);
     if (vf > 0.f && va < INFINITY) {
-      c8 = codes_of(e, vf, 1.0f / vf);
+      c8 = codes_of(e, vf, reciprocal(vf));
     } else if (vf > 0.f) {
 #pragma unroll 1
       for (int i = 0; i < 8; ++i) {
