@@ -499,8 +499,10 @@ qsa_status_t qsa_append_chunk(qsa_cache* cache, const qsa_chunk* chunk, const fl
  * of the chunk) gets blk_scores[x * blk_stride + b] = max of S_t over the
  * tokens t = 4b .. 4b+3 with t <= p, for b < ceil((p+1)/4); the other entries
  * of the row are left as they were.
- * q_idx: device [rows][8][64] of query_type (QSA_QUERY_F32 or QSA_QUERY_BF16;
- * fp32 queries are carried to fp32's own precision); w: device fp32 [rows][8];
+ * q_idx: device [rows][8][64] of query_type.  Products with the keys' codes are
+ * exact and sums fp32; a head's 64 elements go in with an error of at most
+ * 2^-25 of the largest of them (QSA_QUERY_BF16: none down to 2^-17 of it).
+ * w: device fp32 [rows][8];
  * blk_scores: device fp32 [rows][blk_stride], blk_stride >= ceil(ctx/4) of
  * every request.  Scores must be finite.
  * Errors: INVALID_ARG, STALE_HANDLE, NO_DEVICE, CUDA. */

@@ -17,7 +17,8 @@ constexpr int kWarps = kThreads / 32;
 // One warp per (layer, token): the source row is found through the parent's
 // slot table (pool row, or the host history for a cold token) and stored in
 // the child's region and / or host history; the token's key, scale and slot go
-// with it.  32001 x 12 BF16 rows take 227 us, the rate of a plain copy.
+// with it.  32001 x 12 BF16 rows (1.62 GB in and out) take 227 us, a little above the
+// measured copy rate; 1021 x 12 FP8 rows 8 us.
 __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkParams p) {
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -145,7 +146,7 @@ cudaError_t launch_move_rows(uint8_t* pool, int64_t row_bytes, int64_t from, int
   const int64_t per = row_bytes / 16;
   const int64_t chains = (from - to < rows ? from - to : rows) * per;
   // chains side by side once they fill the device eight deep (eight CTAs on
-  // each of 152 SMs): 3 x 196608 BF16 rows, each down by as many, 581 -> 403 us
+  // each of 152 SMs): 3 x 196608 BF16 rows, each down by as many, 581 -> 379 us
   const bool wide = chains >= (int64_t)152 * 8 * kThreads * kDepth;
   const int64_t block = wide ? (int64_t)kThreads * kDepth : kThreads;
   int64_t blocks = (chains + block - 1) / block;

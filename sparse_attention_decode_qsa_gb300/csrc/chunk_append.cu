@@ -9,7 +9,9 @@
 // elements 2l, 2l+1 and the row's 16-byte pieces l, l+32, l+64, l+96; an FP8
 // row's head vector is 16 pieces, so its absmax is a reduction over half a
 // warp.  The kernel moves 2304 bytes in and 2118 (BF16) or 1110 (FP8) bytes
-// out per token and is bound by that traffic.
+// out per token: 4 x 8191 tokens as FP8 rows (112 MB) take 25 us, 0.67 of the
+// measured copy rate (33 with a division per element; the grid's shape and the
+// occupancy change nothing); 14 BF16 tokens 3.9 us, a launch's latency.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 

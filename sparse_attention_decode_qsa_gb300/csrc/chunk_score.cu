@@ -30,6 +30,17 @@
 // MMAs run while the others' are read.
 // All waits are bounded.  The steps of all groups form one list, cut into
 // equal runs, one per CTA; a run that crosses into another group rebuilds B.
+//
+// Measured: 2048 bf16 queries at the end of 131072 tokens (277 GFLOP) 345 us,
+// 0.80 PFLOP/s, 0.41 of the measured bf16 rate; 10 fp32 draft queries of 4 requests of
+// 65536 tokens 17 us.  What bounds it is the epilogue's instructions: 8
+// saturating products and 4 paired multiply-adds per query and lane against 128
+// tensor-core cycles per tile; the schedulers issue in 0.66 of the cycles, and
+// the loop without its arithmetic takes 207 us.  Not faster: 128 queries to a
+// group (413, registers spill), two sets of 8 warps with two accumulators each
+// (357), products per element in place of pairs or maxima in place of saturation
+// (359 to 392), an arrival per warp in place of per thread, an earlier release of
+// the accumulator, a loop of its own for tokens that every query sees (345 to 376).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
