@@ -116,6 +116,8 @@ constexpr uint32_t kColO = 0, kColS = 256;        // + 128 per half
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWindow = 24576;                // blocks of one bitmap window (192 KiB)
 constexpr int kRowFloats = kHeadDim + 2;          // partial of a row: O, m, l
+constexpr int kMaxShares = 64;                    // where tiles are split: two tiles per lane
+constexpr int kLeastSteps = 2;                     // a share's steps at least, where its tile has them
 
 struct ChunkAttnParams {
   ChunkDesc c;
@@ -124,7 +126,7 @@ struct ChunkAttnParams {
   const int32_t* sel;            // [rows][k_max]
   const int32_t* n_sel;          // [rows]
   int32_t k_max;
-  int32_t splits;
+  int32_t shares;                // CTAs per KV head: the tiles, or more, dealt out by share_of
   float scale_log2;              // |softmax_scale| * log2(e)
   float sign;                    // the scale's sign (goes into Q)
   uint16_t* out;                 // [rows][16][128] bf16 bits
@@ -133,7 +135,8 @@ struct ChunkAttnParams {
   int32_t* count;                // [tiles]
   int32_t* block;                // [tiles][cap]
   uint32_t* mask;                // [tiles][2][cap]
-  float* part;                   // [tiles][4][splits][256][kRowFloats]
+  int2* dealt;                   // [tiles]: a tile's first share, and how many it has
+  float* part;                   // [shares][4][256][kRowFloats]
 
   __device__ int unit_of_tile(int t) const {
     int lo = 0, hi = c.b.n_units - 1;
@@ -325,6 +328,60 @@ static_assert(kPlanWarps == 32, "one lane per warp in the scan");
 
 // ------------------------------------------------------------------ split
 
+// Which part of which tile share c is: where there are more shares than tiles,
+// every tile gets ceil(steps / q) of them (one at least), q the smallest number
+// of steps that the shares suffice for, so that the longest share is as short as
+// it can be, whatever the lists' lengths.  Whole warps; false: nothing is left
+// for share c.
+__device__ __forceinline__ bool share_of(const ChunkAttnParams& p, int c, int* tile, int* split, int* n) {
+  const int tiles = p.tile0[p.c.b.n_units], lane = threadIdx.x & 31;
+  *tile = c;
+  *split = 0;
+  *n = 1;
+  if (p.shares == tiles) return true;
+  int steps[2], total = 0, longest = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    steps[i] = lane + 32 * i < tiles ? (p.count[lane + 32 * i] + kStepBlocks - 1) / kStepBlocks : 0;
+    total += steps[i];
+    longest = steps[i] > longest ? steps[i] : longest;
+  }
+  total = __reduce_add_sync(0xFFFFFFFFu, total);
+  longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+  auto shares = [&](int i, int q) {                  // of tile lane + 32 i
+    return lane + 32 * i >= tiles ? 0 : (steps[i] > q ? (steps[i] + q - 1) / q : 1);
+  };
+  int q = (total + p.shares - 1) / p.shares;
+  q = q < kLeastSteps ? kLeastSteps : q;
+  for (int enough = longest > q ? longest : q; q < enough;) {
+    const int mid = (q + enough) / 2;
+    if (__reduce_add_sync(0xFFFFFFFFu, shares(0, mid) + shares(1, mid)) <= p.shares) enough = mid;
+    else q = mid + 1;
+  }
+  const int got[2] = {shares(0, q), shares(1, q)};
+  int before = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    int upto = got[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    upto += before;
+    const uint32_t mine = __ballot_sync(0xFFFFFFFFu, upto > c);
+    if (mine) {
+      const int l = __ffs(mine) - 1;
+      *tile = 32 * i + l;
+      *n = __shfl_sync(0xFFFFFFFFu, got[i], l);
+      *split = c - (__shfl_sync(0xFFFFFFFFu, upto, l) - *n);
+      return true;
+    }
+    before = __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
+  return false;
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -386,8 +443,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   ErrorWord* err = p.c.b.err;
 
-  // grid: (tile, split) x KV head
-  const int g = blockIdx.y, tile = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
+  // grid: share x KV head
+  const int g = blockIdx.y;
+  int tile, split, splits;
+  grid_dependency_wait();
+  if (!share_of(p, blockIdx.x, &tile, &split, &splits)) return;
+  if (g == 0 && split == 0 && tid == 0) p.dealt[tile] = make_int2(blockIdx.x, splits);
   const int u = p.unit_of_tile(tile);
   const int i0 = (tile - p.tile0[u]) * kTileQueries;
   const int tokens = p.c.unit_tokens(u);
@@ -419,7 +480,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
   __syncthreads();
   fence_after();
   const uint32_t tmem = *slot;
-  grid_dependency_wait();
 
   // The softmax warps bring Q in, while the loaders begin on K.
   if (warp < kSoftWarps) {
@@ -470,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
 
   const int count = p.count[tile];
   const int all = (count + kStepBlocks - 1) / kStepBlocks;
-  const int j0 = (int)((int64_t)all * split / p.splits), steps = (int)((int64_t)all * (split + 1) / p.splits) - j0;
+  const int j0 = (int)((int64_t)all * split / splits), steps = (int)((int64_t)all * (split + 1) / splits) - j0;
   bool ok = true;
 
   if (warp >= kRoleLoad && warp < kRoleMma) {
@@ -835,8 +895,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
     fence_after();
     const int x = x0 + q;
     const bool mine = ok && q < nq;
-    if (p.splits > 1) {
-      float* part = p.part + ((((int64_t)tile * kKvHeads + g) * p.splits + split) * 256 + h * 128 + (warp & 3) * 32 + lane) * kRowFloats;
+    if (splits > 1) {
+      float* part = p.part + (((int64_t)blockIdx.x * kKvHeads + g) * 256 + h * 128 + (warp & 3) * 32 + lane) * kRowFloats;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t v[32];
@@ -907,24 +967,27 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
   if (x >= p.c.rows()) return;
   const int u = p.c.unit_of_row(x), i = x - p.c.row0[u], tile = p.tile0[u] + i / kTileQueries;
   const int q = i % kTileQueries, row = (q >> 5) * 128 + (head % kGroup) * 32 + (q & 31);
-  const float* part = p.part + (((int64_t)tile * kKvHeads + head / kGroup) * p.splits * 256 + row) * kRowFloats;
-  const int64_t stride = 256 * kRowFloats;
+  const int2 dealt = p.dealt[tile];
+  const int splits = dealt.y;
+  if (splits == 1) return;                           // complete
+  const float* part = p.part + (((int64_t)dealt.x * kKvHeads + head / kGroup) * 256 + row) * kRowFloats;
+  const int64_t stride = (int64_t)kKvHeads * 256 * kRowFloats;
   // a lane takes one split's maximum and sum; the splits' O follow, their loads
   // in flight together
   float m = -INFINITY;
-  for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, part[s * stride + kHeadDim]);
+  for (int s = lane; s < splits; s += 32) m = fmaxf(m, part[s * stride + kHeadDim]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   float l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < p.splits; s0 += 32) {
+  for (int s0 = 0; s0 < splits; s0 += 32) {
     float a = 0.f;                                   // 0: nothing selected there
-    if (s0 + lane < p.splits) {
+    if (s0 + lane < splits) {
       const float2 ml = *reinterpret_cast<const float2*>(part + (s0 + lane) * stride + kHeadDim);
       if (ml.y != 0.f) a = exp2f(ml.x - m);
       l = fmaf(ml.y, a, l);
     }
-    const int n = p.splits - s0 < 32 ? p.splits - s0 : 32;
+    const int n = splits - s0 < 32 ? splits - s0 : 32;
 #pragma unroll 4
     for (int s = 0; s < n; ++s) {
       const float w = __shfl_sync(0xFFFFFFFFu, a, s);
@@ -950,10 +1013,15 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
 // ------------------------------------------------------------------- host
 
 struct AttnPlan {
-  int64_t tiles = 0, cap = 0, nb = 0;
-  int splits = 1;
-  int64_t off_block = 0, off_mask = 0, off_part = 0, bytes = 0;
+  int64_t tiles = 0, cap = 0, nb = 0, shares = 0;
+  int64_t off_dealt = 0, off_block = 0, off_mask = 0, off_part = 0, bytes = 0;
 };
+
+// Steps of a tile of nq queries of unit u, at most.
+int64_t longest_list(const ChunkDesc& c, int u, int64_t nq, int32_t budget_tokens) {
+  const int64_t nb = (c.b.u[u].n + 3) / 4, most = nq * (budget_tokens / 4);
+  return ((nb < most ? nb : most) + kStepBlocks - 1) / kStepBlocks;
+}
 
 AttnPlan make_plan(const ChunkDesc& c, int32_t budget_tokens, int sms, int32_t* tile0) {
   AttnPlan a;
@@ -968,16 +1036,35 @@ AttnPlan make_plan(const ChunkDesc& c, int32_t budget_tokens, int sms, int32_t* 
   }
   if (tile0) tile0[c.b.n_units] = (int32_t)a.tiles;
   a.cap = (a.cap + kStepBlocks - 1) / kStepBlocks * kStepBlocks;
-  // fewer CTAs than SMs: split the lists, down to four steps each
-  const int64_t ctas = a.tiles * kKvHeads, steps = a.cap / kStepBlocks;
-  int64_t s = ctas > 0 ? sms / ctas : 1;
-  if (s > (steps + 3) / 4) s = (steps + 3) / 4;
-  a.splits = (int)(s < 1 ? 1 : s);
+  // Fewer CTAs than SMs: the lists may be split.  The shares are dealt out on the
+  // device, by the lists' lengths (share_of).  Whether it pays is judged here by
+  // the longest that they can be: not where the longest share stays above 3/4 of
+  // the longest list (equal lists and few spare shares: 178 -> 184 us for 32 tiles
+  // of 64 queries on 38 shares), since the join comes on top.
+  a.shares = a.tiles;
+  const int64_t most = sms / kKvHeads < kMaxShares ? sms / kKvHeads : kMaxShares;
+  if (a.tiles < most) {
+    auto dealt = [&](int64_t q) {                    // shares of at most q steps
+      int64_t sum = 0;
+      for (int u = 0; u < c.b.n_units; ++u) {
+        const int64_t t = c.unit_tokens(u), whole = t / kTileQueries;
+        if (whole > 0) sum += whole * ((longest_list(c, u, kTileQueries, budget_tokens) + q - 1) / q);
+        if (t % kTileQueries) sum += (longest_list(c, u, t % kTileQueries, budget_tokens) + q - 1) / q;
+      }
+      return sum;
+    };
+    const int64_t longest = a.cap / kStepBlocks;
+    if (dealt(longest - longest / 4) <= most) {
+      a.shares = dealt(kLeastSteps);
+      if (a.shares > most) a.shares = most;
+    }
+  }
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
-  a.off_block = up(4 * a.tiles);
+  a.off_dealt = up(4 * a.tiles);
+  a.off_block = a.off_dealt + up(8 * a.tiles);
   a.off_mask = a.off_block + up(4 * a.tiles * a.cap);
   a.off_part = a.off_mask + up(8 * a.tiles * a.cap);
-  a.bytes = a.off_part + (a.splits > 1 ? up(a.tiles * kKvHeads * a.splits * 256 * kRowFloats * 4) : 0);
+  a.bytes = a.off_part + (a.shares > a.tiles ? up(a.shares * kKvHeads * 256 * kRowFloats * 4) : 0);
   return a;
 }
 
@@ -1010,7 +1097,7 @@ cudaError_t launch_chunk_attn(const ChunkDesc& c, const uint16_t* q, const int32
   p.sel = sel_blocks;
   p.n_sel = n_sel;
   p.k_max = budget_tokens / 4;
-  p.splits = a.splits;
+  p.shares = (int32_t)a.shares;
   p.scale_log2 = fabsf(softmax_scale) * kLog2e;
   p.sign = softmax_scale < 0.f ? -1.f : 1.f;
   p.out = out;
@@ -1018,6 +1105,7 @@ cudaError_t launch_chunk_attn(const ChunkDesc& c, const uint16_t* q, const int32
   p.cap = (int32_t)a.cap;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.count = reinterpret_cast<int32_t*>(ws);
+  p.dealt = reinterpret_cast<int2*>(ws + a.off_dealt);
   p.block = reinterpret_cast<int32_t*>(ws + a.off_block);
   p.mask = reinterpret_cast<uint32_t*>(ws + a.off_mask);
   p.part = reinterpret_cast<float*>(ws + a.off_part);
@@ -1025,11 +1113,11 @@ cudaError_t launch_chunk_attn(const ChunkDesc& c, const uint16_t* q, const int32
   e = launch_kernel(chunk_plan_kernel, dim3((unsigned)a.tiles), dim3(kPlanThreads), (size_t)window * 8, s, 0, dim3(1),
                     p, window);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(a.tiles * a.splits), kKvHeads);
+  const dim3 grid((unsigned)a.shares, kKvHeads);
   e = c.b.row_bytes == kRowBytesFp8
           ? launch_kernel(chunk_split_kernel<true>, grid, dim3(kThreads), kSmemBytes, s, 0, dim3(1), p)
           : launch_kernel(chunk_split_kernel<false>, grid, dim3(kThreads), kSmemBytes, s, 0, dim3(1), p);
-  if (e != cudaSuccess || a.splits == 1) return e;
+  if (e != cudaSuccess || a.shares == a.tiles) return e;
   const int64_t warps = (int64_t)c.rows() * kQHeads;
   return launch_kernel(chunk_join_kernel, dim3((unsigned)((warps + 7) / 8)), dim3(kJoinThreads), 0, s, 0, dim3(1), p);
 }
