@@ -14,10 +14,10 @@
 // 2048 rows of 2 KiB each would read 8.6 GB).  Three kernels:
 //  * plan: per tile the ascending list of blocks that any query selects, with
 //    a 64-bit mask of the queries that do (bitmaps in shared memory);
-//  * split: one CTA per (tile, KV head, split of the list), flash attention
-//    over 128 tokens (32 blocks) at a time;
-//  * join (when the list is split, so that few tiles still fill the device):
-//    log-sum-exp merge of the splits.
+//  * split: one CTA per (tile, KV head), or several where tiles are few, each
+//    with a share of the tile's list; flash attention over 128 tokens (32 blocks)
+//    at a time;
+//  * join (where lists are split): log-sum-exp merge of a tile's shares.
 //
 // Split kernel.  The tile's 64 queries x 4 heads of the group are 256 rows, two
 // halves of 128 = the tensor core's M: row = head * 32 + query, so a warp is a
@@ -43,17 +43,17 @@
 // select it.
 //
 // Measured: 2048 BF16 queries, 2048 of 32768 tokens each (34 GFLOP of selected
-// pairs; the unions, 2600 blocks here, make 175 of it), 178 us (plan 11, split
+// pairs; the unions, 2600 blocks here, make 175 of it), 179 us (plan 11, split
 // 170): 0.50 of the measured bf16 rate on 128 of 152 SMs, bound by the softmax
 // warps' instructions and by the hand-overs between them and the tensor core (the
-// schedulers issue in 0.62 of the cycles).  The same with FP8 rows 275 us: the four loader warps' conversions
-// and the products with both scales are added instructions.  14 FP8 draft queries
-// of 8 requests (30 MB of rows at most) 39 us (plan 8, split 33, join 4): seven
-// steps per CTA, each the latency of rows, conversion and softmax one after the
-// other.  Not faster: K and V split over the loader warps (310 us at 2048 FP8
-// queries), the next step's codes loaded into the registers just stored (321), the
-// idle half's warps on every other 64 tokens of a draft (43), the dependent
-// kernels' launches triggered early (38).
+// schedulers issue in 0.62 of the cycles).  The same with FP8 rows 276 us: the
+// loaders' conversions and the products with both scales are added instructions.
+// 14 FP8 draft queries of 8 requests (30 MB of rows at most) 34 us: five steps
+// per CTA, each the latency of rows, conversion and softmax one after the other,
+// and three launches.  Not faster: K and V split over the loader warps (310 us at
+// 2048 FP8 queries), the next step's codes loaded into the registers just stored
+// (321), the idle half's warps on every other 64 tokens of a draft (43 where 39
+// was), the dependent kernels' launches triggered early (38 where 38 was).
 //
 // Rounding: P to bf16 (at most 2^-8 of each term; the tensor core takes no wider
 // type beside bf16 rows; P to f16 with FP8 rows, 2^-11), and the output to bf16;
@@ -972,33 +972,45 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
   if (splits == 1) return;                           // complete
   const float* part = p.part + (((int64_t)dealt.x * kKvHeads + head / kGroup) * 256 + row) * kRowFloats;
   const int64_t stride = (int64_t)kKvHeads * 256 * kRowFloats;
-  // a lane takes one split's maximum and sum; the splits' O follow, their loads
-  // in flight together
-  float m = -INFINITY;
-  for (int s = lane; s < splits; s += 32) m = fmaxf(m, part[s * stride + kHeadDim]);
+  // a lane takes two shares' maxima and sums; the first shares' O are on their
+  // way with them
+  constexpr int kFirst = 16;
+  static_assert(kMaxShares == 64, "two shares per lane");
+  auto piece = [&](int s) {
+    const float* o = part + s * stride + 4 * lane;
+    const float2 lo = *reinterpret_cast<const float2*>(o), hi = *reinterpret_cast<const float2*>(o + 2);
+    return make_float4(lo.x, lo.y, hi.x, hi.y);
+  };
+  float4 first[kFirst];
+#pragma unroll
+  for (int s = 0; s < kFirst; ++s)
+    if (s < splits) first[s] = piece(s);
+  float2 ml[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    ml[i] = lane + 32 * i < splits ? *reinterpret_cast<const float2*>(part + (lane + 32 * i) * stride + kHeadDim)
+                                   : make_float2(-INFINITY, 0.f);
+  float m = fmaxf(ml[0].x, ml[1].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  float l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < splits; s0 += 32) {
-    float a = 0.f;                                   // 0: nothing selected there
-    if (s0 + lane < splits) {
-      const float2 ml = *reinterpret_cast<const float2*>(part + (s0 + lane) * stride + kHeadDim);
-      if (ml.y != 0.f) a = exp2f(ml.x - m);
-      l = fmaf(ml.y, a, l);
-    }
-    const int n = splits - s0 < 32 ? splits - s0 : 32;
-#pragma unroll 4
-    for (int s = 0; s < n; ++s) {
-      const float w = __shfl_sync(0xFFFFFFFFu, a, s);
-      const float* o = part + (s0 + s) * stride + 4 * lane;
-      const float2 o0 = *reinterpret_cast<const float2*>(o), o1 = *reinterpret_cast<const float2*>(o + 2);
-      if (w != 0.f)
-        acc = make_float4(fmaf(o0.x, w, acc.x), fmaf(o0.y, w, acc.y), fmaf(o1.x, w, acc.z), fmaf(o1.y, w, acc.w));
-    }
+  float a[2], l = 0.f;                               // a = 0: nothing selected there
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    a[i] = ml[i].y != 0.f ? exp2f(ml[i].x - m) : 0.f;
+    l = fmaf(ml[i].y, a[i], l);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](int s, float4 o) {
+    const float w = __shfl_sync(0xFFFFFFFFu, s < 32 ? a[0] : a[1], s & 31);
+    if (w != 0.f) acc = make_float4(fmaf(o.x, w, acc.x), fmaf(o.y, w, acc.y), fmaf(o.z, w, acc.z), fmaf(o.w, w, acc.w));
+  };
+#pragma unroll
+  for (int s = 0; s < kFirst; ++s)
+    if (s < splits) add(s, first[s]);
+#pragma unroll 4
+  for (int s = kFirst; s < splits; ++s) add(s, piece(s));
   const bool fine = l > 0x1p-100f && isfinite(acc.x) && isfinite(acc.y) && isfinite(acc.z) && isfinite(acc.w);
   if (!__all_sync(0xFFFFFFFFu, fine)) {
     attend_row(p, u, x, head);
