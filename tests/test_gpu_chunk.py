@@ -866,3 +866,30 @@ def test_fp8_codes_of_a_chunk_are_the_quotients_of_single_appends():
         _clean(c)
     finally:
         c.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("requests", [1, 13, 37, 38, 39])
+def test_lists_of_very_different_lengths_share_the_device(requests, fp8):
+    """Few tiles, each with as many CTAs as its list asks for: one long list,
+    short ones, empty ones; and as many tiles as there are shares, or one more."""
+    ctxs = [6000 if i == requests // 2 else 5 + (37 * i) % 400 for i in range(requests)]
+    n_tokens = [min(n, 33 if i == requests // 2 else 1 + i % 3) for i, n in enumerate(ctxs)]
+    if requests > 13:
+        n_tokens[3] = 0
+    f = Filled(ctxs, fp8=fp8, seed=21, budget=1024)
+    try:
+        rows = sum(n_tokens)
+        q = _queries(rows, 5, f.dev)
+        sel, nsel, t, n = _random_selection(f, n_tokens, 1024, seed=8)
+        for x in range(0, rows, 4):                  # rows without a block: whole tiles among them
+            if f.positions(n_tokens)[x][0] != requests // 2:
+                nsel[x] = 0
+        n = torch.tensor(nsel, dtype=torch.int32)
+        out, lse = _run_attention(f, n_tokens, q, t, n, 1024)
+        _check_attention(f, n_tokens, q, sel, nsel, out, lse, sample=70)
+        again, lse2 = _run_attention(f, n_tokens, q, t, n, 1024)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+        _clean(f.c)
+    finally:
+        f.close()
