@@ -12,9 +12,10 @@
 // out ascending, lowest ids first among the keys equal to T.  So a row is read
 // once, and no histogram sees the whole row, whose few crowded bins would
 // serialise their atomic additions (222 us for 2048 rows of 32768 scores;
-// collecting the keys themselves during the pass took 153; 100 as it is, two
-// fifths of the copy rate: what is left are the short steps after the pass, each
-// a few thousand cycles of latency, three rows to an SM).
+// collecting the keys themselves during the pass took 153; 95 as it is, 0.43 of
+// the copy rate, with four rows to an SM, 100 with three: what is left are the
+// short steps after the pass, each a few thousand cycles of latency).  14 rows of
+// draft tokens take 16 us, those latencies alone.
 //
 // Where the pivot catches fewer than K or more than kCand keys (long runs of
 // equal scores), or the row is longer than the bitmaps (kWindow blocks), the
@@ -117,7 +118,7 @@ __device__ __forceinline__ void find_pivot(const uint32_t* sample, uint32_t r, u
   if (part == 0 && above < r) atomicMin(pivot, key);
 }
 
-__global__ void __launch_bounds__(kThreads, 3) chunk_topk_kernel(const __grid_constant__ ChunkTopkParams p) {
+__global__ void __launch_bounds__(kThreads, 4) chunk_topk_kernel(const __grid_constant__ ChunkTopkParams p) {
   extern __shared__ __align__(16) uint32_t bits[];     // two bitmaps of a window
   __shared__ __align__(16) uint32_t hist[kBins];
   __shared__ __align__(16) uint32_t cand_key[kCand];
