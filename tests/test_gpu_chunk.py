@@ -893,3 +893,105 @@ def test_lists_of_very_different_lengths_share_the_device(requests, fp8):
         _clean(f.c)
     finally:
         f.close()
+
+
+def _check_device_rows(c, h, pos, q, sel, out, lse):
+    """Attention of one query against float64, its rows read from the pool."""
+    toks = [t for b in sel for t in range(4 * b, min(4 * b + 4, pos + 1))]
+    rows = c.pool[c.slot_table[h.index, 0, torch.tensor(toks, device=c.pool.device)].long()].cpu().numpy()
+    K, V = O.split_kv(rows)
+    o, ls, mag, lmag = _attend(QC.bits16(q), K, V)
+    assert np.all(np.abs(out.double().cpu().numpy() - o) <= 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 1e-4) * mag + 1e-30)
+    assert np.all(np.abs(lse.double().cpu().numpy() - ls) <= 2.0 ** -17 * lmag + 1e-5)
+
+
+def _check_device_scores(c, h, pos, q, w, got):
+    """Scores of one query against float64 on the device."""
+    n = pos + 1
+    code = torch.from_numpy(O.decode_e4m3(np.arange(256, dtype=np.uint8))).to(c.pool.device)
+    key = code[c.index_keys[h.index, 0, :n].long()] * c.index_scales[h.index, 0, :n].double()[:, None]
+    wd = w.double()
+    s = (key @ q.double().T).relu() @ wd
+    mag = (key.abs() @ q.double().abs().T) @ wd.abs()
+    pad = -n % 4
+    s = torch.nn.functional.pad(s, (0, pad), value=-np.inf).view(-1, 4).amax(1)
+    mag = torch.nn.functional.pad(mag, (0, pad)).view(-1, 4).amax(1)
+    assert bool(((got[:len(s)].double() - s).abs() <= QC.SCORE_REL_TOL * mag + 1e-30).all())
+
+
+def test_a_context_past_a_million_tokens_behind_other_requests():
+    """A chunk appended to, scored, selected and attended in a request whose
+    keys and rows lie past 2^31 and 2^32 bytes of their buffers."""
+    n, k, R = 1100003, 70, 40
+    Q.lib()
+    c = Q.Cache(n_layers=1, max_requests=R, ctx_capacity=n, hbm_pool_rows=2 * n + R, budget_tokens=2048,
+                ring_tokens=64, staging_rows=0)
+    try:
+        dev = c.pool.device
+        c.request_begin(n)
+        for _ in range(R - 2):
+            c.request_begin(1)
+        h = c.request_begin(n - k, max_ctx=n)
+        assert h.index == R - 1 and c.slot_table[h.index, 0, n - k - 1].item() * 2048 > 2 ** 32
+        assert h.index * n * 64 > 2 ** 31
+        g = torch.Generator(device=dev).manual_seed(1)
+        c.index_keys[h.index, 0] = torch.randint(0, 127, (n, 64), generator=g, device=dev, dtype=torch.uint8)
+        c.index_keys[h.index, 0] |= torch.randint(0, 2, (n, 64), generator=g, device=dev, dtype=torch.uint8) << 7
+        c.index_scales[h.index, 0] = torch.rand(n, generator=g, device=dev).half()
+        base = c.slot_table[h.index, 0, 0].item()
+        for a in range(0, n - k, 1 << 18):
+            e = min(n - k, a + (1 << 18))
+            c.pool[base + a:base + e] = torch.randn(e - a, 1024, generator=g, device=dev).bfloat16().view(torch.uint8)
+        c.advance(h, k)
+        kv = torch.randn(k, 1024, generator=g, device=dev).bfloat16().view(torch.uint8)
+        c.append_chunk([h], [k], 0, 1, torch.randn(k, 64, generator=g, device=dev), kv)
+        qi, w = torch.randn(k, 8, 64, generator=g, device=dev), torch.rand(k, 8, generator=g, device=dev)
+        blk = torch.full((k, (n + 3) // 4), NEG, device=dev)
+        sel = torch.full((k, 512), -9, dtype=torch.int32, device=dev)
+        nsel = torch.zeros(k, dtype=torch.int32, device=dev)
+        c.chunk_index_score([h], [k], 0, 1, qi, w, blk)
+        c.chunk_select_topk([h], [k], 0, 1, blk, 2048, sel, nsel)
+        sel[:, 0] = 0                                   # the first blocks and the last ones too
+        sel[:, -1] = (n - k) // 4
+        sel[:, -1] = torch.maximum(sel[:, -1], sel[:, -2] + 1)
+        pos = torch.arange(n - k, n, device=dev)
+        late = sel[:, -1] > pos // 4
+        nsel -= late.int()
+        q = _queries(k, 7, dev)
+        out, lse = torch.zeros_like(q), torch.zeros(k, 16, device=dev)
+        c.chunk_sparse_attn([h], [k], 0, 1, q, sel, nsel, 2048, SCALE, out, lse)
+        torch.cuda.synchronize()
+        _clean(c)
+        assert torch.equal(c.pool[base + n - k:base + n], kv)
+        for x in (0, 33, k - 1):
+            _check_device_scores(c, h, n - k + x, qi[x], w[x], blk[x])
+            assert bool((blk[x, (n - k + x) // 4 + 1:] == NEG).all())
+            _check_device_rows(c, h, n - k + x, q[x], sel[x, :nsel[x]].tolist(), out[x], lse[x])
+    finally:
+        c.close()
+
+
+def test_as_many_rows_as_one_call_takes():
+    R, m, budget = 64, 1024, 256
+    f = Filled([m] * R, seed=4, budget=budget)
+    try:
+        c, dev, nt, rows = f.c, f.dev, [m] * R, R * m
+        assert rows == 65536
+        g = torch.Generator(device=dev).manual_seed(2)
+        qi, w = torch.randn(rows, 8, 64, generator=g, device=dev).bfloat16(), torch.rand(rows, 8, generator=g, device=dev)
+        blk = torch.full((rows, m // 4), NEG, device=dev)
+        sel = torch.full((rows, budget // 4), -9, dtype=torch.int32, device=dev)
+        nsel = torch.zeros(rows, dtype=torch.int32, device=dev)
+        q = torch.randn(rows, 16, 128, generator=g, device=dev).bfloat16()
+        out, lse = torch.zeros_like(q), torch.zeros(rows, 16, device=dev)
+        c.chunk_index_score(f.hs, nt, 0, 1, qi, w, blk)
+        c.chunk_select_topk(f.hs, nt, 0, 1, blk, budget, sel, nsel)
+        c.chunk_sparse_attn(f.hs, nt, 0, 1, q, sel, nsel, budget, SCALE, out, lse)
+        torch.cuda.synchronize()
+        _clean(c)
+        _check_scores(f, nt, qi, w, blk)
+        at = torch.tensor([0, 1, 257, 1023, 1024, 40001, 65534, 65535])
+        _check_selection(blk[at.to(dev)], [int(i) % m for i in at], budget, sel[at.to(dev)], nsel[at.to(dev)])
+        _check_attention(f, nt, q, sel.cpu().numpy(), nsel.cpu().numpy(), out, lse, sample=30)
+    finally:
+        f.close()
