@@ -29,6 +29,15 @@ def _stream(stream) -> int | None:
     return int(stream)
 
 
+def _stream_of(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# the current stream of a device (by its index) as an address, without the
+# Stream object around it (2 us of a call's 15 in Python)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
+
+
 def _batch(handles, layer0: int, n_layers: int):
     arr = (N.Handle * len(handles))(*[N.Handle(h.index, h.generation) for h in handles])
     b = N.Batch(len(handles), layer0, n_layers, 0, C.cast(arr, C.POINTER(N.Handle)))
@@ -312,7 +321,7 @@ class Cache:
     def _current(self, stream):
         """The stream given, else the current one of the cache's device."""
         if stream is None and self.device is not None:
-            return torch.cuda.current_stream(self.pool.device).cuda_stream
+            return _raw_stream(self.pool.device.index)
         return _stream(stream)
 
     # ------------------------------------------------ several tokens at once
