@@ -184,7 +184,7 @@ class Cache:
         if host_rows is not None:
             d.host_rows = host_rows.data_ptr() if isinstance(host_rows, torch.Tensor) else int(host_rows)
         out = N.Handle()
-        check(self.L.qsa_request_begin(self.h, C.byref(d), _stream(stream) if self.device else None,
+        check(self.L.qsa_request_begin(self.h, C.byref(d), self._current(stream) if self.device else None,
                                        C.byref(out)), "qsa_request_begin")
         if isinstance(host_rows, torch.Tensor):
             self._host[out.index] = host_rows
@@ -242,7 +242,7 @@ class Cache:
         if host_rows is not None:
             d.host_rows = host_rows.data_ptr() if isinstance(host_rows, torch.Tensor) else int(host_rows)
         out = N.Handle()
-        check(self.L.qsa_request_fork(self.h, parent, C.byref(d), _stream(stream) if self.device else None,
+        check(self.L.qsa_request_fork(self.h, parent, C.byref(d), self._current(stream) if self.device else None,
                                       C.byref(out)), "qsa_request_fork")
         if isinstance(host_rows, torch.Tensor):
             self._host[out.index] = host_rows
@@ -251,7 +251,7 @@ class Cache:
     def compact(self, stream=None) -> int:
         """Close the gaps of the pool; returns the number of rows moved."""
         moved = C.c_int64()
-        check(self.L.qsa_cache_compact(self.h, _stream(stream) if self.device else None, C.byref(moved)),
+        check(self.L.qsa_cache_compact(self.h, self._current(stream) if self.device else None, C.byref(moved)),
               "qsa_cache_compact")
         return moved.value
 
