@@ -117,7 +117,9 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanWindow = 24576;                // blocks of one bitmap window (192 KiB)
 constexpr int kRowFloats = kHeadDim + 2;          // partial of a row: O, m, l
 constexpr int kMaxShares = 64;                    // where tiles are split: two tiles per lane
-constexpr int kLeastSteps = 2;                     // a share's steps at least, where its tile has them
+// A share's steps at least, where its tile has them: 4 queries of one request of
+// 65536 tokens 26.8, 26.5, 27.6, 29.3 us with 1, 2, 3, 4.
+constexpr int kLeastSteps = 2;
 
 struct ChunkAttnParams {
   ChunkDesc c;
