@@ -33,7 +33,7 @@
 //
 // Measured: 2048 bf16 queries at the end of 131072 tokens (277 GFLOP) 345 us,
 // 0.80 PFLOP/s, 0.41 of the measured bf16 rate; 10 fp32 draft queries of 4 requests of
-// 65536 tokens 17 us.  What bounds it is the epilogue's instructions: 8
+// 65536 tokens 14 us.  What bounds it is the epilogue's instructions: 8
 // saturating products and 4 paired multiply-adds per query and lane against 128
 // tensor-core cycles per tile; the schedulers issue in 0.66 of the cycles, and
 // the loop without its arithmetic takes 207 us.  Not faster: 128 queries to a
@@ -56,6 +56,7 @@ constexpr int kAccs = 4;                          // tiles, each with its accumu
 constexpr int kAccCols = 512 / kAccs;
 constexpr int kTileQueries = kAccCols / kIndexHeads;             // at most, per tile: 16
 constexpr int kGroup = kAccs * kTileQueries;      // queries per group: 64
+constexpr int kFewQueries = 4;                    // that a single tile takes
 constexpr int kEpiWarps = 4;                      // epilogue warps per accumulator
 constexpr int kConvWarps = 2;
 constexpr int kConvLoads = 512 / (32 * kConvWarps);              // 16-byte loads per lane and phase
@@ -138,10 +139,17 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return d;
 }
 
-template <bool kBf16>
+// kFew: no group has more than kFewQueries (draft tokens), which all fall into
+// one tile.  Its phases then take the four accumulators in turn, and the warps of
+// the missing tiles convert too (the kernel alone, with cold caches: 14 bf16
+// queries over 8 x 32768 tokens 20.2 -> 16.4 us, 10 fp32 queries over 4 x 65536
+// 20.1 -> 16.9, with half of the teams 20).  Run-time choices in one kernel cost
+// the full groups 10 %.  Both pieces of fp32 queries side by side in one product,
+// added in the epilogue, are slower (21.3).
+template <bool kBf16, bool kFew>
 __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_constant__ ChunkScoreParams p) {
   using L = Layout<kBf16>;
-  constexpr int kPieces = L::kPieces, kStages = L::kStages;
+  constexpr int kPieces = L::kPieces, kStages = L::kStages, kQueries = kFew ? kFewQueries : kTileQueries;
   constexpr int kOffB = L::kOffB, kOffW = L::kOffW, kOffBar = L::kOffBar, kOffSlot = L::kOffSlot;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -178,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
   int64_t at = total * blockIdx.x / gridDim.x;
   const int64_t end = total * (blockIdx.x + 1) / gridDim.x;
   int phase = 0;      // phases streamed by this CTA (ring position)
-  int fills = 0;      // epilogue: times its accumulator was filled
+  int fills = 0;      // epilogue: times its accumulator was filled (kFew: its accumulators, in turn)
   uint32_t used = 0, turn = 0;   // MMA warp, a bit per accumulator: filled before, parity of the next wait
   while (at < end) {
     // ---- the group and its part of the run
@@ -213,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
     const int64_t row0 = p.c.b.unit_row(u);
     // queries per tile (a multiple of 4: 32 columns) and tiles with queries
     const int qt = ((nq + kAccs - 1) / kAccs + 3) / 4 * 4;
-    const int tiles = (nq + qt - 1) / qt;
+    const int tiles = kFew ? 1 : (nq + qt - 1) / qt;
 
     // ---- B and the head weights (all threads; the previous run is complete).
     // Row r of a tile is head r & 7 of the tile's query r >> 3, scaled by 2^-k
@@ -260,11 +268,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
 
     const int steps = (int)(s1 - s0);
     bool ok = true;
-    if (warp >= kRoleConv && warp < kRoleMma) {
+    // teams of kConvWarps converter warps, each with every kTeams-th phase
+    constexpr int kTeams = kFew ? 4 : 1;
+    const int spare = warp - kEpiWarps;
+    const int team = warp >= kRoleConv ? 0 : 1 + spare / kConvWarps;
+    if (kFew ? spare >= 0 && warp < kRoleMma && team < kTeams : warp >= kRoleConv && warp < kRoleMma) {
       // ---- converters: 16 codes per lane and load; lanes 4i .. 4i+3 hold one
       // token, a load of a warp 8 blocks, the next phase's loads in flight.  A
       // negative scale turns the code's sign.
-      const int wc = warp - kRoleConv, sub = lane >> 2, part = lane & 3;
+      const int wc = (warp >= kRoleConv ? warp - kRoleConv : spare) % kConvWarps, sub = lane >> 2, part = lane & 3;
       const uint8_t* keys = p.c.b.index_keys + row0 * kIndexDim + part * 16;
       const uint16_t* scales = p.c.b.index_scales + row0;
       uint4 v[2][kConvLoads];
@@ -280,13 +292,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
           negative[e] |= in ? (uint32_t)(__ldg(scales + t) >> 15) << j : 0u;
         }
       };
-      load(0, 0);
-      load(1, 1);
+      const int first_phase = kFew ? team : 0;
+      load(0, first_phase);
+      load(1, first_phase + kTeams);
 #pragma unroll 1
-      for (int i0 = 0; i0 < 4 * steps && ok; i0 += 2) {
+      for (int i0 = first_phase; i0 < 4 * steps && ok; i0 += 2 * kTeams) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int ph = phase + i0 + e, st = ph % kStages;
+          if (kFew && i0 + e * kTeams >= 4 * steps) break;
+          const int ph = phase + i0 + e * kTeams, st = ph % kStages;
           if (ok && ph >= kStages) ok = mbar_wait(a_empty(st), (uint32_t)(ph / kStages - 1) & 1u, err, kKernChunkScore);
           if (!ok) break;
           uint8_t* A = smem + st * kABytes;
@@ -300,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
             *reinterpret_cast<uint4*>(A + r * 128 + (((2 * part + 1) ^ (r & 7)) << 4)) =
                 make_uint4(c.x, c.y, d.x, d.y);
           }
-          load(e, i0 + e + 2);
+          load(e, i0 + (e + 2) * kTeams);
           fence_async_smem();
           mbar_arrive(a_full(st));
         }
@@ -315,20 +329,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
         ok = mbar_wait_warp(a_full(st), lap, err, kKernChunkScore);
 #pragma unroll 1
         for (int t = 0; t < tiles && ok; ++t) {
-          if ((used >> t) & 1u) ok = mbar_wait_warp(d_empty(t), (turn >> t) & 1u, err, kKernChunkScore);
+          const int acc = kFew ? i % kAccs : t;
+          if ((used >> acc) & 1u) ok = mbar_wait_warp(d_empty(acc), (turn >> acc) & 1u, err, kKernChunkScore);
           if (!ok) break;
-          turn ^= ((used >> t) & 1u) << t;
-          used |= 1u << t;
+          turn ^= ((used >> acc) & 1u) << acc;
+          used |= 1u << acc;
           fence_after();
           if (elect_one()) {
-            const uint32_t d = tm + (uint32_t)(kAccCols * t), a = sb + st * kABytes;
+            const uint32_t d = tm + (uint32_t)(kAccCols * acc), a = sb + st * kABytes;
             const uint64_t a0 = desc_sw128(a, 16), b0 = desc_sw128(sb + kOffB + t * kBTile, 16);
 #pragma unroll
             for (int pc = 0; pc < kPieces; ++pc)
 #pragma unroll
               for (int ks = 0; ks < kIndexDim / 16; ++ks)
                 mma_ss(d, a0 + 2 * ks, b0 + (uint64_t)(pc * kAccs * kBTile / 16 + 2 * ks), idesc, (pc | ks) != 0);
-            commit(d_full(t));
+            commit(d_full(acc));
             if (t == tiles - 1) commit(a_empty(st));
           }
           __syncwarp();
@@ -341,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
       // roles' code outgrew the instruction cache.
       const int tile = warp / kEpiWarps, row = (warp & 3) * 32 + lane;
       const int q0 = tile * qt, mine = nq - q0 < qt ? nq - q0 : qt;      // the tile's queries
-      const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(kAccCols * tile);
+      const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (kFew ? 0u : (uint32_t)(kAccCols * tile));
       const uint16_t* scales = p.c.b.index_scales + row0;
       const ulonglong2* wq = reinterpret_cast<const ulonglong2*>(sw + q0 * kIndexHeads);
       uint16_t next[4];
@@ -363,23 +378,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
         if (s + 1 < steps) load_scales(s0 + s + 1);
         // every token of the step within every query's context?
         const bool whole = (s0 + s + 1) * kStepTokens - 1 <= pos0;
-        float best[kTileQueries];
+        float best[kQueries];
 #pragma unroll
-        for (int i = 0; i < kTileQueries; ++i) best[i] = -INFINITY;
+        for (int i = 0; i < kQueries; ++i) best[i] = -INFINITY;
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
           const float m = k < 2 ? (k == 0 ? mag[0] : mag[1]) : (k == 2 ? mag[2] : mag[3]);
-          ok = mbar_wait(d_full(tile), (uint32_t)fills & 1u, err, kKernChunkScore);
+          const int acc = kFew ? k : tile;
+          ok = mbar_wait(d_full(acc), (uint32_t)(kFew ? fills >> 2 : fills) & 1u, err, kKernChunkScore);
           ++fills;
           if (!ok) break;
           fence_after();
           // the tile's queries before `from` do not see this token
           const int64_t from = t0 + k - pos0 - q0;
 #pragma unroll
-          for (int c = 0; c < kTileQueries / 4; ++c) {         // four queries: 32 columns
+          for (int c = 0; c < kQueries / 4; ++c) {             // four queries: 32 columns
             if (4 * c >= mine) break;
             uint32_t v[32];
-            ld32(lane_base + 32u * (uint32_t)c, v);
+            ld32(lane_base + (kFew ? (uint32_t)(kAccCols * k) : 0u) + 32u * (uint32_t)c, v);
             wait_ld();
             reg_fence(v);
             float y[4];
@@ -402,12 +418,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
             for (int i = 0; i < 4; ++i) best[4 * c + i] = fmaxf(best[4 * c + i], y[i]);
           }
           fence_before();
-          mbar_arrive(d_empty(tile));
+          mbar_arrive(d_empty(acc));
         }
         if (!ok) break;
         float* o = p.blk + (int64_t)(x0 + q0) * p.blk_stride + b0 + row;
 #pragma unroll
-        for (int i = 0; i < kTileQueries; ++i) {
+        for (int i = 0; i < kQueries; ++i) {
           if (i >= mine) break;
           if (whole || t0 <= pos0 + q0 + i) *o = best[i];
           o += p.blk_stride;
@@ -432,11 +448,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
   }
 }
 
-template <bool kBf16>
+template <bool kBf16, bool kFew>
 cudaError_t launch(ChunkScoreParams& p, cudaStream_t s) {
   constexpr int kSmemBytes = Layout<kBf16>::kSmemBytes;
   static PerDeviceOnce setup;
-  cudaError_t e = setup.run([] { return prefer_max_shared(chunk_score_kernel<kBf16>, kSmemBytes); });
+  cudaError_t e = setup.run([] { return prefer_max_shared(chunk_score_kernel<kBf16, kFew>, kSmemBytes); });
   int sms = 0;
   if (e == cudaSuccess) e = current_sm_count(&sms);
   if (e != cudaSuccess) return e;
@@ -448,7 +464,7 @@ cudaError_t launch(ChunkScoreParams& p, cudaStream_t s) {
   }
   p.step0[p.c.b.n_units] = (int32_t)total;
   const unsigned grid = (unsigned)(total < sms ? total : sms);
-  return launch_kernel(chunk_score_kernel<kBf16>, dim3(grid), dim3(kThreads), kSmemBytes, s, 0, dim3(1), p);
+  return launch_kernel(chunk_score_kernel<kBf16, kFew>, dim3(grid), dim3(kThreads), kSmemBytes, s, 0, dim3(1), p);
 }
 
 }  // namespace
@@ -461,7 +477,10 @@ cudaError_t launch_chunk_score(const ChunkDesc& c, const void* q_idx, bool q_bf1
   p.w = w;
   p.blk = blk_scores;
   p.blk_stride = blk_stride;
-  return q_bf16 ? launch<true>(p, s) : launch<false>(p, s);
+  bool few = true;
+  for (int u = 0; u < c.b.n_units; ++u) few = few && c.unit_tokens(u) <= kFewQueries;
+  if (few) return q_bf16 ? launch<true, true>(p, s) : launch<false, true>(p, s);
+  return q_bf16 ? launch<true, false>(p, s) : launch<false, false>(p, s);
 }
 
 }  // namespace qsa
