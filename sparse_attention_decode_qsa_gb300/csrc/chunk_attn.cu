@@ -614,14 +614,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
       };
       if (!kFp8) {
         // 16 lanes copy the 256 bytes of a token's K[g] (or V[g]); two tokens per turn
+        // (row r = 2 i + hi; its swizzle takes one of four values per lane)
         const uint32_t c = lane & 15, hi = lane >> 4;
+        const uint32_t there = __ballot_sync(0xFFFFFFFFu, src != nullptr) >> hi;
+        const uintptr_t at = src ? from : reinterpret_cast<uintptr_t>(p.c.b.pool);
         auto copy = [&](uint32_t dst, int off) {
-#pragma unroll 8
+          const uint32_t to = sb + dst + (c >> 3) * kPanel + hi * 128;
+          const int o = off + (int)c * 16;
+#pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const uint32_t r = 2 * i + hi;
-            const uint8_t* s = reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, from, (int)r));
-            cp_async16(sb + dst + (c >> 3) * kPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4), s ? s + off + c * 16 : p.c.b.pool,
-                       s ? 16u : 0u);
+            const uint8_t* s = reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, at, (int)(2 * i + hi)));
+            cp_async16(to + i * 256 + ((((c & 7) ^ hi) ^ (2 * i & 7)) << 4), s + o, (there >> (2 * i)) & 1u ? 16u : 0u);
           }
           asm volatile("cp.async.commit_group;" ::: "memory");
         };
