@@ -43,8 +43,8 @@
 // select it.
 //
 // Measured: 2048 BF16 queries, 2048 of 32768 tokens each (34 GFLOP of selected
-// pairs; the unions, 2600 blocks here, make 175 of it), 179 us (plan 11, split
-// 170): 0.50 of the measured bf16 rate on 128 of 152 SMs, bound by the softmax
+// pairs; the unions, 2600 blocks here, make 175 of it), 171 us (plan 11, split
+// 163): 0.52 of the measured bf16 rate on 128 of 152 SMs, bound by the softmax
 // warps' instructions and by the hand-overs between them and the tensor core (the
 // schedulers issue in 0.62 of the cycles).  The same with FP8 rows 276 us: the
 // loaders' conversions and the products with both scales are added instructions.
