@@ -787,8 +787,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
       wait_ld();
       reg_fence(v[0]);
       reg_fence(v[1]);
-      // ---- maximum over the selected blocks (in a step with tokens past the
-      // query, or without a row, over these too: it is a reference only)
       if (kFp8) {
 #pragma unroll
         for (int i = 0; i < kSubTokens; i += 4) {
@@ -801,6 +799,26 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
           x[3] = (uint32_t)(b >> 32);
         }
       }
+      // tokens past the query, or without a row, count nowhere: a maximum that
+      // they set could leave the row's own products below f16's range
+      uint32_t tok[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};  // per token: its row exists and q sees it
+      if (special) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          uint32_t seen = sm.valid[2 * c + w];
+#pragma unroll 1
+          for (int b = 0; b < 8; ++b) {
+            const int64_t left = pos - 4 * (int64_t)sm.block[16 * c + 8 * w + b];   // tokens of the block that q sees, - 1
+            const uint32_t four = left >= 3 ? 0xFu : (left < 0 ? 0u : (2u << (int)left) - 1u);
+            seen &= ~(0xFu << (4 * b)) | (four << (4 * b));
+          }
+          tok[w] = seen;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!((seen >> i) & 1u)) v[w][i] = __float_as_uint(-INFINITY);
+        }
+      }
+      // ---- maximum over the selected blocks
       auto at = [&](int i) { return __uint_as_float(v[i >> 5][i & 31]); };
       float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -850,16 +868,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
 #pragma unroll
       for (int w = 0; w < 2; ++w) {                  // 32 tokens
         uint32_t o[16];
-        uint32_t tok = 0xFFFFFFFFu;                  // per token: its row exists and q sees it
-        if (special) {
-          tok = sm.valid[2 * c + w];
-#pragma unroll 1
-          for (int b = 0; b < 8; ++b) {
-            const int64_t left = pos - 4 * (int64_t)sm.block[16 * c + 8 * w + b];   // tokens of the block that q sees, - 1
-            const uint32_t seen = left >= 3 ? 0xFu : (left < 0 ? 0u : (2u << (int)left) - 1u);
-            tok &= ~(0xFu << (4 * b)) | (seen << (4 * b));
-          }
-        }
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
           // a block that the query does not select: exp2(s f - inf) = 0 (NaN
@@ -872,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
           if (special) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (!((tok >> (4 * b + i)) & 1u)) e[i] = 0.f;
+              if (!((tok[w] >> (4 * b + i)) & 1u)) e[i] = 0.f;
           }
           l2 = add2(l2, pair(e[0], e[1]));
           l2 = add2(l2, pair(e[2], e[3]));

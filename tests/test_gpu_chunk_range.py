@@ -1,0 +1,139 @@
+"""Chunk operators where values lie far apart: logits of tokens that a query
+does not see, V scales from 2^-24 to 2^15 in one selection, query elements far
+below the largest.  Against float64.
+
+Tolerances of the attention, per element and in units of mag = sum p|v|.  The
+output is rounded to bf16 (2^-8 of it).  Probabilities go to the tensor cores
+as bf16 beside BF16 rows (2^-8 of each term); beside FP8 rows p times the V
+scale goes in as f16, off by 2^-11 of itself or by 2^-25 in units in which the
+row's largest product is 2^-4 at least, so by 2^-21 of that one.  128 products
+in fp32 leave a logit off by 2^-17 of scale * sum |q_d k_d|, a probability by
+twice that (its own and the sum's), and fp32 sums add less than 1e-4."""
+import numpy as np
+import pytest
+import torch
+
+import sparse_attention_decode_qsa_gb300 as Q
+from oracle import qsa_oracle as O
+from tests import qsa_check as QC
+from tests.test_gpu_chunk import SCALE, Filled, _attend, _clean, _queries, _random_selection, _run_attention
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    Q.lib()
+
+
+def _v_scales(f, r, toks):
+    rows = f.kv[r][0][torch.as_tensor(toks, dtype=torch.long)].numpy()
+    return O.decode_fp16(np.ascontiguousarray(rows[:, 1032:1040]).view(np.uint16))
+
+
+def _floor(q_bits, K, V, vs):
+    """2^-21 of the largest p |scale| of a row, times the sum of its codes."""
+    q = O.decode_bf16(q_bits).reshape(16, 128)
+    out = np.zeros((16, 128))
+    for h in range(16):
+        x = SCALE * (K[:, h // 4] @ q[h])
+        p = np.exp(x - x.max())
+        s = np.abs(vs[:, h // 4])
+        codes = np.abs(V[:, h // 4]) / np.where(s > 0, s, 1)[:, None]
+        out[h] = 2.0 ** -21 * (p * s).max() / p.sum() * codes.sum(0)
+    return out
+
+
+def _check(f, n_tokens, q, sel, nsel, out, lse, rows=None):
+    pos = f.positions(n_tokens)
+    for x in range(len(pos)) if rows is None else rows:
+        r, p = pos[x]
+        toks = [t for b in sel[x][:nsel[x]] for t in range(4 * int(b), min(4 * int(b) + 4, p + 1))]
+        K, V = f.values(r, 0, toks)
+        bits = QC.bits16(q[x])
+        o, ls, mag, lmag = _attend(bits, K, V)
+        part = (2.0 ** -11 if f.fp8 else 2.0 ** -8) + 2 * 2.0 ** -17 * lmag[:, None] + 1e-4
+        tol = 2.0 ** -8 * np.abs(o) + part * mag
+        if f.fp8:
+            tol += _floor(bits, K, V, _v_scales(f, r, toks))
+        got, gl = out[x].double().cpu().numpy(), lse[x].double().cpu().numpy()
+        assert np.all(np.abs(got - o) <= tol), (x, r, p, (np.abs(got - o) / tol).max(), np.abs(got).max(), np.abs(o).max())
+        assert np.all(np.abs(gl - ls) <= 2.0 ** -17 * lmag + 1e-5), (x, np.abs(gl - ls).max())
+
+
+def _store(f, r):
+    """The rows that the test has changed go to the pool."""
+    rows = f.c.slot_table[f.hs[r].index, 0, :f.ctxs[r]].long()
+    f.c.pool[rows] = f.kv[r][0].to(f.dev)
+
+
+SIGNS = torch.where(torch.randn(128, generator=torch.Generator().manual_seed(4)) < 0, -1.0, 1.0)
+
+
+def _set_logits(f, r, logits):
+    """Keys along one direction: with the query SIGNS token t's logit is
+    logits[t], up to the row format's rounding of it."""
+    c = torch.as_tensor(logits, dtype=torch.float32) / (128 * SCALE)
+    raw = f.kv[r][0]
+    if f.fp8:
+        codes = torch.where((c[:, None] < 0) != (SIGNS[None] < 0), 0xFE, 0x7E).to(torch.uint8)      # -448, 448
+        raw[:, :512] = codes.repeat(1, 4)
+        raw[:, 1024:1032] = (c.abs() / 448).half()[:, None].repeat(1, 4).view(torch.uint8)
+    else:
+        raw[:, :1024] = (c[:, None] * SIGNS).bfloat16().repeat(1, 4).view(torch.uint8)
+    _store(f, r)
+
+
+def _table(sel, budget):
+    t = torch.full((len(sel), budget // 4), -7, dtype=torch.int32)
+    for x, s in enumerate(sel):
+        t[x, :len(s)] = torch.as_tensor(np.asarray(s), dtype=torch.int32)
+    return t, torch.tensor([len(s) for s in sel], dtype=torch.int32)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("logit", [-20.0, -60.0])
+@pytest.mark.parametrize("ctx", [1, 2, 3, 5])
+def test_places_past_the_context_leave_low_logits_alone(fp8, logit, ctx):
+    """The last block's places without a token count as logit 0 nowhere."""
+    f = Filled([ctx], fp8=fp8, budget=64, seed=3)
+    try:
+        _set_logits(f, 0, [logit] * ctx)
+        q = SIGNS.bfloat16().expand(1, 16, 128).contiguous().to(f.dev)
+        sel = [np.arange((ctx + 3) // 4)]
+        out, lse = _run_attention(f, [1], q, *_table(sel, 64), 64)
+        _clean(f.c)
+        _check(f, [1], q, sel, [len(sel[0])], out, lse)
+    finally:
+        f.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("step", [4.0, 12.0, 40.0])
+@pytest.mark.parametrize("ctxs,n_tokens,others", [
+    ([400], [70], 0), ([400], [70], 31), ([9000], [70], 400), ([300] * 39, [5] * 39, 20)])
+def test_later_tokens_of_a_querys_block_do_not_reach_it(fp8, step, ctxs, n_tokens, others):
+    """In the chunk, every token's logit is `step` nats above that of the token
+    before it in its block; a query sees some of its own block's only.  Lists
+    cut into shares and whole ones."""
+    f = Filled(ctxs, fp8=fp8, budget=2048, seed=3)
+    try:
+        rng = np.random.RandomState(8)
+        for r, (n, k) in enumerate(zip(ctxs, n_tokens)):
+            logits = rng.randn(n)
+            at = np.arange(n - k, n)
+            logits[at] = step * (at % 4)
+            _set_logits(f, r, logits)
+        sel = []
+        for r, p in f.positions(n_tokens):
+            old = rng.choice((ctxs[r] - n_tokens[r]) // 4, others, replace=False)
+            sel.append(np.sort(np.append(old, p // 4)))
+        q = SIGNS.bfloat16().expand(len(sel), 16, 128).contiguous().to(f.dev)
+        out, lse = _run_attention(f, n_tokens, q, *_table(sel, 2048), 2048)
+        _clean(f.c)
+        rows = range(len(sel)) if len(sel) <= 70 else range(0, len(sel), 3)
+        _check(f, n_tokens, q, sel, [len(s) for s in sel], out, lse, rows)
+    finally:
+        f.close()
