@@ -534,8 +534,11 @@ int64_t qsa_chunk_attn_workspace_bytes(qsa_cache* cache, const qsa_chunk* chunk,
  * q: device bf16 bits [rows][16][128]; sel_blocks, n_sel: as written by
  * qsa_chunk_select_topk; out: device bf16 bits [rows][16][128], rounded once
  * from the fp32 sums; lse: device fp32 [rows][16] or NULL (-inf, and out = 0,
- * for a row with no tokens).  A key or value that is not finite reaches only
- * the queries that select its token.
+ * for a row with no tokens).  Each term p_t V_t of the output's sum is off by at
+ * most 2^-8 of itself beside BF16 rows; beside FP8 rows by 2^-11 of itself or by
+ * 2^-19 of the row's largest p_s * (V scale of s) times the code, whichever is
+ * more.  A key or value that is not finite reaches only the queries that select
+ * its token.
  * workspace: device, 16-byte aligned, qsa_chunk_attn_workspace_bytes bytes,
  * used by one call at a time: calls that may overlap need one each.
  * Errors: INVALID_ARG, STALE_HANDLE, NO_DEVICE, CUDA; bad blocks, counts and

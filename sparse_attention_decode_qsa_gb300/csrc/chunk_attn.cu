@@ -56,8 +56,11 @@
 // was), the dependent kernels' launches triggered early (38 where 38 was).
 //
 // Rounding: P to bf16 (at most 2^-8 of each term; the tensor core takes no wider
-// type beside bf16 rows; P to f16 with FP8 rows, 2^-11), and the output to bf16;
-// the sum l is taken from the unrounded probabilities, S, O, m and l are fp32.
+// type beside bf16 rows), and the output to bf16; the sum l is taken from the
+// unrounded probabilities, S, O, m and l are fp32.  With FP8 rows P times the V
+// scale goes in as f16: off by 2^-11 of itself, or by 2^-25 in units in which the
+// largest of the row's products is 2^-6 at least, whatever the scales are and
+// whoever else selects what (the reference follows the row's own products).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -91,10 +94,12 @@ struct StepMeta {
   uint32_t valid[4];            // bit per token of the step: its row exists
   int32_t block[kStepBlocks];   // block ids
   int32_t special[4];           // per loader warp: a row is missing, or a block reaches past the first query
+  uint32_t exps[4];             // FP8, per loader warp: bit e, a row has a V scale with the f16 exponent field e
 };
 struct __align__(16) Scales {   // FP8 rows
   float k[kStepTokens];         // K scale (times softmax scale and log2 e)
-  float v[kStepTokens];
+  float v[kStepTokens];         // V scale
+  float size[kStepTokens];      // log2 of its size
 };
 constexpr int kOffKv = kQBytes;
 constexpr int kOffMeta = kOffKv + kStages * kStageBytes;
@@ -393,6 +398,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// log2 of a V scale's size.
+__device__ __forceinline__ float log2_size(float s) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fabsf(s)));
+  return fmaxf(y, -100.f);
+}
+
 // Pairs of fp32 values: one instruction for two multiply-adds or additions.
 __device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) { return (uint64_t)a | ((uint64_t)b << 32); }
 __device__ __forceinline__ uint64_t pair(float a, float b) { return pair(__float_as_uint(a), __float_as_uint(b)); }
@@ -423,6 +435,45 @@ __device__ __forceinline__ uint4 codes8_f16(uint2 w) {
   return make_uint4(codes2_f16(w.x & 0xFFFFu), codes2_f16(w.x >> 16), codes2_f16(w.y & 0xFFFFu), codes2_f16(w.y >> 16));
 }
 
+// The tokens of 64 c + 4 b .. + 3 of a step that exist and that position pos
+// sees, a bit each.
+__device__ __forceinline__ uint32_t seen_tokens(const StepMeta& sm, int c, int b, int64_t pos) {
+  const int64_t left = pos - 4 * (int64_t)sm.block[16 * c + b];    // tokens of the block that pos sees, - 1
+  return (left >= 3 ? 0xFu : (left < 0 ? 0u : (2u << (int)left) - 1u)) & (sm.valid[2 * c + (b >> 3)] >> (4 * (b & 7)));
+}
+
+// FP8: the largest logit + log2 (V scale) of a row's tokens among 64, each by its
+// own scale (2048 queries where every 64 tokens need it: 272 -> 340 us).  S is read
+// from tensor memory for this alone: among the registers of the usual path the
+// scales would spill (309 us for rows that never come here).
+__device__ __forceinline__ float wide_max(uint32_t colS, const StepMeta& sm, const Scales& sc, int c, uint32_t mine,
+                                          bool special, int64_t pos, float f) {
+  float most = -INFINITY;
+#pragma unroll 1
+  for (int b0 = 0; b0 < kSubTokens / 4; b0 += 4) {
+    uint32_t x[16];
+    ld16(colS + 4u * (uint32_t)b0, x);
+    wait_ld();
+    reg_fence(x);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int t = kSubTokens * c + 4 * (b0 + b);
+      const float4 k = *reinterpret_cast<const float4*>(&sc.k[t]), s = *reinterpret_cast<const float4*>(&sc.size[t]);
+      float y[4] = {fmaf(__uint_as_float(x[4 * b]) * k.x, f, s.x), fmaf(__uint_as_float(x[4 * b + 1]) * k.y, f, s.y),
+                    fmaf(__uint_as_float(x[4 * b + 2]) * k.z, f, s.z), fmaf(__uint_as_float(x[4 * b + 3]) * k.w, f, s.w)};
+      if (special) {
+        const uint32_t seen = seen_tokens(sm, c, b0 + b, pos);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!((seen >> i) & 1u)) y[i] = -INFINITY;
+      }
+      const float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+      most = fmaxf(most, (mine >> (b0 + b)) & 1u ? top : -INFINITY);
+    }
+  }
+  return most;
+}
+
 template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_constant__ ChunkAttnParams p) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -441,7 +492,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
   const uint32_t q_full = bars + 8u * (uint32_t)(4 * kStages + 12);
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kOffSlot);
   __shared__ float row_factor[kFp8 ? 256 : 1];
-  __shared__ uint32_t v_most;      // FP8: bits of the first step's largest V scale
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   ErrorWord* err = p.c.b.err;
 
@@ -462,7 +512,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
   if (warp == kRoleMma) {
     tmem_alloc<kTmemCols>(slot);
     if (lane == 0) {
-      v_most = 0;
       for (int i = 0; i < kStages; ++i) {
         mbar_init(k_full(i), 32 * kLoadWarps);
         mbar_init(k_empty(i), (uint32_t)halves);
@@ -666,10 +715,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
         const float ks = __half2float(__ushort_as_half(kraw)), vs = __half2float(__ushort_as_half(vraw));
         scales[j % kMetas].k[32 * w + lane] = ks * p.scale_log2;
         scales[j % kMetas].v[32 * w + lane] = vs;
-        if (j == 0) {
-          const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(vs)));
-          if (lane == 0) atomicMax(&v_most, most);
-        }
+        scales[j % kMetas].size[32 * w + lane] = log2_size(vs);
+        const uint32_t exps = __reduce_or_sync(0xFFFFFFFFu, src ? 1u << ((vraw >> 10) & 31) : 0u);
+        if (lane == 0) m.exps[w] = exps;
         // codes 16 c .. +15 are chunks 2 c, 2 c + 1 of the row's 16
         auto store = [&](uint32_t dst, const uint4 (&x)[8]) {
 #pragma unroll
@@ -769,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
     // FP8: the K scales hold the softmax scale
     const float f = kFp8 ? row_factor[128 * h + (warp & 3) * 32 + lane] : p.scale_log2;
     const uint64_t f2 = pair(f, f);
-    float m = -INFINITY, l = 0.f, ve = 0.f;          // in units of log2
+    float m = -INFINITY, l = 0.f;                    // in units of log2
 #pragma unroll 1
     for (int jc = 0; jc < 2 * steps; ++jc) {
       const int j = jc >> 1, c = jc & 1;             // tokens 64 c .. of step j
@@ -777,13 +825,28 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
       ok = mbar_wait_warp(s_full(h, c), (uint32_t)j & 1u, err, kKernChunkAttn);
       if (!ok) break;
       fence_after();
+      const StepMeta& sm = meta[j % kMetas];
+      const Scales& sc = scales[j % kMetas];
+      // FP8: probabilities times V scales go in as f16, so the reference follows
+      // the largest of these products that the row has, not of the probabilities:
+      // log2 of both, x + log2 s.  Where the 64 tokens' scales lie within a factor
+      // of 64, s counts as the upper end of that range (`above`); elsewhere (also at
+      // zeros, subnormals, infinities and NaN) each as it is, a zero as 2^-100: its
+      // token still keeps the sum l in range.
+      const uint32_t mine = sm.mine[h][lane] >> (16 * c);
+      const bool special = (sm.special[0] | sm.special[1] | sm.special[2] | sm.special[3]) != 0;
+      float above = 0.f, most = -INFINITY;
+      bool wide = false;
+      if (kFp8) {
+        const uint32_t exps = sm.exps[2 * c] | sm.exps[2 * c + 1];
+        const int high = 31 - __clz(exps);
+        above = (float)(high - 14);
+        wide = (exps & 0x80000001u) || high - (__ffs(exps) - 1) > 5;
+        if (wide) most = wide_max(colS, sm, sc, c, mine, special, pos, f);
+      }
       uint32_t v[2][32];
       ld32(colS, v[0]);
       ld32(colS + 32u, v[1]);
-      const StepMeta& sm = meta[j % kMetas];
-      const Scales& sc = scales[j % kMetas];
-      const uint32_t mine = sm.mine[h][lane] >> (16 * c);
-      const bool special = (sm.special[0] | sm.special[1] | sm.special[2] | sm.special[3]) != 0;
       wait_ld();
       reg_fence(v[0]);
       reg_fence(v[1]);
@@ -826,7 +889,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
         const float top = fmaxf(fmaxf(at(4 * b), at(4 * b + 1)), fmaxf(at(4 * b + 2), at(4 * b + 3)));
         mx4[b & 3] = fmaxf(mx4[b & 3], (mine >> b) & 1u ? top : -INFINITY);
       }
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * f;
+      float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * f;
+      if (kFp8) mx = wide ? most : mx + above;
       // the reference goes up only when the maximum has left it 2^8 behind
       const bool up = mx > m + 8.f;                  // true for the first tokens
       if (__any_sync(0xFFFFFFFFu, up)) {
@@ -852,17 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
           wait_st();
         }
       }
-      // FP8: probabilities times V scales go in as f16.  The reference holds the
-      // binary exponent of the first step's largest V scale too, so that these
-      // products stay below 2^9 there (they overflow only where a V scale is 64
-      // times that one; the row is then computed again).
-      if (kFp8 && jc == 0) {
-        int e = 0;
-        const float most = __uint_as_float(v_most);
-        if (most > 0.f && most < INFINITY) frexpf(most, &e);
-        ve = (float)e;
-      }
-      const float ref = (m == -INFINITY ? 0.f : m) + ve;
+      const float ref = m == -INFINITY ? 0.f : m;
       uint64_t l2 = pair(l, 0.f);
       // ---- probabilities, masked, over S's columns
 #pragma unroll
@@ -902,7 +956,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
       fence_before();
       mbar_arrive(p_full(h, c));
     }
-    m += ve;                                         // l and O are in units of 2^m
     // ---- the row's result
     if (ok && steps > 0) ok = mbar_wait_warp(o_full(h, 1), (uint32_t)(steps - 1) & 1u, err, kKernChunkAttn);
     fence_after();
@@ -928,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
       if (mine) *reinterpret_cast<float2*>(part + kHeadDim) = make_float2(m, l);
     } else {
       const float r = 1.f / l;
-      bool good = l > 0x1p-100f;                     // false for NaN
+      bool good = l > 0x1p-100f && l < 0x1p125f;     // false for NaN
       uint16_t* out = p.out + ((int64_t)x * kQHeads + head) * kHeadDim;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
@@ -1024,7 +1077,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
     if (s < splits) add(s, first[s]);
 #pragma unroll 4
   for (int s = kFirst; s < splits; ++s) add(s, piece(s));
-  const bool fine = l > 0x1p-100f && isfinite(acc.x) && isfinite(acc.y) && isfinite(acc.z) && isfinite(acc.w);
+  const bool fine = l > 0x1p-100f && l < 0x1p125f && isfinite(acc.x) && isfinite(acc.y) && isfinite(acc.z) && isfinite(acc.w);
   if (!__all_sync(0xFFFFFFFFu, fine)) {
     attend_row(p, u, x, head);
     return;
