@@ -184,8 +184,7 @@ class Cache:
         if host_rows is not None:
             d.host_rows = host_rows.data_ptr() if isinstance(host_rows, torch.Tensor) else int(host_rows)
         out = N.Handle()
-        check(self.L.qsa_request_begin(self.h, C.byref(d), self._current(stream) if self.device else None,
-                                       C.byref(out)), "qsa_request_begin")
+        check(self.L.qsa_request_begin(self.h, C.byref(d), self._current(stream), C.byref(out)), "qsa_request_begin")
         if isinstance(host_rows, torch.Tensor):
             self._host[out.index] = host_rows
         return out
@@ -242,8 +241,8 @@ class Cache:
         if host_rows is not None:
             d.host_rows = host_rows.data_ptr() if isinstance(host_rows, torch.Tensor) else int(host_rows)
         out = N.Handle()
-        check(self.L.qsa_request_fork(self.h, parent, C.byref(d), self._current(stream) if self.device else None,
-                                      C.byref(out)), "qsa_request_fork")
+        check(self.L.qsa_request_fork(self.h, parent, C.byref(d), self._current(stream), C.byref(out)),
+              "qsa_request_fork")
         if isinstance(host_rows, torch.Tensor):
             self._host[out.index] = host_rows
         return out
@@ -251,8 +250,7 @@ class Cache:
     def compact(self, stream=None) -> int:
         """Close the gaps of the pool; returns the number of rows moved."""
         moved = C.c_int64()
-        check(self.L.qsa_cache_compact(self.h, self._current(stream) if self.device else None, C.byref(moved)),
-              "qsa_cache_compact")
+        check(self.L.qsa_cache_compact(self.h, self._current(stream), C.byref(moved)), "qsa_cache_compact")
         return moved.value
 
     # ------------------------------------------------------ producer side
@@ -319,10 +317,11 @@ class Cache:
         return _ptr(t)
 
     def _current(self, stream):
-        """The stream given, else the current one of the cache's device."""
-        if stream is None and self.device is not None:
-            return _raw_stream(self.pool.device.index)
-        return _stream(stream)
+        """The stream given, else the current one of the cache's device (a cache
+        without device storage takes none)."""
+        if self.device is None:
+            return None
+        return _raw_stream(self.pool.device.index) if stream is None else _stream(stream)
 
     # ------------------------------------------------ several tokens at once
     # handles: requests; n_tokens: how many of each request's newest tokens.
