@@ -500,8 +500,9 @@ qsa_status_t qsa_append_chunk(qsa_cache* cache, const qsa_chunk* chunk, const fl
  * tokens t = 4b .. 4b+3 with t <= p, for b < ceil((p+1)/4); the other entries
  * of the row are left as they were.
  * q_idx: device [rows][8][64] of query_type.  Products with the keys' codes are
- * exact and sums fp32; a head's 64 elements go in with an error of at most
- * 2^-25 of the largest of them (QSA_QUERY_BF16: none down to 2^-17 of it).
+ * exact and sums fp32; an element goes in with an error of at most 2^-23 of
+ * itself or 2^-39 of the largest of its head's 64, whichever is more
+ * (QSA_QUERY_BF16: none down to 2^-31 of the largest, 2^-39 of it below).
  * w: device fp32 [rows][8];
  * blk_scores: device fp32 [rows][blk_stride], blk_stride >= ceil(ctx/4) of
  * every request.  Scores must be finite.

@@ -10,11 +10,12 @@
 // q^T[64][queries x 8 heads], on the tensor cores (tcgen05, kind::f16, fp32
 // accumulators) with f16 operands.  An e4m3 code is exact in f16, one
 // conversion instruction for two.  A query row (one head) is scaled by a power
-// of two until its largest element is in [1/2, 1); there f16 holds a bf16
-// element exactly down to 2^-17 of the largest and to 2^-25 of it below; an
-// fp32 query goes in as two pieces (the round-to-nearest f16, and that of what
-// is left), which together are off by at most 2^-25 of the row's largest
-// element.  Products are exact and sums are fp32.
+// of two until its largest element is in [2^14, 2^15), the upper end of f16's
+// range; there f16 holds a bf16 element exactly down to 2^-31 of the largest and
+// to 2^-39 of it below; an fp32 query goes in as two pieces (the round-to-nearest
+// f16, and that of what is left: 11 bits each), which together are off by at most
+// 2^-23 of the element, or 2^-39 of the row's largest.  Products are exact and
+// sums are fp32.
 //
 // Tiling.  A group of 64 queries stays in shared memory as the B operand, four
 // tiles of up to 128 columns (16 queries x 8 heads), while the keys stream
@@ -116,13 +117,13 @@ __device__ __forceinline__ uint2 convert4(uint32_t w) {
   return make_uint2((uint32_t)a.x | ((uint32_t)a.y << 16), (uint32_t)b.x | ((uint32_t)b.y << 16));
 }
 
-// relu(x) * 2^-15 of dot products |x| <= 2^15 (64 elements below 1 by codes up
+// relu(x) * 2^-30 of dot products |x| <= 2^30 (64 elements up to 2^15 by codes up
 // to 448), two as a pair: a saturating multiplication, which runs on the
 // multiply-add pipe; the one that takes maxima is half as wide.  Products and
 // multiply-adds of pairs.
 __device__ __forceinline__ uint64_t relu2(uint32_t a, uint32_t b) {
   uint64_t d;
-  asm("{\n .reg .f32 x, y;\n mul.sat.f32 x, %1, 0f38000000;\n mul.sat.f32 y, %2, 0f38000000;\n"
+  asm("{\n .reg .f32 x, y;\n mul.sat.f32 x, %1, 0f30800000;\n mul.sat.f32 y, %2, 0f30800000;\n"
       " mov.b64 %0, {x, y};\n}\n"
       : "=l"(d)
       : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
@@ -224,9 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
     const int tiles = kFew ? 1 : (nq + qt - 1) / qt;
 
     // ---- B and the head weights (all threads; the previous run is complete).
-    // Row r of a tile is head r & 7 of the tile's query r >> 3, scaled by 2^-k
+    // Row r of a tile is head r & 7 of the tile's query r >> 3, scaled by 2^(15-k)
     // (its largest element is in [2^(k-1), 2^k)); its head weight takes the
-    // inverse, and the 2^15 of relu2.  Rows past the group are 0.
+    // inverse, and the 2^30 of relu2.  Rows past the group are 0.
     for (int i = tid; i < tiles * qt * kIndexHeads * (kIndexDim / 8); i += kThreads) {
       const int c = i & 7, r = i >> 3;                         // chunk of 8 places, row over all tiles
       const int q = r >> 3;
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
       int k = 0;
       if (top > 0.f) frexpf(top, &k);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], -k);
+      for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], 15 - k);
       if (c == 0) sw[r] = q < nq ? ldexpf(p.w[(int64_t)x0 * kIndexHeads + r], k + 15) : 0.f;
       const int tile = q / qt, tr = r - tile * qt * kIndexHeads;
       uint8_t* dst = smem + kOffB + tile * kBTile + tr * 128 + ((c ^ (tr & 7)) << 4);

@@ -270,3 +270,57 @@ def test_fp8_rows_lose_f16_roundings_only(ctxs, n_tokens, budget):
         _check(f, n_tokens, q, sel, nsel, out, lse, range(0, len(sel), 5))
     finally:
         f.close()
+
+
+# ----------------------------------------- query elements below the largest
+
+def _keys_without_the_first_dimension(f, r, rng):
+    n = f.ctxs[r]
+    codes = rng.randint(0, 127, (n, 64)).astype(np.uint8) | (rng.randint(0, 2, (n, 64)) << 7).astype(np.uint8)
+    codes[:, 0] = 0
+    f.codes[r] = codes[None]
+    f.c.index_keys[f.hs[r].index, 0, :n] = torch.from_numpy(codes).to(f.dev)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("ctxs,n_tokens", [([700], [3]), ([1300, 70], [70, 5])])
+@pytest.mark.parametrize("top", [1.0, 0.5, 1.99, 1e30, 1e-30])
+def test_index_query_elements_far_below_the_largest(bf16, ctxs, n_tokens, top):
+    """Every head's largest element meets zero codes, so the scores are the
+    others', 2^-1 to 2^-30 of it.  An fp32 element goes in within 2^-23 of
+    itself, or 2^-39 of the largest, a bf16 element exactly down to 2^-31 of the
+    largest (and within 2^-39 of it); 64 products and 8 heads in fp32 add (64 +
+    8 + 4) 2^-24 of the sum of magnitudes."""
+    f = Filled(ctxs, budget=64, seed=2)
+    try:
+        rng = np.random.RandomState(4)
+        for r in range(len(ctxs)):
+            _keys_without_the_first_dimension(f, r, rng)
+        rows = sum(n_tokens)
+        q = rng.randn(rows, 8, 64) * np.exp2(-rng.randint(1, 31, (rows, 8, 1)).astype(np.float64))
+        q[0, :, 1:] = np.exp2(-18) * (1 + 2.0 ** -7)
+        q[1, :, 1:] = 2.0 ** -13 + 2.0 ** -24
+        q[..., 0] = 1
+        q = torch.from_numpy(q * top).float()
+        q = q.bfloat16() if bf16 else q
+        w = torch.rand(rows, 8, generator=torch.Generator().manual_seed(1))
+        stride = (max(ctxs) + 3) // 4
+        blk = torch.zeros(rows, stride, device=f.dev)
+        f.c.chunk_index_score(f.hs, n_tokens, 0, 1, q.to(f.dev), w.to(f.dev), blk)
+        torch.cuda.synchronize()
+        _clean(f.c)
+        got = blk.double().cpu().numpy()
+        for x, (r, pos) in enumerate(f.positions(n_tokens)):
+            if x % 7 > 2:
+                continue
+            codes, sc = f.codes[r][0, :pos + 1], f.scales[r][0, :pos + 1]
+            qd, wd = q[x].double().numpy(), w[x].double().numpy()
+            ref = O.c4_block_scores(O.token_scores(codes, sc, qd, wd))
+            key = np.abs(O.decode_e4m3(codes)) * np.abs(O.decode_fp16(sc))[:, None]
+            off = 76 * 2.0 ** -24 * np.abs(qd) + 2.0 ** -39 * np.abs(qd).max(1)[:, None]
+            if not bf16:
+                off += 2.0 ** -23 * np.abs(qd)
+            tol = O.c4_block_scores((key @ off.T) @ wd)
+            assert np.all(np.abs(got[x, :len(ref)] - ref) <= tol), (x, (np.abs(got[x, :len(ref)] - ref) / tol).max())
+    finally:
+        f.close()
