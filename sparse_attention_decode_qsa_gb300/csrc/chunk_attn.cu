@@ -536,9 +536,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
   if (warp < kSoftWarps) {
     // ---- Q: row head * 32 + query of each half, two panels of 64 dims.  Against
     // FP8 rows it goes in as f16, beside the K codes, which f16 holds exactly: a
-    // row scaled by the power of two that puts its largest element into [1/2, 1),
-    // where f16 holds a bf16 element exactly down to 2^-17 of the largest and to
-    // 2^-25 of it below; the inverse goes to the logits (row_factor).
+    // row scaled by the power of two that puts its largest element into [2^14,
+    // 2^15), the upper end of f16's range, where f16 holds a bf16 element exactly
+    // down to 2^-31 of the largest and to 2^-39 of it below; the inverse goes to
+    // the logits (row_factor).
     constexpr int kBatch = 4;                        // loads in flight
     for (int i0 = tid; i0 < halves * 128 * 16; i0 += kBatch * 32 * kSoftWarps) {      // (whole warps)
       uint4 in[kBatch];
@@ -566,10 +567,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
           if (top > 0.f && top < INFINITY) frexpf(top, &e);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const __half2 o = __floats2half2_rn(ldexpf(bf16_lo(*w[k]), -e), ldexpf(bf16_hi(*w[k]), -e));
+            const __half2 o = __floats2half2_rn(ldexpf(bf16_lo(*w[k]), 15 - e), ldexpf(bf16_hi(*w[k]), 15 - e));
             *w[k] = *reinterpret_cast<const uint32_t*>(&o);
           }
-          if (c == 0) row_factor[h * 128 + r] = ldexpf(1.f, e);
+          if (c == 0) row_factor[h * 128 + r] = ldexpf(1.f, e - 15);
         }
         *reinterpret_cast<uint4*>(smem + (h * 2 + (c >> 3)) * kPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
       }

@@ -324,3 +324,26 @@ def test_index_query_elements_far_below_the_largest(bf16, ctxs, n_tokens, top):
             assert np.all(np.abs(got[x, :len(ref)] - ref) <= tol), (x, (np.abs(got[x, :len(ref)] - ref) / tol).max())
     finally:
         f.close()
+
+
+def test_query_elements_far_below_the_largest_beside_fp8_rows():
+    """The largest element of every query meets K codes of 0; the others, 2^-20
+    of it, meet keys 2^20 times as large."""
+    f = Filled([900], fp8=True, budget=512, seed=3)
+    try:
+        rng = np.random.RandomState(4)
+        raw = f.kv[0][0]
+        raw[:, 0:512:128] = 0
+        ks = raw[:, 1024:1032].clone().view(torch.float16).float() * 2.0 ** 20
+        raw[:, 1024:1032] = ks.half().view(torch.uint8)
+        assert bool(ks.isfinite().all()) and ks.max() < 65504
+        _store(f, 0)
+        q = _queries(40, 5, "cpu").float() * 2.0 ** -20
+        q[..., 0] = 1
+        q = q.bfloat16().to(f.dev)
+        sel = [np.sort(rng.choice(860 // 4, 100, replace=False)) for _ in range(40)]
+        out, lse = _run_attention(f, [40], q, *_table(sel, 512), 512)
+        _clean(f.c)
+        _check(f, [40], q, sel, [100] * 40, out, lse)
+    finally:
+        f.close()
