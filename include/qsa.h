@@ -531,7 +531,8 @@ int64_t qsa_chunk_attn_workspace_bytes(qsa_cache* cache, const qsa_chunk* chunk,
  * attends over the tokens t <= p of its selected blocks (distinct block ids,
  * in any order; a block past p/4 is skipped and reported as BAD_BLOCK).  Rows
  * are read through the slot table (pool rows from HBM, cold rows from the host
- * history); no planned miss of qsa_hot_cache_plan may be pending.
+ * history).  A pending plan of qsa_hot_cache_plan is completed first: the call
+ * copies its misses' rows, as the attention after the plan would have.
  * q: device bf16 bits [rows][16][128]; sel_blocks, n_sel: as written by
  * qsa_chunk_select_topk; out: device bf16 bits [rows][16][128], rounded once
  * from the fp32 sums; lse: device fp32 [rows][16] or NULL (-inf, and out = 0,

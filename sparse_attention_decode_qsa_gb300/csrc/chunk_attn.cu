@@ -329,7 +329,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) chunk_plan_kernel(const __gri
     at += (int)__shfl_sync(0xFFFFFFFFu, v, 31);
     __syncthreads();
   }
-  if (tid == 0) p.count[tile] = at;
+  if (tid == 0) {
+    p.count[tile] = at;
+    // the unit's planned misses are in their hot rows (launch_hot_complete)
+    if (p.c.b.u[u].hot_base >= 0) p.c.b.hot_pend_on[p.c.b.unit_state(u)] = 0;
+  }
 }
 static_assert(kPlanWarps == 32, "one lane per warp in the scan");
 
@@ -1188,6 +1192,8 @@ cudaError_t launch_chunk_attn(const ChunkDesc& c, const uint16_t* q, const int32
   p.block = reinterpret_cast<int32_t*>(ws + a.off_block);
   p.mask = reinterpret_cast<uint32_t*>(ws + a.off_mask);
   p.part = reinterpret_cast<float*>(ws + a.off_part);
+  e = launch_hot_complete(c.b, s);
+  if (e != cudaSuccess) return e;
   const int window = (int)(a.nb < kPlanWindow ? (a.nb + 3) / 4 * 4 : kPlanWindow);
   e = launch_kernel(chunk_plan_kernel, dim3((unsigned)a.tiles), dim3(kPlanThreads), (size_t)window * 8, s, 0, dim3(1),
                     p, window);

@@ -24,7 +24,9 @@
 // qsa_hot_cache_plan runs the plan alone and also writes, per selected
 // position, the row its miss goes to: the next attention of the unit reads
 // those rows from host memory (once, as a zero-copy read would) and writes
-// them into their hot rows, so a miss costs no separate copy pass.
+// them into their hot rows, so a miss costs no separate copy pass.  Calls that
+// read the unit's rows before that attention (chunk attention, fork) have
+//   hot_complete_kernel  make the copies first.
 #include "qsa_internal.cuh"
 
 namespace qsa {
@@ -274,7 +276,48 @@ __global__ void __launch_bounds__(kFillThreads) hot_fill_kernel(const HotParams 
   }
 }
 
+// The copies that a plan has left to an attention: per row of the pending map the
+// host row of the token that owns it, one warp per row.  (Entries past the plan's
+// selection are older ones: their rows' owners are copied again, which changes
+// nothing.)
+template <int kChunksPerRow>
+__global__ void __launch_bounds__(kFillThreads) hot_complete_kernel(const __grid_constant__ BatchDesc b) {
+  grid_dependency_wait();
+  const int u = blockIdx.y, lane = threadIdx.x & 31;
+  const int64_t hb = b.u[u].hot_base, st = b.unit_state(u);
+  const uint8_t* host = b.u[u].host_rows;
+  if (hb < 0 || !host || !b.hot_pend_on[st]) return;
+  constexpr int kWarps = kFillThreads / 32;
+  for (int r = blockIdx.x * kWarps + (threadIdx.x >> 5); r < b.hot_fill_stride; r += gridDim.x * kWarps) {
+    const int64_t row = b.hot_pend[st * b.hot_fill_stride + r], v = row - hb;
+    if (v < 0 || v >= b.hot_rows) continue;
+    const int32_t t = b.hot_owner[st * b.hot_rows + v];
+    if (t < 0 || t >= b.u[u].n) continue;
+    const uint8_t* src = host + (int64_t)t * (kChunksPerRow * 16);
+    uint8_t* dst = b.pool + row * (kChunksPerRow * 16);
+    constexpr int kPer = (kChunksPerRow + 31) / 32;
+    uint4 x[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (lane + 32 * k < kChunksPerRow) x[k] = ld_nc_v4(src + (lane + 32 * k) * 16);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (lane + 32 * k < kChunksPerRow) *reinterpret_cast<uint4*>(dst + (lane + 32 * k) * 16) = x[k];
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_hot_complete(const BatchDesc& b, cudaStream_t s) {
+  bool any = false;
+  for (int u = 0; u < b.n_units; ++u) any = any || b.u[u].hot_base >= 0;
+  if (!any) return cudaSuccess;
+  // 32 CTAs of 8 warps per unit: where no plan is pending they only look (1 us)
+  const dim3 grid(32, b.n_units);
+  return launch_kernel(b.row_bytes == kRowBytesFp8 ? hot_complete_kernel<kRowBytesFp8 / 16>
+                                                   : hot_complete_kernel<kRowBytes / 16>,
+                       grid, dim3(kFillThreads), 0, s, 0, dim3(1), b);
+}
 
 cudaError_t launch_hot_fetch(const BatchDesc& b, const int32_t* sel_blocks, const int32_t* n_sel,
                              int32_t budget_tokens, bool copy_rows, cudaStream_t s) {

@@ -343,6 +343,10 @@ cudaError_t launch_append_token(const BatchDesc& b, const AppendTargets& tg, con
 cudaError_t launch_hot_fetch(const BatchDesc& b, const int32_t* sel_blocks, const int32_t* n_sel,
                              int32_t budget_tokens, bool copy_rows, cudaStream_t s);
 
+// Copy the planned misses of the units whose plan is pending into their hot rows.
+// The caller clears hot_pend_on behind it.
+cudaError_t launch_hot_complete(const BatchDesc& b, cudaStream_t s);
+
 // Chunk forms: as the launchers above for every row of a chunk.  row_base: the
 // first pool row of each unit's region at its layer (-1: none), ring: its ring
 // length (0: a resident region, token t in region row t).
