@@ -449,8 +449,9 @@ qsa_status_t qsa_hot_cache_fetch(qsa_cache* cache, const qsa_batch* batch,
  * zero-copy read would, and writes them into their hot rows as it goes;
  * afterwards the units are in the state qsa_hot_cache_fetch leaves.  Until that attention has run, the misses'
  * hot rows hold stale bytes: no other call may read those units' rows
- * (qsa_gather_rows, attention with `gathered`), and the pending map is
- * replaced by the next plan or fetch of the unit.
+ * (qsa_gather_rows, attention with `gathered`) but qsa_chunk_sparse_attn and
+ * qsa_request_fork, which make the copies first; the pending map is replaced by
+ * the next plan or fetch of the unit.
  * [RTX4090 port, memory-ledger section: missing blocks moved back on
  * demand; here the move rides on the attention's own read.]
  * Errors: as qsa_hot_cache_fetch. */
@@ -568,8 +569,9 @@ qsa_status_t qsa_request_truncate(qsa_cache* cache, qsa_handle request, int64_t 
  * parent's slot tables and stored where the child's placement keeps them
  * (region rows; host history; host history and tail ring).  Nothing is shared
  * afterwards.  desc->host_rows must not overlap the parent's host history.
- * The child's hot rows start free.  No planned miss of the parent
- * (qsa_hot_cache_plan) may be pending.
+ * The child's hot rows start free.  Pending plans of the parent
+ * (qsa_hot_cache_plan) are completed first: their misses' rows are copied, as
+ * the attention after the plan would have.
  * Errors: as qsa_request_begin, INVALID_ARG, STALE_HANDLE (parent); nothing is
  * leased on error.  A bad slot of the parent goes to the device error word
  * (BAD_SLOT), and its row is not copied. */

@@ -316,6 +316,20 @@ qsa_status_t check_stride(const ChunkDesc& d, int64_t blk_stride) {
   return QSA_OK;
 }
 
+// Copy the planned misses of a request, all layers, into its hot rows and clear
+// its plans.
+cudaError_t complete_plans(const qsa_cache* c, qsa_handle h, cudaStream_t s) {
+  BatchDesc d;
+  for (int32_t l0 = 0; l0 < c->cfg.n_layers; l0 += kMaxUnits) {
+    const int32_t n = c->cfg.n_layers - l0 < kMaxUnits ? c->cfg.n_layers - l0 : kMaxUnits;
+    const qsa_batch b = {1, l0, n, 0, &h};
+    if (c->build_batch(&b, &d) != QSA_OK) return cudaErrorInvalidValue;
+    if (const cudaError_t e = launch_hot_complete(d, s)) return e;
+  }
+  return cudaMemsetAsync(d.hot_pend_on + (int64_t)h.index * c->cfg.n_layers, 0,
+                         (size_t)c->cfg.n_layers * sizeof(int32_t), s);
+}
+
 // Change every slot (and pending row) of every live request that names a
 // moved row.  Moves are ascending and go down, so a row's new place is never
 // inside the old place of a later move: they can be applied in pieces.
@@ -970,6 +984,7 @@ qsa_status_t qsa_request_fork(qsa_cache* c, qsa_handle parent, const qsa_request
     p.dst_ring = l.placement == QSA_KV_HOST_RING;
     p.err = c->err();
     cudaError_t e = guard.status();
+    if (e == cudaSuccess && pl->hot_base >= 0) e = complete_plans(c, parent, static_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) e = launch_fork(p, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) {
       qsa_request_end(c, child);

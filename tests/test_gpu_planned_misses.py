@@ -1,4 +1,4 @@
-"""Chunk attention between a hot-cache plan and the attention that
+"""Chunk attention and fork between a hot-cache plan and the attention that
 fills its rows: the slots of the planned misses already name rows that hold
 other tokens' bytes."""
 import numpy as np
@@ -6,8 +6,10 @@ import pytest
 import torch
 
 import sparse_attention_decode_qsa_gb300 as Q
+from sparse_attention_decode_qsa_gb300 import workloads
 from tests import qsa_check as QC
 from tests.test_gpu_chunk import SCALE, Filled, _attend, _check_attention, _clean, _queries, _run_attention
+from tests.test_gpu_pages import _read
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +79,29 @@ def test_chunk_attention_reads_planned_misses_from_the_host(fp8, place):
     finally:
         torch.cuda.synchronize()
         f.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("child", [Q.KV_HBM, Q.KV_HOST])
+def test_fork_copies_planned_misses_from_the_host(fp8, child):
+    L, n = 2, 700
+    f = Filled([n], [Q.KV_HOST_RING], layers=L, ring=16, hot_rows=128, budget=128, fp8=fp8, seed=9, spare=3 * L * (n + 128))
+    host = workloads.alloc_host((L, n, f.c.row_bytes), f.dev, "vmm") if child != Q.KV_HBM else None
+    try:
+        c = f.c
+        sel, k = _planned(f, 1)
+        for filled in (False, True):
+            if filled:
+                _decode(f, 1, sel, k)
+            h = c.request_fork(f.hs[0], n - 30, child, host_rows=host, max_ctx=n)
+            torch.cuda.synchronize()
+            _clean(c)
+            for l in range(L):
+                assert torch.equal(_read(c, h, l, n - 30, host), f.kv[0][l][:n - 30]), (filled, l)
+            c.request_end(h)
+        assert torch.equal(_read(c, f.hs[0], 1, n, f.host[0]), f.kv[0][1])
+    finally:
+        torch.cuda.synchronize()
+        f.close()
+        if host is not None:
+            workloads.free_host(host)
