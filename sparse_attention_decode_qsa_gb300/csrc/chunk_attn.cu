@@ -110,8 +110,8 @@ constexpr int kMetas = 4;
 constexpr int kOffScales = kOffMeta + kMetas * (int)sizeof(StepMeta);
 constexpr int kOffBar = kOffScales + kMetas * (int)sizeof(Scales);
 // k_full[2], k_empty[2], v_full[2], v_empty[2], then per (half, 64 tokens)
-// s_full[4], p_full[4], o_full[4], q_full
-constexpr int kNumBars = 4 * kStages + 13;
+// s_full[4], p_full[4], o_full[4], then q_full, done[2]
+constexpr int kNumBars = 4 * kStages + 15;
 constexpr int kOffSlot = (kOffBar + 8 * kNumBars + 15) / 16 * 16;
 constexpr int kSmemBytes = kOffSlot + 16 + 1024;
 static_assert(kSmemBytes <= 227 * 1024 && sizeof(StepMeta) % 16 == 0, "one CTA's shared memory");
@@ -494,6 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
   auto p_full = [&](int h, int c) { return bars + 8u * (uint32_t)(4 * kStages + 4 + 2 * h + c); };
   auto o_full = [&](int h, int c) { return bars + 8u * (uint32_t)(4 * kStages + 8 + 2 * h + c); };
   const uint32_t q_full = bars + 8u * (uint32_t)(4 * kStages + 12);
+  auto done = [&](int h) { return bars + 8u * (uint32_t)(4 * kStages + 13 + h); };
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kOffSlot);
   __shared__ float row_factor[kFp8 ? 256 : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -528,6 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
         mbar_init(o_full(i >> 1, i & 1), 1);
       }
       mbar_init(q_full, 32 * kSoftWarps);
+      mbar_init(done(0), 1);
+      mbar_init(done(1), 1);
       mbar_fence_init();
     }
   }
@@ -812,7 +815,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
       }
     }
     // every product is complete before tensor memory is given back
-    if (ok && steps > 0) mbar_wait_warp(o_full(h, 1), (uint32_t)(steps - 1) & 1u, err, kKernChunkAttn);
+    if (elect_one()) commit(done(h));
+    __syncwarp();
+    mbar_wait_warp(done(h), 0, err, kKernChunkAttn);
   } else if (warp / 4 < halves) {
     // ---- softmax: thread = row (head warp & 3, query lane) of half h
     const int h = warp >> 2, head = g * kGroup + (warp & 3), q = 32 * h + lane;

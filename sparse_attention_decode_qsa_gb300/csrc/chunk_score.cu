@@ -163,12 +163,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
   auto d_empty = [&](int i) { return bars + 8u * (uint32_t)(2 * kStages + kAccs + i); };
   const uint32_t done = bars + 8u * (uint32_t)(2 * kStages + 2 * kAccs);
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kOffSlot);
-  __shared__ int s_fail;
+  __shared__ int s_fail, s_leader;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   ErrorWord* err = p.c.b.err;
 
   if (warp == kRoleMma) {
     tmem_alloc<kTmemCols>(slot);
+    if (elect_one()) s_leader = lane;          // the lane that issues MMAs
     if (lane == 0) {
       for (int i = 0; i < kStages; ++i) { mbar_init(a_full(i), 32 * kConvWarps); mbar_init(a_empty(i), 1); }
       for (int i = 0; i < kAccs; ++i) { mbar_init(d_full(i), 1); mbar_init(d_empty(i), 32 * kEpiWarps); }
@@ -440,7 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
   }
 
   if (warp == kRoleMma) {
-    if (lane == 0) {
+    // (chosen by s_leader, not by elect_one(): with that here the prompt case takes
+    // 383 us in place of 345, its main loop is compiled differently)
+    if (lane == s_leader) {
       commit(done);                 // every MMA issued above is complete once this arrives
       mbar_wait(done, 0, err, kKernChunkScore);
     }
