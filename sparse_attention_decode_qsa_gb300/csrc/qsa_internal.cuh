@@ -54,7 +54,6 @@ enum KernelId : int32_t {
   kKernHot = 8,
   kKernChunkAppend = 9,
   kKernChunkScore = 10,
-  kKernChunkTopk = 11,
   kKernChunkAttn = 12,
   kKernFork = 13,
 };
