@@ -145,12 +145,14 @@ cudaError_t launch_move_rows(uint8_t* pool, int64_t row_bytes, int64_t from, int
                              cudaStream_t s) {
   const int64_t per = row_bytes / 16;
   const int64_t chains = (from - to < rows ? from - to : rows) * per;
-  // chains side by side once they fill the device eight deep (eight CTAs on
-  // each of 152 SMs): 3 x 196608 BF16 rows, each down by as many, 581 -> 379 us
-  const bool wide = chains >= (int64_t)152 * 8 * kThreads * kDepth;
+  int sms = 0;
+  if (const cudaError_t e = current_sm_count(&sms)) return e;
+  // chains side by side once they fill the device eight deep (eight CTAs per SM):
+  // 3 x 196608 BF16 rows, each down by as many, 581 -> 379 us
+  const bool wide = chains >= (int64_t)sms * 8 * kThreads * kDepth;
   const int64_t block = wide ? (int64_t)kThreads * kDepth : kThreads;
   int64_t blocks = (chains + block - 1) / block;
-  if (blocks > 152 * 8) blocks = 152 * 8;
+  if (blocks > sms * 8) blocks = sms * 8;
   return launch_kernel(wide ? move_rows_kernel<false> : move_rows_kernel<true>, dim3((unsigned)blocks), dim3(kThreads), 0,
                        s, 0, dim3(1), reinterpret_cast<uint4*>(pool), from * per, to * per, rows * per);
 }
