@@ -227,8 +227,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
 
     // ---- B and the head weights (all threads; the previous run is complete).
     // Row r of a tile is head r & 7 of the tile's query r >> 3, scaled by 2^(15-k)
-    // (its largest element is in [2^(k-1), 2^k)); its head weight takes the
-    // inverse, and the 2^30 of relu2.  Rows past the group are 0.
+    // (its largest element is in [2^(k-1), 2^k)); its head weight takes 2^k, the
+    // key's scale the rest: 2^30 of relu2 over 2^15.  So a weighted dot product
+    // overflows where the score's own terms do.  Rows past the group are 0.
     for (int i = tid; i < tiles * qt * kIndexHeads * (kIndexDim / 8); i += kThreads) {
       const int c = i & 7, r = i >> 3;                         // chunk of 8 places, row over all tiles
       const int q = r >> 3;
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
       if (top > 0.f) frexpf(top, &k);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], 15 - k);
-      if (c == 0) sw[r] = q < nq ? ldexpf(p.w[(int64_t)x0 * kIndexHeads + r], k + 15) : 0.f;
+      if (c == 0) sw[r] = q < nq ? ldexpf(p.w[(int64_t)x0 * kIndexHeads + r], k) : 0.f;
       const int tile = q / qt, tr = r - tile * qt * kIndexHeads;
       uint8_t* dst = smem + kOffB + tile * kBTile + tr * 128 + ((c ^ (tr & 7)) << 4);
 #pragma unroll
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_c
         const int64_t t0 = 4 * (b0 + row);                     // the block's first token
         float mag[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mag[k] = fabsf(__half2float(__ushort_as_half(next[k])));
+        for (int k = 0; k < 4; ++k) mag[k] = fabsf(__half2float(__ushort_as_half(next[k]))) * 0x1p15f;
         if (s + 1 < steps) load_scales(s0 + s + 1);
         // every token of the step within every query's context?
         const bool whole = (s0 + s + 1) * kStepTokens - 1 <= pos0;

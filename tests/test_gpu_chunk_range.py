@@ -347,3 +347,30 @@ def test_query_elements_far_below_the_largest_beside_fp8_rows():
         _check(f, [40], q, sel, [100] * 40, out, lse)
     finally:
         f.close()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("tokens", [3, 70])
+@pytest.mark.parametrize("size", [1e34, 1e35, 1e-34])
+def test_index_queries_near_the_ends_of_fp32(bf16, tokens, size):
+    """Scores that fp32 holds: up to about 1e37, or down to 1e-34."""
+    f = Filled([700], budget=64, seed=2)
+    try:
+        q = size * torch.randn(tokens, 8, 64, generator=torch.Generator().manual_seed(3))
+        q = q.bfloat16() if bf16 else q
+        w = torch.rand(tokens, 8, generator=torch.Generator().manual_seed(1)) + 0.5
+        blk = torch.zeros(tokens, 175, device=f.dev)
+        f.c.chunk_index_score(f.hs, [tokens], 0, 1, q.to(f.dev), w.to(f.dev), blk)
+        torch.cuda.synchronize()
+        _clean(f.c)
+        got = blk.double().cpu().numpy()
+        for x, (r, pos) in enumerate(f.positions([tokens])):
+            codes, sc = f.codes[0][0, :pos + 1], f.scales[0][0, :pos + 1]
+            qd, wd = q[x].double().numpy(), w[x].double().numpy()
+            ref = O.c4_block_scores(O.token_scores(codes, sc, qd, wd))
+            assert np.abs(ref).max() < 1e38
+            key = np.abs(O.decode_e4m3(codes)) * np.abs(O.decode_fp16(sc))[:, None]
+            mag = O.c4_block_scores((key @ np.abs(qd).T) @ wd)
+            assert np.all(np.abs(got[x, :len(ref)] - ref) <= QC.SCORE_REL_TOL * mag), x
+    finally:
+        f.close()
