@@ -225,7 +225,10 @@ typedef struct qsa_batch {
  * to its own.  Per-row arrays hold layer after layer, request after request:
  * with N = sum of n_tokens, row = i_layer * N + (n_tokens[0] + .. +
  * n_tokens[i-1]) + j.  At most QSA_MAX_CHUNK_ROWS rows and QSA_MAX_UNITS
- * (request, layer) pairs in one call; a call with no rows does nothing. */
+ * (request, layer) pairs in one call; a call with no rows does nothing.  Lengths,
+ * positions and pool rows are read from the requests when the call is made: a
+ * captured call keeps those of its capture, and is captured again once a request
+ * of it has grown, shrunk or moved. */
 typedef struct qsa_chunk {
   int32_t n_req;
   int32_t layer0;
@@ -543,7 +546,8 @@ int64_t qsa_chunk_attn_workspace_bytes(qsa_cache* cache, const qsa_chunk* chunk,
  * more.  A key or value that is not finite reaches only the queries that select
  * its token.
  * workspace: device, 16-byte aligned, qsa_chunk_attn_workspace_bytes bytes,
- * used by one call at a time: calls that may overlap need one each.
+ * used by one call at a time: calls that may overlap need one each.  out, lse
+ * and the workspace overlap no input and not each other.
  * Errors: INVALID_ARG, STALE_HANDLE, NO_DEVICE, CUDA; bad blocks, counts and
  * slots go to the device error word (BAD_BLOCK, BAD_SLOT). */
 qsa_status_t qsa_chunk_sparse_attn(qsa_cache* cache, const qsa_chunk* chunk, const uint16_t* q,

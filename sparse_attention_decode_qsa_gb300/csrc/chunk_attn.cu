@@ -43,12 +43,12 @@
 // select it.
 //
 // Measured: 2048 BF16 queries, 2048 of 32768 tokens each (34 GFLOP of selected
-// pairs; the unions, 2600 blocks here, make 175 of it), 171 us (plan 11, split
-// 163): 0.52 of the measured bf16 rate on 128 of 152 SMs, bound by the softmax
+// pairs; the unions, 2600 blocks here, make 175 of it), 167 us (plan 11, split
+// 159): 0.54 of the measured bf16 rate on 128 of 152 SMs, bound by the softmax
 // warps' instructions and by the hand-overs between them and the tensor core (the
-// schedulers issue in 0.62 of the cycles).  The same with FP8 rows 276 us: the
+// schedulers issue in 0.60 of the cycles).  The same with FP8 rows 272 us: the
 // loaders' conversions and the products with both scales are added instructions.
-// 14 FP8 draft queries of 8 requests (30 MB of rows at most) 32 us (plan 8, split
+// 14 FP8 draft queries of 8 requests (30 MB of rows at most) 33 us (plan 8, split
 // 27, join 4 each alone): five steps per CTA, each the latency of rows, conversion
 // and softmax one after the other.  Not faster: K and V split over the loader warps (310 us at
 // 2048 FP8 queries), the next step's codes loaded into the registers just stored
@@ -186,7 +186,9 @@ __device__ __forceinline__ float4 row_values(const uint8_t* row, int hv, int lan
 
 // One warp, one query row x and head h: online softmax over the row's own
 // selected tokens.  (Bad blocks and slots have been reported by the plan and
-// the loaders.)
+// the loaders.)  Slow, for values that are not finite only: where one V scale in
+// 4096 is infinite, so that nearly every row comes here, 2048 FP8 queries take 47
+// ms and 14 draft queries 1.4.
 __device__ __noinline__ void attend_row(const ChunkAttnParams& p, int u, int x, int h) {
   const int lane = threadIdx.x & 31, g = h / kGroup;
   const bool fp8 = p.c.b.row_bytes == kRowBytesFp8;

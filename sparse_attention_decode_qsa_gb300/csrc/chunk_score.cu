@@ -33,11 +33,14 @@
 // equal runs, one per CTA; a run that crosses into another group rebuilds B.
 //
 // Measured: 2048 bf16 queries at the end of 131072 tokens (277 GFLOP) 345 us,
-// 0.80 PFLOP/s, 0.41 of the measured bf16 rate; 10 fp32 draft queries of 4 requests of
+// 0.80 PFLOP/s, 0.41 of the measured bf16 rate; 2048 fp32 queries 417 us; 10 fp32 draft queries of 4 requests of
 // 65536 tokens 14 us.  What bounds it is the epilogue's instructions: 8
 // saturating products and 4 paired multiply-adds per query and lane against 128
 // tensor-core cycles per tile; the schedulers issue in 0.66 of the cycles, and
-// the loop without its arithmetic takes 207 us.  Not faster: 128 queries to a
+// the loop without its arithmetic takes 207 us.  The shared-memory port is the next
+// limit, busy in 0.7 of the cycles: of a phase's 3500, 1024 for the operands of the
+// products and 1340 for the head weights, which every epilogue warp reads in each
+// of the four phases (40 M load wavefronts).  Not faster: 128 queries to a
 // group (413, registers spill), two sets of 8 warps with two accumulators each
 // (357), products per element in place of pairs or maxima in place of saturation
 // (359 to 392), an arrival per warp in place of per thread, an earlier release of
@@ -145,7 +148,9 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // the missing tiles convert too (the kernel alone, with cold caches: 14 bf16
 // queries over 8 x 32768 tokens 20.2 -> 16.4 us, 10 fp32 queries over 4 x 65536
 // 20.1 -> 16.9, with half of the teams 20).  Run-time choices in one kernel cost
-// the full groups 10 %.  Both pieces of fp32 queries side by side in one product,
+// the full groups 10 %.  One request with five queries takes the call to the
+// general form: 8 requests of 32768 tokens with 1, 4, 5, 8, 16, 32 bf16 queries each
+// 14.1, 13.6, 17.5, 17.8, 24.0, 27.6 us in a loop.  Both pieces of fp32 queries side by side in one product,
 // added in the epilogue, are slower (21.3).
 template <bool kBf16, bool kFew>
 __global__ void __launch_bounds__(kThreads, 1) chunk_score_kernel(const __grid_constant__ ChunkScoreParams p) {

@@ -20,7 +20,10 @@
 // Where the pivot catches fewer than K or more than kCand keys (long runs of
 // equal scores), or the row is longer than the bitmaps (kWindow blocks), the
 // general path does the radix select on the row itself and walks it, window by
-// window, with two bitmaps (above T, equal to T).
+// window, with two bitmaps (above T, equal to T).  Budgets from 8192 tokens on
+// (K = kCand / 2) take it always.  2048 rows of 32768 blocks: 356 us at a budget of
+// 8192, 382 with all scores equal, 169 with scores rounded to halves, where some
+// rows take it; 14 rows 64 to 75 us.
 #include "qsa_internal.cuh"
 
 namespace qsa {
