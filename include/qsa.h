@@ -543,7 +543,8 @@ int64_t qsa_chunk_attn_workspace_bytes(qsa_cache* cache, const qsa_chunk* chunk,
  * for a row with no tokens).  Each term p_t V_t of the output's sum is off by at
  * most 2^-8 of itself beside BF16 rows; beside FP8 rows by 2^-11 of itself or by
  * 2^-19 of the row's largest p_s * (V scale of s) times the code, whichever is
- * more.  A key or value that is not finite reaches only the queries that select
+ * more (or by 2^-117 times the code, where tokens with V scale 0 outweigh all
+ * others).  A key or value that is not finite reaches only the queries that select
  * its token.
  * workspace: device, 16-byte aligned, qsa_chunk_attn_workspace_bytes bytes,
  * used by one call at a time: calls that may overlap need one each.  out, lse

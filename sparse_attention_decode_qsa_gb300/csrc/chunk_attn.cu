@@ -844,7 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_split_kernel(const __grid_c
       // log2 of both, x + log2 s.  Where the 64 tokens' scales lie within a factor
       // of 64, s counts as the upper end of that range (`above`); elsewhere (also at
       // zeros, subnormals, infinities and NaN) each as it is, a zero as 2^-100: its
-      // token still keeps the sum l in range.
+      // token still keeps the sum l in range (and where such tokens outweigh all
+      // others, f16's 2^-25 is 2^-117 of the row's weight).
       const uint32_t mine = sm.mine[h][lane] >> (16 * c);
       const bool special = (sm.special[0] | sm.special[1] | sm.special[2] | sm.special[3]) != 0;
       float above = 0.f, most = -INFINITY;

@@ -6,7 +6,9 @@ Tolerances of the attention, per element and in units of mag = sum p|v|.  The
 output is rounded to bf16 (2^-8 of it).  Probabilities go to the tensor cores
 as bf16 beside BF16 rows (2^-8 of each term); beside FP8 rows p times the V
 scale goes in as f16, off by 2^-11 of itself or by 2^-25 in units in which the
-row's largest product is 2^-6 at least, so by 2^-19 of that one.  128 products
+row's largest product is 2^-6 at least, so by 2^-19 of that one; where tokens
+with a V scale of 0 outweigh all others, the unit is 2^100 below their weight, to
+2^8, so that it is off by 2^-117 of the row's whole weight.  128 products
 in fp32 leave a logit off by 2^-17 of scale * sum |q_d k_d|, a probability by
 twice that (its own and the sum's), and fp32 sums add less than 1e-4."""
 import numpy as np
@@ -34,7 +36,8 @@ def _v_scales(f, r, toks):
 
 
 def _floor(q_bits, K, V, vs):
-    """2^-19 of the largest p |scale| of a row, times the sum of its codes."""
+    """2^-19 of the largest p |scale| of a row, or 2^-117, times the sum of its
+    codes."""
     q = O.decode_bf16(q_bits).reshape(16, 128)
     out = np.zeros((16, 128))
     for h in range(16):
@@ -42,7 +45,7 @@ def _floor(q_bits, K, V, vs):
         p = np.exp(x - x.max())
         s = np.abs(vs[:, h // 4])
         codes = np.abs(V[:, h // 4]) / np.where(s > 0, s, 1)[:, None]
-        out[h] = 2.0 ** -19 * (p * s).max() / p.sum() * codes.sum(0)
+        out[h] = max(2.0 ** -19 * (p * s).max() / p.sum(), 2.0 ** -117) * codes.sum(0)
     return out
 
 
@@ -208,7 +211,7 @@ def test_v_scales_of_every_size(ctxs, n_tokens, signed):
 
 
 @pytest.mark.parametrize("ctxs,n_tokens", LAYOUTS)
-@pytest.mark.parametrize("logit", [0.0, 30.0, 55.0])
+@pytest.mark.parametrize("logit", [0.0, 30.0, 55.0, 90.0])
 def test_small_values_behind_tokens_without_any(ctxs, n_tokens, logit):
     """The first 40 blocks' V rows are zero, with scale 0, their logits
     `logit` nats above the others'; the rest have scales of 2^-20."""
