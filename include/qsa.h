@@ -26,6 +26,11 @@
  * qsa_chunk_sparse_attn run the same steps for every token of a chunk, each
  * with its own causal context and its own selection; qsa_request_truncate
  * takes back tokens (rejected drafts).
+ * Attention without a selection, over the same caches: qsa_window_attn (the
+ * newest tokens and the context's first ones), qsa_shared_attn (a prefix that a
+ * batch has in common, read once for all, and each request's own tokens).
+ * qsa_window_weights adds up the weight that such attention gives each cached
+ * token, and qsa_request_evict drops the tokens with the least of it.
  * Pages of the cache: qsa_request_fork starts a request with the first tokens
  * of another one, qsa_cache_compact closes the gaps of the pool.
  *
@@ -557,10 +562,108 @@ qsa_status_t qsa_chunk_sparse_attn(qsa_cache* cache, const qsa_chunk* chunk, con
                                    float* lse, void* workspace, int64_t workspace_bytes,
                                    void* stream);
 
+/* ----------------------------------------------- attention without a selection */
+
+/* Attention of every query of a chunk over a window of the newest tokens and the
+ * context's first ones, which stay visible (sinks): row x at position p, head h,
+ * KV head g = h/4, attends over the tokens t <= p with t < sinks or
+ * t > p - window; out[x][h] = sum_t softmax(logits)_t V_t[g], logits_t =
+ * softmax_scale * q[x][h] . K_t[g], lse[x][h] = log sum_t exp(logits_t).
+ * sinks, window >= 0; a window of the context's length or more is causal
+ * attention over all of it; a row that sees no token (sinks = window = 0, or only
+ * tokens with bad slots) gets out = 0 and lse = -inf.  n_tokens of 1 is the decode
+ * step.  Rows are read through the slot table (pool rows from HBM, cold rows from
+ * the host history); a pending plan of qsa_hot_cache_plan is completed first.
+ * q: device bf16 bits [rows][16][128]; out: device bf16 bits [rows][16][128],
+ * rounded once from fp32 sums; lse: device fp32 [rows][16] or NULL.  Each term
+ * p_t V_t of the output's sum is off by as much as qsa_chunk_sparse_attn's.  A key
+ * or value that is not finite reaches only the queries that see its token.
+ * workspace: device, 16-byte aligned, qsa_window_attn_workspace_bytes bytes, used
+ * by one call at a time.  out, lse and the workspace overlap no input and not each
+ * other.
+ * Errors: INVALID_ARG, STALE_HANDLE, NO_DEVICE, CUDA; bad slots go to the device
+ * error word (BAD_SLOT). */
+qsa_status_t qsa_window_attn(qsa_cache* cache, const qsa_chunk* chunk, const uint16_t* q,
+                             int32_t sinks, int32_t window, float softmax_scale, uint16_t* out,
+                             float* lse, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace qsa_window_attn needs for this chunk (its requests' present
+ * lengths), or -1 (qsa_last_error_string() tells).  Ask again when any of them
+ * changes. */
+int64_t qsa_window_attn_workspace_bytes(qsa_cache* cache, const qsa_chunk* chunk, int32_t sinks,
+                                        int32_t window);
+
+/* Attention of a batch that shares a prefix: row x at position p of its request r
+ * attends over the tokens 0 .. prefix_len-1 of request `prefix` (0 <= prefix_len <=
+ * its ctx_len) and over the tokens own_first .. p of r (none where own_first > p).
+ * The prefix's rows are read once per 64 rows of a layer, whichever requests these
+ * belong to.  The requests may hold copies of the prefix (qsa_request_fork;
+ * own_first = prefix_len then), or only their own tokens (own_first = 0);
+ * `prefix` may be one of the chunk's requests, and every row sees all of its
+ * prefix_len tokens.  Everything else as for qsa_window_attn. */
+qsa_status_t qsa_shared_attn(qsa_cache* cache, const qsa_chunk* chunk, qsa_handle prefix,
+                             int32_t prefix_len, int32_t own_first, const uint16_t* q,
+                             float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+
+int64_t qsa_shared_attn_workspace_bytes(qsa_cache* cache, const qsa_chunk* chunk, qsa_handle prefix,
+                                        int32_t prefix_len, int32_t own_first);
+
+/* The weight that attention gives each cached token: for unit u (request r, layer
+ * l) and t < ctx_len,
+ *   W_t = sum_x sum_h exp(softmax_scale * q[x][h] . K_t[h/4] - lse[x][h])
+ * over the unit's rows x that see t (sinks and window as for qsa_window_attn) and
+ * the 16 heads; weights[u * stride + t] = W_t (accumulate 0) or += W_t (accumulate
+ * 1).  lse: as returned by the attention whose weights these are; a row with lse =
+ * -inf adds nothing.  The same inputs give the same bits.  Entries at and past
+ * ctx_len are left as they were.  A token that no row sees has W_t = 0 whatever
+ * its key holds, and so has a token with a bad slot.
+ * q: device bf16 bits [rows][16][128]; lse: device fp32 [rows][16]; weights: device
+ * fp32 [units][stride], stride >= ctx_len of every request.
+ * Errors: INVALID_ARG, STALE_HANDLE, NO_DEVICE, CUDA; BAD_SLOT in the device error
+ * word. */
+qsa_status_t qsa_window_weights(qsa_cache* cache, const qsa_chunk* chunk, const uint16_t* q,
+                                const float* lse, int32_t sinks, int32_t window,
+                                float softmax_scale, float* weights, int64_t stride,
+                                int32_t accumulate, void* stream);
+
 /* ------------------------------------------------------ pages of the cache */
 
+/* Drop tokens of a QSA_KV_HBM request until `keep` remain (1 <= keep <= ctx_len),
+ * at every layer of the cache by that layer's weights: the first `first` and the
+ * last `last` tokens stay (first + last <= keep), and of the others those with the
+ * largest weights (equal weights: the lower position; -0 equals +0, NaN comes
+ * last).  The kept tokens become the tokens 0 .. keep-1 in their order: index keys,
+ * scales and slots close up, ctx_len becomes keep, and the request can grow to its
+ * max_ctx again.  Rows: a kept token whose row is among the first `keep` of the
+ * request's region at its layer keeps it; the others in the region, in ascending
+ * order, take the free rows there in ascending order.  A row outside the region
+ * (qsa_slot_table_set) stays where it is.  Entries of the arrays from `keep` on are
+ * left as they were.  Afterwards qsa_request_truncate takes back no kept token (it
+ * refuses lengths below keep), since their rows are in no order.
+ * weights: device fp32, layer l at weights + l * weight_stride (>= ctx_len).
+ * kept: device int32 [n_layers][keep] or NULL, the kept tokens' former positions.
+ * weights_out: device fp32, layer l at weights_out + l * out_stride (>= keep), or
+ * NULL: the kept tokens' weights.  workspace: device, 16-byte aligned,
+ * qsa_evict_workspace_bytes bytes.  Outputs and the workspace overlap no input and
+ * not each other.  Work on the request that is in flight on other streams must have
+ * finished, and later work must be ordered behind `stream`.  Graphs that captured
+ * calls on the request must be captured again; a stream that is being captured is
+ * refused.
+ * Errors: INVALID_ARG (also for host placements: their histories keep every token),
+ * STALE_HANDLE, NO_DEVICE, CUDA; a kept token's bad slot goes to the device error
+ * word (BAD_SLOT) and stays. */
+qsa_status_t qsa_request_evict(qsa_cache* cache, qsa_handle request, const float* weights,
+                               int64_t weight_stride, int64_t keep, int64_t first, int64_t last,
+                               int32_t* kept, float* weights_out, int64_t out_stride,
+                               void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace qsa_request_evict needs, or -1. */
+int64_t qsa_evict_workspace_bytes(qsa_cache* cache, qsa_handle request, int64_t keep);
+
 /* Take back the newest tokens of a request: ctx_len becomes new_ctx_len
- * (1 <= new_ctx_len <= ctx_len).  Host bookkeeping only; work already
+ * (1 <= new_ctx_len <= ctx_len, and not below the `keep` of an eviction before).
+ * Host bookkeeping only; work already
  * enqueued must not use the tokens taken back afterwards.  Their positions
  * can be advanced over and appended to again.  Tokens whose ring row the
  * tokens taken back had been given stay cold (read from the host history).

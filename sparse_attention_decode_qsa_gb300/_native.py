@@ -134,6 +134,17 @@ SIGNATURES = {
     "qsa_chunk_sparse_attn": (C.c_int, [C.c_void_p, C.POINTER(Chunk), C.c_void_p, C.c_void_p,
                                         C.c_void_p, C.c_int32, C.c_float, C.c_void_p, C.c_void_p,
                                         C.c_void_p, C.c_int64, C.c_void_p]),
+    "qsa_window_attn": (C.c_int, [C.c_void_p, C.POINTER(Chunk), C.c_void_p, C.c_int32, C.c_int32, C.c_float,
+                                  C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
+    "qsa_window_attn_workspace_bytes": (C.c_int64, [C.c_void_p, C.POINTER(Chunk), C.c_int32, C.c_int32]),
+    "qsa_shared_attn": (C.c_int, [C.c_void_p, C.POINTER(Chunk), Handle, C.c_int32, C.c_int32, C.c_void_p,
+                                  C.c_float, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
+    "qsa_shared_attn_workspace_bytes": (C.c_int64, [C.c_void_p, C.POINTER(Chunk), Handle, C.c_int32, C.c_int32]),
+    "qsa_window_weights": (C.c_int, [C.c_void_p, C.POINTER(Chunk), C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
+                                     C.c_float, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p]),
+    "qsa_request_evict": (C.c_int, [C.c_void_p, Handle, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_int64,
+                                    C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p]),
+    "qsa_evict_workspace_bytes": (C.c_int64, [C.c_void_p, Handle, C.c_int64]),
     "qsa_request_truncate": (C.c_int, [C.c_void_p, Handle, C.c_int64]),
     "qsa_request_fork": (C.c_int, [C.c_void_p, Handle, C.POINTER(RequestDesc), C.c_void_p,
                                    C.POINTER(Handle)]),

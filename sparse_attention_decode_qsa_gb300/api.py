@@ -323,6 +323,19 @@ class Cache:
             return None
         return _raw_stream(self.pool.device.index) if stream is None else _stream(stream)
 
+    def _scratch(self, nbytes, stream):
+        """Workspace of one call, allocated in the order of the stream that uses
+        it: memory of the current stream may still be at work there."""
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.pool.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(nbytes, dtype=torch.uint8, device=self.pool.device)
+
+    def _bytes(self, n, func) -> int:
+        if n < 0:
+            raise QsaError(N.ERR_INVALID_ARG, func, self.L.qsa_last_error_string().decode(errors="replace"))
+        return n
+
     # ------------------------------------------------ several tokens at once
     # handles: requests; n_tokens: how many of each request's newest tokens.
     # Rows: layer after layer, request after request.
@@ -361,11 +374,8 @@ class Cache:
 
     def chunk_attn_workspace_bytes(self, handles, n_tokens, layer0, n_layers, budget_tokens) -> int:
         ch = _chunk(handles, n_tokens, layer0, n_layers)
-        n = self.L.qsa_chunk_attn_workspace_bytes(self.h, C.byref(ch), budget_tokens)
-        if n < 0:
-            raise QsaError(N.ERR_INVALID_ARG, "qsa_chunk_attn_workspace_bytes",
-                           self.L.qsa_last_error_string().decode(errors="replace"))
-        return n
+        return self._bytes(self.L.qsa_chunk_attn_workspace_bytes(self.h, C.byref(ch), budget_tokens),
+                           "qsa_chunk_attn_workspace_bytes")
 
     def chunk_sparse_attn(self, handles, n_tokens, layer0, n_layers, q, sel_blocks, n_sel, budget_tokens,
                           softmax_scale, out, lse=None, workspace=None, stream=None):
@@ -375,13 +385,8 @@ class Cache:
         ch = _chunk(handles, n_tokens, layer0, n_layers)
         rows = n_layers * sum(n_tokens)
         if workspace is None:
-            need = self.chunk_attn_workspace_bytes(handles, n_tokens, layer0, n_layers, budget_tokens)
-            # allocated in the order of the stream that uses it: memory of the
-            # current stream may still be at work there
-            if stream is not None and not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=self.pool.device)
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=self.pool.device)
+            workspace = self._scratch(self.chunk_attn_workspace_bytes(handles, n_tokens, layer0, n_layers,
+                                                                      budget_tokens), stream)
         heads = (rows, N.Q_HEADS, N.HEAD_DIM)
         check(self.L.qsa_chunk_sparse_attn(
             self.h, C.byref(ch), self._rows(q, "q", (torch.bfloat16,), heads),
@@ -391,3 +396,95 @@ class Cache:
             self._rows(lse, "lse", (torch.float32,), (rows, N.Q_HEADS)),
             self._rows(workspace, "workspace", (torch.uint8,), (workspace.numel(),)), workspace.numel(),
             self._current(stream)), "qsa_chunk_sparse_attn")
+
+    # --------------------------------------- attention without a selection
+    def window_attn_workspace_bytes(self, handles, n_tokens, layer0, n_layers, sinks, window) -> int:
+        ch = _chunk(handles, n_tokens, layer0, n_layers)
+        return self._bytes(self.L.qsa_window_attn_workspace_bytes(self.h, C.byref(ch), sinks, window),
+                           "qsa_window_attn_workspace_bytes")
+
+    def window_attn(self, handles, n_tokens, layer0, n_layers, q, sinks, window, softmax_scale, out, lse=None,
+                    workspace=None, stream=None):
+        """Attention of every query over the newest `window` tokens up to its own
+        and the context's first `sinks`: q and out bf16 [rows][16][128], lse fp32
+        [rows][16].  workspace: uint8 of window_attn_workspace_bytes bytes;
+        allocated for the call when None."""
+        ch = _chunk(handles, n_tokens, layer0, n_layers)
+        heads = (n_layers * sum(n_tokens), N.Q_HEADS, N.HEAD_DIM)
+        if workspace is None:
+            workspace = self._scratch(self.window_attn_workspace_bytes(handles, n_tokens, layer0, n_layers, sinks,
+                                                                       window), stream)
+        check(self.L.qsa_window_attn(
+            self.h, C.byref(ch), self._rows(q, "q", (torch.bfloat16,), heads), sinks, window, float(softmax_scale),
+            self._rows(out, "out", (torch.bfloat16,), heads), self._rows(lse, "lse", (torch.float32,), heads[:2]),
+            self._rows(workspace, "workspace", (torch.uint8,), (workspace.numel(),)), workspace.numel(),
+            self._current(stream)), "qsa_window_attn")
+
+    def shared_attn_workspace_bytes(self, handles, n_tokens, layer0, n_layers, prefix, prefix_len, own_first) -> int:
+        ch = _chunk(handles, n_tokens, layer0, n_layers)
+        return self._bytes(self.L.qsa_shared_attn_workspace_bytes(self.h, C.byref(ch), prefix, prefix_len, own_first),
+                           "qsa_shared_attn_workspace_bytes")
+
+    def shared_attn(self, handles, n_tokens, layer0, n_layers, prefix, prefix_len, own_first, q, softmax_scale, out,
+                    lse=None, workspace=None, stream=None):
+        """Attention of every query over the first prefix_len tokens of the request
+        `prefix`, read once for the batch, and over its own request's tokens from
+        own_first (prefix_len for requests that hold a copy of the prefix, 0 for
+        those that do not) up to its own.  Arrays as for window_attn."""
+        ch = _chunk(handles, n_tokens, layer0, n_layers)
+        heads = (n_layers * sum(n_tokens), N.Q_HEADS, N.HEAD_DIM)
+        if workspace is None:
+            workspace = self._scratch(self.shared_attn_workspace_bytes(handles, n_tokens, layer0, n_layers, prefix,
+                                                                       prefix_len, own_first), stream)
+        check(self.L.qsa_shared_attn(
+            self.h, C.byref(ch), prefix, prefix_len, own_first, self._rows(q, "q", (torch.bfloat16,), heads),
+            float(softmax_scale), self._rows(out, "out", (torch.bfloat16,), heads),
+            self._rows(lse, "lse", (torch.float32,), heads[:2]),
+            self._rows(workspace, "workspace", (torch.uint8,), (workspace.numel(),)), workspace.numel(),
+            self._current(stream)), "qsa_shared_attn")
+
+    def window_weights(self, handles, n_tokens, layer0, n_layers, q, lse, sinks, window, softmax_scale, weights,
+                       accumulate=False, stream=None):
+        """The weight that the chunk's queries give each cached token (heads
+        together), from the lse of window_attn: weights fp32 [units][stride], stride
+        >= every context, overwritten or added to."""
+        ch = _chunk(handles, n_tokens, layer0, n_layers)
+        heads = (n_layers * sum(n_tokens), N.Q_HEADS, N.HEAD_DIM)
+        units = (n_layers * len(handles), weights.shape[-1])
+        check(self.L.qsa_window_weights(
+            self.h, C.byref(ch), self._rows(q, "q", (torch.bfloat16,), heads),
+            self._rows(lse, "lse", (torch.float32,), heads[:2]), sinks, window, float(softmax_scale),
+            self._rows(weights, "weights", (torch.float32,), units), units[1], int(bool(accumulate)),
+            self._current(stream)), "qsa_window_weights")
+
+    def evict_workspace_bytes(self, handle: N.Handle, keep: int) -> int:
+        return self._bytes(self.L.qsa_evict_workspace_bytes(self.h, handle, int(keep)), "qsa_evict_workspace_bytes")
+
+    def _layers(self, t, what, least):
+        """Address and layer stride of a tensor fp32 [n_layers][>= least], whose
+        layers may lie apart (one request of window_weights' units)."""
+        if t is None:
+            return None, 0
+        if t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] != self.n_layers or t.shape[1] < least:
+            raise ValueError(f"{what}: {t.dtype} {tuple(t.shape)}, expected float32 [{self.n_layers}][>= {least}]")
+        if self.device is not None and t.device != self.pool.device:
+            raise ValueError(f"{what}: on {t.device}, the cache on {self.pool.device}")
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{what}: a layer's weights must be contiguous")
+        return t.data_ptr(), t.stride(0)
+
+    def evict(self, handle: N.Handle, weights, keep: int, first: int = 0, last: int = 0, kept=None, weights_out=None,
+              workspace=None, stream=None):
+        """Drop tokens of a resident request until `keep` remain: the first, the
+        last, and of the rest those with the largest weights (fp32
+        [n_layers][>= context]) of each layer.  kept int32 [n_layers][keep]: their
+        former positions; weights_out fp32 [n_layers][>= keep]: their weights."""
+        w, stride = self._layers(weights, "weights", self.request_info(handle).ctx_len)
+        o, out_stride = self._layers(weights_out, "weights_out", keep)
+        if workspace is None:
+            workspace = self._scratch(self.evict_workspace_bytes(handle, keep), stream)
+        check(self.L.qsa_request_evict(
+            self.h, handle, w, stride, int(keep), int(first), int(last),
+            self._rows(kept, "kept", (torch.int32,), (self.n_layers, keep)), o, out_stride,
+            self._rows(workspace, "workspace", (torch.uint8,), (workspace.numel(),)), workspace.numel(),
+            self._current(stream)), "qsa_request_evict")

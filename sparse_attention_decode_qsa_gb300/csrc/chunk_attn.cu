@@ -61,19 +61,13 @@
 // scale goes in as f16: off by 2^-11 of itself, or by 2^-25 in units in which the
 // largest of the row's products is 2^-6 at least, whatever the scales are and
 // whoever else selects what (the reference follows the row's own products).
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
-#include "tc_common.cuh"
+#include "attn_common.cuh"
 
 namespace qsa {
 namespace {
 
 using namespace tc;
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+using namespace attn;
 
 constexpr int kTileQueries = 64;                  // two halves of 32
 constexpr int kStepBlocks = 32, kStepTokens = 4 * kStepBlocks;
@@ -155,34 +149,7 @@ struct ChunkAttnParams {
   }
 };
 
-__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 b = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-
 // ------------------------------------------------------- one row, plain fp32
-
-// Four values at dims 4 lane .. 4 lane + 3 of head vector hv (K heads 0-3,
-// then V heads 0-3) of a row.
-__device__ __forceinline__ float4 row_values(const uint8_t* row, int hv, int lane, bool fp8) {
-  if (!fp8) {
-    const uint2 v = reinterpret_cast<const uint2*>(row + hv * kHeadDim * 2)[lane];
-    return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
-  }
-  const uint32_t c = reinterpret_cast<const uint32_t*>(row + hv * kHeadDim)[lane];
-  const float s = __half2float(
-      __ushort_as_half(reinterpret_cast<const uint16_t*>(row + 2 * kKvHeads * kHeadDim)[hv]));
-  const __half2 a(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xFFFFu), __NV_E4M3));
-  const __half2 b(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3));
-  return make_float4(s * __low2float(a), s * __high2float(a), s * __low2float(b), s * __high2float(b));
-}
 
 // One warp, one query row x and head h: online softmax over the row's own
 // selected tokens.  (Bad blocks and slots have been reported by the plan and
@@ -393,52 +360,6 @@ __device__ __forceinline__ bool share_of(const ChunkAttnParams& p, int c, int* t
     before = __shfl_sync(0xFFFFFFFFu, upto, 31);
   }
   return false;
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// log2 of a V scale's size.
-__device__ __forceinline__ float log2_size(float s) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fabsf(s)));
-  return fmaxf(y, -100.f);
-}
-
-// Pairs of fp32 values: one instruction for two multiply-adds or additions.
-__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) { return (uint64_t)a | ((uint64_t)b << 32); }
-__device__ __forceinline__ uint64_t pair(float a, float b) { return pair(__float_as_uint(a), __float_as_uint(b)); }
-__device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float((uint32_t)x); }
-__device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-// Eight e4m3 codes as f16, exactly.
-__device__ __forceinline__ uint32_t codes2_f16(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
-}
-__device__ __forceinline__ uint4 codes8_f16(uint2 w) {
-  return make_uint4(codes2_f16(w.x & 0xFFFFu), codes2_f16(w.x >> 16), codes2_f16(w.y & 0xFFFFu), codes2_f16(w.y >> 16));
 }
 
 // The tokens of 64 c + 4 b .. + 3 of a step that exist and that position pos

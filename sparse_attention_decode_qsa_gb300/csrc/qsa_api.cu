@@ -62,6 +62,7 @@ struct Lease {
   int64_t row_base = 0;
   int64_t rows = 0;
   int64_t hot_base = -1;               // first hot row, or -1
+  int64_t packed = 0;                  // tokens an eviction kept: their region rows are in no order
   const uint8_t* host_rows = nullptr;  // device-usable address
 };
 
@@ -330,6 +331,76 @@ cudaError_t complete_plans(const qsa_cache* c, qsa_handle h, cudaStream_t s) {
                          (size_t)c->cfg.n_layers * sizeof(int32_t), s);
 }
 
+// Copy the planned misses of a call's units into their hot rows and clear their
+// plans.
+cudaError_t complete_units(const BatchDesc& b, cudaStream_t s) {
+  cudaError_t e = launch_hot_complete(b, s);
+  for (int u = 0; e == cudaSuccess && u < b.n_units; ++u)
+    if (b.u[u].hot_base >= 0) e = cudaMemsetAsync(b.hot_pend_on + b.unit_state(u), 0, sizeof(int32_t), s);
+  return e;
+}
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+qsa_status_t window_desc(const qsa_cache* c, const qsa_chunk* chunk, int32_t sinks, int32_t window, DenseAttn* d) {
+  if (qsa_status_t st = c->build_chunk(chunk, &d->c)) return st;
+  if (sinks < 0 || window < 0) return fail(QSA_ERR_INVALID_ARG, "sinks %d and window %d must be >= 0", sinks, window);
+  d->prefix_len = d->prefix_stride = 0;
+  d->prefix_host = nullptr;
+  d->prefix_req = 0;
+  d->own_first = 0;
+  d->sinks = sinks;
+  d->window = window;
+  return QSA_OK;
+}
+
+// prefix: the units of the prefix's request at the chunk's layers.
+qsa_status_t shared_desc(const qsa_cache* c, const qsa_chunk* chunk, qsa_handle prefix, int32_t prefix_len,
+                         int32_t own_first, DenseAttn* d, BatchDesc* prefix_units) {
+  if (qsa_status_t st = window_desc(c, chunk, 0, 0x7FFFFFFF, d)) return st;
+  const Lease* l;
+  if (qsa_status_t st = c->check_handle(prefix, &l)) return st;
+  if (prefix_len < 0 || prefix_len > l->ctx_len)
+    return fail(QSA_ERR_INVALID_ARG, "prefix_len %d outside [0, %lld], the prefix request's tokens", prefix_len,
+                (long long)l->ctx_len);
+  if (own_first < 0) return fail(QSA_ERR_INVALID_ARG, "own_first %d must be >= 0", own_first);
+  const qsa_batch b = {1, chunk->layer0, chunk->n_layers, 0, &prefix};
+  if (qsa_status_t st = c->build_batch(&b, prefix_units)) return st;
+  d->prefix_len = prefix_len;
+  d->prefix_stride = l->max_ctx;
+  d->prefix_host = l->host_rows;
+  d->prefix_req = (int32_t)prefix.index;
+  d->own_first = own_first;
+  return QSA_OK;
+}
+
+int64_t dense_workspace(const DenseAttn& d) {
+  const int64_t bytes = dense_attn_workspace(d);
+  if (bytes < 0) { fail(QSA_ERR_CUDA, "the device's SM count is unknown"); return -1; }
+  ok();
+  return bytes;
+}
+
+qsa_status_t dense_attn(const DenseAttn& d, const BatchDesc* prefix_units, const uint16_t* q, float softmax_scale,
+                        uint16_t* out, float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!(softmax_scale == softmax_scale)) return fail(QSA_ERR_INVALID_ARG, "softmax_scale is NaN");
+  if (d.c.rows() == 0) return ok();
+  if (!q || !out || !workspace) return fail(QSA_ERR_INVALID_ARG, "null array");
+  if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(workspace))
+    return fail(QSA_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+  const int64_t need = dense_attn_workspace(d);
+  if (need < 0) return fail(QSA_ERR_CUDA, "the device's SM count is unknown");
+  if (workspace_bytes < need)
+    return fail(QSA_ERR_INVALID_ARG, "workspace has %lld bytes, needs %lld", (long long)workspace_bytes,
+                (long long)need);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = complete_units(d.c.b, s);
+  if (e == cudaSuccess && prefix_units) e = complete_units(*prefix_units, s);
+  if (e == cudaSuccess) e = launch_dense_attn(d, q, softmax_scale, out, lse, workspace, s);
+  if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+  return ok();
+}
+
 // Change every slot (and pending row) of every live request that names a
 // moved row.  Moves are ascending and go down, so a row's new place is never
 // inside the old place of a later move: they can be applied in pieces.
@@ -555,6 +626,7 @@ qsa_status_t begin_lease(qsa_cache* c, const qsa_request_desc* desc, void* strea
   l.row_base = base;
   l.rows = rows;
   l.hot_base = hot ? base + ring_rows : -1;
+  l.packed = 0;
   l.host_rows = host_dev;
   out->index = (uint32_t)slot;
   out->generation = l.generation;
@@ -931,6 +1003,155 @@ qsa_status_t qsa_chunk_sparse_attn(qsa_cache* c, const qsa_chunk* chunk, const u
   return ok();
 }
 
+int64_t qsa_window_attn_workspace_bytes(qsa_cache* c, const qsa_chunk* chunk, int32_t sinks, int32_t window) {
+  if (!c) { fail(QSA_ERR_INVALID_ARG, "null cache"); return -1; }
+  DeviceGuard guard(c->device);
+  if (guard.status() != cudaSuccess) { cuda_fail(guard.status(), "making the cache's device current"); return -1; }
+  DenseAttn d;
+  if (window_desc(c, chunk, sinks, window, &d) != QSA_OK) return -1;
+  return dense_workspace(d);
+}
+
+qsa_status_t qsa_window_attn(qsa_cache* c, const qsa_chunk* chunk, const uint16_t* q, int32_t sinks, int32_t window,
+                             float softmax_scale, uint16_t* out, float* lse, void* workspace,
+                             int64_t workspace_bytes, void* stream) {
+  if (!c) return fail(QSA_ERR_INVALID_ARG, "null cache");
+  DeviceGuard guard(c->device);
+  if (qsa_status_t st = c->check_stream(stream, guard)) return st;
+  DenseAttn d;
+  if (qsa_status_t st = window_desc(c, chunk, sinks, window, &d)) return st;
+  return dense_attn(d, nullptr, q, softmax_scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+int64_t qsa_shared_attn_workspace_bytes(qsa_cache* c, const qsa_chunk* chunk, qsa_handle prefix, int32_t prefix_len,
+                                        int32_t own_first) {
+  if (!c) { fail(QSA_ERR_INVALID_ARG, "null cache"); return -1; }
+  DeviceGuard guard(c->device);
+  if (guard.status() != cudaSuccess) { cuda_fail(guard.status(), "making the cache's device current"); return -1; }
+  DenseAttn d;
+  BatchDesc prefix_units;
+  if (shared_desc(c, chunk, prefix, prefix_len, own_first, &d, &prefix_units) != QSA_OK) return -1;
+  return dense_workspace(d);
+}
+
+qsa_status_t qsa_shared_attn(qsa_cache* c, const qsa_chunk* chunk, qsa_handle prefix, int32_t prefix_len,
+                             int32_t own_first, const uint16_t* q, float softmax_scale, uint16_t* out, float* lse,
+                             void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!c) return fail(QSA_ERR_INVALID_ARG, "null cache");
+  DeviceGuard guard(c->device);
+  if (qsa_status_t st = c->check_stream(stream, guard)) return st;
+  DenseAttn d;
+  BatchDesc prefix_units;
+  if (qsa_status_t st = shared_desc(c, chunk, prefix, prefix_len, own_first, &d, &prefix_units)) return st;
+  return dense_attn(d, &prefix_units, q, softmax_scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+qsa_status_t qsa_window_weights(qsa_cache* c, const qsa_chunk* chunk, const uint16_t* q, const float* lse,
+                                int32_t sinks, int32_t window, float softmax_scale, float* weights, int64_t stride,
+                                int32_t accumulate, void* stream) {
+  if (!c) return fail(QSA_ERR_INVALID_ARG, "null cache");
+  DeviceGuard guard(c->device);
+  if (qsa_status_t st = c->check_stream(stream, guard)) return st;
+  DenseAttn d;
+  if (qsa_status_t st = window_desc(c, chunk, sinks, window, &d)) return st;
+  if (!(softmax_scale == softmax_scale)) return fail(QSA_ERR_INVALID_ARG, "softmax_scale is NaN");
+  if (accumulate != 0 && accumulate != 1)
+    return fail(QSA_ERR_INVALID_ARG, "accumulate %d must be 0 or 1", accumulate);
+  for (int u = 0; u < d.c.b.n_units; ++u)
+    if (stride < d.c.b.u[u].n)
+      return fail(QSA_ERR_INVALID_ARG, "stride %lld < %lld tokens of unit %d", (long long)stride,
+                  (long long)d.c.b.u[u].n, u);
+  if (!weights || (d.c.rows() > 0 && (!q || !lse))) return fail(QSA_ERR_INVALID_ARG, "null array");
+  if (!aligned16(q) || !aligned16(lse) || !aligned16(weights))
+    return fail(QSA_ERR_INVALID_ARG, "device buffers must be 16-byte aligned");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = complete_units(d.c.b, s);
+  if (e == cudaSuccess)
+    e = launch_window_weights(d, q, lse, softmax_scale, weights, stride, accumulate != 0, s);
+  if (e != cudaSuccess) return cuda_fail(e, "weight launch");
+  return ok();
+}
+
+namespace {
+
+qsa_status_t evict_desc(qsa_cache* c, qsa_handle h, int64_t keep, EvictParams* p) {
+  if (!c->has_device) return fail(QSA_ERR_NO_DEVICE, "cache has no device storage");
+  const Lease* l;
+  if (qsa_status_t st = c->check_handle(h, &l)) return st;
+  if (l->placement != QSA_KV_HBM)
+    return fail(QSA_ERR_INVALID_ARG, "only a QSA_KV_HBM request can give up tokens: a host history keeps them all");
+  if (keep < 1 || keep > l->ctx_len)
+    return fail(QSA_ERR_INVALID_ARG, "keep %lld outside [1, %lld]", (long long)keep, (long long)l->ctx_len);
+  std::memset(p, 0, sizeof *p);
+  p->req = (int32_t)h.index;
+  p->n_layers = c->cfg.n_layers;
+  p->ctx_cap = c->cfg.ctx_capacity;
+  p->pool_rows = c->cfg.hbm_pool_rows;
+  p->n = l->ctx_len;
+  p->keep = keep;
+  p->index_keys = c->cfg.index_keys;
+  p->index_scales = c->cfg.index_scales;
+  p->slot_table = c->cfg.slot_table;
+  p->pool = static_cast<uint8_t*>(c->cfg.hbm_pool);
+  p->row_bytes = (int32_t)c->row_bytes();
+  p->row_base = l->row_base;
+  p->layer_rows = l->layer_rows;
+  p->err = c->err();
+  return QSA_OK;
+}
+
+}  // namespace
+
+int64_t qsa_evict_workspace_bytes(qsa_cache* c, qsa_handle request, int64_t keep) {
+  if (!c) { fail(QSA_ERR_INVALID_ARG, "null cache"); return -1; }
+  EvictParams p;
+  if (evict_desc(c, request, keep, &p) != QSA_OK) return -1;
+  ok();
+  return evict_layout(&p, nullptr);
+}
+
+qsa_status_t qsa_request_evict(qsa_cache* c, qsa_handle request, const float* weights, int64_t weight_stride,
+                               int64_t keep, int64_t first, int64_t last, int32_t* kept, float* weights_out,
+                               int64_t out_stride, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!c) return fail(QSA_ERR_INVALID_ARG, "null cache");
+  DeviceGuard guard(c->device);
+  if (qsa_status_t st = c->check_stream(stream, guard)) return st;
+  EvictParams p;
+  if (qsa_status_t st = evict_desc(c, request, keep, &p)) return st;
+  if (first < 0 || last < 0 || first > keep || last > keep - first)
+    return fail(QSA_ERR_INVALID_ARG, "first %lld and last %lld must be >= 0 and at most keep %lld together",
+                (long long)first, (long long)last, (long long)keep);
+  if (!weights || !workspace) return fail(QSA_ERR_INVALID_ARG, "null array");
+  if (!aligned16(workspace) || !aligned16(kept) || reinterpret_cast<uintptr_t>(weights) % 4 ||
+      reinterpret_cast<uintptr_t>(weights_out) % 4)
+    return fail(QSA_ERR_INVALID_ARG, "misaligned device buffer");
+  if (p.n_layers > 1 && (weight_stride < p.n || (weights_out && out_stride < keep)))
+    return fail(QSA_ERR_INVALID_ARG, "weight_stride %lld < %lld tokens, or out_stride %lld < %lld",
+                (long long)weight_stride, (long long)p.n, (long long)out_stride, (long long)keep);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(s, &cs);
+  if (e != cudaSuccess) return cuda_fail(e, "querying the stream's capture status");
+  if (cs != cudaStreamCaptureStatusNone)
+    return fail(QSA_ERR_INVALID_ARG, "a request's length cannot change in a captured graph");
+  const int64_t need = evict_layout(&p, workspace);
+  if (workspace_bytes < need)
+    return fail(QSA_ERR_INVALID_ARG, "workspace has %lld bytes, needs %lld", (long long)workspace_bytes,
+                (long long)need);
+  p.first = first;
+  p.last = last;
+  p.weights = weights;
+  p.weight_stride = weight_stride;
+  p.weights_out = weights_out;
+  p.out_stride = out_stride;
+  if (kept) p.kept = kept;
+  e = launch_evict(p, s);
+  if (e != cudaSuccess) return cuda_fail(e, "eviction launch");
+  c->leases[request.index].ctx_len = keep;
+  c->leases[request.index].packed = keep;
+  return ok();
+}
+
 qsa_status_t qsa_request_truncate(qsa_cache* c, qsa_handle h, int64_t new_ctx_len) {
   if (!c) return fail(QSA_ERR_INVALID_ARG, "null cache");
   const Lease* cl;
@@ -938,6 +1159,9 @@ qsa_status_t qsa_request_truncate(qsa_cache* c, qsa_handle h, int64_t new_ctx_le
   if (new_ctx_len < 1 || new_ctx_len > cl->ctx_len)
     return fail(QSA_ERR_INVALID_ARG, "new_ctx_len %lld outside [1, %lld]", (long long)new_ctx_len,
                 (long long)cl->ctx_len);
+  if (new_ctx_len < cl->packed)
+    return fail(QSA_ERR_INVALID_ARG, "new_ctx_len %lld is less than the %lld tokens an eviction has kept",
+                (long long)new_ctx_len, (long long)cl->packed);
   c->leases[h.index].ctx_len = new_ctx_len;
   return ok();
 }

@@ -56,6 +56,9 @@ enum KernelId : int32_t {
   kKernChunkScore = 10,
   kKernChunkAttn = 12,
   kKernFork = 13,
+  kKernDenseAttn = 14,
+  kKernWeights = 15,
+  kKernEvict = 16,
 };
 
 // One decode unit (request slot, layer) of a call.
@@ -368,6 +371,59 @@ int64_t chunk_attn_workspace(const ChunkDesc& c, int32_t budget_tokens);
 cudaError_t launch_chunk_attn(const ChunkDesc& c, const uint16_t* q, const int32_t* sel_blocks,
                               const int32_t* n_sel, int32_t budget_tokens, float softmax_scale,
                               uint16_t* out, float* lse, void* workspace, cudaStream_t s);
+
+// Attention over tokens that the query's position decides.  Row at position p
+// sees the tokens 0 .. prefix_len - 1 of request slot prefix_req (prefix_host: row
+// 0 of layer 0 of its host history, or nullptr; prefix_stride: its rows per layer),
+// and of its own request the tokens t <= p, t >= own_first, with t < sinks or
+// t > p - window.
+struct DenseAttn {
+  ChunkDesc c;
+  int64_t prefix_len, prefix_stride;
+  const uint8_t* prefix_host;
+  int32_t prefix_req;
+  int64_t own_first, sinks, window;
+};
+
+int64_t dense_attn_workspace(const DenseAttn& d);
+
+cudaError_t launch_dense_attn(const DenseAttn& d, const uint16_t* q, float softmax_scale, uint16_t* out, float* lse,
+                              void* workspace, cudaStream_t s);
+
+cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const float* lse, float softmax_scale,
+                                  float* weights, int64_t stride, bool accumulate, cudaStream_t s);
+
+// Eviction: keep `keep` of a resident request's n tokens at every layer.
+struct EvictParams {
+  int32_t req, n_layers;
+  int64_t ctx_cap, pool_rows, n, keep, first, last;
+  uint8_t* index_keys;
+  uint16_t* index_scales;
+  int32_t* slot_table;
+  uint8_t* pool;
+  int32_t row_bytes;
+  int64_t row_base, layer_rows;  // the request's region, rows per layer
+  const float* weights;          // [n_layers] rows of n, weight_stride apart
+  int64_t weight_stride;
+  float* weights_out;            // [n_layers] rows of keep, out_stride apart, or nullptr
+  int64_t out_stride;
+  ErrorWord* err;
+  // in the workspace (evict_layout)
+  int32_t* n_moves;              // [n_layers]
+  int32_t* kept;                 // [n_layers][keep] positions, ascending (or the caller's array)
+  int32_t* new_slot;             // [n_layers][keep]
+  int32_t* holes;                // [n_layers][keep] free rows below keep, ascending
+  int64_t used_words;
+  uint32_t* used;                // [n_layers][used_words] rows below keep in use, a bit each
+  int2* moves;                   // [n_layers][keep] {from, to} pool rows
+  uint8_t* keys_ws;              // [n_layers][keep][64]
+  uint16_t* scales_ws;           // [n_layers][keep]
+};
+
+// Lays the workspace's arrays out from `workspace` on; returns its bytes.
+int64_t evict_layout(EvictParams* p, void* workspace);
+
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
 
 // Pages: copy the first n_tokens tokens of a request (all layers) to another,
 // and write the latter's slot-table rows.
