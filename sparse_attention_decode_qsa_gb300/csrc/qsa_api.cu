@@ -348,6 +348,7 @@ qsa_status_t window_desc(const qsa_cache* c, const qsa_chunk* chunk, int32_t sin
   d->prefix_len = d->prefix_stride = 0;
   d->prefix_host = nullptr;
   d->prefix_req = 0;
+  d->n_req = chunk->n_req;
   d->own_first = 0;
   d->sinks = sinks;
   d->window = window;

@@ -382,6 +382,7 @@ struct DenseAttn {
   int64_t prefix_len, prefix_stride;
   const uint8_t* prefix_host;
   int32_t prefix_req;
+  int32_t n_req;                 // requests of the chunk: units per layer
   int64_t own_first, sinks, window;
 };
 
