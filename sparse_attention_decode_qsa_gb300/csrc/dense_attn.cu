@@ -17,7 +17,7 @@
 // tiles of its own, over the rows of all requests; else every tile reads it in
 // front of its own tokens.  A row's partial results are joined by their maxima and
 // sums.
-#include "attn_common.cuh"
+#include "dense_common.cuh"
 
 namespace qsa {
 namespace {
@@ -26,7 +26,6 @@ using namespace tc;
 using namespace attn;
 
 constexpr int kTileQueries = 64;                  // wide: two halves of 32
-constexpr int kFewQueries = 4;
 constexpr int kStepTokens = 128;                  // wide
 constexpr int kFewStep = 32;                      // few: two halves of 16 tokens
 constexpr int kRowFloats = kHeadDim + 2;          // partial of a row and head: O, m, l
@@ -52,17 +51,6 @@ struct Tile {
   int u, x0, nq;
   int64_t pos0, np, na, b0, total;
 };
-
-// Own tokens that any query at the positions p0 .. p1 sees: 0 .. na - 1 (sinks in
-// front of the rest, seen by all of them) and from b0 on nb of them.
-__host__ __device__ __forceinline__ void own_range(const DenseAttn& d, int64_t p0, int64_t p1, int64_t* na,
-                                                   int64_t* b0, int64_t* nb) {
-  int64_t low = p0 - d.window + 1;
-  if (low < d.own_first) low = d.own_first;
-  *na = d.sinks < low ? d.sinks : low;
-  *b0 = low;
-  *nb = p1 + 1 > low ? p1 + 1 - low : 0;
-}
 
 // Own tile of rows i0 .. of unit u.
 __host__ __device__ __forceinline__ Tile own_tile(const DenseAttn& d, bool grouped, int u, int i0) {
@@ -229,28 +217,6 @@ struct FewLayout {
 constexpr int kMergeBytes = kKvHeads * 16 * kRowFloats * 4;       // O, m, l of the second halves' rows
 static_assert(FewLayout<true>::kSmem >= kMergeBytes && FewLayout<false>::kSmem <= 227 * 1024, "shared memory");
 
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-template <bool kF16>
-__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if (kF16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 template <bool kFp8>
 __global__ void __launch_bounds__(kFewThreads, 1) dense_few_kernel(const __grid_constant__ DenseParams p) {
   using L = FewLayout<kFp8>;
@@ -280,50 +246,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) dense_few_kernel(const __grid_
   const int steps = (int)(all * (blockIdx.x + 1) / shares - s0);
   const Source src = source_of(p.d, t.u);
 
-  // ---- Q as A fragments: rows query * 4 + head of KV head g.  Against FP8 rows as
-  // f16, each row scaled by the power of two that puts its largest element into
-  // [2^14, 2^15); the inverse goes to the logits.
   uint32_t qa[8][4];
-  float f[2] = {p.sign * p.scale_log2, p.sign * p.scale_log2};   // rows r, r + 8
-#pragma unroll
-  for (int hi = 0; hi < 2; ++hi) {
-    const int row = r + 8 * hi, qi = row >> 2;
-    const uint16_t* q = p.q + ((int64_t)(t.x0 + qi) * kQHeads + g * kGroup + (row & 3)) * kHeadDim;
-    const bool have = qi < t.nq;
-    float top = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      uint32_t w0 = 0, w1 = 0;
-      if (have) {
-        if (kFp8) {
-          const uint2 v = *reinterpret_cast<const uint2*>(q + 16 * k + 4 * j4);
-          w0 = v.x;
-          w1 = v.y;
-        } else {
-          w0 = *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * j4);
-          w1 = *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * j4 + 8);
-        }
-      }
-      qa[k][hi] = w0;
-      qa[k][2 + hi] = w1;
-      top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(w0)), fabsf(bf16_hi(w0))), fmaxf(fabsf(bf16_lo(w1)), fabsf(bf16_hi(w1)))));
-    }
-    if (kFp8) {
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      int e = 0;
-      if (top > 0.f && top < INFINITY) frexpf(top, &e);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t& w = qa[k][2 * c + hi];
-          w = pack_f16(ldexpf(bf16_lo(w), 15 - e), ldexpf(bf16_hi(w), 15 - e));
-        }
-      }
-      f[hi] *= ldexpf(1.f, e - 15);
-    }
-  }
+  float f[2];                                                    // rows r, r + 8
+  few_queries<kFp8>(p.q, t.x0, t.nq, g, p.sign * p.scale_log2, qa, f);
 
   const uint32_t ring = smem_u32(smem) + warp * kFewStages * L::kStage;
   const int64_t first = s0 * kFewStep + half * kFewTokens;       // the warp's first token in the tile's list
@@ -394,18 +319,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) dense_few_kernel(const __grid_
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       uint32_t kb[4];
-      if (!kFp8) {
-        const int tok = ((lane >> 4) << 3) + (lane & 7), c = 2 * k + ((lane >> 3) & 1);
-        ldsm4(st + tok * L::kVec + ((c ^ (tok & 7)) << 4), kb);
-      } else {
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          uint32_t w;
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(st + (8 * n + r) * L::kVec + ((k ^ r) << 4) + 4 * j4));
-          kb[2 * n] = codes2_f16(w & 0xFFFFu);
-          kb[2 * n + 1] = codes2_f16(w >> 16);
-        }
-      }
+      few_keys<kFp8>(st, k, kb);
       mma16<kFp8>(x[0], qa[k], kb[0], kb[1]);
       mma16<kFp8>(x[1], qa[k], kb[2], kb[3]);
     }

@@ -3,11 +3,21 @@
 // over the chunk's queries x that see t (the window and sinks of dense_attn.cu)
 // and all heads h, with the log-sum-exp that the attention returned.  A row
 // without tokens (lse = -inf) adds nothing.
-#include "attn_common.cuh"
+//
+// Tokens are the rows of the product K Q^T, so that a thread holds one token and
+// sums over queries and heads in its own registers: no atomics, no order that
+// could change, one store per token.  The queries that see a token are a range of
+// the chunk, hence a range of columns.
+//
+// exp(x - lse) goes through 2^y with y = x log2 e - lse log2 e: a rounding of the
+// second product would scale a whole row's weights by up to 2^-20, so its
+// remainder stays as a factor beside the column.
+#include "dense_common.cuh"
 
 namespace qsa {
 namespace {
 
+using namespace tc;
 using namespace attn;
 
 struct WeightParams {
@@ -18,45 +28,513 @@ struct WeightParams {
   float* weights;                // [units][stride]
   int64_t stride;
   int32_t accumulate;
+  int32_t few_tokens;            // tokens of a CTA of the few kernel
 };
 
-constexpr int kThreads = 256;
-__global__ void __launch_bounds__(kThreads) weight_token_kernel(const __grid_constant__ WeightParams p) {
-  const int u = blockIdx.y, lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+// Whether a query at position pos sees token t.
+__device__ __forceinline__ bool sees(const DenseAttn& d, int64_t pos, int64_t t) {
+  return t <= pos && (t < d.sinks || t > pos - d.window);
+}
+// Whether any query of unit u sees token t.
+__device__ __forceinline__ bool seen_by_any(const DenseAttn& d, int u, int64_t t) {
+  const int n = d.c.unit_tokens(u);
+  const int64_t p1 = d.c.b.u[u].n - 1, p0 = p1 - n + 1;
+  return n > 0 && t <= p1 && (t < d.sinks || t > p0 - d.window);
+}
+// -lse in units of log2, and the factor that its rounding leaves.
+__device__ __forceinline__ float2 column_of(float lse) {
+  const float y = lse * kLog2e;
+  const float rest = fmaf(lse, kLog2e, -y) + lse * 1.925963033500e-08f;      // log2(e) past its fp32 value
+  return make_float2(-y, isfinite(y) ? exp2f(-rest) : 1.f);
+}
+__device__ __forceinline__ void store_weight(const WeightParams& p, int u, int64_t t, float w) {
+  float* to = p.weights + u * p.stride + t;
+  *to = p.accumulate ? *to + w : w;
+}
+
+// ------------------------------------------------------------------- few
+
+// Units of at most four queries: one CTA per run of tokens, all KV heads; warp w
+// serves KV head w % 4 for the tokens 16 (w / 4) .. + 15 of every step of 32, copied
+// by itself into its own ring of three stages, as in dense_attn.cu; S = Q K^T by 16
+// mma of m16n8k16 per stage, whose 16 rows are summed over the lanes.  Bound by the
+// keys' bytes.
+constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32, kFewStages = 3, kFewStep = 32, kFewTokens = 16;
+constexpr int kFewMost = 1024;                    // tokens of a CTA at most
+template <bool kFp8>
+struct FewLayout {
+  static constexpr int kVec = kFp8 ? 128 : 256;
+  static constexpr int kScales = kFewTokens * kVec;              // FP8: the rows' 8 scales, 16 bytes a token
+  static constexpr int kStage = kScales + (kFp8 ? kFewTokens * 16 : 0);
+  static constexpr int kSums = kFewWarps * kFewStages * kStage;  // float [4][few_tokens]
+  static constexpr int kSmem = kSums + kKvHeads * kFewMost * 4;
+};
+
+template <bool kFp8>
+__global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid_constant__ WeightParams p) {
+  using L = FewLayout<kFp8>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint32_t there[kFewWarps][kFewStages];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = warp & 3, half = warp >> 2;
+  const int r = lane >> 2, j4 = lane & 3;
+  const BatchDesc& b = p.d.c.b;
+  const int u = blockIdx.y, nq = p.d.c.unit_tokens(u);
+  const int64_t n = b.u[u].n, t0 = (int64_t)blockIdx.x * p.few_tokens;
+  if (nq > kFewQueries || t0 >= n) return;
+  const int64_t t1 = t0 + p.few_tokens < n ? t0 + p.few_tokens : n;
+  const int x0 = p.d.c.row0[u];
+  const int64_t pos0 = n - nq;
   grid_dependency_wait();
-  const ChunkDesc& c = p.d.c;
-  if (t >= c.b.u[u].n) return;
-  const bool fp8 = c.b.row_bytes == kRowBytesFp8;
-  float sum = 0.f;
-  const uint8_t* row = c.unit_tokens(u) > 0 ? row_source(c.b, u, t, kKernWeights) : nullptr;
-  if (row) {
-    for (int g = 0; g < kKvHeads; ++g) {
-      const float4 k = row_values(row, g, lane, fp8);
-      for (int x = c.row0[u]; x < c.row0[u + 1]; ++x) {
-        const int64_t pos = c.position(u, x);
-        if (t > pos || (t >= p.d.sinks && t <= pos - p.d.window)) continue;
-        for (int h = g * kGroup; h < (g + 1) * kGroup; ++h) {
-          const uint2 w = reinterpret_cast<const uint2*>(p.q + ((int64_t)x * kQHeads + h) * kHeadDim)[lane];
-          float s = fmaf(bf16_hi(w.y), k.w, fmaf(bf16_lo(w.y), k.z, fmaf(bf16_hi(w.x), k.y, bf16_lo(w.x) * k.x)));
+  // steps that some query sees: from the first to the last token it sees here
+  const bool all_hidden = nq == 0 || (t0 >= p.d.sinks && t1 - 1 <= pos0 - p.d.window);
+  const int steps = all_hidden ? 0 : (int)((t1 - t0 + kFewStep - 1) / kFewStep);
+
+  uint32_t qa[8][4];
+  float f[2];
+  few_queries<kFp8>(p.q, x0, nq, g, p.scale_log2, qa, f);
+  float2 col[2];                                                 // rows r and r + 8: query * 4 + head
+  bool live[2];
+  int64_t pos[2];
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-          const float lse = p.lse[(int64_t)x * kQHeads + h];
-          if (lse != -INFINITY) sum += exp2f(fmaf(s, p.scale_log2, -lse * kLog2e));
+  for (int hi = 0; hi < 2; ++hi) {
+    const int row = r + 8 * hi, qi = row >> 2;
+    const float lse = qi < nq ? p.lse[(int64_t)(x0 + qi) * kQHeads + g * kGroup + (row & 3)] : -INFINITY;
+    live[hi] = lse != -INFINITY;
+    col[hi] = column_of(lse);
+    pos[hi] = pos0 + qi;
+  }
+  const int32_t* slots = b.slot_table + b.unit_row(u);
+  const uint32_t ring = smem_u32(smem) + warp * kFewStages * L::kStage;
+  float* sums = reinterpret_cast<float*>(smem + L::kSums) + g * p.few_tokens;
+  const int64_t first = t0 + half * kFewTokens;
+  auto token_of = [&](int s) {                                   // lane l < 16: token l of a stage, -1: none that counts
+    const int64_t t = first + (int64_t)s * kFewStep + lane;
+    return lane < kFewTokens && s < steps && t < t1 && seen_by_any(p.d, u, t) ? t : (int64_t)-1;
+  };
+  auto slot_of = [&](int s) {
+    const int64_t t = token_of(s);
+    return t >= 0 ? slots[t] : -2;
+  };
+  auto issue = [&](int s, int32_t slot) {
+    const int64_t t = token_of(s);
+    const uint8_t* row = nullptr;
+    if (t >= 0) {
+      if (slot >= 0 && (int64_t)slot < b.pool_rows) row = b.pool + (int64_t)slot * b.row_bytes;
+      else if (slot == -1 && b.u[u].host_rows) row = b.u[u].host_rows + t * b.row_bytes;
+      else report_error(b.err, QSA_ERR_BAD_SLOT, kKernWeights, ((int64_t)u << 40) | (t & 0xFFFFFFFFFFll));
+    }
+    const uint32_t have = __ballot_sync(0xFFFFFFFFu, row != nullptr);
+    if (lane == 0) there[warp][s % kFewStages] = have;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row ? row : b.pool);
+    const uint32_t to = ring + (s % kFewStages) * L::kStage;
+    constexpr int kLanes = L::kVec / 16, kPer = 32 / kLanes;     // lanes of a key, keys of a turn
+    const int c = lane % kLanes;
+    const uint32_t off = g * L::kVec + c * 16;
+#pragma unroll
+    for (int i = 0; i < kFewTokens / kPer; ++i) {
+      const int k = i * kPer + lane / kLanes;
+      const uintptr_t a = __shfl_sync(0xFFFFFFFFu, at, k);
+      cp_async16(to + k * L::kVec + ((c ^ (k & 7)) << 4), reinterpret_cast<const uint8_t*>(a) + off,
+                 (have >> k) & 1u ? 16u : 0u);
+    }
+    if (kFp8 && lane < kFewTokens)
+      cp_async16(to + L::kScales + lane * 16, reinterpret_cast<const uint8_t*>(at) + 2 * kKvHeads * kHeadDim,
+                 (have >> lane) & 1u ? 16u : 0u);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  {
+    const int32_t a = slot_of(0), c = slot_of(1);
+    issue(0, a);
+    issue(1, c);
+  }
+  int32_t slot_next = slot_of(2);
+#pragma unroll 1
+  for (int s = 0; s < steps; ++s) {
+    const int32_t slot = slot_next;
+    slot_next = slot_of(s + 3);
+    issue(s + 2, slot);
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+    __syncwarp();
+    const uint32_t st = ring + (s % kFewStages) * L::kStage;
+    const uint32_t have = there[warp][s % kFewStages];
+    float x[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t kb[4];
+      few_keys<kFp8>(st, k, kb);
+      mma16<kFp8>(x[0], qa[k], kb[0], kb[1]);
+      mma16<kFp8>(x[1], qa[k], kb[2], kb[3]);
+    }
+    float w[4];                                                  // tokens 2 j4, + 1, 8 + 2 j4, + 1; rows r and r + 8
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = 8 * i + 2 * j4 + e;
+        const int64_t t = first + (int64_t)s * kFewStep + c;
+        float ks = 1.f;
+        if (kFp8) ks = __half2float(*reinterpret_cast<const __half*>(smem + (st - smem_u32(smem)) + L::kScales + c * 16 + 2 * g));
+        float sum = 0.f;
+#pragma unroll
+        for (int hi = 0; hi < 2; ++hi) {
+          const float y = exp2_fast(fmaf(x[i][2 * hi + e] * ks, f[hi], col[hi].x)) * col[hi].y;
+          if (live[hi] && ((have >> c) & 1u) && sees(p.d, pos[hi], t)) sum += y;
         }
+        w[2 * i + e] = sum;
       }
+    // sums over the lanes of a column: lane keeps token 8 (lane >> 4 & 1) + 2 j4 + (lane >> 3 & 1)
+    const bool hi16 = lane & 16, hi8 = lane & 8;
+    float a = (hi16 ? w[2] : w[0]) + __shfl_xor_sync(0xFFFFFFFFu, hi16 ? w[0] : w[2], 16);
+    float c = (hi16 ? w[3] : w[1]) + __shfl_xor_sync(0xFFFFFFFFu, hi16 ? w[1] : w[3], 16);
+    float v = (hi8 ? c : a) + __shfl_xor_sync(0xFFFFFFFFu, hi8 ? a : c, 8);
+    v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+    if (!(lane & 4)) sums[s * kFewStep + half * kFewTokens + 8 * (lane >> 4) + 2 * j4 + ((lane >> 3) & 1)] = v;
+    __syncwarp();
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  const float* all = reinterpret_cast<const float*>(smem + L::kSums);
+  for (int i = tid; i < (int)(t1 - t0); i += kFewThreads) {
+    if (steps == 0 && p.accumulate) break;
+    float w = 0.f;
+    if (steps > 0)
+      w = (all[i] + all[p.few_tokens + i]) + (all[2 * p.few_tokens + i] + all[3 * p.few_tokens + i]);
+    store_weight(p, u, t0 + i, w);
+  }
+}
+
+// ------------------------------------------------------------------- wide
+
+// Units of more queries: one CTA per 256 tokens, in two tiles of 128 = the tensor
+// core's M; a turn is 32 queries x 4 heads of a KV head = 128 columns (N), K = 128
+// dims, both operands in shared memory under the 128-byte swizzle.  K[g] of the 256
+// tokens (64 KiB, two buffers) stays for all of the chunk's queries, Q streams past
+// (32 KiB a turn, two buffers, from L2): 64 KiB of Q per 128 tokens and turn would
+// be more than L2 gives.  Tensor memory: two buffers of two accumulators of 128
+// columns.  Warps: 8 epilogue (thread = token), 4 loaders, 1 MMA; all waits bounded.
+// Bound by the exponentials: 16 a cycle and SM, twice the tensor core's time.
+constexpr int kTokens = 256, kTurnQueries = 32, kTurnCols = kTurnQueries * kGroup;
+constexpr int kEpiWarps = 8, kLoadWarps = 4;
+constexpr int kWideThreads = 32 * (kEpiWarps + kLoadWarps + 1);
+constexpr int kRoleLoad = kEpiWarps, kRoleMma = kEpiWarps + kLoadWarps;
+constexpr int kPanel = 128 * 128;
+constexpr int kKBytes = 2 * 2 * kPanel, kQBytes = 2 * kPanel;     // two tiles, two panels of 64 dims
+struct __align__(16) Columns {
+  float minus[kTurnCols];        // -lse (log2)
+  float factor[kTurnCols];       // what its rounding leaves
+  float scale[kTurnCols];        // of the product (FP8: with the query row's power of two)
+  int32_t dead[kLoadWarps];      // per loader warp: a column without weight
+  int32_t pad[4];
+};
+// Columns of turn i are written behind the products of turn i - 2, whose
+// accumulators the epilogue of turn i - 4 had left: four of them.
+constexpr int kColumns = 4;
+constexpr int kOffK = 0, kOffQ = 2 * kKBytes, kOffCols = kOffQ + 2 * kQBytes;
+constexpr int kOffKs = kOffCols + kColumns * (int)sizeof(Columns);              // float [4][256]: K scales
+constexpr int kOffThere = kOffKs + kKvHeads * kTokens * 4;                      // uint32 [8]: tokens that count
+constexpr int kOffBar = kOffThere + 32;
+constexpr int kNumBars = 8;      // full[2], empty[2], d_full[2], d_empty[2]
+constexpr int kOffSlot = kOffBar + 8 * kNumBars;
+constexpr int kWideSmem = kOffSlot + 16 + 1024;
+static_assert(kWideSmem <= 227 * 1024 && kOffCols % 16 == 0 && kOffBar % 8 == 0, "one CTA's shared memory");
+constexpr uint32_t kTmemCols = 512;
+
+template <bool kFp8>
+__global__ void __launch_bounds__(kWideThreads, 1) weight_wide_kernel(const __grid_constant__ WeightParams p) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sb = smem_u32(smem);
+  Columns* columns = reinterpret_cast<Columns*>(smem + kOffCols);
+  float* key_scale = reinterpret_cast<float*>(smem + kOffKs);
+  uint32_t* there = reinterpret_cast<uint32_t*>(smem + kOffThere);
+  const uint32_t bars = sb + kOffBar;
+  auto full = [&](int i) { return bars + 8u * (uint32_t)(i & 1); };
+  auto empty = [&](int i) { return bars + 8u * (uint32_t)(2 + (i & 1)); };
+  auto d_full = [&](int i) { return bars + 8u * (uint32_t)(4 + (i & 1)); };
+  auto d_empty = [&](int i) { return bars + 8u * (uint32_t)(6 + (i & 1)); };
+  uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kOffSlot);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const BatchDesc& b = p.d.c.b;
+  ErrorWord* err = b.err;
+  const int u = blockIdx.y, nq = p.d.c.unit_tokens(u), x0 = p.d.c.row0[u];
+  const int64_t n = b.u[u].n, t0 = (int64_t)blockIdx.x * kTokens;
+  if (nq <= kFewQueries || t0 >= n) return;
+  const int64_t pos0 = n - nq, t1 = t0 + kTokens < n ? t0 + kTokens : n;
+  grid_dependency_wait();
+
+  // ---- the queries that see any of the tokens: q0 .. q1 - 1 in whole turns
+  int64_t low = t0 - pos0, high = t0 < p.d.sinks ? nq : t1 - 1 + p.d.window - pos0;       // positions t0 .. t1 - 1 + window - 1
+  if (low < 0) low = 0;
+  if (high > nq) high = nq;
+  const int c0 = (int)(low / kTurnQueries), c1 = high > low ? (int)((high + kTurnQueries - 1) / kTurnQueries) : c0;
+  const int per = c1 - c0, turns = kKvHeads * per;               // turn i: KV head i / per, queries 32 (c0 + i % per) ..
+  if (turns == 0) {
+    if (!p.accumulate && tid < t1 - t0) store_weight(p, u, t0 + tid, 0.f);
+    return;
+  }
+
+  if (warp == kRoleMma) {
+    tmem_alloc<kTmemCols>(slot);
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(full(i), 32 * kLoadWarps);
+        mbar_init(empty(i), 1);
+        mbar_init(d_full(i), 2);
+        mbar_init(d_empty(i), 32 * kEpiWarps);
+      }
+      mbar_fence_init();
     }
   }
-  if (lane == 0) {
-    float* w = p.weights + u * p.stride + t;
-    *w = p.accumulate ? *w + sum : sum;
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *slot;
+  bool ok = true;
+
+  if (warp >= kRoleLoad && warp < kRoleMma) {
+    // ---- loaders: warp w has the tokens 64 w .. 64 w + 63, lane = token of 32
+    const int w = warp - kRoleLoad;
+    const uint8_t* row[2];
+    uint32_t exist[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int64_t t = t0 + 64 * w + 32 * k + lane;
+      row[k] = nullptr;
+      if (t < t1 && seen_by_any(p.d, u, t)) {
+        const int32_t s = b.slot_table[b.unit_row(u) + t];
+        if (s >= 0 && (int64_t)s < b.pool_rows) row[k] = b.pool + (int64_t)s * b.row_bytes;
+        else if (s == -1 && b.u[u].host_rows) row[k] = b.u[u].host_rows + t * b.row_bytes;
+        else report_error(err, QSA_ERR_BAD_SLOT, kKernWeights, ((int64_t)u << 40) | (t & 0xFFFFFFFFFFll));
+      }
+      exist[k] = __ballot_sync(0xFFFFFFFFu, row[k] != nullptr);
+      if (lane == 0) there[2 * w + k] = exist[k];
+    }
+    // K[g] of the warp's tokens into buffer g % 2
+    auto load_keys = [&](int g) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t r0 = (w & 1) * 64 + 32 * k;               // row in the tile of 128
+        const uint32_t dst = kOffK + (g & 1) * kKBytes + (w >> 1) * 2 * kPanel + r0 * 128;
+        const uintptr_t from = reinterpret_cast<uintptr_t>(row[k] ? row[k] : b.pool);
+        const uint32_t have = exist[k];
+        if (!kFp8) {
+          const uint32_t c = lane & 15, hi = lane >> 4;
+          const uint32_t to = sb + dst + (c >> 3) * kPanel;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t t = 2 * i + hi;
+            const uintptr_t a = __shfl_sync(0xFFFFFFFFu, from, (int)t);
+            cp_async16(to + t * 128 + (((c & 7) ^ (t & 7)) << 4), reinterpret_cast<const uint8_t*>(a) + g * 256 + c * 16,
+                       (have >> t) & 1u ? 16u : 0u);
+          }
+        } else {
+          const uint32_t c = lane & 7, four = lane >> 3;
+          uint4 kv[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t t = 4 * i + four;
+            const uintptr_t a = __shfl_sync(0xFFFFFFFFu, from, (int)t);
+            kv[i] = (have >> t) & 1u ? *reinterpret_cast<const uint4*>(a + g * kHeadDim + c * 16) : make_uint4(0, 0, 0, 0);
+          }
+          uint16_t raw = 0;
+          if (row[k]) raw = reinterpret_cast<const uint16_t*>(row[k] + 2 * kKvHeads * kHeadDim)[g];
+          key_scale[g * kTokens + 64 * w + 32 * k + lane] = __half2float(__ushort_as_half(raw));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t t = 4 * i + four, ch = (2 * c) & 7, sw = (r0 + t) & 7;
+            uint8_t* to = smem + dst + (c >> 2) * kPanel + t * 128;
+            *reinterpret_cast<uint4*>(to + ((ch ^ sw) << 4)) = codes8_f16(make_uint2(kv[i].x, kv[i].y));
+            *reinterpret_cast<uint4*>(to + (((ch + 1) ^ sw) << 4)) = codes8_f16(make_uint2(kv[i].z, kv[i].w));
+          }
+        }
+      }
+    };
+    // turn i's Q (column query * 4 + head) and columns
+    auto load_queries = [&](int i) {
+      const int g = i / per, qa = (c0 + i % per) * kTurnQueries;
+      Columns& m = columns[i % kColumns];
+      const uint32_t dst = kOffQ + (i & 1) * kQBytes;
+      const int col = 32 * w + lane, qc = qa + col / kGroup;     // this thread's column
+      float scale = p.scale_log2;
+#pragma unroll
+      for (int k0 = 0; k0 < 16; k0 += 8) {                       // 16 turns of 2 columns, 16 lanes each
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int cc = 32 * w + 2 * (k0 + k) + (lane >> 4), q = qa + cc / kGroup;
+          const uint16_t* from = p.q + ((int64_t)(x0 + q) * kQHeads + g * kGroup + cc % kGroup) * kHeadDim;
+          if (!kFp8)
+            cp_async16(sb + dst + ((lane & 15) >> 3) * kPanel + cc * 128 + (((lane & 7) ^ (cc & 7)) << 4),
+                       q < nq ? from + (lane & 15) * 8 : p.q, q < nq ? 16u : 0u);
+          else
+            v[k] = q < nq ? reinterpret_cast<const uint4*>(from)[lane & 15] : make_uint4(0, 0, 0, 0);
+        }
+        if (kFp8) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int cc = 32 * w + 2 * (k0 + k) + (lane >> 4);
+            uint32_t* e4[4] = {&v[k].x, &v[k].y, &v[k].z, &v[k].w};
+            float top = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(*e4[e])), fabsf(bf16_hi(*e4[e]))));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));   // the column's 16 lanes
+            int ex = 0;
+            if (top > 0.f && top < INFINITY) frexpf(top, &ex);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) *e4[e] = pack_f16(ldexpf(bf16_lo(*e4[e]), 15 - ex), ldexpf(bf16_hi(*e4[e]), 15 - ex));
+            *reinterpret_cast<uint4*>(smem + dst + ((lane & 15) >> 3) * kPanel + cc * 128 + (((lane & 7) ^ (cc & 7)) << 4)) = v[k];
+            const int e0 = __shfl_sync(0xFFFFFFFFu, ex, 0), e1 = __shfl_sync(0xFFFFFFFFu, ex, 16);
+            if ((lane >> 1) == k0 + k) scale = p.scale_log2 * ldexpf(1.f, ((lane & 1) ? e1 : e0) - 15);
+          }
+        }
+      }
+      const float lse = qc < nq ? p.lse[(int64_t)(x0 + qc) * kQHeads + g * kGroup + col % kGroup] : -INFINITY;
+      const float2 k = column_of(lse);
+      m.minus[col] = k.x;
+      m.factor[col] = k.y;
+      m.scale[col] = scale;
+      const bool dead = __any_sync(0xFFFFFFFFu, lse == -INFINITY);
+      if (lane == 0) m.dead[w] = dead;
+    };
+    for (int i = 0; i <= turns && ok; ++i) {
+      if (i < turns) {
+        if (i >= 2) ok = mbar_wait_warp(empty(i), (uint32_t)(i / 2 - 1) & 1u, err, kKernWeights);
+        if (!ok) break;
+        if (i % per == 0) load_keys(i / per);
+        load_queries(i);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (i > 0) {                                   // turn i - 1 has landed
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        fence_async_smem();
+        mbar_arrive(full(i - 1));
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  } else if (warp == kRoleMma) {
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    for (int i = 0; i < turns && ok; ++i) {
+      const int g = i / per, left = nq - (c0 + i % per) * kTurnQueries;
+      const uint32_t cols = left >= kTurnQueries ? kTurnCols : (uint32_t)((left * kGroup + 15) / 16 * 16);
+      ok = mbar_wait_warp(full(i), (uint32_t)(i / 2) & 1u, err, kKernWeights);
+      if (ok && i >= 2) ok = mbar_wait_warp(d_empty(i), (uint32_t)(i / 2 - 1) & 1u, err, kKernWeights);
+      if (!ok) break;
+      fence_after();
+      if (elect_one()) {
+        const uint32_t id = kFp8 ? idesc_f16(cols, false) : idesc_bf16(cols, false);
+        const uint64_t qd = desc_sw128(sb + kOffQ + (i & 1) * kQBytes, 16);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const uint64_t kd = desc_sw128(sb + kOffK + (g & 1) * kKBytes + m * 2 * kPanel, 16);
+#pragma unroll
+          for (int k = 0; k < kHeadDim / 16; ++k) {
+            const uint64_t o = (uint64_t)(((k >> 2) * kPanel + (k & 3) * 32) >> 4);
+            mma_ss(tm + (uint32_t)((i & 1) * 2 + m) * 128u, kd + o, qd + o, id, k != 0);
+          }
+        }
+        mbar_arrive(d_full(i));                      // passes on the loaders' writes of the columns
+        commit(d_full(i));
+        commit(empty(i));
+      }
+      __syncwarp();
+    }
+    // every product is complete before tensor memory is given back
+    for (int i = turns - 2; i < turns; ++i)
+      if (i >= 0) mbar_wait_warp(empty(i), (uint32_t)(i / 2) & 1u, err, kKernWeights);
+  } else if (warp < kRoleLoad) {
+    // ---- epilogue: thread = token
+    const int m = warp >> 2, at = 128 * m + 32 * (warp & 3) + lane;
+    const int64_t t = t0 + at;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    // queries that see the token
+    int64_t qlo = t - pos0, qhi = t < p.d.sinks ? nq : t + p.d.window - pos0;
+    if (qlo < 0) qlo = 0;
+    if (qhi > nq) qhi = nq;
+    float total = 0.f, ks = 1.f;
+    bool mine = false;
+#pragma unroll 1
+    for (int i = 0; i < turns; ++i) {
+      const int g = i / per, qa = (c0 + i % per) * kTurnQueries;
+      ok = mbar_wait_warp(d_full(i), (uint32_t)(i / 2) & 1u, err, kKernWeights);
+      if (!ok) break;
+      fence_after();
+      if (i == 0) mine = (there[at >> 5] >> (at & 31)) & 1u;
+      if (kFp8) ks = key_scale[g * kTokens + at];
+      const Columns& cm = columns[i % kColumns];
+      // columns a .. z - 1 count for this token
+      const int a = qlo > qa ? (qlo - qa > kTurnQueries ? kTurnCols : (int)(qlo - qa) * kGroup) : 0;
+      const int z = qhi < qa ? 0 : (qhi - qa > kTurnQueries ? kTurnCols : (int)(qhi - qa) * kGroup);
+      const bool plain = __all_sync(0xFFFFFFFFu, a == 0 && z == kTurnCols) && !(cm.dead[0] | cm.dead[1] | cm.dead[2] | cm.dead[3]);
+      const uint32_t d = lane_base + (uint32_t)((i & 1) * 2 + m) * 128u;
+      const int left = (nq - qa) * kGroup;           // columns there are
+      const uint64_t ks2 = pair(ks, ks);
+      uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll 1
+      for (int c = 0; c < kTurnCols && c < left; c += 32) {
+        uint32_t v[32];
+        ld32(d + (uint32_t)c, v);
+        wait_ld();
+        reg_fence(v);
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+          const ulonglong2 mi = *reinterpret_cast<const ulonglong2*>(&cm.minus[c + k]);
+          const ulonglong2 fa = *reinterpret_cast<const ulonglong2*>(&cm.factor[c + k]);
+          uint64_t x01 = pair(v[k], v[k + 1]), x23 = pair(v[k + 2], v[k + 3]);
+          if (kFp8) {
+            const ulonglong2 sc = *reinterpret_cast<const ulonglong2*>(&cm.scale[c + k]);
+            x01 = fma2(mul2(x01, ks2), sc.x, mi.x);
+            x23 = fma2(mul2(x23, ks2), sc.y, mi.y);
+          } else {
+            const uint64_t f2 = pair(p.scale_log2, p.scale_log2);
+            x01 = fma2(x01, f2, mi.x);
+            x23 = fma2(x23, f2, mi.y);
+          }
+          float e[4] = {exp2_fast(lo_of(x01)), exp2_fast(hi_of(x01)), exp2_fast(lo_of(x23)), exp2_fast(hi_of(x23))};
+          if (!plain) {
+            const float mm[4] = {lo_of(mi.x), hi_of(mi.x), lo_of(mi.y), hi_of(mi.y)};
+            const bool in = c + k >= a && c + k < z; // (a query's four heads together)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (!in || mm[j] == -INFINITY || mm[j] == INFINITY) e[j] = 0.f;
+          }
+          sum[0] = fma2(pair(e[0], e[1]), fa.x, sum[0]);
+          sum[1] = fma2(pair(e[2], e[3]), fa.y, sum[1]);
+        }
+      }
+      fence_before();
+      mbar_arrive(d_empty(i));
+      const uint64_t s2 = add2(sum[0], sum[1]);
+      total += lo_of(s2) + hi_of(s2);
+    }
+    if (ok && t < t1) store_weight(p, u, t, mine ? total : 0.f);
   }
+
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == kRoleMma) tmem_free<kTmemCols>(tmem);
 }
 
 }  // namespace
 
 cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const float* lse, float softmax_scale,
                                   float* weights, int64_t stride, bool accumulate, cudaStream_t s) {
+  static PerDeviceOnce setup;
+  cudaError_t e = setup.run([] {
+    cudaError_t r = prefer_max_shared(weight_wide_kernel<false>, kWideSmem);
+    if (r == cudaSuccess) r = prefer_max_shared(weight_wide_kernel<true>, kWideSmem);
+    if (r == cudaSuccess) r = prefer_max_shared(weight_few_kernel<false>, FewLayout<false>::kSmem);
+    if (r == cudaSuccess) r = prefer_max_shared(weight_few_kernel<true>, FewLayout<true>::kSmem);
+    return r;
+  });
+  int sms = 0;
+  if (e == cudaSuccess) e = current_sm_count(&sms);
+  if (e != cudaSuccess) return e;
   WeightParams p;
   p.d = d;
   p.q = q;
@@ -65,10 +543,32 @@ cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const f
   p.weights = weights;
   p.stride = stride;
   p.accumulate = accumulate;
-  int64_t most = 0;
-  for (int u = 0; u < d.c.b.n_units; ++u) most = d.c.b.u[u].n > most ? d.c.b.u[u].n : most;
-  return launch_kernel(weight_token_kernel, dim3((unsigned)((most + 7) / 8), d.c.b.n_units), dim3(kThreads), 0, s, 0,
-                       dim3(1), p);
+  const bool fp8 = d.c.b.row_bytes == kRowBytesFp8;
+  int64_t wide = 0, few = 0, few_all = 0;            // the longest contexts; all tokens of few queries
+  for (int u = 0; u < d.c.b.n_units; ++u) {
+    const int64_t n = d.c.b.u[u].n;
+    if (d.c.unit_tokens(u) > kFewQueries) {
+      wide = n > wide ? n : wide;
+    } else {
+      few = n > few ? n : few;
+      few_all += n;
+    }
+  }
+  if (wide > 0)
+    e = launch_kernel(fp8 ? weight_wide_kernel<true> : weight_wide_kernel<false>,
+                      dim3((unsigned)((wide + kTokens - 1) / kTokens), d.c.b.n_units), dim3(kWideThreads), kWideSmem, s, 0,
+                      dim3(1), p);
+  if (e == cudaSuccess && few > 0) {
+    // two CTAs on an SM: as many runs of tokens as that, a step of 32 tokens to each warp pair
+    int64_t run = (few_all + 2 * sms - 1) / (2 * sms);
+    run = (run + kFewStep - 1) / kFewStep * kFewStep;
+    run = run < 2 * kFewStep ? 2 * kFewStep : (run > kFewMost ? kFewMost : run);
+    p.few_tokens = (int32_t)run;
+    e = launch_kernel(fp8 ? weight_few_kernel<true> : weight_few_kernel<false>,
+                      dim3((unsigned)((few + run - 1) / run), d.c.b.n_units), dim3(kFewThreads),
+                      fp8 ? FewLayout<true>::kSmem : FewLayout<false>::kSmem, s, 0, dim3(1), p);
+  }
+  return e;
 }
 
 }  // namespace qsa
