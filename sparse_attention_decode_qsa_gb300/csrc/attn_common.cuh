@@ -57,6 +57,19 @@ __device__ __forceinline__ float log2_size(float s) {
   return fmaxf(y, -100.f);
 }
 
+// The power of two that puts a largest size `top` into [2^14, 2^15), as two factors
+// (it may be past fp32's range as one), and its inverse; 1 for 0 and values that are
+// not finite.
+struct RowScale {
+  float a, b, inverse;
+};
+__device__ __forceinline__ RowScale row_scale(float top) {
+  int e = 15;
+  if (top > 0.f && top < INFINITY) frexpf(top, &e);
+  const int k = 15 - e, h = k >> 1;                  // -113 .. 164
+  return {__int_as_float((127 + h) << 23), __int_as_float((127 + k - h) << 23), ldexpf(1.f, -k)};
+}
+
 // Pairs of fp32 values: one instruction for two multiply-adds or additions.
 __device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) { return (uint64_t)a | ((uint64_t)b << 32); }
 __device__ __forceinline__ uint64_t pair(float a, float b) { return pair(__float_as_uint(a), __float_as_uint(b)); }

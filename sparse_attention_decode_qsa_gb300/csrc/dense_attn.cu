@@ -698,11 +698,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) dense_wide_kernel(const __gri
           for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(bf16_lo(*w[k])), fabsf(bf16_hi(*w[k]))));
 #pragma unroll
           for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));   // the row's 16 lanes
-          int e = 0;
-          if (top > 0.f && top < INFINITY) frexpf(top, &e);
+          const RowScale rs = row_scale(top);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) *w[k] = pack_f16(ldexpf(bf16_lo(*w[k]), 15 - e), ldexpf(bf16_hi(*w[k]), 15 - e));
-          if (c == 0) row_factor[h * 128 + r] = ldexpf(1.f, e - 15);
+          for (int k = 0; k < 4; ++k) *w[k] = pack_f16(bf16_lo(*w[k]) * rs.a * rs.b, bf16_hi(*w[k]) * rs.a * rs.b);
+          if (c == 0) row_factor[h * 128 + r] = rs.inverse;
         }
         *reinterpret_cast<uint4*>(smem + (h * 2 + (c >> 3)) * kPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
       }

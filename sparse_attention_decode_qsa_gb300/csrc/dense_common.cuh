@@ -80,17 +80,16 @@ __device__ __forceinline__ void few_queries(const uint16_t* q, int x0, int nq, i
     if (kFp8) {
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      int e = 0;
-      if (top > 0.f && top < INFINITY) frexpf(top, &e);
+      const RowScale sc = row_scale(top);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t& w = qa[k][2 * c + hi];
-          w = pack_f16(ldexpf(bf16_lo(w), 15 - e), ldexpf(bf16_hi(w), 15 - e));
+          w = pack_f16(bf16_lo(w) * sc.a * sc.b, bf16_hi(w) * sc.a * sc.b);
         }
       }
-      f[hi] *= ldexpf(1.f, e - 15);
+      f[hi] *= sc.inverse;
     }
   }
 }

@@ -9,9 +9,12 @@
 // could change, one store per token.  The queries that see a token are a range of
 // the chunk, hence a range of columns.
 //
-// exp(x - lse) goes through 2^y with y = x log2 e - lse log2 e: a rounding of the
-// second product would scale a whole row's weights by up to 2^-20, so its
-// remainder stays as a factor beside the column.
+// exp(x - lse) goes through 2^y with y = x log2 e - lse log2 e.  Roundings of
+// scale * log2 e and of lse * log2 e would go the same way in all of a row's weights
+// (2^-19 of them where logits reach 40), so both are kept in two parts: the first
+// in the multiplication, the second as a factor beside the column.
+#include <cmath>
+
 #include "dense_common.cuh"
 
 namespace qsa {
@@ -24,7 +27,7 @@ struct WeightParams {
   DenseAttn d;
   const uint16_t* q;             // [rows][16][128] bf16 bits
   const float* lse;              // [rows][16]
-  float scale_log2;              // softmax_scale * log2(e)
+  float scale_log2, scale_rest;  // softmax_scale * log2(e), in two parts
   float* weights;                // [units][stride]
   int64_t stride;
   int32_t accumulate;
@@ -92,7 +95,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
 
   uint32_t qa[8][4];
   float f[2];
-  few_queries<kFp8>(p.q, x0, nq, g, p.scale_log2, qa, f);
+  few_queries<kFp8>(p.q, x0, nq, g, 1.f, qa, f);
   float2 col[2];                                                 // rows r and r + 8: query * 4 + head
   bool live[2];
   int64_t pos[2];
@@ -181,7 +184,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
         float sum = 0.f;
 #pragma unroll
         for (int hi = 0; hi < 2; ++hi) {
-          const float y = exp2_fast(fmaf(x[i][2 * hi + e] * ks, f[hi], col[hi].x)) * col[hi].y;
+          const float z = x[i][2 * hi + e] * ks * f[hi];
+          const float y = exp2_fast(fmaf(z, p.scale_log2, fmaf(z, p.scale_rest, col[hi].x))) * col[hi].y;
           if (live[hi] && ((have >> c) & 1u) && sees(p.d, pos[hi], t)) sum += y;
         }
         w[2 * i + e] = sum;
@@ -209,69 +213,82 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
 
 // ------------------------------------------------------------------- wide
 
-// Units of more queries: one CTA per 256 tokens, in two tiles of 128 = the tensor
-// core's M; a turn is 32 queries x 4 heads of a KV head = 128 columns (N), K = 128
-// dims, both operands in shared memory under the 128-byte swizzle.  K[g] of the 256
-// tokens (64 KiB, two buffers) stays for all of the chunk's queries, Q streams past
-// (32 KiB a turn, two buffers, from L2): 64 KiB of Q per 128 tokens and turn would
-// be more than L2 gives.  Tensor memory: two buffers of two accumulators of 128
-// columns.  Warps: 8 epilogue (thread = token), 4 loaders, 1 MMA; all waits bounded.
-// Bound by the exponentials: 16 a cycle and SM, twice the tensor core's time.
-constexpr int kTokens = 256, kTurnQueries = 32, kTurnCols = kTurnQueries * kGroup;
+// Units of more queries: one CTA per 128 kTiles tokens, in tiles of 128 = the tensor
+// core's M; a turn is 32 / kTiles queries x 4 heads of a KV head = 128 / kTiles
+// columns (N), K = 128 dims, both operands in shared memory under the 128-byte
+// swizzle.  K[g] of the tokens (two buffers) stays for all of the chunk's queries,
+// Q streams past in a ring of four turns (from L2: with two tiles every query is
+// read half as often, with one there are twice as many CTAs).  Tensor memory: a ring
+// of four turns of 128 columns.  Warps: 8 epilogue (thread = token, 64 columns a
+// turn), 4 load K, 4 load Q, 1 MMA; all waits bounded.  Bound by the exponentials:
+// 16 a cycle and SM, 1024 cycles a turn, twice the tensor core's time.
 constexpr int kEpiWarps = 8, kLoadWarps = 4;
-constexpr int kWideThreads = 32 * (kEpiWarps + kLoadWarps + 1);
-constexpr int kRoleLoad = kEpiWarps, kRoleMma = kEpiWarps + kLoadWarps;
-constexpr int kPanel = 128 * 128;
-constexpr int kKBytes = 2 * 2 * kPanel, kQBytes = 2 * kPanel;     // two tiles, two panels of 64 dims
-struct __align__(16) Columns {
-  float minus[kTurnCols];        // -lse (log2)
-  float factor[kTurnCols];       // what its rounding leaves
-  float scale[kTurnCols];        // of the product (FP8: with the query row's power of two)
-  int32_t dead[kLoadWarps];      // per loader warp: a column without weight
-  int32_t pad[4];
-};
-// Columns of turn i are written behind the products of turn i - 2, whose
-// accumulators the epilogue of turn i - 4 had left: four of them.
-constexpr int kColumns = 4;
-constexpr int kOffK = 0, kOffQ = 2 * kKBytes, kOffCols = kOffQ + 2 * kQBytes;
-constexpr int kOffKs = kOffCols + kColumns * (int)sizeof(Columns);              // float [4][256]: K scales
-constexpr int kOffThere = kOffKs + kKvHeads * kTokens * 4;                      // uint32 [8]: tokens that count
-constexpr int kOffBar = kOffThere + 32;
-constexpr int kNumBars = 8;      // full[2], empty[2], d_full[2], d_empty[2]
-constexpr int kOffSlot = kOffBar + 8 * kNumBars;
-constexpr int kWideSmem = kOffSlot + 16 + 1024;
-static_assert(kWideSmem <= 227 * 1024 && kOffCols % 16 == 0 && kOffBar % 8 == 0, "one CTA's shared memory");
+constexpr int kWideThreads = 32 * (kEpiWarps + 2 * kLoadWarps + 1);
+constexpr int kRoleKeys = kEpiWarps, kRoleQueries = kRoleKeys + kLoadWarps, kRoleMma = kRoleQueries + kLoadWarps;
+constexpr int kRing = 4;
+constexpr int kPanel = 128 * 128;                 // 128 rows of 64 16-bit elements
+constexpr int kEpiCols = 64;
 constexpr uint32_t kTmemCols = 512;
 
-template <bool kFp8>
+template <int kTiles>
+struct Wide {
+  static constexpr int kTokens = 128 * kTiles, kQueries = 32 / kTiles, kCols = kQueries * kGroup;
+  struct __align__(16) Columns {
+    float minus[kCols];            // -lse (log2)
+    float factor[kCols];           // what its rounding leaves
+    float scale[kCols];            // FP8: the inverse of the query row's power of two
+    int32_t dead[kLoadWarps];      // per loader warp: a column without weight
+  };
+  // Columns of turn i are written once the products of turn i - 4 are complete,
+  // before which the epilogue of turn i - 8 had left its accumulators: eight.
+  static constexpr int kColumns = 2 * kRing;
+  static constexpr int kKBytes = kTiles * 2 * kPanel, kQPanel = kCols * 128, kQBytes = 2 * kQPanel;
+  static constexpr int kOffQ = 2 * kKBytes, kOffCols = kOffQ + kRing * kQBytes;
+  static constexpr int kOffKs = kOffCols + kColumns * (int)sizeof(Columns);     // float [4][kTokens]: K scales
+  static constexpr int kOffSum = kOffKs + kKvHeads * kTokens * 4;               // float [128]: the second column half's sums
+  static constexpr int kOffThere = kOffSum + 128 * 4;                           // uint32 [8]: tokens that count
+  static constexpr int kOffBar = kOffThere + 32;
+  static constexpr int kNumBars = 4 * kRing + 4;   // full, empty, d_full, d_empty [4], k_full, k_empty [2]
+  static constexpr int kOffSlot = kOffBar + 8 * kNumBars;
+  static constexpr int kSmem = kOffSlot + 16 + 1024;
+  static_assert(kSmem <= 227 * 1024 && kOffCols % 16 == 0 && kOffBar % 8 == 0 && kQBytes % 1024 == 0, "shared memory");
+};
+
+template <bool kFp8, int kTiles>
 __global__ void __launch_bounds__(kWideThreads, 1) weight_wide_kernel(const __grid_constant__ WeightParams p) {
+  using W = Wide<kTiles>;
+  using Columns = typename W::Columns;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
-  Columns* columns = reinterpret_cast<Columns*>(smem + kOffCols);
-  float* key_scale = reinterpret_cast<float*>(smem + kOffKs);
-  uint32_t* there = reinterpret_cast<uint32_t*>(smem + kOffThere);
-  const uint32_t bars = sb + kOffBar;
-  auto full = [&](int i) { return bars + 8u * (uint32_t)(i & 1); };
-  auto empty = [&](int i) { return bars + 8u * (uint32_t)(2 + (i & 1)); };
-  auto d_full = [&](int i) { return bars + 8u * (uint32_t)(4 + (i & 1)); };
-  auto d_empty = [&](int i) { return bars + 8u * (uint32_t)(6 + (i & 1)); };
-  uint32_t* slot = reinterpret_cast<uint32_t*>(smem + kOffSlot);
+  Columns* columns = reinterpret_cast<Columns*>(smem + W::kOffCols);
+  float* key_scale = reinterpret_cast<float*>(smem + W::kOffKs);
+  float* half_sum = reinterpret_cast<float*>(smem + W::kOffSum);
+  uint32_t* there = reinterpret_cast<uint32_t*>(smem + W::kOffThere);
+  const uint32_t bars = sb + W::kOffBar;
+  auto full = [&](int i) { return bars + 8u * (uint32_t)(i % kRing); };
+  auto empty = [&](int i) { return bars + 8u * (uint32_t)(kRing + i % kRing); };
+  auto d_full = [&](int i) { return bars + 8u * (uint32_t)(2 * kRing + i % kRing); };
+  auto d_empty = [&](int i) { return bars + 8u * (uint32_t)(3 * kRing + i % kRing); };
+  auto k_full = [&](int g) { return bars + 8u * (uint32_t)(4 * kRing + (g & 1)); };
+  auto k_empty = [&](int g) { return bars + 8u * (uint32_t)(4 * kRing + 2 + (g & 1)); };
+  auto turn_of = [](int i) { return (uint32_t)(i / kRing) & 1u; };
+  uint32_t* slot = reinterpret_cast<uint32_t*>(smem + W::kOffSlot);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const BatchDesc& b = p.d.c.b;
   ErrorWord* err = b.err;
   const int u = blockIdx.y, nq = p.d.c.unit_tokens(u), x0 = p.d.c.row0[u];
-  const int64_t n = b.u[u].n, t0 = (int64_t)blockIdx.x * kTokens;
+  const int64_t n = b.u[u].n, t0 = (int64_t)blockIdx.x * W::kTokens;
   if (nq <= kFewQueries || t0 >= n) return;
-  const int64_t pos0 = n - nq, t1 = t0 + kTokens < n ? t0 + kTokens : n;
+  const int64_t pos0 = n - nq, t1 = t0 + W::kTokens < n ? t0 + W::kTokens : n;
   grid_dependency_wait();
 
-  // ---- the queries that see any of the tokens: q0 .. q1 - 1 in whole turns
-  int64_t low = t0 - pos0, high = t0 < p.d.sinks ? nq : t1 - 1 + p.d.window - pos0;       // positions t0 .. t1 - 1 + window - 1
+  // ---- the queries that see any of the tokens (positions t0 .. t1 - 1 + window - 1), in whole turns
+  int64_t low = t0 - pos0, high = t0 < p.d.sinks ? nq : t1 - 1 + p.d.window - pos0;
   if (low < 0) low = 0;
   if (high > nq) high = nq;
-  const int c0 = (int)(low / kTurnQueries), c1 = high > low ? (int)((high + kTurnQueries - 1) / kTurnQueries) : c0;
-  const int per = c1 - c0, turns = kKvHeads * per;               // turn i: KV head i / per, queries 32 (c0 + i % per) ..
+  const int c0 = (int)(low / W::kQueries), c1 = high > low ? (int)((high + W::kQueries - 1) / W::kQueries) : c0;
+  const int per = c1 - c0, turns = kKvHeads * per;   // turn i: KV head i / per, queries kQueries (c0 + i % per) ..
   if (turns == 0) {
     if (!p.accumulate && tid < t1 - t0) store_weight(p, u, t0 + tid, 0.f);
     return;
@@ -280,11 +297,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) weight_wide_kernel(const __gr
   if (warp == kRoleMma) {
     tmem_alloc<kTmemCols>(slot);
     if (lane == 0) {
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kRing; ++i) {
         mbar_init(full(i), 32 * kLoadWarps);
         mbar_init(empty(i), 1);
         mbar_init(d_full(i), 2);
         mbar_init(d_empty(i), 32 * kEpiWarps);
+      }
+      for (int g = 0; g < 2; ++g) {
+        mbar_init(k_full(g), 32 * kLoadWarps);
+        mbar_init(k_empty(g), 1);
       }
       mbar_fence_init();
     }
@@ -295,14 +316,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) weight_wide_kernel(const __gr
   const uint32_t tmem = *slot;
   bool ok = true;
 
-  if (warp >= kRoleLoad && warp < kRoleMma) {
-    // ---- loaders: warp w has the tokens 64 w .. 64 w + 63, lane = token of 32
-    const int w = warp - kRoleLoad;
-    const uint8_t* row[2];
-    uint32_t exist[2];
+  if (warp >= kRoleKeys && warp < kRoleQueries) {
+    // ---- K: warp w has the tokens 32 kTiles w .. of the CTA's, lane = token of 32
+    const int w = warp - kRoleKeys;
+    const uint8_t* row[kTiles];
+    uint32_t exist[kTiles];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int64_t t = t0 + 64 * w + 32 * k + lane;
+    for (int k = 0; k < kTiles; ++k) {
+      const int64_t t = t0 + 32 * (kTiles * w + k) + lane;
       row[k] = nullptr;
       if (t < t1 && seen_by_any(p.d, u, t)) {
         const int32_t s = b.slot_table[b.unit_row(u) + t];
@@ -311,16 +332,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) weight_wide_kernel(const __gr
         else report_error(err, QSA_ERR_BAD_SLOT, kKernWeights, ((int64_t)u << 40) | (t & 0xFFFFFFFFFFll));
       }
       exist[k] = __ballot_sync(0xFFFFFFFFu, row[k] != nullptr);
-      if (lane == 0) there[2 * w + k] = exist[k];
+      if (lane == 0) there[kTiles * w + k] = exist[k];
     }
-    // K[g] of the warp's tokens into buffer g % 2
-    auto load_keys = [&](int g) {
+    for (int g = 0; g < kKvHeads && ok; ++g) {
+      if (g >= 2) ok = mbar_wait_warp(k_empty(g), 0, err, kKernWeights);
+      if (!ok) break;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t r0 = (w & 1) * 64 + 32 * k;               // row in the tile of 128
-        const uint32_t dst = kOffK + (g & 1) * kKBytes + (w >> 1) * 2 * kPanel + r0 * 128;
+      for (int k = 0; k < kTiles; ++k) {
+        const int at = 32 * (kTiles * w + k);                    // of the CTA's tokens
+        const uint32_t r0 = at & 127;                            // row in its tile
+        const uint32_t dst = (g & 1) * W::kKBytes + (at >> 7) * 2 * kPanel + r0 * 128;
         const uintptr_t from = reinterpret_cast<uintptr_t>(row[k] ? row[k] : b.pool);
-        const uint32_t have = exist[k];
         if (!kFp8) {
           const uint32_t c = lane & 15, hi = lane >> 4;
           const uint32_t to = sb + dst + (c >> 3) * kPanel;
@@ -329,7 +351,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) weight_wide_kernel(const __gr
             const uint32_t t = 2 * i + hi;
             const uintptr_t a = __shfl_sync(0xFFFFFFFFu, from, (int)t);
             cp_async16(to + t * 128 + (((c & 7) ^ (t & 7)) << 4), reinterpret_cast<const uint8_t*>(a) + g * 256 + c * 16,
-                       (have >> t) & 1u ? 16u : 0u);
+                       (exist[k] >> t) & 1u ? 16u : 0u);
           }
         } else {
           const uint32_t c = lane & 7, four = lane >> 3;
@@ -338,166 +360,176 @@ __global__ void __launch_bounds__(kWideThreads, 1) weight_wide_kernel(const __gr
           for (int i = 0; i < 8; ++i) {
             const uint32_t t = 4 * i + four;
             const uintptr_t a = __shfl_sync(0xFFFFFFFFu, from, (int)t);
-            kv[i] = (have >> t) & 1u ? *reinterpret_cast<const uint4*>(a + g * kHeadDim + c * 16) : make_uint4(0, 0, 0, 0);
+            kv[i] = (exist[k] >> t) & 1u ? *reinterpret_cast<const uint4*>(a + g * kHeadDim + c * 16) : make_uint4(0, 0, 0, 0);
           }
           uint16_t raw = 0;
           if (row[k]) raw = reinterpret_cast<const uint16_t*>(row[k] + 2 * kKvHeads * kHeadDim)[g];
-          key_scale[g * kTokens + 64 * w + 32 * k + lane] = __half2float(__ushort_as_half(raw));
+          key_scale[g * W::kTokens + at + lane] = __half2float(__ushort_as_half(raw));
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint32_t t = 4 * i + four, ch = (2 * c) & 7, sw = (r0 + t) & 7;
+            const uint32_t t = 4 * i + four, ch = (2 * c) & 7, sw = t & 7;
             uint8_t* to = smem + dst + (c >> 2) * kPanel + t * 128;
             *reinterpret_cast<uint4*>(to + ((ch ^ sw) << 4)) = codes8_f16(make_uint2(kv[i].x, kv[i].y));
             *reinterpret_cast<uint4*>(to + (((ch + 1) ^ sw) << 4)) = codes8_f16(make_uint2(kv[i].z, kv[i].w));
           }
         }
       }
+      if (!kFp8) asm volatile("cp.async.commit_group;\n cp.async.wait_group 0;" ::: "memory");
+      fence_async_smem();
+      mbar_arrive(k_full(g));
+    }
+  } else if (warp >= kRoleQueries && warp < kRoleMma) {
+    // ---- Q: warp w has the columns kCols / 4 w .. of a turn, column query * 4 + head
+    const int w = warp - kRoleQueries;
+    constexpr int kMine = W::kCols / kLoadWarps;                 // 32 or 16
+    auto lse_of = [&](int i) {                                   // of this lane's column
+      const int g = i / per, col = kMine * w + lane, q = (c0 + i % per) * W::kQueries + col / kGroup;
+      return i < turns && lane < kMine && q < nq ? p.lse[(int64_t)(x0 + q) * kQHeads + g * kGroup + col % kGroup] : -INFINITY;
     };
-    // turn i's Q (column query * 4 + head) and columns
-    auto load_queries = [&](int i) {
-      const int g = i / per, qa = (c0 + i % per) * kTurnQueries;
-      Columns& m = columns[i % kColumns];
-      const uint32_t dst = kOffQ + (i & 1) * kQBytes;
-      const int col = 32 * w + lane, qc = qa + col / kGroup;     // this thread's column
-      float scale = p.scale_log2;
+    float lse_next = lse_of(0);
+    // cp.async: turn i - 2 has landed once turn i is on its way; FP8 has none
+    constexpr int kBehind = kFp8 ? 0 : 2;
+    for (int i = 0; i < turns + kBehind && ok; ++i) {
+      if (i < turns) {
+        const float lse = lse_next;
+        lse_next = lse_of(i + 1);
+        if (i >= kRing) ok = mbar_wait_warp(empty(i), turn_of(i - kRing), err, kKernWeights);
+        if (!ok) break;
+        const int g = i / per, qa = (c0 + i % per) * W::kQueries;
+        Columns& m = columns[i % W::kColumns];
+        const uint32_t dst = W::kOffQ + (i % kRing) * W::kQBytes;
+        float scale = 1.f;
 #pragma unroll
-      for (int k0 = 0; k0 < 16; k0 += 8) {                       // 16 turns of 2 columns, 16 lanes each
-        uint4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int cc = 32 * w + 2 * (k0 + k) + (lane >> 4), q = qa + cc / kGroup;
-          const uint16_t* from = p.q + ((int64_t)(x0 + q) * kQHeads + g * kGroup + cc % kGroup) * kHeadDim;
-          if (!kFp8)
-            cp_async16(sb + dst + ((lane & 15) >> 3) * kPanel + cc * 128 + (((lane & 7) ^ (cc & 7)) << 4),
-                       q < nq ? from + (lane & 15) * 8 : p.q, q < nq ? 16u : 0u);
-          else
-            v[k] = q < nq ? reinterpret_cast<const uint4*>(from)[lane & 15] : make_uint4(0, 0, 0, 0);
-        }
-        if (kFp8) {
+        for (int k0 = 0; k0 < kMine / 2; k0 += 8) {              // two columns at a time, 16 lanes each
+          uint4 v[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const int cc = 32 * w + 2 * (k0 + k) + (lane >> 4);
-            uint32_t* e4[4] = {&v[k].x, &v[k].y, &v[k].z, &v[k].w};
-            float top = 0.f;
+            const int cc = kMine * w + 2 * (k0 + k) + (lane >> 4), q = qa + cc / kGroup;
+            const uint16_t* from = p.q + ((int64_t)(x0 + q) * kQHeads + g * kGroup + cc % kGroup) * kHeadDim;
+            if (!kFp8)
+              cp_async16(sb + dst + ((lane & 15) >> 3) * W::kQPanel + cc * 128 + (((lane & 7) ^ (cc & 7)) << 4),
+                         q < nq ? from + (lane & 15) * 8 : p.q, q < nq ? 16u : 0u);
+            else
+              v[k] = q < nq ? reinterpret_cast<const uint4*>(from)[lane & 15] : make_uint4(0, 0, 0, 0);
+          }
+          if (kFp8) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(*e4[e])), fabsf(bf16_hi(*e4[e]))));
+            for (int k = 0; k < 8; ++k) {
+              const int cc = kMine * w + 2 * (k0 + k) + (lane >> 4);
+              uint32_t* e4[4] = {&v[k].x, &v[k].y, &v[k].z, &v[k].w};
+              float top = 0.f;
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));   // the column's 16 lanes
-            int ex = 0;
-            if (top > 0.f && top < INFINITY) frexpf(top, &ex);
+              for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(*e4[e])), fabsf(bf16_hi(*e4[e]))));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) *e4[e] = pack_f16(ldexpf(bf16_lo(*e4[e]), 15 - ex), ldexpf(bf16_hi(*e4[e]), 15 - ex));
-            *reinterpret_cast<uint4*>(smem + dst + ((lane & 15) >> 3) * kPanel + cc * 128 + (((lane & 7) ^ (cc & 7)) << 4)) = v[k];
-            const int e0 = __shfl_sync(0xFFFFFFFFu, ex, 0), e1 = __shfl_sync(0xFFFFFFFFu, ex, 16);
-            if ((lane >> 1) == k0 + k) scale = p.scale_log2 * ldexpf(1.f, ((lane & 1) ? e1 : e0) - 15);
+              for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));   // the column's 16 lanes
+              const RowScale rs = row_scale(top);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) *e4[e] = pack_f16(bf16_lo(*e4[e]) * rs.a * rs.b, bf16_hi(*e4[e]) * rs.a * rs.b);
+              *reinterpret_cast<uint4*>(smem + dst + ((lane & 15) >> 3) * W::kQPanel + cc * 128 + (((lane & 7) ^ (cc & 7)) << 4)) = v[k];
+              const float s0 = __shfl_sync(0xFFFFFFFFu, rs.inverse, 0), s1 = __shfl_sync(0xFFFFFFFFu, rs.inverse, 16);
+              if ((lane >> 1) == k0 + k) scale = lane & 1 ? s1 : s0;
+            }
           }
         }
+        const float2 k = column_of(lse);
+        if (lane < kMine) {
+          m.minus[kMine * w + lane] = k.x;
+          m.factor[kMine * w + lane] = k.y;
+          m.scale[kMine * w + lane] = scale;
+        }
+        const bool dead = __any_sync(0xFFFFFFFFu, lane < kMine && lse == -INFINITY);
+        if (lane == 0) m.dead[w] = dead;
       }
-      const float lse = qc < nq ? p.lse[(int64_t)(x0 + qc) * kQHeads + g * kGroup + col % kGroup] : -INFINITY;
-      const float2 k = column_of(lse);
-      m.minus[col] = k.x;
-      m.factor[col] = k.y;
-      m.scale[col] = scale;
-      const bool dead = __any_sync(0xFFFFFFFFu, lse == -INFINITY);
-      if (lane == 0) m.dead[w] = dead;
-    };
-    for (int i = 0; i <= turns && ok; ++i) {
-      if (i < turns) {
-        if (i >= 2) ok = mbar_wait_warp(empty(i), (uint32_t)(i / 2 - 1) & 1u, err, kKernWeights);
-        if (!ok) break;
-        if (i % per == 0) load_keys(i / per);
-        load_queries(i);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      if (i > 0) {                                   // turn i - 1 has landed
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      if (!kFp8) asm volatile("cp.async.commit_group;\n cp.async.wait_group 2;" ::: "memory");
+      if (i >= kBehind) {
         fence_async_smem();
-        mbar_arrive(full(i - 1));
+        mbar_arrive(full(i - kBehind));
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp == kRoleMma) {
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     for (int i = 0; i < turns && ok; ++i) {
-      const int g = i / per, left = nq - (c0 + i % per) * kTurnQueries;
-      const uint32_t cols = left >= kTurnQueries ? kTurnCols : (uint32_t)((left * kGroup + 15) / 16 * 16);
-      ok = mbar_wait_warp(full(i), (uint32_t)(i / 2) & 1u, err, kKernWeights);
-      if (ok && i >= 2) ok = mbar_wait_warp(d_empty(i), (uint32_t)(i / 2 - 1) & 1u, err, kKernWeights);
+      const int g = i / per, left = (nq - (c0 + i % per) * W::kQueries) * kGroup;
+      const uint32_t cols = left >= W::kCols ? W::kCols : (uint32_t)((left + 15) / 16 * 16);
+      if (i % per == 0) ok = mbar_wait_warp(k_full(g), (uint32_t)(g >> 1), err, kKernWeights);
+      if (ok) ok = mbar_wait_warp(full(i), turn_of(i), err, kKernWeights);
+      if (ok && i >= kRing) ok = mbar_wait_warp(d_empty(i), turn_of(i - kRing), err, kKernWeights);
       if (!ok) break;
       fence_after();
       if (elect_one()) {
         const uint32_t id = kFp8 ? idesc_f16(cols, false) : idesc_bf16(cols, false);
-        const uint64_t qd = desc_sw128(sb + kOffQ + (i & 1) * kQBytes, 16);
+        const uint64_t qd = desc_sw128(sb + W::kOffQ + (i % kRing) * W::kQBytes, 16);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const uint64_t kd = desc_sw128(sb + kOffK + (g & 1) * kKBytes + m * 2 * kPanel, 16);
+        for (int m = 0; m < kTiles; ++m) {
+          const uint64_t kd = desc_sw128(sb + (g & 1) * W::kKBytes + m * 2 * kPanel, 16);
 #pragma unroll
-          for (int k = 0; k < kHeadDim / 16; ++k) {
-            const uint64_t o = (uint64_t)(((k >> 2) * kPanel + (k & 3) * 32) >> 4);
-            mma_ss(tm + (uint32_t)((i & 1) * 2 + m) * 128u, kd + o, qd + o, id, k != 0);
-          }
+          for (int k = 0; k < kHeadDim / 16; ++k)
+            mma_ss(tm + (uint32_t)((i % kRing) * 128 + m * W::kCols), kd + (uint64_t)(((k >> 2) * kPanel + (k & 3) * 32) >> 4),
+                   qd + (uint64_t)(((k >> 2) * W::kQPanel + (k & 3) * 32) >> 4), id, k != 0);
         }
         mbar_arrive(d_full(i));                      // passes on the loaders' writes of the columns
         commit(d_full(i));
         commit(empty(i));
+        if (i % per == per - 1) commit(k_empty(g));
       }
       __syncwarp();
     }
     // every product is complete before tensor memory is given back
-    for (int i = turns - 2; i < turns; ++i)
-      if (i >= 0) mbar_wait_warp(empty(i), (uint32_t)(i / 2) & 1u, err, kKernWeights);
-  } else if (warp < kRoleLoad) {
-    // ---- epilogue: thread = token
-    const int m = warp >> 2, at = 128 * m + 32 * (warp & 3) + lane;
+    for (int i = turns > kRing ? turns - kRing : 0; i < turns; ++i) mbar_wait_warp(empty(i), turn_of(i), err, kKernWeights);
+  } else {
+    // ---- epilogue: thread = token; with one tile, warps 4 .. 7 take the second half of the columns
+    const int half = warp >> 2, at = (kTiles == 2 ? 128 * half : 0) + 32 * (warp & 3) + lane;
+    const int first = kTiles == 2 ? 0 : kEpiCols * half;         // its columns of a turn
     const int64_t t = t0 + at;
-    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(kEpiCols * half);
     // queries that see the token
     int64_t qlo = t - pos0, qhi = t < p.d.sinks ? nq : t + p.d.window - pos0;
     if (qlo < 0) qlo = 0;
     if (qhi > nq) qhi = nq;
-    float total = 0.f, ks = 1.f;
+    const uint64_t hi2 = pair(p.scale_log2, p.scale_log2), lo2 = pair(p.scale_rest, p.scale_rest);
+    float total = 0.f;
     bool mine = false;
 #pragma unroll 1
     for (int i = 0; i < turns; ++i) {
-      const int g = i / per, qa = (c0 + i % per) * kTurnQueries;
-      ok = mbar_wait_warp(d_full(i), (uint32_t)(i / 2) & 1u, err, kKernWeights);
+      const int g = i / per, qa = (c0 + i % per) * W::kQueries;
+      ok = mbar_wait_warp(d_full(i), turn_of(i), err, kKernWeights);
       if (!ok) break;
       fence_after();
       if (i == 0) mine = (there[at >> 5] >> (at & 31)) & 1u;
-      if (kFp8) ks = key_scale[g * kTokens + at];
-      const Columns& cm = columns[i % kColumns];
-      // columns a .. z - 1 count for this token
-      const int a = qlo > qa ? (qlo - qa > kTurnQueries ? kTurnCols : (int)(qlo - qa) * kGroup) : 0;
-      const int z = qhi < qa ? 0 : (qhi - qa > kTurnQueries ? kTurnCols : (int)(qhi - qa) * kGroup);
-      const bool plain = __all_sync(0xFFFFFFFFu, a == 0 && z == kTurnCols) && !(cm.dead[0] | cm.dead[1] | cm.dead[2] | cm.dead[3]);
-      const uint32_t d = lane_base + (uint32_t)((i & 1) * 2 + m) * 128u;
-      const int left = (nq - qa) * kGroup;           // columns there are
+      const float ks = kFp8 ? key_scale[g * W::kTokens + at] : 1.f;
       const uint64_t ks2 = pair(ks, ks);
+      const Columns& cm = columns[i % W::kColumns];
+      // columns a .. z - 1 count for this token
+      const int a = qlo > qa ? (qlo - qa > W::kQueries ? W::kCols : (int)(qlo - qa) * kGroup) : 0;
+      const int z = qhi < qa ? 0 : (qhi - qa > W::kQueries ? W::kCols : (int)(qhi - qa) * kGroup);
+      const bool plain = __all_sync(0xFFFFFFFFu, a == 0 && z == W::kCols) && !(cm.dead[0] | cm.dead[1] | cm.dead[2] | cm.dead[3]);
+      const uint32_t d = lane_base + (uint32_t)(i % kRing) * 128u;
+      const int left = (nq - qa) * kGroup;           // columns there are
       uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll 1
-      for (int c = 0; c < kTurnCols && c < left; c += 32) {
+      for (int c = 0; c < kEpiCols && first + c < left; c += 32) {
         uint32_t v[32];
         ld32(d + (uint32_t)c, v);
         wait_ld();
         reg_fence(v);
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
-          const ulonglong2 mi = *reinterpret_cast<const ulonglong2*>(&cm.minus[c + k]);
-          const ulonglong2 fa = *reinterpret_cast<const ulonglong2*>(&cm.factor[c + k]);
+          const int cc = first + c + k;
+          const ulonglong2 mi = *reinterpret_cast<const ulonglong2*>(&cm.minus[cc]);
+          const ulonglong2 fa = *reinterpret_cast<const ulonglong2*>(&cm.factor[cc]);
           uint64_t x01 = pair(v[k], v[k + 1]), x23 = pair(v[k + 2], v[k + 3]);
           if (kFp8) {
-            const ulonglong2 sc = *reinterpret_cast<const ulonglong2*>(&cm.scale[c + k]);
-            x01 = fma2(mul2(x01, ks2), sc.x, mi.x);
-            x23 = fma2(mul2(x23, ks2), sc.y, mi.y);
-          } else {
-            const uint64_t f2 = pair(p.scale_log2, p.scale_log2);
-            x01 = fma2(x01, f2, mi.x);
-            x23 = fma2(x23, f2, mi.y);
+            const ulonglong2 sc = *reinterpret_cast<const ulonglong2*>(&cm.scale[cc]);
+            x01 = mul2(mul2(x01, ks2), sc.x);
+            x23 = mul2(mul2(x23, ks2), sc.y);
           }
+          x01 = fma2(x01, hi2, fma2(x01, lo2, mi.x));
+          x23 = fma2(x23, hi2, fma2(x23, lo2, mi.y));
           float e[4] = {exp2_fast(lo_of(x01)), exp2_fast(hi_of(x01)), exp2_fast(lo_of(x23)), exp2_fast(hi_of(x23))};
           if (!plain) {
             const float mm[4] = {lo_of(mi.x), hi_of(mi.x), lo_of(mi.y), hi_of(mi.y)};
-            const bool in = c + k >= a && c + k < z; // (a query's four heads together)
+            const bool in = cc >= a && cc < z;       // (a query's four heads together)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (!in || mm[j] == -INFINITY || mm[j] == INFINITY) e[j] = 0.f;
@@ -511,7 +543,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) weight_wide_kernel(const __gr
       const uint64_t s2 = add2(sum[0], sum[1]);
       total += lo_of(s2) + hi_of(s2);
     }
-    if (ok && t < t1) store_weight(p, u, t, mine ? total : 0.f);
+    if (kTiles == 1) {
+      if (half == 1) half_sum[at] = total;
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+      total += half_sum[at];
+    }
+    if (ok && t < t1 && (kTiles == 2 || half == 0)) store_weight(p, u, t, mine ? total : 0.f);
   }
 
   fence_before();
@@ -526,8 +563,10 @@ cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const f
                                   float* weights, int64_t stride, bool accumulate, cudaStream_t s) {
   static PerDeviceOnce setup;
   cudaError_t e = setup.run([] {
-    cudaError_t r = prefer_max_shared(weight_wide_kernel<false>, kWideSmem);
-    if (r == cudaSuccess) r = prefer_max_shared(weight_wide_kernel<true>, kWideSmem);
+    cudaError_t r = prefer_max_shared(weight_wide_kernel<false, 1>, Wide<1>::kSmem);
+    if (r == cudaSuccess) r = prefer_max_shared(weight_wide_kernel<true, 1>, Wide<1>::kSmem);
+    if (r == cudaSuccess) r = prefer_max_shared(weight_wide_kernel<false, 2>, Wide<2>::kSmem);
+    if (r == cudaSuccess) r = prefer_max_shared(weight_wide_kernel<true, 2>, Wide<2>::kSmem);
     if (r == cudaSuccess) r = prefer_max_shared(weight_few_kernel<false>, FewLayout<false>::kSmem);
     if (r == cudaSuccess) r = prefer_max_shared(weight_few_kernel<true>, FewLayout<true>::kSmem);
     return r;
@@ -539,25 +578,38 @@ cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const f
   p.d = d;
   p.q = q;
   p.lse = lse;
-  p.scale_log2 = softmax_scale * kLog2e;
+  const double f = (double)softmax_scale * 1.4426950408889634;
+  // both parts of one sign, and neither 0: an infinite logit stays one
+  p.scale_log2 = (float)f;
+  if (fabs((double)p.scale_log2) > fabs(f)) p.scale_log2 = nextafterf(p.scale_log2, 0.f);
+  p.scale_rest = (float)(f - (double)p.scale_log2);
+  if (p.scale_rest == 0.f) p.scale_rest = p.scale_log2 * 0x1p-40f;
   p.weights = weights;
   p.stride = stride;
   p.accumulate = accumulate;
   const bool fp8 = d.c.b.row_bytes == kRowBytesFp8;
   int64_t wide = 0, few = 0, few_all = 0;            // the longest contexts; all tokens of few queries
+  int64_t seen = 0;                                  // tokens that more than a few queries see
   for (int u = 0; u < d.c.b.n_units; ++u) {
     const int64_t n = d.c.b.u[u].n;
-    if (d.c.unit_tokens(u) > kFewQueries) {
+    const int nq = d.c.unit_tokens(u);
+    if (nq > kFewQueries) {
       wide = n > wide ? n : wide;
+      const int64_t low = n - nq - d.window + 1;
+      seen += low > 0 ? n - low : n;
     } else {
       few = n > few ? n : few;
       few_all += n;
     }
   }
-  if (wide > 0)
-    e = launch_kernel(fp8 ? weight_wide_kernel<true> : weight_wide_kernel<false>,
-                      dim3((unsigned)((wide + kTokens - 1) / kTokens), d.c.b.n_units), dim3(kWideThreads), kWideSmem, s, 0,
-                      dim3(1), p);
+  if (wide > 0) {
+    // two tiles a CTA where that fills the device
+    const int tiles = seen >= (int64_t)sms * Wide<2>::kTokens ? 2 : 1;
+    const dim3 grid((unsigned)((wide + 128 * tiles - 1) / (128 * tiles)), d.c.b.n_units);
+    auto* kernel = fp8 ? (tiles == 2 ? weight_wide_kernel<true, 2> : weight_wide_kernel<true, 1>)
+                       : (tiles == 2 ? weight_wide_kernel<false, 2> : weight_wide_kernel<false, 1>);
+    e = launch_kernel(kernel, grid, dim3(kWideThreads), tiles == 2 ? Wide<2>::kSmem : Wide<1>::kSmem, s, 0, dim3(1), p);
+  }
   if (e == cudaSuccess && few > 0) {
     // two CTAs on an SM: as many runs of tokens as that, a step of 32 tokens to each warp pair
     int64_t run = (few_all + 2 * sms - 1) / (2 * sms);
