@@ -64,10 +64,15 @@ struct RowScale {
   float a, b, inverse;
 };
 __device__ __forceinline__ RowScale row_scale(float top) {
-  int e = 15;
-  if (top > 0.f && top < INFINITY) frexpf(top, &e);
-  const int k = 15 - e, h = k >> 1;                  // -113 .. 164
-  return {__int_as_float((127 + h) << 23), __int_as_float((127 + k - h) << 23), ldexpf(1.f, -k)};
+  int k = 0;
+  if (top > 0.f && top < INFINITY) {
+    const bool tiny = top < 0x1p-100f;               // (subnormals have no exponent to read)
+    const int e = (int)(__float_as_uint(tiny ? top * 0x1p60f : top) >> 23) - 127 - (tiny ? 60 : 0);
+    k = 14 - e;                                      // -113 .. 163
+  }
+  const int h = k >> 1;
+  return {__int_as_float((127 + h) << 23), __int_as_float((127 + k - h) << 23),
+          __int_as_float((127 - h) << 23) * __int_as_float((127 - k + h) << 23)};
 }
 
 // Pairs of fp32 values: one instruction for two multiply-adds or additions.

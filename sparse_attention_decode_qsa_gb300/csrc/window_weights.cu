@@ -213,21 +213,35 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
 
 // ------------------------------------------------------------------- wide
 
+// Two e4m3 codes (the low 16 bits) as bf16, exactly: their exponent and mantissa at
+// the low end of bf16's make 2^-120 times the value (a subnormal code a subnormal),
+// which the product puts right.  A NaN code (nan_codes) comes out as 480.
+__device__ __forceinline__ uint32_t codes2_bf16(uint32_t two) {
+  const uint32_t h = __byte_perm(two, 0, 0x1404);
+  const uint32_t x = (h & 0x80008000u) | ((h >> 4) & 0x07F007F0u);
+  const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x),
+                                   __nv_bfloat162(__ushort_as_bfloat16(0x7B80), __ushort_as_bfloat16(0x7B80)));    // 2^120
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+// Not 0 where one of four codes is a NaN.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
 // Units of more queries: one CTA per 128 kTiles tokens, in tiles of 128 = the tensor
 // core's M; a turn is 32 / kTiles queries x 4 heads of a KV head = 128 / kTiles
 // columns (N), K = 128 dims, both operands in shared memory under the 128-byte
 // swizzle.  K[g] of the tokens (two buffers) stays for all of the chunk's queries,
 // Q streams past in a ring of four turns (from L2: with two tiles every query is
 // read half as often, with one there are twice as many CTAs).  Tensor memory: a ring
-// of four turns of 128 columns.  Warps: 8 epilogue (thread = token, 64 columns a
-// turn), 4 load K, 4 load Q, 1 MMA; all waits bounded.  Bound by the exponentials:
+// of four turns of 128 columns.  Warps: 16 epilogue (thread = token, 32 columns a
+// turn: four warps to a scheduler hide each other's waits), 4 load K, 3 load Q, 1
+// MMA; all waits bounded.  Bound by the exponentials:
 // 16 a cycle and SM, 1024 cycles a turn, twice the tensor core's time.
-constexpr int kEpiWarps = 8, kLoadWarps = 4;
-constexpr int kWideThreads = 32 * (kEpiWarps + 2 * kLoadWarps + 1);
-constexpr int kRoleKeys = kEpiWarps, kRoleQueries = kRoleKeys + kLoadWarps, kRoleMma = kRoleQueries + kLoadWarps;
+constexpr int kEpiWarps = 16, kKeyWarps = 4, kQueryWarps = 3;     // 24 with the MMA warp: six to a scheduler, 80 registers
+constexpr int kWideThreads = 32 * (kEpiWarps + kKeyWarps + kQueryWarps + 1);
+constexpr int kRoleKeys = kEpiWarps, kRoleQueries = kRoleKeys + kKeyWarps, kRoleMma = kRoleQueries + kQueryWarps;
 constexpr int kRing = 4;
 constexpr int kPanel = 128 * 128;                 // 128 rows of 64 16-bit elements
-constexpr int kEpiCols = 64;
+constexpr int kEpiCols = 32;
 constexpr uint32_t kTmemCols = 512;
 
 template <int kTiles>
@@ -236,8 +250,7 @@ struct Wide {
   struct __align__(16) Columns {
     float minus[kCols];            // -lse (log2)
     float factor[kCols];           // what its rounding leaves
-    float scale[kCols];            // FP8: the inverse of the query row's power of two
-    int32_t dead[kLoadWarps];      // per loader warp: a column without weight
+    int32_t dead, pad[3];          // a column has no weight
   };
   // Columns of turn i are written once the products of turn i - 4 are complete,
   // before which the epilogue of turn i - 8 had left its accumulators: eight.
@@ -245,8 +258,8 @@ struct Wide {
   static constexpr int kKBytes = kTiles * 2 * kPanel, kQPanel = kCols * 128, kQBytes = 2 * kQPanel;
   static constexpr int kOffQ = 2 * kKBytes, kOffCols = kOffQ + kRing * kQBytes;
   static constexpr int kOffKs = kOffCols + kColumns * (int)sizeof(Columns);     // float [4][kTokens]: K scales
-  static constexpr int kOffSum = kOffKs + kKvHeads * kTokens * 4;               // float [128]: the second column half's sums
-  static constexpr int kOffThere = kOffSum + 128 * 4;                           // uint32 [8]: tokens that count
+  static constexpr int kOffSum = kOffKs + kKvHeads * kTokens * 4;               // float [4][128]: sums of the column parts
+  static constexpr int kOffThere = kOffSum + 4 * 128 * 4;                       // uint32 [8]: tokens that count
   static constexpr int kOffBar = kOffThere + 32;
   static constexpr int kNumBars = 4 * kRing + 4;   // full, empty, d_full, d_empty [4], k_full, k_empty [2]
   static constexpr int kOffSlot = kOffBar + 8 * kNumBars;
@@ -263,7 +276,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) weight_wide_kernel(const __gr
   const uint32_t sb = smem_u32(smem);
   Columns* columns = reinterpret_cast<Columns*>(smem + W::kOffCols);
   float* key_scale = reinterpret_cast<float*>(smem + W::kOffKs);
-  float* half_sum = reinterpret_cast<float*>(smem + W::kOffSum);
+  float* part_sum = reinterpret_cast<float*>(smem + W::kOffSum);
   uint32_t* there = reinterpret_cast<uint32_t*>(smem + W::kOffThere);
   const uint32_t bars = sb + W::kOffBar;
   auto full = [&](int i) { return bars + 8u * (uint32_t)(i % kRing); };
@@ -298,13 +311,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) weight_wide_kernel(const __gr
     tmem_alloc<kTmemCols>(slot);
     if (lane == 0) {
       for (int i = 0; i < kRing; ++i) {
-        mbar_init(full(i), 32 * kLoadWarps);
+        mbar_init(full(i), 1);
         mbar_init(empty(i), 1);
         mbar_init(d_full(i), 2);
-        mbar_init(d_empty(i), 32 * kEpiWarps);
+        mbar_init(d_empty(i), kEpiWarps);
       }
       for (int g = 0; g < 2; ++g) {
-        mbar_init(k_full(g), 32 * kLoadWarps);
+        mbar_init(k_full(g), 32 * kKeyWarps);
         mbar_init(k_empty(g), 1);
       }
       mbar_fence_init();
@@ -333,132 +346,137 @@ __global__ void __launch_bounds__(kWideThreads, 1) weight_wide_kernel(const __gr
       }
       exist[k] = __ballot_sync(0xFFFFFFFFu, row[k] != nullptr);
       if (lane == 0) there[kTiles * w + k] = exist[k];
+      // the other heads' keys are on their way to L2 meanwhile
+      if (row[k]) {
+#pragma unroll
+        for (int o = 1; o < kKvHeads; ++o)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(row[k] + o * kHeadDim * (kFp8 ? 1 : 2)));
+      }
     }
-    for (int g = 0; g < kKvHeads && ok; ++g) {
-      if (g >= 2) ok = mbar_wait_warp(k_empty(g), 0, err, kKernWeights);
-      if (!ok) break;
+    // FP8: a token's K scales, all heads
+    uint2 scales[kTiles];
 #pragma unroll
-      for (int k = 0; k < kTiles; ++k) {
-        const int at = 32 * (kTiles * w + k);                    // of the CTA's tokens
-        const uint32_t r0 = at & 127;                            // row in its tile
-        const uint32_t dst = (g & 1) * W::kKBytes + (at >> 7) * 2 * kPanel + r0 * 128;
-        const uintptr_t from = reinterpret_cast<uintptr_t>(row[k] ? row[k] : b.pool);
-        if (!kFp8) {
-          const uint32_t c = lane & 15, hi = lane >> 4;
-          const uint32_t to = sb + dst + (c >> 3) * kPanel;
+    for (int k = 0; k < kTiles; ++k)
+      scales[k] = kFp8 && row[k] ? *reinterpret_cast<const uint2*>(row[k] + 2 * kKvHeads * kHeadDim) : make_uint2(0, 0);
+    // K[g] is on its way while K[g - 1] is turned over
+    for (int i = 0; i <= kKvHeads && ok; ++i) {
+      if (i < kKvHeads) {
+        const int g = i;
+        if (g >= 2) ok = mbar_wait_warp(k_empty(g), 0, err, kKernWeights);
+        if (!ok) break;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t t = 2 * i + hi;
+        for (int k = 0; k < kTiles; ++k) {
+          const int at = 32 * (kTiles * w + k);                  // of the CTA's tokens
+          const uint32_t dst = sb + (g & 1) * W::kKBytes + (at >> 7) * 2 * kPanel + (at & 127) * 128;
+          const uintptr_t from = reinterpret_cast<uintptr_t>(row[k] ? row[k] : b.pool);
+          // BF16: 16 lanes a token, 8 in each panel.  FP8: 8 lanes, the codes as they
+          // are in the token's row of the second panel
+          constexpr int kLanes = kFp8 ? 8 : 16, kPer = 32 / kLanes;
+          const uint32_t c = lane % kLanes;
+          const uint32_t to = dst + (kFp8 ? kPanel : (c >> 3) * kPanel);
+#pragma unroll
+          for (int j = 0; j < 32 / kPer; ++j) {
+            const uint32_t t = kPer * j + lane / kLanes;
             const uintptr_t a = __shfl_sync(0xFFFFFFFFu, from, (int)t);
-            cp_async16(to + t * 128 + (((c & 7) ^ (t & 7)) << 4), reinterpret_cast<const uint8_t*>(a) + g * 256 + c * 16,
+            cp_async16(to + t * 128 + (((c & 7) ^ (t & 7)) << 4),
+                       reinterpret_cast<const uint8_t*>(a) + g * (kFp8 ? kHeadDim : 2 * kHeadDim) + c * 16,
                        (exist[k] >> t) & 1u ? 16u : 0u);
-          }
-        } else {
-          const uint32_t c = lane & 7, four = lane >> 3;
-          uint4 kv[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t t = 4 * i + four;
-            const uintptr_t a = __shfl_sync(0xFFFFFFFFu, from, (int)t);
-            kv[i] = (exist[k] >> t) & 1u ? *reinterpret_cast<const uint4*>(a + g * kHeadDim + c * 16) : make_uint4(0, 0, 0, 0);
-          }
-          uint16_t raw = 0;
-          if (row[k]) raw = reinterpret_cast<const uint16_t*>(row[k] + 2 * kKvHeads * kHeadDim)[g];
-          key_scale[g * W::kTokens + at + lane] = __half2float(__ushort_as_half(raw));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t t = 4 * i + four, ch = (2 * c) & 7, sw = t & 7;
-            uint8_t* to = smem + dst + (c >> 2) * kPanel + t * 128;
-            *reinterpret_cast<uint4*>(to + ((ch ^ sw) << 4)) = codes8_f16(make_uint2(kv[i].x, kv[i].y));
-            *reinterpret_cast<uint4*>(to + (((ch + 1) ^ sw) << 4)) = codes8_f16(make_uint2(kv[i].z, kv[i].w));
           }
         }
       }
-      if (!kFp8) asm volatile("cp.async.commit_group;\n cp.async.wait_group 0;" ::: "memory");
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (i == 0) continue;
+      const int g = i - 1;
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      if (kFp8) {
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kTiles; ++k) {
+          const int at = 32 * (kTiles * w + k);
+          uint8_t* panel = smem + (g & 1) * W::kKBytes + (at >> 7) * 2 * kPanel + (at & 127) * 128;
+          const uint32_t c = lane & 7;
+          uint32_t bad = 0;                                      // tokens of the 32 with a NaN among their codes
+#pragma unroll 2
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t t = 4 * j + (lane >> 3), sw = t & 7;
+            const uint4 v = *reinterpret_cast<const uint4*>(panel + kPanel + t * 128 + ((c ^ sw) << 4));
+            uint4 o[2];
+            o[0] = make_uint4(codes2_bf16(v.x), codes2_bf16(v.x >> 16), codes2_bf16(v.y), codes2_bf16(v.y >> 16));
+            o[1] = make_uint4(codes2_bf16(v.z), codes2_bf16(v.z >> 16), codes2_bf16(v.w), codes2_bf16(v.w >> 16));
+            const uint32_t nan = nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w);
+            const uint32_t which = __ballot_sync(0xFFFFFFFFu, nan != 0);       // (and all four rows have been read)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) bad |= (which >> (8 * x)) & 0xFFu ? 1u << (4 * j + x) : 0u;
+            // codes 16 c .. + 15 are the chunks 2 c and 2 c + 1 of the row's 16
+            uint8_t* to = panel + (c >> 2) * kPanel + t * 128;
+            const uint32_t ch = (2 * c) & 7;
+            *reinterpret_cast<uint4*>(to + ((ch ^ sw) << 4)) = o[0];
+            *reinterpret_cast<uint4*>(to + (((ch + 1) ^ sw) << 4)) = o[1];
+          }
+          const uint32_t two = g < 2 ? scales[k].x : scales[k].y;
+          const float ks = __half2float(__ushort_as_half((uint16_t)(g & 1 ? two >> 16 : two & 0xFFFFu)));
+          key_scale[g * W::kTokens + at + lane] = (bad >> lane) & 1u ? __int_as_float(0x7FC00000) : ks;
+        }
+      }
       fence_async_smem();
       mbar_arrive(k_full(g));
     }
-  } else if (warp >= kRoleQueries && warp < kRoleMma) {
-    // ---- Q: warp w has the columns kCols / 4 w .. of a turn, column query * 4 + head
-    const int w = warp - kRoleQueries;
-    constexpr int kMine = W::kCols / kLoadWarps;                 // 32 or 16
-    auto lse_of = [&](int i) {                                   // of this lane's column
-      const int g = i / per, col = kMine * w + lane, q = (c0 + i % per) * W::kQueries + col / kGroup;
-      return i < turns && lane < kMine && q < nq ? p.lse[(int64_t)(x0 + q) * kQHeads + g * kGroup + col % kGroup] : -INFINITY;
-    };
-    float lse_next = lse_of(0);
-    // cp.async: turn i - 2 has landed once turn i is on its way; FP8 has none
-    constexpr int kBehind = kFp8 ? 0 : 2;
-    for (int i = 0; i < turns + kBehind && ok; ++i) {
-      if (i < turns) {
-        const float lse = lse_next;
-        lse_next = lse_of(i + 1);
-        if (i >= kRing) ok = mbar_wait_warp(empty(i), turn_of(i - kRing), err, kKernWeights);
-        if (!ok) break;
-        const int g = i / per, qa = (c0 + i % per) * W::kQueries;
-        Columns& m = columns[i % W::kColumns];
-        const uint32_t dst = W::kOffQ + (i % kRing) * W::kQBytes;
-        float scale = 1.f;
-#pragma unroll
-        for (int k0 = 0; k0 < kMine / 2; k0 += 8) {              // two columns at a time, 16 lanes each
-          uint4 v[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int cc = kMine * w + 2 * (k0 + k) + (lane >> 4), q = qa + cc / kGroup;
-            const uint16_t* from = p.q + ((int64_t)(x0 + q) * kQHeads + g * kGroup + cc % kGroup) * kHeadDim;
-            if (!kFp8)
-              cp_async16(sb + dst + ((lane & 15) >> 3) * W::kQPanel + cc * 128 + (((lane & 7) ^ (cc & 7)) << 4),
-                         q < nq ? from + (lane & 15) * 8 : p.q, q < nq ? 16u : 0u);
-            else
-              v[k] = q < nq ? reinterpret_cast<const uint4*>(from)[lane & 15] : make_uint4(0, 0, 0, 0);
-          }
-          if (kFp8) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int cc = kMine * w + 2 * (k0 + k) + (lane >> 4);
-              uint32_t* e4[4] = {&v[k].x, &v[k].y, &v[k].z, &v[k].w};
-              float top = 0.f;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(*e4[e])), fabsf(bf16_hi(*e4[e]))));
-#pragma unroll
-              for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));   // the column's 16 lanes
-              const RowScale rs = row_scale(top);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) *e4[e] = pack_f16(bf16_lo(*e4[e]) * rs.a * rs.b, bf16_hi(*e4[e]) * rs.a * rs.b);
-              *reinterpret_cast<uint4*>(smem + dst + ((lane & 15) >> 3) * W::kQPanel + cc * 128 + (((lane & 7) ^ (cc & 7)) << 4)) = v[k];
-              const float s0 = __shfl_sync(0xFFFFFFFFu, rs.inverse, 0), s1 = __shfl_sync(0xFFFFFFFFu, rs.inverse, 16);
-              if ((lane >> 1) == k0 + k) scale = lane & 1 ? s1 : s0;
-            }
-          }
-        }
-        const float2 k = column_of(lse);
-        if (lane < kMine) {
-          m.minus[kMine * w + lane] = k.x;
-          m.factor[kMine * w + lane] = k.y;
-          m.scale[kMine * w + lane] = scale;
-        }
-        const bool dead = __any_sync(0xFFFFFFFFu, lane < kMine && lse == -INFINITY);
-        if (lane == 0) m.dead[w] = dead;
-      }
-      if (!kFp8) asm volatile("cp.async.commit_group;\n cp.async.wait_group 2;" ::: "memory");
-      if (i >= kBehind) {
-        fence_async_smem();
-        mbar_arrive(full(i - kBehind));
-      }
-    }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+  } else if (warp >= kRoleQueries && warp < kRoleMma) {
+    // ---- Q: warp w has the turns w, w + 3, ..., so that three are on their way, and
+    // each arrives as soon as it has landed; column query * 4 + head.
+    const int w = warp - kRoleQueries;
+    int g = 0, c = w;                                            // of turn i
+    while (c >= per) c -= per, ++g;
+    for (int i = w; i < turns && ok; i += kQueryWarps) {
+      if (i >= kRing) ok = mbar_wait_warp(empty(i), turn_of(i - kRing), err, kKernWeights);
+      if (!ok) break;
+      const int qa = (c0 + c) * W::kQueries, have = nq - qa < W::kQueries ? nq - qa : W::kQueries;
+      const uint32_t dst = W::kOffQ + (i % kRing) * W::kQBytes + ((lane & 15) >> 3) * W::kQPanel;
+      // two columns at a time, 16 lanes each: heads 2 (k & 1) + (lane >> 4) of query k / 2
+      const uint16_t* from = p.q + ((int64_t)(x0 + qa) * kQHeads + g * kGroup + (lane >> 4)) * kHeadDim + (lane & 15) * 8;
+      auto place = [&](int k) {
+        const int cc = 2 * k + (lane >> 4);
+        return dst + cc * 128 + (((lane & 7) ^ (cc & 7)) << 4);
+      };
+#pragma unroll 8
+      for (int k = 0; k < W::kCols / 2; ++k) {
+        const bool there_is = (k >> 1) < have;
+        cp_async16(sb + place(k), there_is ? from + ((k >> 1) * kQHeads + 2 * (k & 1)) * kHeadDim : p.q, there_is ? 16u : 0u);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      Columns& m = columns[i % W::kColumns];
+      bool dead = false;
+#pragma unroll
+      for (int k = 0; k < W::kCols / 32; ++k) {
+        const int col = 32 * k + lane, q = col / kGroup;
+        const float lse = q < have ? p.lse[(int64_t)(x0 + qa + q) * kQHeads + g * kGroup + col % kGroup] : -INFINITY;
+        const float2 y = column_of(lse);
+        m.minus[col] = y.x;
+        m.factor[col] = y.y;
+        dead = dead || lse == -INFINITY;
+      }
+      dead = __any_sync(0xFFFFFFFFu, dead);
+      if (lane == 0) m.dead = dead;
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full(i));
+      for (c += kQueryWarps; c >= per; c -= per) ++g;
+    }
   } else if (warp == kRoleMma) {
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-    for (int i = 0; i < turns && ok; ++i) {
-      const int g = i / per, left = (nq - (c0 + i % per) * W::kQueries) * kGroup;
+    for (int i = 0, g = 0, c = 0; i < turns && ok; ++i, ++c) {
+      if (c == per) c = 0, ++g;
+      const int left = (nq - (c0 + c) * W::kQueries) * kGroup;
       const uint32_t cols = left >= W::kCols ? W::kCols : (uint32_t)((left + 15) / 16 * 16);
-      if (i % per == 0) ok = mbar_wait_warp(k_full(g), (uint32_t)(g >> 1), err, kKernWeights);
+      if (c == 0) ok = mbar_wait_warp(k_full(g), (uint32_t)(g >> 1), err, kKernWeights);
       if (ok) ok = mbar_wait_warp(full(i), turn_of(i), err, kKernWeights);
       if (ok && i >= kRing) ok = mbar_wait_warp(d_empty(i), turn_of(i - kRing), err, kKernWeights);
       if (!ok) break;
       fence_after();
       if (elect_one()) {
-        const uint32_t id = kFp8 ? idesc_f16(cols, false) : idesc_bf16(cols, false);
+        const uint32_t id = idesc_bf16(cols, false);
         const uint64_t qd = desc_sw128(sb + W::kOffQ + (i % kRing) * W::kQBytes, 16);
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
@@ -471,84 +489,109 @@ __global__ void __launch_bounds__(kWideThreads, 1) weight_wide_kernel(const __gr
         mbar_arrive(d_full(i));                      // passes on the loaders' writes of the columns
         commit(d_full(i));
         commit(empty(i));
-        if (i % per == per - 1) commit(k_empty(g));
+        if (c == per - 1) commit(k_empty(g));
       }
       __syncwarp();
     }
     // every product is complete before tensor memory is given back
     for (int i = turns > kRing ? turns - kRing : 0; i < turns; ++i) mbar_wait_warp(empty(i), turn_of(i), err, kKernWeights);
   } else {
-    // ---- epilogue: thread = token; with one tile, warps 4 .. 7 take the second half of the columns
-    const int half = warp >> 2, at = (kTiles == 2 ? 128 * half : 0) + 32 * (warp & 3) + lane;
-    const int first = kTiles == 2 ? 0 : kEpiCols * half;         // its columns of a turn
+    // ---- epilogue: thread = token; part `part` of four: of the columns, and with
+    // two tiles of these
+    const int part = warp >> 2, at = (kTiles == 2 ? 128 * (part >> 1) : 0) + 32 * (warp & 3) + lane;
+    const int first = kEpiCols * (kTiles == 2 ? part & 1 : part);            // its columns of a turn
     const int64_t t = t0 + at;
-    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(kEpiCols * half);
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(kEpiCols * part);
     // queries that see the token
     int64_t qlo = t - pos0, qhi = t < p.d.sinks ? nq : t + p.d.window - pos0;
     if (qlo < 0) qlo = 0;
     if (qhi > nq) qhi = nq;
-    const uint64_t hi2 = pair(p.scale_log2, p.scale_log2), lo2 = pair(p.scale_rest, p.scale_rest);
+    float hi = p.scale_log2, lo = p.scale_rest;
+    uint64_t hi2 = pair(hi, hi), lo2 = pair(lo, lo);
     float total = 0.f;
     bool mine = false;
 #pragma unroll 1
-    for (int i = 0; i < turns; ++i) {
-      const int g = i / per, qa = (c0 + i % per) * W::kQueries;
+    for (int i = 0, g = 0, c = 0; i < turns; ++i, ++c) {
+      if (c == per) c = 0, ++g;
+      const int qa = (c0 + c) * W::kQueries;
       ok = mbar_wait_warp(d_full(i), turn_of(i), err, kKernWeights);
       if (!ok) break;
       fence_after();
       if (i == 0) mine = (there[at >> 5] >> (at & 31)) & 1u;
-      const float ks = kFp8 ? key_scale[g * W::kTokens + at] : 1.f;
-      const uint64_t ks2 = pair(ks, ks);
+      if (kFp8 && c == 0) {                          // times the token's K scale, the rounding into the rest
+        const float ks = key_scale[g * W::kTokens + at];
+        hi = p.scale_log2 * ks;
+        lo = fmaf(p.scale_rest, ks, fmaf(p.scale_log2, ks, -hi));
+        hi2 = pair(hi, hi);
+        lo2 = pair(lo, lo);
+      }
       const Columns& cm = columns[i % W::kColumns];
       // columns a .. z - 1 count for this token
       const int a = qlo > qa ? (qlo - qa > W::kQueries ? W::kCols : (int)(qlo - qa) * kGroup) : 0;
       const int z = qhi < qa ? 0 : (qhi - qa > W::kQueries ? W::kCols : (int)(qhi - qa) * kGroup);
-      const bool plain = __all_sync(0xFFFFFFFFu, a == 0 && z == W::kCols) && !(cm.dead[0] | cm.dead[1] | cm.dead[2] | cm.dead[3]);
       const uint32_t d = lane_base + (uint32_t)(i % kRing) * 128u;
-      const int left = (nq - qa) * kGroup;           // columns there are
       uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-#pragma unroll 1
-      for (int c = 0; c < kEpiCols && first + c < left; c += 32) {
-        uint32_t v[32];
-        ld32(d + (uint32_t)c, v);
+      // four columns (a query's heads) of a turn
+      auto four = [&](uint32_t* v, int cc, ulonglong2& mi, float (&e)[4]) {
+        mi = *reinterpret_cast<const ulonglong2*>(&cm.minus[cc]);
+        uint64_t x01 = pair(v[0], v[1]), x23 = pair(v[2], v[3]);
+        x01 = fma2(x01, hi2, fma2(x01, lo2, mi.x));
+        x23 = fma2(x23, hi2, fma2(x23, lo2, mi.y));
+        e[0] = exp2_fast(lo_of(x01));
+        e[1] = exp2_fast(hi_of(x01));
+        e[2] = exp2_fast(lo_of(x23));
+        e[3] = exp2_fast(hi_of(x23));
+      };
+      auto add = [&](int cc, const float (&e)[4]) {
+        const ulonglong2 fa = *reinterpret_cast<const ulonglong2*>(&cm.factor[cc]);
+        sum[0] = fma2(pair(e[0], e[1]), fa.x, sum[0]);
+        sum[1] = fma2(pair(e[2], e[3]), fa.y, sum[1]);
+      };
+      const bool some = __any_sync(0xFFFFFFFFu, a < z && z > first && a < first + kEpiCols);
+      const bool plain = __all_sync(0xFFFFFFFFu, a <= first && z >= first + kEpiCols) &&
+                         !cm.dead;
+      if (some) {
+        uint32_t v[kEpiCols];
+        ld32(d, v);
         wait_ld();
         reg_fence(v);
+        if (plain) {
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          const int cc = first + c + k;
-          const ulonglong2 mi = *reinterpret_cast<const ulonglong2*>(&cm.minus[cc]);
-          const ulonglong2 fa = *reinterpret_cast<const ulonglong2*>(&cm.factor[cc]);
-          uint64_t x01 = pair(v[k], v[k + 1]), x23 = pair(v[k + 2], v[k + 3]);
-          if (kFp8) {
-            const ulonglong2 sc = *reinterpret_cast<const ulonglong2*>(&cm.scale[cc]);
-            x01 = mul2(mul2(x01, ks2), sc.x);
-            x23 = mul2(mul2(x23, ks2), sc.y);
+          for (int k = 0; k < kEpiCols; k += 4) {
+            ulonglong2 mi;
+            float e[4];
+            four(&v[k], first + k, mi, e);
+            add(first + k, e);
           }
-          x01 = fma2(x01, hi2, fma2(x01, lo2, mi.x));
-          x23 = fma2(x23, hi2, fma2(x23, lo2, mi.y));
-          float e[4] = {exp2_fast(lo_of(x01)), exp2_fast(hi_of(x01)), exp2_fast(lo_of(x23)), exp2_fast(hi_of(x23))};
-          if (!plain) {
+        } else {
+#pragma unroll
+          for (int k = 0; k < kEpiCols; k += 4) {
+            const int cc = first + k;
+            ulonglong2 mi;
+            float e[4];
+            four(&v[k], cc, mi, e);
+            const bool in = cc >= a && cc < z;
             const float mm[4] = {lo_of(mi.x), hi_of(mi.x), lo_of(mi.y), hi_of(mi.y)};
-            const bool in = cc >= a && cc < z;       // (a query's four heads together)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (!in || mm[j] == -INFINITY || mm[j] == INFINITY) e[j] = 0.f;
+            for (int j = 0; j < 4; ++j)              // (columns without weight, and past the queries: minus is infinite)
+              if (!in || fabsf(mm[j]) == INFINITY) e[j] = 0.f;
+            add(cc, e);
           }
-          sum[0] = fma2(pair(e[0], e[1]), fa.x, sum[0]);
-          sum[1] = fma2(pair(e[2], e[3]), fa.y, sum[1]);
         }
       }
       fence_before();
-      mbar_arrive(d_empty(i));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(d_empty(i));
       const uint64_t s2 = add2(sum[0], sum[1]);
       total += lo_of(s2) + hi_of(s2);
     }
-    if (kTiles == 1) {
-      if (half == 1) half_sum[at] = total;
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
-      total += half_sum[at];
+    part_sum[part * 128 + 32 * (warp & 3) + lane] = total;
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+    const float* sums = part_sum + 32 * (warp & 3) + lane;
+    if (kTiles == 2 ? (part & 1) == 0 : part == 0) {
+      total = kTiles == 2 ? sums[part * 128] + sums[part * 128 + 128] : (sums[0] + sums[128]) + (sums[256] + sums[384]);
+      if (ok && t < t1) store_weight(p, u, t, mine ? total : 0.f);
     }
-    if (ok && t < t1 && (kTiles == 2 || half == 0)) store_weight(p, u, t, mine ? total : 0.f);
   }
 
   fence_before();
