@@ -23,6 +23,16 @@ namespace {
 using namespace tc;
 using namespace attn;
 
+// The tensor core cuts partial sums off instead of rounding them: half a unit in the
+// last place of the running sum on average, eight times (K = 16 each) while it grows
+// to a large logit's product.  With a unit 2^-23 / 1.39 of the sum on average and the
+// sum at step i i/8 of the whole, that is 0.5 / 1.39 * (1 + .. + 8) / 8 units = 1.62
+// 2^-23, always towards 0, so that every weight of a large logit x came out 1.9e-7 x
+// too small beside BF16 rows (1.4e-6 of the sums where logits reach 10, 3e-7 with the
+// scale taking it back).  Products of e4m3 codes have their last bits above the sum's:
+// nothing is cut off there.
+constexpr double kCutOff = 1.62 / 8388608;
+
 struct WeightParams {
   DenseAttn d;
   const uint16_t* q;             // [rows][16][128] bf16 bits
@@ -621,7 +631,8 @@ cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const f
   p.d = d;
   p.q = q;
   p.lse = lse;
-  const double f = (double)softmax_scale * 1.4426950408889634;
+  const bool fp8 = d.c.b.row_bytes == kRowBytesFp8;
+  const double f = (double)softmax_scale * 1.4426950408889634 * (fp8 ? 1 : 1 + kCutOff);
   // both parts of one sign, and neither 0: an infinite logit stays one
   p.scale_log2 = (float)f;
   if (fabs((double)p.scale_log2) > fabs(f)) p.scale_log2 = nextafterf(p.scale_log2, 0.f);
@@ -630,7 +641,6 @@ cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const f
   p.weights = weights;
   p.stride = stride;
   p.accumulate = accumulate;
-  const bool fp8 = d.c.b.row_bytes == kRowBytesFp8;
   int64_t wide = 0, few = 0, few_all = 0;            // the longest contexts; all tokens of few queries
   int64_t seen = 0;                                  // tokens that more than a few queries see
   for (int u = 0; u < d.c.b.n_units; ++u) {
