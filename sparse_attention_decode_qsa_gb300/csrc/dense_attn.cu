@@ -193,17 +193,18 @@ __device__ __forceinline__ bool good_sum(float l) { return l > 0x1p-100f && l < 
 
 // ------------------------------------------------------------------- few
 
-// One CTA: a share of a tile of at most four queries, all KV heads.  Warp w serves
+// One CTA: a share of a tile of at most 2 kN queries, all KV heads.  Warp w serves
 // KV head w % 4 for the tokens 16 (w / 4) .. + 15 of every step of 32, copied by
 // itself into its own ring of three stages (cp.async, K[g] and V[g] alone, 16-byte
-// chunks at chunk ^ (row % 8)), so that no barrier is needed while streaming and
-// two stages (128 KiB per SM with BF16 rows) are in flight.  Its 16 rows are query
-// * 4 + head.  Per stage: S = Q K^T, 16 mma of m16n8k16; online softmax in the
-// accumulators' registers; O += P V, 16 mma, V's fragments by transposing loads.
-// FP8 codes become f16 on the way into registers, exactly: a K word of four codes
-// serves as the dims that the fragment asks for, with Q's dims in the same order;
-// V words, transposed as pairs of dims, are split into an even and an odd dim's
-// fragment, so that a lane's four accumulators of both are four dims in a row.
+// chunks at chunk ^ (row % 8)), so that no barrier is needed while streaming.  Per
+// stage S^T = K Q^T and O^T += V^T P^T by mma of m16n8k16, 8 each per 8 columns
+// (query * 4 + head): with tokens and dims as the 16 rows, one or two queries fill
+// half of what four do, in registers and instructions, and with FP8 rows two CTAs
+// share an SM.  P changes sides by a transposing move, V's fragments come by transposing loads; the
+// online softmax is in the accumulators' registers.  FP8 codes become f16 on the way
+// into registers, exactly: a K word of four codes serves as the dims that the
+// fragment asks for, with Q's dims in the same order; V words, transposed as pairs
+// of dims, are split into the even dims (the rows 0 .. 7 of a fragment) and the odd.
 constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32, kFewStages = 3;
 constexpr int kFewTokens = 16;                    // of a warp and step
 template <bool kFp8>
@@ -214,25 +215,24 @@ struct FewLayout {
   static constexpr int kStage = kScales + (kFp8 ? kFewTokens * 16 : 0);
   static constexpr int kSmem = kFewWarps * kFewStages * kStage;
 };
-constexpr int kMergeBytes = kKvHeads * 16 * kRowFloats * 4;       // O, m, l of the second halves' rows
-static_assert(FewLayout<true>::kSmem >= kMergeBytes && FewLayout<false>::kSmem <= 227 * 1024, "shared memory");
+static_assert(FewLayout<true>::kSmem >= kKvHeads * 16 * kRowFloats * 4, "room for the halves to come together");
 
-template <bool kFp8>
-__global__ void __launch_bounds__(kFewThreads, 1) dense_few_kernel(const __grid_constant__ DenseParams p) {
+template <bool kFp8, int kN>
+__global__ void __launch_bounds__(kFewThreads, kFp8 && kN == 1 ? 2 : 1) dense_few_kernel(const __grid_constant__ DenseParams p) {
   using L = FewLayout<kFp8>;
+  constexpr int kStages = kFewStages;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint32_t there[kFewWarps][kFewStages];              // tokens of a stage whose row exists
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ uint32_t there[kFewWarps][kFewStages];                       // tokens of a stage whose row exists
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = warp & 3, half = warp >> 2;
   const BatchDesc& b = p.d.c.b;
-  const int r = lane >> 2, j4 = lane & 3;                        // rows r and r + 8, columns 2 j4, 2 j4 + 1
+  const int r = lane >> 2, j4 = lane & 3;                        // rows r and r + 8, columns 8 n + 2 j4 + e
 
   // grid: shares x (units, then the prefix at every layer)
   Tile t;
   const bool pre = (int)blockIdx.y >= b.n_units;
   if (pre) {
-    const int l = blockIdx.y - b.n_units;
-    t = prefix_tile(p.d, l, 0);
+    t = prefix_tile(p.d, blockIdx.y - b.n_units, 0);
   } else {
     const int n = p.d.c.unit_tokens(blockIdx.y);
     if (n == 0 || n > kFewQueries) return;
@@ -246,11 +246,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) dense_few_kernel(const __grid_
   const int steps = (int)(all * (blockIdx.x + 1) / shares - s0);
   const Source src = source_of(p.d, t.u);
 
-  uint32_t qa[8][4];
-  float f[2];                                                    // rows r, r + 8
-  few_queries<kFp8>(p.q, t.x0, t.nq, g, p.sign * p.scale_log2, qa, f);
-
-  const uint32_t ring = smem_u32(smem) + warp * kFewStages * L::kStage;
+  const uint32_t ring = smem_u32(smem) + warp * kStages * L::kStage;
   const int64_t first = s0 * kFewStep + half * kFewTokens;       // the warp's first token in the tile's list
   // lane l < 16: token l of a stage
   auto slot_of = [&](int s) {
@@ -260,88 +256,75 @@ __global__ void __launch_bounds__(kFewThreads, 1) dense_few_kernel(const __grid_
     const uint8_t* row = nullptr;
     if (lane < kFewTokens && s < steps) row = row_at(b, src, t, first + (int64_t)s * kFewStep + lane, slot);
     const uint32_t have = __ballot_sync(0xFFFFFFFFu, row != nullptr);
-    if (lane == 0) there[warp][s % kFewStages] = have;
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row ? row : b.pool);
-    const uint32_t to = ring + (s % kFewStages) * L::kStage;
-    if (!kFp8) {
-      // a token per turn: lanes 0 .. 15 copy K[g], the others V[g]
-      const int c = lane & 15;
-      const uint32_t off = (lane >> 4) ? (kKvHeads + g) * kHeadDim * 2 + c * 16 : g * kHeadDim * 2 + c * 16;
-      const uint32_t dst = to + (lane >> 4) * L::kV;
-#pragma unroll
-      for (int i = 0; i < kFewTokens; ++i) {
-        const uintptr_t a = __shfl_sync(0xFFFFFFFFu, at, i);
-        cp_async16(dst + i * L::kVec + ((c ^ (i & 7)) << 4), reinterpret_cast<const uint8_t*>(a) + off,
-                   (have >> i) & 1u ? 16u : 0u);
-      }
-    } else {
-      // two tokens per turn, 8 lanes for K[g] and 8 for V[g] of each
-      const int c = lane & 7, v = (lane >> 3) & 1, two = lane >> 4;
-      const uint32_t off = (v ? kKvHeads + g : g) * kHeadDim + c * 16;
-#pragma unroll
-      for (int i = 0; i < kFewTokens / 2; ++i) {
-        const int k = 2 * i + two;
-        const uintptr_t a = __shfl_sync(0xFFFFFFFFu, at, k);
-        cp_async16(to + v * L::kV + k * L::kVec + ((c ^ (k & 7)) << 4), reinterpret_cast<const uint8_t*>(a) + off,
-                   (have >> k) & 1u ? 16u : 0u);
-      }
-      if (lane < kFewTokens)
-        cp_async16(to + L::kScales + lane * 16, reinterpret_cast<const uint8_t*>(at) + 2 * kKvHeads * kHeadDim,
-                   (have >> lane) & 1u ? 16u : 0u);
-    }
+    if (lane == 0) there[warp][s % kStages] = have;
+    const uint32_t to = ring + (s % kStages) * L::kStage;
+    // a lane's 16 bytes of K[g] or V[g]: BF16 a token, FP8 two tokens a turn
+    constexpr int kPer = kFp8 ? 2 : 1, kLanes = L::kVec / 16;
+    const int c = lane % kLanes, v = (lane / kLanes) & 1;
+    const uint32_t off = (v ? kKvHeads + g : g) * L::kVec + c * 16;
+    few_copies<kPer>(b, row, slot, [&](int k, const uint8_t* from) {
+      cp_async16(to + v * L::kV + k * L::kVec + ((c ^ (k & 7)) << 4), from + off, (have >> k) & 1u ? 16u : 0u);
+    });
+    if (kFp8 && lane < kFewTokens)
+      cp_async16(to + L::kScales + lane * 16, (row ? row : b.pool) + 2 * kKvHeads * kHeadDim, row ? 16u : 0u);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-
-  float o[16][4];                                                // dims of tile n: see the end
-#pragma unroll
-  for (int n = 0; n < 16; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};        // rows r, r + 8, in units of log2; l of this lane's columns
-
+  int32_t slot_next;
   {
-    const int32_t a = slot_of(0), c = slot_of(1);
-    issue(0, a);
-    issue(1, c);
+    int32_t a[kStages - 1];
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) a[i] = slot_of(i);
+    slot_next = slot_of(kStages - 1);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i, a[i]);
   }
-  int32_t slot_next = slot_of(2);
+  uint32_t qb[kN][8][2];
+  float f[kN][2];
+  few_queries<kFp8, kN>(p.q, t.x0, t.nq, g, p.sign * p.scale_log2, qb, f);
+
+  float o[8][kN][4];             // rows of tile i: dims 16 i + r, + 8; FP8: 16 i + 2 r, + 1
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int n = 0; n < kN; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+  float m[kN][2], l[kN][2];      // of the lane's columns, in units of log2; l over its own rows
+#pragma unroll
+  for (int n = 0; n < kN; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
+
 #pragma unroll 1
   for (int s = 0; s < steps; ++s) {
     const int32_t slot = slot_next;
-    slot_next = slot_of(s + 3);
-    issue(s + 2, slot);                                          // its stage was last read at s - 1
-    asm volatile("cp.async.wait_group 2;" ::: "memory");
+    slot_next = slot_of(s + kStages);
+    issue(s + kStages - 1, slot);                                // its stage was last read at s - 1
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     __syncwarp();
-    const uint32_t st = ring + (s % kFewStages) * L::kStage;
-    const uint32_t have = there[warp][s % kFewStages];
-    // ---- S = Q K^T: tokens 8 n + 2 j4, + 1 of rows r and r + 8
-    float x[2][4];
+    const uint32_t st = ring + (s % kStages) * L::kStage;
+    const uint32_t have = there[warp][s % kStages];
+    // ---- S^T = K Q^T: tokens r (elements 0, 1) and r + 8 (2, 3)
+    float x[kN][4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+    for (int n = 0; n < kN; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      uint32_t kb[4];
-      few_keys<kFp8>(st, k, kb);
-      mma16<kFp8>(x[0], qa[k], kb[0], kb[1]);
-      mma16<kFp8>(x[1], qa[k], kb[2], kb[3]);
+      uint32_t ka[4];
+      few_keys<kFp8>(st, k, ka);
+#pragma unroll
+      for (int n = 0; n < kN; ++n) mma16<kFp8>(x[n], ka, qb[n][k][0], qb[n][k][1]);
     }
-    float vs[2][2], lv[2][2];                                    // FP8: V scales of the tokens, log2 of their sizes
+    float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};        // FP8: scales of tokens r, r + 8
+    if (kFp8) {
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float ks = 1.f;
-        if (kFp8) {
-          const __half* sc = reinterpret_cast<const __half*>(smem + (st - smem_u32(smem)) + L::kScales +
-                                                             (8 * n + 2 * j4 + e) * 16);
-          ks = __half2float(sc[g]);
-          vs[n][e] = __half2float(sc[kKvHeads + g]);
-          lv[n][e] = log2_size(vs[n][e]);
-        } else {
-          vs[n][e] = 1.f;
-          lv[n][e] = 0.f;
-        }
-        x[n][e] *= ks * f[0];
-        x[n][2 + e] *= ks * f[1];
+      for (int i = 0; i < 2; ++i) {
+        const __half* sc = reinterpret_cast<const __half*>(smem + (st - smem_u32(smem)) + L::kScales + (r + 8 * i) * 16);
+        ks[i] = __half2float(sc[g]);
+        vs[i] = __half2float(sc[kKvHeads + g]);
+        lv[i] = log2_size(vs[i]);
       }
+    }
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[n][e] *= kFp8 ? ks[e >> 1] * f[n][e & 1] : f[n][e & 1];
     // ---- tokens without a row, and tokens that a query does not see
     const int64_t i0 = first + (int64_t)s * kFewStep;
     const int64_t t0 = t.b0 + i0 - t.np - t.na;                  // the first token's position, if it is one of b
@@ -350,77 +333,79 @@ __global__ void __launch_bounds__(kFewThreads, 1) dense_few_kernel(const __grid_
                                              (t0 + kFewTokens - 1 <= t.pos0 && t0 > last - p.d.window));
     if (!free_of) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < kN; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int c = 8 * n + 2 * j4 + (e & 1);
-          const int64_t pos = t.pos0 + ((r + 8 * (e >> 1)) >> 2), tok = t0 + c;
+          const int c = r + 8 * (e >> 1);
+          const int64_t pos = t.pos0 + 2 * n + ((2 * j4 + (e & 1)) >> 2), tok = t0 + c;
           const bool seen = i0 + c < t.np + t.na || (tok <= pos && (tok < p.d.sinks || tok > pos - p.d.window));
           if (!seen || !((have >> c) & 1u)) x[n][e] = -INFINITY;
         }
     }
     // ---- online softmax; the reference follows the largest product of a
     // probability and its V scale (FP8: it has to fit f16)
-    float mx[2];
+    float mx[kN][2];
+    bool up = false;
 #pragma unroll
-    for (int hi = 0; hi < 2; ++hi) {
-      float y = fmaxf(fmaxf(x[0][2 * hi] + lv[0][0], x[0][2 * hi + 1] + lv[0][1]),
-                      fmaxf(x[1][2 * hi] + lv[1][0], x[1][2 * hi + 1] + lv[1][1]));
-      y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 1));
-      mx[hi] = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 2));
-    }
-    if (__any_sync(0xFFFFFFFFu, mx[0] > m[0] || mx[1] > m[1])) {
+    for (int n = 0; n < kN; ++n)
 #pragma unroll
-      for (int hi = 0; hi < 2; ++hi) {
-        const float mn = fmaxf(m[hi], mx[hi]), a = mn == -INFINITY ? 1.f : exp2_fast(m[hi] - mn);
-        m[hi] = mn;
-        l[hi] *= a;
+      for (int e = 0; e < 2; ++e) {
+        float y = fmaxf(x[n][e] + lv[0], x[n][2 + e] + lv[1]);
 #pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          o[n][2 * hi] *= a;
-          o[n][2 * hi + 1] *= a;
-        }
+        for (int k = 4; k < 32; k <<= 1) y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, k));
+        mx[n][e] = y;
+        up = up || y > m[n][e];
       }
+    if (__any_sync(0xFFFFFFFFu, up)) {
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float mn = fmaxf(m[n][e], mx[n][e]), a = mn == -INFINITY ? 1.f : exp2_fast(m[n][e] - mn);
+          m[n][e] = mn;
+          l[n][e] *= a;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            o[i][n][e] *= a;
+            o[i][n][2 + e] *= a;
+          }
+        }
     }
-    uint32_t pa[4];
+    uint32_t pb[kN][2];                                          // P^T as B fragments
 #pragma unroll
-    for (int hi = 0; hi < 2; ++hi) {
-      const float ref = m[hi] == -INFINITY ? 0.f : m[hi];
-      float e[2][2];
+    for (int n = 0; n < kN; ++n) {
+      float e[4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int k = 0; k < 4; ++k) e[k] = exp2_fast(x[n][k] - (m[n][k & 1] == -INFINITY ? 0.f : m[n][k & 1]));
+      l[n][0] += e[0] + e[2];
+      l[n][1] += e[1] + e[3];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) e[n][c] = exp2_fast(x[n][2 * hi + c] - ref);
-      l[hi] += (e[0][0] + e[0][1]) + (e[1][0] + e[1][1]);
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-        pa[2 * n + hi] = kFp8 ? pack_f16(e[n][0] * vs[n][0], e[n][1] * vs[n][1]) : pack_bf16(e[n][0], e[n][1]);
+      for (int i = 0; i < 2; ++i)
+        pb[n][i] = transpose8x8(kFp8 ? pack_f16(e[2 * i] * vs[i], e[2 * i + 1] * vs[i]) : pack_bf16(e[2 * i], e[2 * i + 1]));
     }
-    // ---- O += P V
+    // ---- O^T += V^T P^T, two chunks of 8 dims (FP8: of 16) per load
+    const int tok = lane & 15;                                   // of the transposing loads: rows, then rows + 8
 #pragma unroll
-    for (int n = 0; n < 16; n += 2) {
-      uint32_t vb[4];
+    for (int i = 0; i < 8; i += kFp8 ? 2 : 1) {
+      uint32_t v[4];
+      const int c = kFp8 ? i + (lane >> 4) : 2 * i + (lane >> 4);
+      ldsm4_t(st + L::kV + tok * L::kVec + ((c ^ (tok & 7)) << 4), v);
       if (!kFp8) {
-        const int tok = (((lane >> 3) & 1) << 3) + (lane & 7), c = n + (lane >> 4);
-        ldsm4_t(st + L::kV + tok * L::kVec + ((c ^ (tok & 7)) << 4), vb);
-        mma16<false>(o[n], pa, vb[0], vb[1]);
-        mma16<false>(o[n + 1], pa, vb[2], vb[3]);
+        const uint32_t va[4] = {v[0], v[2], v[1], v[3]};
+#pragma unroll
+        for (int n = 0; n < kN; ++n) mma16<false>(o[i][n], va, pb[n][0], pb[n][1]);
       } else {
-        // chunks n and n + 1 of 16 dims, every other turn
-        if (n & 2) continue;
-        const int tok = (((lane >> 3) & 1) << 3) + (lane & 7), c = n / 2 + (lane >> 4);
-        ldsm4_t(st + L::kV + tok * L::kVec + ((c ^ (tok & 7)) << 4), vb);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          uint32_t ev[2], od[2];
+          uint32_t va[4];                                        // even dims, odd dims; then tokens + 8
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t a = codes2_f16(vb[2 * k + i] & 0xFFFFu), d = codes2_f16(vb[2 * k + i] >> 16);
-            ev[i] = __byte_perm(a, d, 0x5410);
-            od[i] = __byte_perm(a, d, 0x7632);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a = codes2_f16(v[2 * k + h] & 0xFFFFu), d = codes2_f16(v[2 * k + h] >> 16);
+            va[2 * h] = __byte_perm(a, d, 0x5410);
+            va[2 * h + 1] = __byte_perm(a, d, 0x7632);
           }
-          mma16<true>(o[n + 2 * k], pa, ev[0], ev[1]);
-          mma16<true>(o[n + 2 * k + 1], pa, od[0], od[1]);
+#pragma unroll
+          for (int n = 0; n < kN; ++n) mma16<true>(o[i + k][n], va, pb[n][0], pb[n][1]);
         }
       }
     }
@@ -428,76 +413,76 @@ __global__ void __launch_bounds__(kFewThreads, 1) dense_few_kernel(const __grid_
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
-  for (int hi = 0; hi < 2; ++hi) {
-    l[hi] += __shfl_xor_sync(0xFFFFFFFFu, l[hi], 1);
-    l[hi] += __shfl_xor_sync(0xFFFFFFFFu, l[hi], 2);
-  }
-
-  // ---- the two halves of a KV head come together
-  __syncthreads();
-  // dims of accumulators (n, c): 8 n + 2 j4 + c; FP8: of the pair (n, n + 1) the
-  // four dims 8 n + 4 j4 .. + 3 are (n, 0), (n + 1, 0), (n, 1), (n + 1, 1)
-  float* other = reinterpret_cast<float*>(smem) + g * 16 * kRowFloats;
-  auto pairs = [&](int hi, auto&& fn) {                          // fn(dim, value, value of dim + 1)
+  for (int n = 0; n < kN; ++n)
 #pragma unroll
-    for (int n = 0; n < 16; n += 2) {
-      if (kFp8) {
-        fn(8 * n + 4 * j4, o[n][2 * hi], o[n + 1][2 * hi]);
-        fn(8 * n + 4 * j4 + 2, o[n][2 * hi + 1], o[n + 1][2 * hi + 1]);
-      } else {
-        fn(8 * n + 2 * j4, o[n][2 * hi], o[n][2 * hi + 1]);
-        fn(8 * n + 8 + 2 * j4, o[n + 1][2 * hi], o[n + 1][2 * hi + 1]);
-      }
-    }
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int k = 4; k < 32; k <<= 1) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], k);
+
+  // ---- the two halves of a KV head come together, rows [column][dims, m, l]
+  __syncthreads();
+  float* rows = reinterpret_cast<float*>(smem) + g * 16 * kRowFloats;
+  auto each = [&](auto&& fn) {                                   // fn(place, value of the lane's accumulators)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          fn(rows + (8 * n + 2 * j4 + (e & 1)) * kRowFloats + 16 * i + (kFp8 ? 2 * r + (e >> 1) : r + 8 * (e >> 1)), o[i][n][e],
+             n, e & 1);
   };
   if (half == 1) {
+    each([&](float* at, float v, int, int) { *at = v; });
+    if (r == 0) {
 #pragma unroll
-    for (int hi = 0; hi < 2; ++hi) {
-      float* to = other + (r + 8 * hi) * kRowFloats;
-      pairs(hi, [&](int dim, float& a, float& c) { *reinterpret_cast<float2*>(to + dim) = make_float2(a, c); });
-      if (j4 == 0) *reinterpret_cast<float2*>(to + kHeadDim) = make_float2(m[hi], l[hi]);
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float2*>(rows + (8 * n + 2 * j4 + e) * kRowFloats + kHeadDim) = make_float2(m[n][e], l[n][e]);
     }
   }
   __syncthreads();
   if (half == 1) return;
-  const int u_pieces = pre ? -1 : t.u;
+  float fa[kN][2], fb[kN][2];
 #pragma unroll
-  for (int hi = 0; hi < 2; ++hi) {
-    const int row = r + 8 * hi, qi = row >> 2, x = t.x0 + qi, h = g * kGroup + (row & 3);
-    const float* from = other + row * kRowFloats;
-    const float2 ml = *reinterpret_cast<const float2*>(from + kHeadDim);
-    const float mn = fmaxf(m[hi], ml.x);
-    const float a = m[hi] == -INFINITY ? 0.f : exp2_fast(m[hi] - mn), c = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - mn);
-    const float sum = fmaf(l[hi], a, ml.y * c);
-    pairs(hi, [&](int dim, float& v0, float& v1) {
-      const float2 w = *reinterpret_cast<const float2*>(from + dim);
-      v0 = fmaf(v0, a, w.x * c);
-      v1 = fmaf(v1, a, w.y * c);
-    });
-    const bool mine = qi < t.nq;
+  for (int n = 0; n < kN; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float* at = rows + (8 * n + 2 * j4 + e) * kRowFloats + kHeadDim;
+      const float2 ml = *reinterpret_cast<const float2*>(at);
+      const float mn = fmaxf(m[n][e], ml.x);
+      fa[n][e] = m[n][e] == -INFINITY ? 0.f : exp2_fast(m[n][e] - mn);
+      fb[n][e] = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - mn);
+      __syncwarp();
+      if (r == 0) *reinterpret_cast<float2*>(at) = make_float2(mn, fmaf(l[n][e], fa[n][e], ml.y * fb[n][e]));
+    }
+  each([&](float* at, float v, int n, int e) { *at = fmaf(v, fa[n][e], *at * fb[n][e]); });
+  __syncwarp();
+  // a row at a time, lane l with dims 4 l .. 4 l + 3
+  for (int c = 0; c < kGroup * t.nq; ++c) {
+    const int x = t.x0 + (c >> 2), h = g * kGroup + (c & 3);
+    const float* at = rows + c * kRowFloats;
+    const float2 lo = *reinterpret_cast<const float2*>(at + 4 * lane), hi = *reinterpret_cast<const float2*>(at + 4 * lane + 2);
+    const float2 ml = *reinterpret_cast<const float2*>(at + kHeadDim);
     if (shares > 1 || p.grouped) {
       // pieces of the prefix come behind the row's own
-      if (mine) {
-        const int piece = pre ? pieces_of(p, p.d.c.unit_of_row(x), x).own + blockIdx.x : blockIdx.x;
-        float* to = piece_ptr(p, piece, x, h);
-        pairs(hi, [&](int dim, float& v0, float& v1) { *reinterpret_cast<float2*>(to + dim) = make_float2(v0, v1); });
-        if (j4 == 0) *reinterpret_cast<float2*>(to + kHeadDim) = make_float2(mn, sum);
-      }
+      const int piece = pre ? pieces_of(p, p.d.c.unit_of_row(x), x).own + blockIdx.x : blockIdx.x;
+      float* to = piece_ptr(p, piece, x, h);
+      *reinterpret_cast<float2*>(to + 4 * lane) = lo;
+      *reinterpret_cast<float2*>(to + 4 * lane + 2) = hi;
+      if (lane == 0) *reinterpret_cast<float2*>(to + kHeadDim) = ml;
       continue;
     }
-    const float inv = 1.f / sum;
-    bool fine = good_sum(sum);
-    uint16_t* to = p.out + ((int64_t)x * kQHeads + h) * kHeadDim;
-    pairs(hi, [&](int dim, float& v0, float& v1) {
-      fine = fine && isfinite(v0) && isfinite(v1);
-      if (mine) *reinterpret_cast<uint32_t*>(to + dim) = pack_bf16(v0 * inv, v1 * inv);
-    });
-    if (mine && j4 == 0 && p.lse) p.lse[(int64_t)x * kQHeads + h] = (mn + log2f(sum)) * kLn2;
-    __syncwarp();
-    for (uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && !fine); again; again &= again - 1) {
-      const int bad = ((__ffs(again) - 1) >> 2) + 8 * hi;        // (each of a row's four lanes may have set its bit)
-      attend_row(p, u_pieces, t.x0 + (bad >> 2), g * kGroup + (bad & 3));
+    const bool fine = good_sum(ml.y) && isfinite(lo.x) && isfinite(lo.y) && isfinite(hi.x) && isfinite(hi.y);
+    if (!__all_sync(0xFFFFFFFFu, fine)) {
+      attend_row(p, t.u, x, h);
+      continue;
     }
+    const float inv = 1.f / ml.y;
+    reinterpret_cast<uint2*>(p.out + ((int64_t)x * kQHeads + h) * kHeadDim)[lane] =
+        make_uint2(pack_bf16(lo.x * inv, lo.y * inv), pack_bf16(hi.x * inv, hi.y * inv));
+    if (lane == 0 && p.lse) p.lse[(int64_t)x * kQHeads + h] = (ml.x + log2f(ml.y)) * kLn2;
   }
 }
 
@@ -1182,6 +1167,7 @@ struct Plan {
   int wide_tiles = 0, few_tiles = 0;                 // grid y of the two kernels
   int wide_shares = 0, few_shares = 0;               // grid x
   int wide_q = 1, few_q = 1;
+  int few_rows = 0;                                  // queries of a tile of the few kernel, at most
   int64_t pieces = 1;                                // of a row, at most
   int64_t bytes = 256;
 };
@@ -1223,6 +1209,7 @@ Plan make_plan(const DenseAttn& d, int sms, int32_t* tile0) {
     if (tile0) tile0[u] = own_tiles;
     if (n > kFewQueries) own_tiles += (n + kTileQueries - 1) / kTileQueries;
     if (n == 0 || n > kFewQueries) continue;
+    a.few_rows = n > a.few_rows ? n : a.few_rows;
     few_steps[few_units++] = ceil_div(own_tile(d, a.grouped, u, 0).total, kFewStep);
   }
   if (tile0) tile0[units] = own_tiles;
@@ -1263,7 +1250,9 @@ Plan make_plan(const DenseAttn& d, int sms, int32_t* tile0) {
     int n = few_units;
     if (few_prefix)
       for (int i = 0; i < layers && n <= kMaxUnits; ++i) few_steps[n++] = few_prefix_steps;
-    a.few_q = share_steps(few_steps, n, sms, kLeastFew);
+    if (few_prefix) a.few_rows = layer_rows > a.few_rows ? layer_rows : a.few_rows;
+    // (FP8 rows, two queries: two CTAs to an SM)
+    a.few_q = share_steps(few_steps, n, a.few_rows <= 2 && d.c.b.row_bytes == kRowBytesFp8 ? 2 * sms : sms, kLeastFew);
     const int64_t most = few_prefix && few_prefix_steps > longest_few ? few_prefix_steps : longest_few;
     a.few_shares = (int)ceil_div(most, a.few_q);
     if (a.few_shares == 0) a.few_shares = 1;
@@ -1289,8 +1278,10 @@ cudaError_t launch_dense_attn(const DenseAttn& d, const uint16_t* q, float softm
   cudaError_t e = setup.run([] {
     cudaError_t r = prefer_max_shared(dense_wide_kernel<false>, kWideSmem);
     if (r == cudaSuccess) r = prefer_max_shared(dense_wide_kernel<true>, kWideSmem);
-    if (r == cudaSuccess) r = prefer_max_shared(dense_few_kernel<false>, FewLayout<false>::kSmem);
-    if (r == cudaSuccess) r = prefer_max_shared(dense_few_kernel<true>, FewLayout<true>::kSmem);
+    if (r == cudaSuccess) r = prefer_max_shared(dense_few_kernel<false, 1>, FewLayout<false>::kSmem);
+    if (r == cudaSuccess) r = prefer_max_shared(dense_few_kernel<true, 1>, FewLayout<true>::kSmem);
+    if (r == cudaSuccess) r = prefer_max_shared(dense_few_kernel<false, 2>, FewLayout<false>::kSmem);
+    if (r == cudaSuccess) r = prefer_max_shared(dense_few_kernel<true, 2>, FewLayout<true>::kSmem);
     return r;
   });
   int sms = 0;
@@ -1316,8 +1307,10 @@ cudaError_t launch_dense_attn(const DenseAttn& d, const uint16_t* q, float softm
   }
   if (e == cudaSuccess && a.few_tiles > 0) {
     const dim3 grid((unsigned)a.few_shares, (unsigned)a.few_tiles);
-    e = launch_kernel(fp8 ? dense_few_kernel<true> : dense_few_kernel<false>, grid, dim3(kFewThreads),
-                      fp8 ? FewLayout<true>::kSmem : FewLayout<false>::kSmem, s, 0, dim3(1), p);
+    const int n = a.few_rows > 2 ? 2 : 1;
+    auto* kernel = fp8 ? (n == 1 ? dense_few_kernel<true, 1> : dense_few_kernel<true, 2>)
+                       : (n == 1 ? dense_few_kernel<false, 1> : dense_few_kernel<false, 2>);
+    e = launch_kernel(kernel, grid, dim3(kFewThreads), fp8 ? FewLayout<true>::kSmem : FewLayout<false>::kSmem, s, 0, dim3(1), p);
   }
   if (e != cudaSuccess || (!a.grouped && a.pieces <= 1)) return e;
   const int64_t warps = (int64_t)d.c.rows() * kQHeads;

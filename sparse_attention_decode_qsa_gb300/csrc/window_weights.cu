@@ -83,7 +83,7 @@ struct FewLayout {
   static constexpr int kSmem = kSums + kKvHeads * kFewMost * 4;
 };
 
-template <bool kFp8>
+template <bool kFp8, int kN>
 __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid_constant__ WeightParams p) {
   using L = FewLayout<kFp8>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -103,19 +103,22 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
   const bool all_hidden = nq == 0 || (t0 >= p.d.sinks && t1 - 1 <= pos0 - p.d.window);
   const int steps = all_hidden ? 0 : (int)((t1 - t0 + kFewStep - 1) / kFewStep);
 
-  uint32_t qa[8][4];
-  float f[2];
-  few_queries<kFp8>(p.q, x0, nq, g, 1.f, qa, f);
-  float2 col[2];                                                 // rows r and r + 8: query * 4 + head
-  bool live[2];
-  int64_t pos[2];
+  uint32_t qb[kN][8][2];
+  float f[kN][2];
+  few_queries<kFp8, kN>(p.q, x0, nq, g, 1.f, qb, f);
+  float2 col[kN][2];                                             // columns 8 n + 2 j4 + e: query * 4 + head
+  bool live[kN][2];
+  int64_t pos[kN];
 #pragma unroll
-  for (int hi = 0; hi < 2; ++hi) {
-    const int row = r + 8 * hi, qi = row >> 2;
-    const float lse = qi < nq ? p.lse[(int64_t)(x0 + qi) * kQHeads + g * kGroup + (row & 3)] : -INFINITY;
-    live[hi] = lse != -INFINITY;
-    col[hi] = column_of(lse);
-    pos[hi] = pos0 + qi;
+  for (int n = 0; n < kN; ++n) {
+    const int qi = 2 * n + (j4 >> 1);
+    pos[n] = pos0 + qi;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float lse = qi < nq ? p.lse[(int64_t)(x0 + qi) * kQHeads + g * kGroup + ((2 * j4 + e) & 3)] : -INFINITY;
+      live[n][e] = lse != -INFINITY;
+      col[n][e] = column_of(lse);
+    }
   }
   const int32_t* slots = b.slot_table + b.unit_row(u);
   const uint32_t ring = smem_u32(smem) + warp * kFewStages * L::kStage;
@@ -139,21 +142,15 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
     }
     const uint32_t have = __ballot_sync(0xFFFFFFFFu, row != nullptr);
     if (lane == 0) there[warp][s % kFewStages] = have;
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row ? row : b.pool);
     const uint32_t to = ring + (s % kFewStages) * L::kStage;
-    constexpr int kLanes = L::kVec / 16, kPer = 32 / kLanes;     // lanes of a key, keys of a turn
+    constexpr int kLanes = L::kVec / 16;
     const int c = lane % kLanes;
     const uint32_t off = g * L::kVec + c * 16;
-#pragma unroll
-    for (int i = 0; i < kFewTokens / kPer; ++i) {
-      const int k = i * kPer + lane / kLanes;
-      const uintptr_t a = __shfl_sync(0xFFFFFFFFu, at, k);
-      cp_async16(to + k * L::kVec + ((c ^ (k & 7)) << 4), reinterpret_cast<const uint8_t*>(a) + off,
-                 (have >> k) & 1u ? 16u : 0u);
-    }
+    few_copies<32 / kLanes>(b, row, slot, [&](int k, const uint8_t* from) {
+      cp_async16(to + k * L::kVec + ((c ^ (k & 7)) << 4), from + off, (have >> k) & 1u ? 16u : 0u);
+    });
     if (kFp8 && lane < kFewTokens)
-      cp_async16(to + L::kScales + lane * 16, reinterpret_cast<const uint8_t*>(at) + 2 * kKvHeads * kHeadDim,
-                 (have >> lane) & 1u ? 16u : 0u);
+      cp_async16(to + L::kScales + lane * 16, (row ? row : b.pool) + 2 * kKvHeads * kHeadDim, row ? 16u : 0u);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
@@ -172,41 +169,38 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
     __syncwarp();
     const uint32_t st = ring + (s % kFewStages) * L::kStage;
     const uint32_t have = there[warp][s % kFewStages];
-    float x[2][4];
+    float x[kN][4];                                              // tokens r (elements 0, 1) and r + 8 (2, 3)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+    for (int i = 0; i < kN; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      uint32_t kb[4];
-      few_keys<kFp8>(st, k, kb);
-      mma16<kFp8>(x[0], qa[k], kb[0], kb[1]);
-      mma16<kFp8>(x[1], qa[k], kb[2], kb[3]);
+      uint32_t ka[4];
+      few_keys<kFp8>(st, k, ka);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) mma16<kFp8>(x[i], ka, qb[i][k][0], qb[i][k][1]);
     }
-    float w[4];                                                  // tokens 2 j4, + 1, 8 + 2 j4, + 1; rows r and r + 8
+    float w[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int hi = 0; hi < 2; ++hi) {
+      const int c = r + 8 * hi;
+      const int64_t t = first + (int64_t)s * kFewStep + c;
+      float ks = 1.f;
+      if (kFp8) ks = __half2float(*reinterpret_cast<const __half*>(smem + (st - smem_u32(smem)) + L::kScales + c * 16 + 2 * g));
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int c = 8 * i + 2 * j4 + e;
-        const int64_t t = first + (int64_t)s * kFewStep + c;
-        float ks = 1.f;
-        if (kFp8) ks = __half2float(*reinterpret_cast<const __half*>(smem + (st - smem_u32(smem)) + L::kScales + c * 16 + 2 * g));
-        float sum = 0.f;
+      for (int i = 0; i < kN; ++i) {
+        const bool seen = ((have >> c) & 1u) && sees(p.d, pos[i], t);
 #pragma unroll
-        for (int hi = 0; hi < 2; ++hi) {
-          const float z = x[i][2 * hi + e] * ks * f[hi];
-          const float y = exp2_fast(fmaf(z, p.scale_log2, fmaf(z, p.scale_rest, col[hi].x))) * col[hi].y;
-          if (live[hi] && ((have >> c) & 1u) && sees(p.d, pos[hi], t)) sum += y;
+        for (int e = 0; e < 2; ++e) {
+          const float z = x[i][2 * hi + e] * ks * f[i][e];
+          const float y = exp2_fast(fmaf(z, p.scale_log2, fmaf(z, p.scale_rest, col[i][e].x))) * col[i][e].y;
+          if (seen && live[i][e]) w[hi] += y;
         }
-        w[2 * i + e] = sum;
       }
-    // sums over the lanes of a column: lane keeps token 8 (lane >> 4 & 1) + 2 j4 + (lane >> 3 & 1)
-    const bool hi16 = lane & 16, hi8 = lane & 8;
-    float a = (hi16 ? w[2] : w[0]) + __shfl_xor_sync(0xFFFFFFFFu, hi16 ? w[0] : w[2], 16);
-    float c = (hi16 ? w[3] : w[1]) + __shfl_xor_sync(0xFFFFFFFFu, hi16 ? w[1] : w[3], 16);
-    float v = (hi8 ? c : a) + __shfl_xor_sync(0xFFFFFFFFu, hi8 ? a : c, 8);
-    v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
-    if (!(lane & 4)) sums[s * kFewStep + half * kFewTokens + 8 * (lane >> 4) + 2 * j4 + ((lane >> 3) & 1)] = v;
+    }
+    // sums over the four lanes of a token; lane j4 = 0 keeps token r, j4 = 1 token r + 8
+    float v = (j4 & 1 ? w[1] : w[0]) + __shfl_xor_sync(0xFFFFFFFFu, j4 & 1 ? w[0] : w[1], 1);
+    v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+    if (j4 < 2) sums[s * kFewStep + half * kFewTokens + r + 8 * j4] = v;
     __syncwarp();
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -620,8 +614,10 @@ cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const f
     if (r == cudaSuccess) r = prefer_max_shared(weight_wide_kernel<true, 1>, Wide<1>::kSmem);
     if (r == cudaSuccess) r = prefer_max_shared(weight_wide_kernel<false, 2>, Wide<2>::kSmem);
     if (r == cudaSuccess) r = prefer_max_shared(weight_wide_kernel<true, 2>, Wide<2>::kSmem);
-    if (r == cudaSuccess) r = prefer_max_shared(weight_few_kernel<false>, FewLayout<false>::kSmem);
-    if (r == cudaSuccess) r = prefer_max_shared(weight_few_kernel<true>, FewLayout<true>::kSmem);
+    if (r == cudaSuccess) r = prefer_max_shared(weight_few_kernel<false, 1>, FewLayout<false>::kSmem);
+    if (r == cudaSuccess) r = prefer_max_shared(weight_few_kernel<true, 1>, FewLayout<true>::kSmem);
+    if (r == cudaSuccess) r = prefer_max_shared(weight_few_kernel<false, 2>, FewLayout<false>::kSmem);
+    if (r == cudaSuccess) r = prefer_max_shared(weight_few_kernel<true, 2>, FewLayout<true>::kSmem);
     return r;
   });
   int sms = 0;
@@ -642,6 +638,7 @@ cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const f
   p.stride = stride;
   p.accumulate = accumulate;
   int64_t wide = 0, few = 0, few_all = 0;            // the longest contexts; all tokens of few queries
+  int rows = 0;                                      // queries of a unit of few, at most
   int64_t seen = 0;                                  // tokens that more than a few queries see
   for (int u = 0; u < d.c.b.n_units; ++u) {
     const int64_t n = d.c.b.u[u].n;
@@ -653,6 +650,7 @@ cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const f
     } else {
       few = n > few ? n : few;
       few_all += n;
+      rows = nq > rows ? nq : rows;
     }
   }
   if (wide > 0) {
@@ -669,8 +667,9 @@ cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const f
     run = (run + kFewStep - 1) / kFewStep * kFewStep;
     run = run < 2 * kFewStep ? 2 * kFewStep : (run > kFewMost ? kFewMost : run);
     p.few_tokens = (int32_t)run;
-    e = launch_kernel(fp8 ? weight_few_kernel<true> : weight_few_kernel<false>,
-                      dim3((unsigned)((few + run - 1) / run), d.c.b.n_units), dim3(kFewThreads),
+    auto* kernel = fp8 ? (rows > 2 ? weight_few_kernel<true, 2> : weight_few_kernel<true, 1>)
+                       : (rows > 2 ? weight_few_kernel<false, 2> : weight_few_kernel<false, 1>);
+    e = launch_kernel(kernel, dim3((unsigned)((few + run - 1) / run), d.c.b.n_units), dim3(kFewThreads),
                       fp8 ? FewLayout<true>::kSmem : FewLayout<false>::kSmem, s, 0, dim3(1), p);
   }
   return e;
