@@ -28,13 +28,15 @@ using namespace attn;
 constexpr int kTileQueries = 64;                  // wide: two halves of 32
 constexpr int kStepTokens = 128;                  // wide
 constexpr int kFewStep = 32;                      // few: two halves of 16 tokens
-constexpr int kRowFloats = kHeadDim + 2;          // partial of a row and head: O, m, l
+constexpr int kRowFloats = kHeadDim + 4;          // partial of a row and head: O, m, l (16-byte aligned)
 constexpr int kMaxShares = 64;                    // of a tile
 
 struct DenseParams {
   DenseAttn d;
   int32_t tile0[kMaxUnits + 1];  // prefix sums of the wide tiles per unit
   int32_t grouped;               // 1: the prefix has tiles of its own
+  int32_t prefix_pieces;         // of every row, in front of its own ones (0 where not grouped)
+  int32_t overlap;               // 1: the few kernel runs beside the wide one
   int32_t wide_q, few_q;         // steps of a share
   const uint16_t* q;             // [rows][16][128] bf16 bits
   float scale_log2;              // |softmax_scale| * log2(e)
@@ -79,30 +81,23 @@ __host__ __device__ __forceinline__ Tile prefix_tile(const DenseAttn& d, int l, 
   return t;
 }
 
-// Shares of a tile: one at least where nothing else writes its rows.
+// Shares of a tile: one at least where nothing else writes its rows.  (A list is
+// shorter than 2^33 tokens, its steps fit 32 bits.)
 __host__ __device__ __forceinline__ int shares_of(const Tile& t, int step, int q, bool alone) {
-  const int64_t steps = (t.total + step - 1) / step;
+  const uint32_t steps = (uint32_t)((t.total + step - 1) / step);
   if (steps == 0) return alone ? 1 : 0;
-  return (int)((steps + q - 1) / q);
+  return (int)((steps + (uint32_t)q - 1) / (uint32_t)q);
+}
+// First step of share i of n.
+__device__ __forceinline__ int64_t share_start(uint32_t steps, uint32_t i, uint32_t n) {
+  return (int64_t)((uint64_t)steps / n * i + (uint64_t)(steps % n) * i / n);
 }
 
-// Pieces of row x of unit u: those of its own tile, then those of the prefix.
-struct Pieces {
-  int own, prefix;
-};
-__device__ __forceinline__ Pieces pieces_of(const DenseParams& p, int u, int x) {
-  Pieces r;
+// Own pieces of row x of unit u.
+__device__ __forceinline__ int own_pieces(const DenseParams& p, int u, int x) {
   const bool few = p.d.c.unit_tokens(u) <= kFewQueries;
   const int i0 = few ? 0 : (x - p.d.c.row0[u]) / kTileQueries * kTileQueries;
-  r.own = shares_of(own_tile(p.d, p.grouped, u, i0), few ? kFewStep : kStepTokens, few ? p.few_q : p.wide_q, !p.grouped);
-  r.prefix = 0;
-  if (p.grouped) {
-    const bool some = p.d.c.row0[p.d.n_req] <= kFewQueries;
-    const int64_t steps = (p.d.prefix_len + (some ? kFewStep : kStepTokens) - 1) / (some ? kFewStep : kStepTokens);
-    const int q = some ? p.few_q : p.wide_q;
-    r.prefix = (int)((steps + q - 1) / q);
-  }
-  return r;
+  return shares_of(own_tile(p.d, p.grouped, u, i0), few ? kFewStep : kStepTokens, few ? p.few_q : p.wide_q, !p.grouped);
 }
 
 __device__ __forceinline__ float* piece_ptr(const DenseParams& p, int piece, int x, int h) {
@@ -234,16 +229,18 @@ __global__ void __launch_bounds__(kFewThreads, kFp8 && kN == 1 ? 2 : 1) dense_fe
   if (pre) {
     t = prefix_tile(p.d, blockIdx.y - b.n_units, 0);
   } else {
-    const int n = p.d.c.unit_tokens(blockIdx.y);
-    if (n == 0 || n > kFewQueries) return;
     t = own_tile(p.d, p.grouped, blockIdx.y, 0);
   }
-  const int shares = shares_of(t, kFewStep, p.few_q, !p.grouped);
+  const bool some = pre || (t.nq > 0 && p.d.c.unit_tokens(t.u) <= kFewQueries);
+  const int shares = some ? shares_of(t, kFewStep, p.few_q, !p.grouped) : 0;
+  // Beside the wide kernel (which lets this one start once its own wait is over, so
+  // that what both read is there) the wait comes at the end: whatever follows this
+  // kernel follows both.
+  if (!p.overlap || (int)blockIdx.x >= shares) grid_dependency_wait();
   if ((int)blockIdx.x >= shares) return;
-  grid_dependency_wait();
-  const int64_t all = (t.total + kFewStep - 1) / kFewStep;
-  const int64_t s0 = all * blockIdx.x / shares;
-  const int steps = (int)(all * (blockIdx.x + 1) / shares - s0);
+  const uint32_t all = (uint32_t)((t.total + kFewStep - 1) / kFewStep);
+  const int64_t s0 = share_start(all, blockIdx.x, shares);
+  const int steps = (int)(share_start(all, blockIdx.x + 1, shares) - s0);
   const Source src = source_of(p.d, t.u);
 
   const uint32_t ring = smem_u32(smem) + warp * kStages * L::kStage;
@@ -443,7 +440,10 @@ __global__ void __launch_bounds__(kFewThreads, kFp8 && kN == 1 ? 2 : 1) dense_fe
     }
   }
   __syncthreads();
-  if (half == 1) return;
+  if (half == 1) {
+    if (p.overlap) grid_dependency_wait();
+    return;
+  }
   float fa[kN][2], fb[kN][2];
 #pragma unroll
   for (int n = 0; n < kN; ++n)
@@ -466,11 +466,8 @@ __global__ void __launch_bounds__(kFewThreads, kFp8 && kN == 1 ? 2 : 1) dense_fe
     const float2 lo = *reinterpret_cast<const float2*>(at + 4 * lane), hi = *reinterpret_cast<const float2*>(at + 4 * lane + 2);
     const float2 ml = *reinterpret_cast<const float2*>(at + kHeadDim);
     if (shares > 1 || p.grouped) {
-      // pieces of the prefix come behind the row's own
-      const int piece = pre ? pieces_of(p, p.d.c.unit_of_row(x), x).own + blockIdx.x : blockIdx.x;
-      float* to = piece_ptr(p, piece, x, h);
-      *reinterpret_cast<float2*>(to + 4 * lane) = lo;
-      *reinterpret_cast<float2*>(to + 4 * lane + 2) = hi;
+      float* to = piece_ptr(p, (pre ? 0 : p.prefix_pieces) + blockIdx.x, x, h);
+      *reinterpret_cast<float4*>(to + 4 * lane) = make_float4(lo.x, lo.y, hi.x, hi.y);
       if (lane == 0) *reinterpret_cast<float2*>(to + kHeadDim) = ml;
       continue;
     }
@@ -484,6 +481,7 @@ __global__ void __launch_bounds__(kFewThreads, kFp8 && kN == 1 ? 2 : 1) dense_fe
         make_uint2(pack_bf16(lo.x * inv, lo.y * inv), pack_bf16(hi.x * inv, hi.y * inv));
     if (lane == 0 && p.lse) p.lse[(int64_t)x * kQHeads + h] = (ml.x + log2f(ml.y)) * kLn2;
   }
+  if (p.overlap) grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------- wide
@@ -623,6 +621,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) dense_wide_kernel(const __gri
   const int shares = shares_of(t, kStepTokens, p.wide_q, !p.grouped);
   if ((int)blockIdx.x >= shares) return;
   grid_dependency_wait();
+  if (p.overlap) trigger_dependents();
   const int nq = t.nq, x0 = t.x0;
   const int halves = nq > 32 ? 2 : 1;
   const int64_t pos0 = t.pos0;
@@ -696,9 +695,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) dense_wide_kernel(const __gri
     if (kFp8) asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory");      // row_factor
   }
 
-  const int64_t all = (t.total + kStepTokens - 1) / kStepTokens;
-  const int64_t j0 = all * blockIdx.x / shares;
-  const int steps = (int)(all * (blockIdx.x + 1) / shares - j0);
+  const uint32_t all = (uint32_t)((t.total + kStepTokens - 1) / kStepTokens);
+  const int64_t j0 = share_start(all, blockIdx.x, shares);
+  const int steps = (int)(share_start(all, blockIdx.x + 1, shares) - j0);
   bool ok = true;
 
   if (warp >= kRoleLoad && warp < kRoleMma) {
@@ -1024,66 +1023,46 @@ __global__ void __launch_bounds__(kWideThreads, 1) dense_wide_kernel(const __gri
       fence_before();
       mbar_arrive(p_full(h, c));
     }
-    // ---- the row's result
-    if (ok && steps > 0) ok = mbar_wait_warp(o_full(h, 1), (uint32_t)(steps - 1) & 1u, err, kKernDenseAttn);
+    // ---- the rows' results: from a row to a thread, through the K and V stages once
+    // all products are complete, to a row at a time (16-byte chunks at chunk ^ row)
+    for (int i = 0; i < halves; ++i) ok = mbar_wait_warp(done(i), 0, err, kKernDenseAttn) && ok;
     fence_after();
-    const int x = x0 + q;
-    const bool mine = ok && q < nq;
-    if (shares > 1 || p.grouped) {
-      float* part = nullptr;
-      if (mine) {
-        const int piece = pre ? pieces_of(p, p.d.c.unit_of_row(x), x).own + blockIdx.x : blockIdx.x;
-        part = piece_ptr(p, piece, x, head);
-      }
+    uint8_t* stage = smem + kOffKv + warp * (32 * kHeadDim * 4);
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32];
-        if (steps > 0) {
-          ld32(colO + 32u * c, v);
-          wait_ld();
-          reg_fence(v);
-        }
-        if (mine) {
+    for (int c = 0; c < 4 && ok && steps > 0; ++c) {
+      uint32_t v[32];
+      ld32(colO + 32u * c, v);
+      wait_ld();
+      reg_fence(v);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            *reinterpret_cast<float2*>(part + 32 * c + i) =
-                steps > 0 ? make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])) : make_float2(0.f, 0.f);
-        }
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4*>(stage + lane * (kHeadDim * 4) + (((8 * c + i) ^ lane) << 4)) =
+            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+    __syncwarp();
+    const int rows = !ok ? 0 : (nq - 32 * h < 32 ? nq - 32 * h : 32);
+    const bool whole = shares == 1 && !p.grouped;
+#pragma unroll 4
+    for (int i = 0; i < rows; ++i) {
+      const int x = x0 + 32 * h + i;
+      const float mi = __shfl_sync(0xFFFFFFFFu, m, i), li = __shfl_sync(0xFFFFFFFFu, l, i);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (steps > 0) v = *reinterpret_cast<const float4*>(stage + i * (kHeadDim * 4) + ((lane ^ i) << 4));
+      if (!whole) {
+        float* to = piece_ptr(p, (pre ? 0 : p.prefix_pieces) + blockIdx.x, x, head);
+        *reinterpret_cast<float4*>(to + 4 * lane) = v;
+        if (lane == 0) *reinterpret_cast<float2*>(to + kHeadDim) = make_float2(mi, li);
+        continue;
       }
-      if (mine) *reinterpret_cast<float2*>(part + kHeadDim) = make_float2(m, l);
-    } else {
-      const float r = 1.f / l;
-      bool good = good_sum(l);
-      uint16_t* out = p.out + ((int64_t)x * kQHeads + head) * kHeadDim;
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32];
-        if (steps > 0) {
-          ld32(colO + 32u * c, v);
-          wait_ld();
-          reg_fence(v);
-        }
-        if (mine && steps > 0) {
-          float far = 0.f;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) far = fmaxf(far, isfinite(__uint_as_float(v[i])) ? 0.f : 1.f);
-          good = good && far == 0.f;
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint4 o;
-            o.x = pack_bf16(__uint_as_float(v[i]) * r, __uint_as_float(v[i + 1]) * r);
-            o.y = pack_bf16(__uint_as_float(v[i + 2]) * r, __uint_as_float(v[i + 3]) * r);
-            o.z = pack_bf16(__uint_as_float(v[i + 4]) * r, __uint_as_float(v[i + 5]) * r);
-            o.w = pack_bf16(__uint_as_float(v[i + 6]) * r, __uint_as_float(v[i + 7]) * r);
-            *reinterpret_cast<uint4*>(out + 32 * c + i) = o;
-          }
-        }
+      const bool fine = good_sum(li) && isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w);
+      if (!__all_sync(0xFFFFFFFFu, fine)) {
+        attend_row(p, t.u, x, head);
+        continue;
       }
-      if (mine && good && p.lse) p.lse[(int64_t)x * kQHeads + head] = (m + log2f(l)) * kLn2;
-      for (uint32_t again = __ballot_sync(0xFFFFFFFFu, mine && !good); again; again &= again - 1) {
-        __syncwarp();
-        attend_row(p, t.u, x0 + 32 * h + __ffs(again) - 1, head);
-      }
+      const float inv = 1.f / li;
+      reinterpret_cast<uint2*>(p.out + ((int64_t)x * kQHeads + head) * kHeadDim)[lane] =
+          make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+      if (p.lse && lane == 0) p.lse[(int64_t)x * kQHeads + head] = (mi + log2f(li)) * kLn2;
     }
   }
 
@@ -1095,59 +1074,74 @@ __global__ void __launch_bounds__(kWideThreads, 1) dense_wide_kernel(const __gri
 
 // ------------------------------------------------------------------- join
 
-// One warp per (row, head): lane l holds dims 4 l .. 4 l + 3.
-constexpr int kJoinThreads = 256;
+// kSplit warps per (row, head), each over every kSplit-th piece (eight where there are
+// many: their loads are what the join waits for); lane l holds dims 4 l .. 4 l + 3.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+template <int kSplit>
 __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_constant__ DenseParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  __shared__ float4 part_o[kSplit > 1 ? kJoinWarps : 1][32];
+  __shared__ float2 part_ml[kSplit > 1 ? kJoinWarps : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s0 = warp % kSplit;
+  const int64_t w = (int64_t)blockIdx.x * (kJoinWarps / kSplit) + warp / kSplit;
   const int x = (int)(w / kQHeads), head = (int)(w % kQHeads);
-  grid_dependency_wait();
-  if (x >= p.d.c.rows()) return;
+  const bool mine = x < p.d.c.rows();                // (with kSplit warps the same for the whole CTA)
+  if (!mine) return;
   const int u = p.d.c.unit_of_row(x);
-  const Pieces np = pieces_of(p, u, x);
-  const int pieces = np.own + np.prefix;
+  const int pieces = p.prefix_pieces + own_pieces(p, u, x);
+  grid_dependency_wait();
   if (!p.grouped && pieces == 1) return;             // complete
-  const float* part = piece_ptr(p, 0, x, head);
-  const int64_t stride = (int64_t)p.d.c.rows() * kQHeads * kRowFloats;
-  auto piece = [&](int s) {
-    const float* o = part + s * stride + 4 * lane;
-    const float2 lo = *reinterpret_cast<const float2*>(o), hi = *reinterpret_cast<const float2*>(o + 2);
-    return make_float4(lo.x, lo.y, hi.x, hi.y);
-  };
-  // the first pieces' O are on their way with the maxima and sums
-  constexpr int kFirst = 16, kPer = 2 * kMaxShares / 32;
-  float4 first[kFirst];
-#pragma unroll
-  for (int s = 0; s < kFirst; ++s)
-    if (s < pieces) first[s] = piece(s);
-  float2 ml[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    ml[i] = lane + 32 * i < pieces ? *reinterpret_cast<const float2*>(part + (lane + 32 * i) * stride + kHeadDim)
-                                   : make_float2(-INFINITY, 0.f);
-  float m = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
-  static_assert(kPer == 4, "four pieces per lane");
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  float a[kPer], l = 0.f;                            // a = 0: nothing there
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    a[i] = ml[i].y != 0.f ? exp2f(ml[i].x - m) : 0.f;
-    l = fmaf(ml[i].y, a[i], l);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+  const int64_t stride = (int64_t)kSplit * p.d.c.rows() * kQHeads * kRowFloats;
+  const float* part = piece_ptr(p, s0, x, head);
+  const int n = pieces > s0 ? (pieces - s0 + kSplit - 1) / kSplit : 0;       // of this warp
+  // eight pieces' O, maxima and sums are on their way at a time
+  constexpr int kTurn = 8;
+  float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](int s, float4 o) {
-    const float mine = s < 64 ? (s < 32 ? a[0] : a[1]) : (s < 96 ? a[2] : a[3]);
-    const float k = __shfl_sync(0xFFFFFFFFu, mine, s & 31);
-    if (k != 0.f) acc = make_float4(fmaf(o.x, k, acc.x), fmaf(o.y, k, acc.y), fmaf(o.z, k, acc.z), fmaf(o.w, k, acc.w));
-  };
+  for (int k0 = 0; k0 < n; k0 += kTurn) {
+    float4 o[kTurn];
+    float2 ml[kTurn];
 #pragma unroll
-  for (int s = 0; s < kFirst; ++s)
-    if (s < pieces) add(s, first[s]);
-#pragma unroll 4
-  for (int s = kFirst; s < pieces; ++s) add(s, piece(s));
+    for (int k = 0; k < kTurn; ++k) {
+      const float* from = part + (k0 + k) * stride;
+      ml[k] = k0 + k < n ? *reinterpret_cast<const float2*>(from + kHeadDim) : make_float2(-INFINITY, 0.f);
+      o[k] = k0 + k < n ? *reinterpret_cast<const float4*>(from + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float mn = m;
+#pragma unroll
+    for (int k = 0; k < kTurn; ++k) mn = fmaxf(mn, ml[k].x);
+    const float a = l != 0.f ? exp2f(m - mn) : 0.f;
+    m = mn;
+    l *= a;
+    acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
+#pragma unroll
+    for (int k = 0; k < kTurn; ++k) {
+      const float c = ml[k].y != 0.f ? exp2f(ml[k].x - mn) : 0.f;            // 0: nothing there
+      if (c == 0.f) continue;
+      l = fmaf(ml[k].y, c, l);
+      acc = make_float4(fmaf(o[k].x, c, acc.x), fmaf(o[k].y, c, acc.y), fmaf(o[k].z, c, acc.z), fmaf(o[k].w, c, acc.w));
+    }
+  }
+  if (kSplit > 1) {
+    part_o[warp][lane] = acc;
+    if (lane == 0) part_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (s0 != 0) return;
+    float mn = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kSplit; ++k) mn = fmaxf(mn, part_ml[warp + k].x);
+    l = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kSplit; ++k) {
+      const float2 ml = part_ml[warp + k];
+      const float4 o = part_o[warp + k][lane];
+      const float c = ml.y != 0.f ? exp2f(ml.x - mn) : 0.f;
+      if (c == 0.f) continue;
+      l = fmaf(ml.y, c, l);
+      acc = make_float4(fmaf(o.x, c, acc.x), fmaf(o.y, c, acc.y), fmaf(o.z, c, acc.z), fmaf(o.w, c, acc.w));
+    }
+    m = mn;
+  }
   const bool fine = good_sum(l) && isfinite(acc.x) && isfinite(acc.y) && isfinite(acc.z) && isfinite(acc.w);
   if (!__all_sync(0xFFFFFFFFu, fine)) {
     attend_row(p, u, x, head);
@@ -1169,6 +1163,7 @@ struct Plan {
   int wide_q = 1, few_q = 1;
   int few_rows = 0;                                  // queries of a tile of the few kernel, at most
   int64_t pieces = 1;                                // of a row, at most
+  int64_t prefix_pieces = 0;
   int64_t bytes = 256;
 };
 
@@ -1259,7 +1254,8 @@ Plan make_plan(const DenseAttn& d, int sms, int32_t* tile0) {
   }
   int64_t own = a.wide_tiles > 0 ? ceil_div(longest_own, a.wide_q) : 0;
   if (few_units > 0 && ceil_div(longest_few, a.few_q) > own) own = ceil_div(longest_few, a.few_q);
-  a.pieces = own + (a.grouped ? (few_prefix ? ceil_div(few_prefix_steps, a.few_q) : ceil_div(prefix_steps, a.wide_q)) : 0);
+  if (a.grouped) a.prefix_pieces = few_prefix ? ceil_div(few_prefix_steps, a.few_q) : ceil_div(prefix_steps, a.wide_q);
+  a.pieces = own + a.prefix_pieces;
   if (a.grouped || a.pieces > 1) a.bytes = a.pieces * d.c.rows() * kQHeads * kRowFloats * 4;
   return a;
 }
@@ -1291,6 +1287,8 @@ cudaError_t launch_dense_attn(const DenseAttn& d, const uint16_t* q, float softm
   const Plan a = make_plan(d, sms, p.tile0);
   p.d = d;
   p.grouped = a.grouped;
+  p.prefix_pieces = (int32_t)a.prefix_pieces;
+  p.overlap = a.wide_tiles > 0 && a.few_tiles > 0;
   p.wide_q = a.wide_q;
   p.few_q = a.few_q;
   p.q = q;
@@ -1313,8 +1311,11 @@ cudaError_t launch_dense_attn(const DenseAttn& d, const uint16_t* q, float softm
     e = launch_kernel(kernel, grid, dim3(kFewThreads), fp8 ? FewLayout<true>::kSmem : FewLayout<false>::kSmem, s, 0, dim3(1), p);
   }
   if (e != cudaSuccess || (!a.grouped && a.pieces <= 1)) return e;
-  const int64_t warps = (int64_t)d.c.rows() * kQHeads;
-  return launch_kernel(dense_join_kernel, dim3((unsigned)((warps + 7) / 8)), dim3(kJoinThreads), 0, s, 0, dim3(1), p);
+  const int64_t rows = (int64_t)d.c.rows() * kQHeads;
+  if (a.pieces > 8)
+    return launch_kernel(dense_join_kernel<kJoinWarps>, dim3((unsigned)rows), dim3(kJoinThreads), 0, s, 0, dim3(1), p);
+  return launch_kernel(dense_join_kernel<1>, dim3((unsigned)ceil_div(rows, kJoinWarps)), dim3(kJoinThreads), 0, s, 0,
+                       dim3(1), p);
 }
 
 }  // namespace qsa
