@@ -1028,41 +1028,65 @@ __global__ void __launch_bounds__(kWideThreads, 1) dense_wide_kernel(const __gri
     for (int i = 0; i < halves; ++i) ok = mbar_wait_warp(done(i), 0, err, kKernDenseAttn) && ok;
     fence_after();
     uint8_t* stage = smem + kOffKv + warp * (32 * kHeadDim * 4);
-#pragma unroll 1
-    for (int c = 0; c < 4 && ok && steps > 0; ++c) {
-      uint32_t v[32];
-      ld32(colO + 32u * c, v);
-      wait_ld();
-      reg_fence(v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<uint4*>(stage + lane * (kHeadDim * 4) + (((8 * c + i) ^ lane) << 4)) =
-            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    }
-    __syncwarp();
     const int rows = !ok ? 0 : (nq - 32 * h < 32 ? nq - 32 * h : 32);
-    const bool whole = shares == 1 && !p.grouped;
-#pragma unroll 4
-    for (int i = 0; i < rows; ++i) {
-      const int x = x0 + 32 * h + i;
-      const float mi = __shfl_sync(0xFFFFFFFFu, m, i), li = __shfl_sync(0xFFFFFFFFu, l, i);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (steps > 0) v = *reinterpret_cast<const float4*>(stage + i * (kHeadDim * 4) + ((lane ^ i) << 4));
-      if (!whole) {
-        float* to = piece_ptr(p, (pre ? 0 : p.prefix_pieces) + blockIdx.x, x, head);
+    if (shares > 1 || p.grouped) {
+#pragma unroll 1
+      for (int c = 0; c < 4 && ok && steps > 0; ++c) {
+        uint32_t v[32];
+        ld32(colO + 32u * c, v);
+        wait_ld();
+        reg_fence(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(stage + lane * (kHeadDim * 4) + (((8 * c + i) ^ lane) << 4)) =
+              make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      }
+      __syncwarp();
+      float* to = piece_ptr(p, (pre ? 0 : p.prefix_pieces) + blockIdx.x, x0 + 32 * h, head);
+#pragma unroll 8
+      for (int i = 0; i < rows; ++i, to += kQHeads * kRowFloats) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (steps > 0) v = *reinterpret_cast<const float4*>(stage + i * (kHeadDim * 4) + ((lane ^ i) << 4));
         *reinterpret_cast<float4*>(to + 4 * lane) = v;
-        if (lane == 0) *reinterpret_cast<float2*>(to + kHeadDim) = make_float2(mi, li);
-        continue;
       }
-      const bool fine = good_sum(li) && isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w);
-      if (!__all_sync(0xFFFFFFFFu, fine)) {
-        attend_row(p, t.u, x, head);
-        continue;
+      if (lane < rows)
+        *reinterpret_cast<float2*>(piece_ptr(p, (pre ? 0 : p.prefix_pieces) + blockIdx.x, x0 + q, head) + kHeadDim) =
+            make_float2(m, l);
+    } else {
+      const float inv = 1.f / l;
+      bool good = good_sum(l) && steps > 0;
+#pragma unroll 1
+      for (int c = 0; c < 4 && ok && steps > 0; ++c) {
+        uint32_t v[32];
+        ld32(colO + 32u * c, v);
+        wait_ld();
+        reg_fence(v);
+        float far = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) far = fmaxf(far, isfinite(__uint_as_float(v[i])) ? 0.f : 1.f);
+        good = good && far == 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = pack_bf16(__uint_as_float(v[8 * i + 2 * k]) * inv, __uint_as_float(v[8 * i + 2 * k + 1]) * inv);
+          *reinterpret_cast<uint4*>(stage + lane * (kHeadDim * 2) + (((4 * c + i) ^ (lane & 15)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
-      const float inv = 1.f / li;
-      reinterpret_cast<uint2*>(p.out + ((int64_t)x * kQHeads + head) * kHeadDim)[lane] =
-          make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
-      if (p.lse && lane == 0) p.lse[(int64_t)x * kQHeads + head] = (mi + log2f(li)) * kLn2;
+      __syncwarp();
+      // 16 lanes a row
+      uint16_t* out = p.out + ((int64_t)(x0 + 32 * h) * kQHeads + head) * kHeadDim;
+#pragma unroll 8
+      for (int i = lane >> 4; i < rows && steps > 0; i += 2)
+        reinterpret_cast<uint4*>(out + (int64_t)i * (kQHeads * kHeadDim))[lane & 15] =
+            *reinterpret_cast<const uint4*>(stage + i * (kHeadDim * 2) + (((lane & 15) ^ (i & 15)) << 4));
+      if (lane < rows && good && p.lse) p.lse[(int64_t)(x0 + q) * kQHeads + head] = (m + log2f(l)) * kLn2;
+      for (uint32_t again = __ballot_sync(0xFFFFFFFFu, lane < rows && !good); again; again &= again - 1) {
+        __syncwarp();
+        attend_row(p, t.u, x0 + 32 * h + __ffs(again) - 1, head);
+      }
     }
   }
 
@@ -1212,7 +1236,7 @@ Plan make_plan(const DenseAttn& d, int sms, int32_t* tile0) {
   a.wide_tiles = own_tiles + layers * per_prefix;
   int64_t longest_own = 0, longest = 0;              // wide
   auto each = [&](auto&& fn) {
-    for (int u = 0; u < units; ++u)
+    for (int u = 0; own_tiles > 0 && u < units; ++u)
       if (d.c.unit_tokens(u) > kFewQueries)
         for (int i = 0; i < d.c.unit_tokens(u); i += kTileQueries)
           fn(ceil_div(own_tile(d, a.grouped, u, i).total, kStepTokens));

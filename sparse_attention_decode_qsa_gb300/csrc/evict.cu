@@ -3,7 +3,7 @@
 // rest those with the largest weights (equal weights: the lower position).
 //
 //  * select: per layer the keep-th largest weight by a radix select over the
-//    weights' bits (11 + 11 + 10), then the kept positions in ascending order;
+//    weights' bits, eight at a time, then the kept positions in ascending order;
 //    the kept tokens' new slots; and the list of rows that have to move.
 //  * move: those rows, and the kept tokens' keys, scales and weights (the keys
 //    and scales into the workspace, since they close up within their own arrays).
@@ -21,13 +21,32 @@
 namespace qsa {
 namespace {
 
-constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectCtas = 8;                    // a cluster per layer
 
 // Descending order of weights as unsigned integers: -0 equals +0, NaN comes last.
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0u;
   const uint32_t b = __float_as_uint(w + 0.0f);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Barrier of the cluster: what its threads wrote before (to shared memory or to
+// global memory) its threads see afterwards.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The word at `local` in the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_read(const uint32_t* local, uint32_t rank) {
+  uint32_t at, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
 }
 
 // Whole CTA: exclusive prefix sums over the warps of one value per warp, and the
@@ -37,7 +56,7 @@ __device__ __forceinline__ uint32_t warp_offsets(uint32_t mine, uint32_t* s_warp
   __syncthreads();
   if (lane == 0) s_warp[warp] = mine;
   __syncthreads();
-  uint32_t v = s_warp[lane];
+  uint32_t v = lane < kSelectWarps ? s_warp[lane] : 0u;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, v, o);
@@ -46,129 +65,241 @@ __device__ __forceinline__ uint32_t warp_offsets(uint32_t mine, uint32_t* s_warp
   *total = __shfl_sync(0xFFFFFFFFu, v, 31);
   return __shfl_sync(0xFFFFFFFFu, v, warp) - mine;
 }
-static_assert(kSelectWarps == 32, "one lane per warp in the scan");
+static_assert(kSelectWarps <= 32, "one lane per warp in the scan");
 
-__global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ uint32_t hist[2048], s_warp[kSelectWarps], s_bin[2];
-  const int layer = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Whole cluster: the sums of two values over the CTAs before this one (both values
+// the same in all threads of a CTA), and over all.  s_pair has been left by the
+// readers of an earlier exchange (a cluster barrier lies in between).
+__device__ __forceinline__ void cta_offsets(uint32_t a, uint32_t b, uint32_t* s_pair, uint32_t rank, uint32_t* a0,
+                                            uint32_t* b0, uint32_t* a_all) {
+  if (threadIdx.x == 0) {
+    s_pair[0] = a;
+    s_pair[1] = b;
+  }
+  cluster_sync();
+  *a0 = *b0 = *a_all = 0;
+#pragma unroll
+  for (uint32_t r = 0; r < kSelectCtas; ++r) {
+    const uint32_t x = cluster_read(s_pair, r), y = cluster_read(s_pair + 1, r);
+    *a_all += x;
+    if (r < rank) {
+      *a0 += x;
+      *b0 += y;
+    }
+  }
+}
+
+// One cluster per layer; each CTA has an eighth of the tokens, and then of the kept
+// ones.  Per digit every CTA counts its own keys and adds up all CTAs' counts from
+// their shared memory: one cluster barrier per digit.  12 layers of 32768 tokens:
+// 50 us with one CTA per layer.
+__global__ void __launch_bounds__(kSelectThreads, 1) __cluster_dims__(kSelectCtas, 1, 1)
+evict_select_kernel(const __grid_constant__ EvictParams p) {
+  __shared__ uint32_t hist[4][256], s_warp[kSelectWarps], s_bin[2], s_pair[2][2];
+  const int layer = blockIdx.x / kSelectCtas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cluster_rank();
   const float* w = p.weights + layer * p.weight_stride;
-  const int64_t n = p.n, keep = p.keep, lo = p.first, hi = p.n - p.last;      // lo .. hi - 1 compete
-  int32_t* kept = p.kept + layer * keep;
-  int32_t* slots = p.slot_table + ((int64_t)p.req * p.n_layers + layer) * p.ctx_cap;
-  int32_t* new_slot = p.new_slot + layer * keep;
-  int32_t* holes = p.holes + layer * keep;
+  // (fewer than 2^31 tokens: places and rows fit 32 bits)
+  const uint32_t n = (uint32_t)p.n, keep = (uint32_t)p.keep, lo = (uint32_t)p.first, hi = (uint32_t)(p.n - p.last);      // lo .. hi - 1 compete
+  int32_t* kept = p.kept + layer * p.keep;
+  const int32_t* slots = p.slot_table + ((int64_t)p.req * p.n_layers + layer) * p.ctx_cap;
+  int32_t* new_slot = p.new_slot + layer * p.keep;
+  int32_t* holes = p.holes + layer * p.keep;
   uint32_t* used = p.used + layer * p.used_words;
-  int2* moves = p.moves + layer * keep;
+  int2* moves = p.moves + layer * p.keep;
+  for (int i = tid; i < 4 * 256; i += kSelectThreads) (&hist[0][0])[i] = 0;
+  // runs of whole 32s: of the tokens per CTA and warp, of the kept ones likewise
+  auto run_of = [&](uint32_t count, uint32_t* from, uint32_t* to) {
+    const uint32_t words = (count + 31) / 32, per = (words + kSelectCtas * kSelectWarps - 1) / (kSelectCtas * kSelectWarps);
+    const uint64_t a = (uint64_t)(rank * kSelectWarps + warp) * per * 32, e = a + per * 32;
+    *from = a < count ? (uint32_t)a : count;
+    *to = e < count ? (uint32_t)e : count;
+  };
+  uint32_t t0, t1, k0, k1;
+  run_of(n, &t0, &t1);
+  run_of(keep, &k0, &k1);
   grid_dependency_wait();
+  for (int64_t i = (int64_t)rank * kSelectThreads + tid; i < p.used_words; i += kSelectCtas * kSelectThreads) used[i] = 0;
+  __syncthreads();
+
+  // eight words of 32 tokens at a time, their loads side by side
+  constexpr int kTurn = 8;
+  auto load = [&](uint32_t t, float (&v)[kTurn]) {
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) v[j] = t + 32 * j + lane < t1 ? w[t + 32 * j + lane] : 0.f;
+  };
 
   // ---- the need-th largest key T, and how many tokens at T stay
   const int64_t need = keep - p.first - p.last;
   uint32_t T = 0, left = (uint32_t)need;
   if (need > 0) {
     uint32_t mask = 0;
+#pragma unroll 1
+    for (int d = 0; d < 4; ++d) {
+      const int shift = 24 - 8 * d;
+      for (uint32_t t = t0; t < t1; t += 32 * kTurn) {
+        float v[kTurn];
+        load(t, v);
 #pragma unroll
-    for (int d = 0; d < 3; ++d) {
-      const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0), bits = d == 2 ? 10 : 11;
-      for (int i = tid; i < 2048; i += kSelectThreads) hist[i] = 0;
-      __syncthreads();
-      for (int64_t t = lo + tid; t < hi; t += kSelectThreads) {
-        const uint32_t k = weight_key(w[t]);
-        if ((k & mask) == T) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+        for (int j = 0; j < kTurn; ++j) {
+          const uint32_t at = t + 32 * j + lane;
+          const uint32_t k = weight_key(v[j]);
+          if (at < t1 && at >= lo && at < hi && (k & mask) == T) atomicAdd(&hist[d][(k >> shift) & 255u], 1u);
+        }
       }
-      __syncthreads();
-      // bins from the top: thread i has the bins 2047 - 2 i and 2046 - 2 i
-      const uint32_t a = hist[2047 - 2 * tid], b = hist[2046 - 2 * tid];
-      uint32_t v = a + b;
+      cluster_sync();
+      // bins from the top, one a thread
+      uint32_t a = 0;
+      if (tid < 256) {
+#pragma unroll
+        for (uint32_t r = 0; r < kSelectCtas; ++r) a += cluster_read(&hist[d][255 - tid], r);
+      }
+      uint32_t v = a;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, v, o);
         if (lane >= o) v += y;
       }
       uint32_t total;
-      const uint32_t before = warp_offsets(__shfl_sync(0xFFFFFFFFu, v, 31), s_warp, &total) + v - a - b;
-      if (before < left && left <= before + a + b) {
-        const bool first = left <= before + a;
-        s_bin[0] = first ? 2047 - 2 * tid : 2046 - 2 * tid;
-        s_bin[1] = left - before - (first ? 0 : a);
+      const uint32_t before = warp_offsets(__shfl_sync(0xFFFFFFFFu, v, 31), s_warp, &total) + v - a;
+      if (before < left && left <= before + a) {
+        s_bin[0] = 255 - tid;
+        s_bin[1] = left - before;
       }
       __syncthreads();
       T |= s_bin[0] << shift;
       left = s_bin[1];
-      mask |= ((1u << bits) - 1u) << shift;
-      __syncthreads();
+      mask |= 255u << shift;
     }
   }
 
-  // ---- kept positions, ascending: a warp owns a run of tokens
-  const int64_t run = ((n + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
-  const int64_t t0 = warp * run < n ? warp * run : n, t1 = t0 + run < n ? t0 + run : n;
-  auto look = [&](int64_t t, uint32_t* more, uint32_t* same) {
+  // ---- kept positions, ascending
+  auto look = [&](uint32_t t, float v, uint32_t* more, uint32_t* same) {
     const bool there = t < t1, mid = there && t >= lo && t < hi;
-    const uint32_t k = mid ? weight_key(w[t]) : 0u;
+    const uint32_t k = weight_key(v);
     *more = __ballot_sync(0xFFFFFFFFu, there && (!mid || (need > 0 && k > T)));
     *same = __ballot_sync(0xFFFFFFFFu, mid && need > 0 && k == T);
   };
-  uint32_t more, same, n_more = 0, n_same = 0, total;
-  for (int64_t t = t0; t < t1; t += 32) {
-    look(t + lane, &more, &same);
-    n_more += __popc(more);
-    n_same += __popc(same);
+  uint32_t more, same, n_more = 0, n_same = 0, all_more, all_same, c_more, c_same, total;
+  for (uint32_t t = t0; t < t1; t += 32 * kTurn) {
+    float v[kTurn];
+    load(t, v);
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) {
+      look(t + 32 * j + lane, v[j], &more, &same);
+      n_more += __popc(more);
+      n_same += __popc(same);
+    }
   }
-  uint32_t b_more = warp_offsets(n_more, s_warp, &total), b_same = warp_offsets(n_same, s_warp, &total);
-  for (int64_t t = t0; t < t1; t += 32) {
-    look(t + lane, &more, &same);
-    const uint32_t below = (1u << lane) - 1u, bit = 1u << lane;
-    const uint32_t rank = b_same + __popc(same & below);
-    if ((more & bit) || ((same & bit) && rank < left))
-      kept[b_more + __popc(more & below) + (rank < left ? rank : left)] = (int32_t)(t + lane);
-    b_more += __popc(more);
-    b_same += __popc(same);
+  uint32_t b_more = warp_offsets(n_more, s_warp, &all_more), b_same = warp_offsets(n_same, s_warp, &all_same);
+  cta_offsets(all_more, all_same, s_pair[0], rank, &c_more, &c_same, &total);
+  b_more += c_more;
+  b_same += c_same;
+  const int32_t base = (int32_t)(p.row_base + layer * p.layer_rows);
+  for (uint32_t t = t0; t < t1; t += 32 * kTurn) {
+    float v[kTurn];
+    int32_t slot[kTurn];
+    load(t, v);
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) slot[j] = t + 32 * j + lane < t1 ? slots[t + 32 * j + lane] : 0;
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) {
+      const uint32_t at = t + 32 * j + lane;
+      look(at, v[j], &more, &same);
+      const uint32_t below = (1u << lane) - 1u, bit = 1u << lane;
+      const uint32_t rank_same = b_same + __popc(same & below);
+      uint32_t row = keep;                           // of the region, `keep` or more: none of its first `keep`
+      if ((more & bit) || ((same & bit) && rank_same < left)) {
+        // the token stays: its place, its slot, and its row if that is among the first `keep`
+        const uint32_t i = b_more + __popc(more & below) + (rank_same < left ? rank_same : left);
+        kept[i] = (int32_t)at;
+        new_slot[i] = slot[j];
+        if (slot[j] < 0 || (int64_t)slot[j] >= p.pool_rows) report_error(p.err, QSA_ERR_BAD_SLOT, kKernEvict, at);
+        row = slot[j] >= base ? (uint32_t)(slot[j] - base) : keep;
+      }
+      // rows in use: a word of 32 rows at once where the warp's rows lie in one
+      const uint32_t low = __ballot_sync(0xFFFFFFFFu, row < keep);
+      if (low) {
+        const uint32_t word = __shfl_sync(0xFFFFFFFFu, row >> 5, __ffs(low) - 1);
+        const bool mine = row < keep;
+        if (__all_sync(0xFFFFFFFFu, !mine || (row >> 5) == word)) {
+          const uint32_t bits = __reduce_or_sync(0xFFFFFFFFu, mine ? 1u << (row & 31) : 0u);
+          if (lane == 0) atomicOr(used + word, bits);
+        } else if (mine) {
+          atomicOr(used + (row >> 5), 1u << (row & 31));
+        }
+      }
+      b_more += __popc(more);
+      b_same += __popc(same);
+    }
   }
-  for (int64_t i = tid; i < p.used_words; i += kSelectThreads) used[i] = 0;
-  __syncthreads();
+  __threadfence();
+  cluster_sync();
 
-  // ---- rows: those below `keep` that stay in use, then the free ones among them
-  const int64_t base = p.row_base + layer * p.layer_rows;
-  auto moves_away = [&](int32_t slot) { return slot >= base + keep && slot < base + p.layer_rows; };
-  for (int64_t i = tid; i < keep; i += kSelectThreads) {
-    const int32_t slot = slots[kept[i]];
-    if (slot < 0 || (int64_t)slot >= p.pool_rows) report_error(p.err, QSA_ERR_BAD_SLOT, kKernEvict, kept[i]);
-    new_slot[i] = slot;
-    const int64_t row = slot - base;
-    if (row >= 0 && row < keep) atomicOr(used + (row >> 5), 1u << (row & 31));
+  // ---- the free rows below `keep`, and the kept tokens whose rows have to move there
+  const uint32_t layer_rows = (uint32_t)p.layer_rows;
+  auto moves_away = [&](int32_t slot) {
+    return slot >= base && (uint32_t)(slot - base) >= keep && (uint32_t)(slot - base) < layer_rows;
+  };
+  // of the 32 kept places (or rows) from i on: free rows, and tokens that move
+  auto rows_at = [&](uint32_t i, uint32_t (&open)[kTurn], int32_t (&slot)[kTurn]) {
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) {
+      const uint32_t at = i + 32 * j;
+      open[j] = at < k1 ? ~__ldcg(used + (at >> 5)) : 0u;
+      if (at < k1 && k1 - at < 32) open[j] &= (1u << (k1 - at)) - 1u;
+      slot[j] = at + lane < k1 ? __ldcg(new_slot + at + lane) : -1;
+    }
+  };
+  uint32_t n_free = 0, n_away = 0, all_free, all_away, c_free, c_away;
+  for (uint32_t i = k0; i < k1; i += 32 * kTurn) {
+    uint32_t open[kTurn];
+    int32_t slot[kTurn];
+    rows_at(i, open, slot);
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) {
+      n_free += __popc(open[j]);
+      n_away += __popc(__ballot_sync(0xFFFFFFFFu, moves_away(slot[j])));
+    }
   }
-  __syncthreads();
-  const int64_t run2 = ((keep + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
-  const int64_t k0 = warp * run2 < keep ? warp * run2 : keep, k1 = k0 + run2 < keep ? k0 + run2 : keep;
-  uint32_t n_free = 0, n_away = 0;
-  for (int64_t i = k0; i < k1; i += 32) {
-    const bool there = i + lane < k1;
-    n_free += __popc(__ballot_sync(0xFFFFFFFFu, there && !((used[i >> 5] >> lane) & 1u)));
-    n_away += __popc(__ballot_sync(0xFFFFFFFFu, there && moves_away(new_slot[i + lane])));
-  }
-  uint32_t b_free = warp_offsets(n_free, s_warp, &total), b_away = warp_offsets(n_away, s_warp, &total);
+  uint32_t b_free = warp_offsets(n_free, s_warp, &all_free), b_away = warp_offsets(n_away, s_warp, &all_away);
+  cta_offsets(all_away, all_free, s_pair[1], rank, &c_away, &c_free, &total);
+  b_free += c_free;
+  b_away += c_away;
   const uint32_t below = (1u << lane) - 1u;
-  for (int64_t i = k0; i < k1; i += 32) {
-    const bool free_row = i + lane < k1 && !((used[i >> 5] >> lane) & 1u);
-    const uint32_t m = __ballot_sync(0xFFFFFFFFu, free_row);
-    if (free_row) holes[b_free + __popc(m & below)] = (int32_t)(i + lane);
-    b_free += __popc(m);
+  for (uint32_t i = k0; i < k1; i += 32 * kTurn) {
+    uint32_t open[kTurn];
+    int32_t slot[kTurn];
+    rows_at(i, open, slot);
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) {
+      if ((open[j] >> lane) & 1u) holes[b_free + __popc(open[j] & below)] = (int32_t)(i + 32 * j + lane);
+      b_free += __popc(open[j]);
+    }
   }
-  __syncthreads();
+  __threadfence();
+  cluster_sync();
   // (there are no fewer free rows than moving ones: the tokens in rows below
   // `keep` use at most one row each)
-  for (int64_t i = k0; i < k1; i += 32) {
-    const bool away = i + lane < k1 && moves_away(new_slot[i + lane]);
-    const uint32_t m = __ballot_sync(0xFFFFFFFFu, away);
-    if (away) {
-      const uint32_t r = b_away + __popc(m & below);
-      const int32_t to = (int32_t)(base + holes[r]);
-      moves[r] = make_int2(new_slot[i + lane], to);
-      new_slot[i + lane] = to;
+  for (uint32_t i = k0; i < k1; i += 32 * kTurn) {
+    uint32_t open[kTurn], r[kTurn];
+    int32_t slot[kTurn], to[kTurn];
+    rows_at(i, open, slot);
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) {
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, moves_away(slot[j]));
+      r[j] = b_away + __popc(m & below);
+      to[j] = moves_away(slot[j]) ? base + (int32_t)__ldcg(holes + r[j]) : 0;
+      b_away += __popc(m);
     }
-    b_away += __popc(m);
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) {
+      if (!moves_away(slot[j])) continue;
+      moves[r[j]] = make_int2(slot[j], to[j]);
+      new_slot[i + 32 * j + lane] = to[j];
+    }
   }
-  if (tid == 0) p.n_moves[layer] = (int32_t)total;
+  if (tid == 0 && rank == 0) p.n_moves[layer] = (int32_t)total;
 }
 
 constexpr int kMoveThreads = 256, kMoveWarps = kMoveThreads / 32;
@@ -245,7 +376,8 @@ int64_t evict_layout(EvictParams* p, void* workspace) {
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
   int sms = 0;
   if (const cudaError_t e = current_sm_count(&sms)) return e;
-  cudaError_t e = launch_kernel(evict_select_kernel, dim3(p.n_layers), dim3(kSelectThreads), 0, s, 0, dim3(1), p);
+  cudaError_t e = launch_kernel(evict_select_kernel, dim3(p.n_layers * kSelectCtas), dim3(kSelectThreads), 0, s, 0,
+                                dim3(1), p);
   if (e != cudaSuccess) return e;
   // eight CTAs per SM over all layers, a row per warp and turn
   int64_t blocks = (p.keep + kMoveWarps - 1) / kMoveWarps;
