@@ -96,13 +96,17 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// Eight e4m3 codes as f16, exactly.
-__device__ __forceinline__ uint32_t codes2_f16(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four and eight e4m3 codes as f16, exactly.
+__device__ __forceinline__ uint2 codes4_f16(uint32_t w) {
+  uint2 h;
+  asm("{\n .reg .b16 x, y;\n mov.b32 {x, y}, %2;\n cvt.rn.f16x2.e4m3x2 %0, x;\n cvt.rn.f16x2.e4m3x2 %1, y;\n}\n"
+      : "=r"(h.x), "=r"(h.y)
+      : "r"(w));
+  return h;
 }
 __device__ __forceinline__ uint4 codes8_f16(uint2 w) {
-  return make_uint4(codes2_f16(w.x & 0xFFFFu), codes2_f16(w.x >> 16), codes2_f16(w.y & 0xFFFFu), codes2_f16(w.y >> 16));
+  const uint2 a = codes4_f16(w.x), b = codes4_f16(w.y);
+  return make_uint4(a.x, a.y, b.x, b.y);
 }
 
 }  // namespace attn

@@ -48,11 +48,20 @@ struct DenseParams {
 
 // Rows x0 .. x0 + nq - 1 (consecutive positions from pos0 on, where they have own
 // tokens) over np tokens of the prefix, the tokens 0 .. na - 1 and b0 .. b0 + nb - 1
-// of unit u, in this order.
+// of unit u, in this order.  (Two contexts of fewer than 2^31 tokens each.)
 struct Tile {
   int u, x0, nq;
-  int64_t pos0, np, na, b0, total;
+  int32_t pos0;
+  uint32_t np, na, b0, total;
 };
+
+__host__ __device__ __forceinline__ void own_part(const DenseAttn& d, int64_t p0, int64_t p1, Tile* t) {
+  int64_t na, b0, nb;
+  own_range(d, p0, p1, &na, &b0, &nb);
+  t->na = (uint32_t)na;
+  t->b0 = (uint32_t)b0;
+  t->total = t->np + (uint32_t)(na + nb);
+}
 
 // Own tile of rows i0 .. of unit u.
 __host__ __device__ __forceinline__ Tile own_tile(const DenseAttn& d, bool grouped, int u, int i0) {
@@ -61,11 +70,9 @@ __host__ __device__ __forceinline__ Tile own_tile(const DenseAttn& d, bool group
   t.u = u;
   t.x0 = d.c.row0[u] + i0;
   t.nq = left < kTileQueries ? left : kTileQueries;
-  t.pos0 = d.c.position(u, t.x0);
-  t.np = grouped ? 0 : d.prefix_len;
-  int64_t nb;
-  own_range(d, t.pos0, t.pos0 + t.nq - 1, &t.na, &t.b0, &nb);
-  t.total = t.np + t.na + nb;
+  t.pos0 = (int32_t)d.c.position(u, t.x0);
+  t.np = grouped ? 0u : (uint32_t)d.prefix_len;
+  own_part(d, t.pos0, t.pos0 + t.nq - 1, &t);
   return t;
 }
 
@@ -76,21 +83,21 @@ __host__ __device__ __forceinline__ Tile prefix_tile(const DenseAttn& d, int l, 
   t.u = l * d.n_req;
   t.x0 = l * layer_rows + i0;
   t.nq = layer_rows - i0 < kTileQueries ? layer_rows - i0 : kTileQueries;
-  t.np = t.total = d.prefix_len;
-  t.pos0 = t.na = t.b0 = 0;
+  t.np = t.total = (uint32_t)d.prefix_len;
+  t.pos0 = 0;
+  t.na = t.b0 = 0;
   return t;
 }
 
-// Shares of a tile: one at least where nothing else writes its rows.  (A list is
-// shorter than 2^33 tokens, its steps fit 32 bits.)
+// Shares of a tile: one at least where nothing else writes its rows.  
 __host__ __device__ __forceinline__ int shares_of(const Tile& t, int step, int q, bool alone) {
-  const uint32_t steps = (uint32_t)((t.total + step - 1) / step);
+  const uint32_t steps = t.total / step + (t.total % step != 0);
   if (steps == 0) return alone ? 1 : 0;
   return (int)((steps + (uint32_t)q - 1) / (uint32_t)q);
 }
 // First step of share i of n.
-__device__ __forceinline__ int64_t share_start(uint32_t steps, uint32_t i, uint32_t n) {
-  return (int64_t)((uint64_t)steps / n * i + (uint64_t)(steps % n) * i / n);
+__device__ __forceinline__ uint32_t share_start(uint32_t steps, uint32_t i, uint32_t n) {
+  return steps / n * i + steps % n * i / n;          // (n <= kMaxShares: no product leaves 32 bits)
 }
 
 // Own pieces of row x of unit u.
@@ -122,19 +129,20 @@ __device__ __forceinline__ Source source_of(const DenseAttn& d, int u) {
   return s;
 }
 // The slot of the i-th token of the tile's list; -2 past its end.
-__device__ __forceinline__ int32_t slot_at(const Source& s, const Tile& t, int64_t i) {
+__device__ __forceinline__ int32_t slot_at(const Source& s, const Tile& t, uint32_t i) {
   if (i >= t.total) return -2;
   if (i < t.np) return s.prefix_slots[i];
-  const int64_t own = i - t.np;
+  const uint32_t own = i - t.np;
   return s.slots[own < t.na ? own : t.b0 + own - t.na];
 }
 // The row behind that slot; nullptr past the end, and (reported) for a bad slot.
-__device__ __forceinline__ const uint8_t* row_at(const BatchDesc& b, const Source& s, const Tile& t, int64_t i,
+__device__ __forceinline__ const uint8_t* row_at(const BatchDesc& b, const Source& s, const Tile& t, uint32_t i,
                                                  int32_t slot) {
   if (slot >= 0 && (int64_t)slot < b.pool_rows) return b.pool + (int64_t)slot * b.row_bytes;
   if (i >= t.total) return nullptr;
   const bool pre = i < t.np;
-  const int64_t own = i - t.np, tok = pre ? i : (own < t.na ? own : t.b0 + own - t.na);
+  const uint32_t own = i - t.np;
+  const int64_t tok = pre ? i : (own < t.na ? own : t.b0 + own - t.na);
   const uint8_t* host = pre ? s.prefix_host : s.host;
   if (slot == -1 && host) return host + tok * b.row_bytes;
   report_error(b.err, QSA_ERR_BAD_SLOT, kKernDenseAttn, ((int64_t)t.u << 40) | (tok & 0xFFFFFFFFFFll));
@@ -156,13 +164,11 @@ __device__ __noinline__ void attend_row(const DenseParams& p, int u, int x, int 
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   Tile t;
   t.u = u;
-  t.np = p.d.prefix_len;
+  t.np = (uint32_t)p.d.prefix_len;
   const int64_t pos = p.d.c.position(u, x);
-  int64_t nb;
-  own_range(p.d, pos, pos, &t.na, &t.b0, &nb);
-  t.total = t.np + t.na + nb;
+  own_part(p.d, pos, pos, &t);
   const Source src = source_of(p.d, u);
-  for (int64_t i = 0; i < t.total; ++i) {
+  for (uint32_t i = 0; i < t.total; ++i) {
     const uint8_t* row = row_at(b, src, t, i, slot_at(src, t, i));
     if (!row) continue;
     const float4 k = row_values(row, g, lane, fp8);
@@ -238,20 +244,20 @@ __global__ void __launch_bounds__(kFewThreads, kFp8 && kN == 1 ? 2 : 1) dense_fe
   // kernel follows both.
   if (!p.overlap || (int)blockIdx.x >= shares) grid_dependency_wait();
   if ((int)blockIdx.x >= shares) return;
-  const uint32_t all = (uint32_t)((t.total + kFewStep - 1) / kFewStep);
-  const int64_t s0 = share_start(all, blockIdx.x, shares);
+  const uint32_t all = t.total / kFewStep + (t.total % kFewStep != 0);
+  const uint32_t s0 = share_start(all, blockIdx.x, shares);
   const int steps = (int)(share_start(all, blockIdx.x + 1, shares) - s0);
   const Source src = source_of(p.d, t.u);
 
   const uint32_t ring = smem_u32(smem) + warp * kStages * L::kStage;
-  const int64_t first = s0 * kFewStep + half * kFewTokens;       // the warp's first token in the tile's list
+  const uint32_t first = s0 * kFewStep + half * kFewTokens;      // the warp's first token in the tile's list
   // lane l < 16: token l of a stage
   auto slot_of = [&](int s) {
-    return lane < kFewTokens && s < steps ? slot_at(src, t, first + (int64_t)s * kFewStep + lane) : -2;
+    return lane < kFewTokens && s < steps ? slot_at(src, t, first + s * kFewStep + lane) : -2;
   };
   auto issue = [&](int s, int32_t slot) {
     const uint8_t* row = nullptr;
-    if (lane < kFewTokens && s < steps) row = row_at(b, src, t, first + (int64_t)s * kFewStep + lane, slot);
+    if (lane < kFewTokens && s < steps) row = row_at(b, src, t, first + s * kFewStep + lane, slot);
     const uint32_t have = __ballot_sync(0xFFFFFFFFu, row != nullptr);
     if (lane == 0) there[warp][s % kStages] = have;
     const uint32_t to = ring + (s % kStages) * L::kStage;
@@ -288,6 +294,9 @@ __global__ void __launch_bounds__(kFewThreads, kFp8 && kN == 1 ? 2 : 1) dense_fe
 #pragma unroll
   for (int n = 0; n < kN; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
 
+  // the newest position that the last query's window leaves out
+  const int64_t gone = (int64_t)t.pos0 + t.nq - 1 - p.d.window;
+  const int32_t newest = gone < -1 ? -1 : (int32_t)gone;
 #pragma unroll 1
   for (int s = 0; s < steps; ++s) {
     const int32_t slot = slot_next;
@@ -323,19 +332,18 @@ __global__ void __launch_bounds__(kFewThreads, kFp8 && kN == 1 ? 2 : 1) dense_fe
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[n][e] *= kFp8 ? ks[e >> 1] * f[n][e & 1] : f[n][e & 1];
     // ---- tokens without a row, and tokens that a query does not see
-    const int64_t i0 = first + (int64_t)s * kFewStep;
-    const int64_t t0 = t.b0 + i0 - t.np - t.na;                  // the first token's position, if it is one of b
-    const int64_t last = t.pos0 + t.nq - 1;
-    const bool free_of = have == 0xFFFFu && (i0 + kFewTokens <= t.np + t.na ||
-                                             (t0 + kFewTokens - 1 <= t.pos0 && t0 > last - p.d.window));
+    const uint32_t i0 = first + s * kFewStep, front = t.np + t.na;            // (front: seen by every query)
+    const int32_t t0 = (int32_t)(t.b0 + i0 - front);             // the first token's position, if it is one of b
+    const bool free_of = have == 0xFFFFu && (i0 + kFewTokens <= front ||
+                                             (i0 >= front && t0 + kFewTokens - 1 <= t.pos0 && t0 > newest));
     if (!free_of) {
 #pragma unroll
       for (int n = 0; n < kN; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int c = r + 8 * (e >> 1);
-          const int64_t pos = t.pos0 + 2 * n + ((2 * j4 + (e & 1)) >> 2), tok = t0 + c;
-          const bool seen = i0 + c < t.np + t.na || (tok <= pos && (tok < p.d.sinks || tok > pos - p.d.window));
+          const int64_t pos = (int64_t)t.pos0 + 2 * n + ((2 * j4 + (e & 1)) >> 2), tok = (int64_t)t.b0 + i0 + c - front;
+          const bool seen = i0 + c < front || (tok <= pos && (tok < p.d.sinks || tok > pos - p.d.window));
           if (!seen || !((have >> c) & 1u)) x[n][e] = -INFINITY;
         }
     }
@@ -397,9 +405,9 @@ __global__ void __launch_bounds__(kFewThreads, kFp8 && kN == 1 ? 2 : 1) dense_fe
           uint32_t va[4];                                        // even dims, odd dims; then tokens + 8
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t a = codes2_f16(v[2 * k + h] & 0xFFFFu), d = codes2_f16(v[2 * k + h] >> 16);
-            va[2 * h] = __byte_perm(a, d, 0x5410);
-            va[2 * h + 1] = __byte_perm(a, d, 0x7632);
+            const uint2 a = codes4_f16(v[2 * k + h]);
+            va[2 * h] = __byte_perm(a.x, a.y, 0x5410);
+            va[2 * h + 1] = __byte_perm(a.x, a.y, 0x7632);
           }
 #pragma unroll
           for (int n = 0; n < kN; ++n) mma16<true>(o[i + k][n], va, pb[n][0], pb[n][1]);
@@ -546,7 +554,7 @@ __device__ __forceinline__ uint64_t low_bits(int64_t k) {
 // Which of the 64 tokens from the i0-th of the tile's list on a query at position
 // pos sees (rows that exist or not).
 __device__ __forceinline__ uint64_t seen_bits(const DenseAttn& d, const Tile& t, int64_t i0, int64_t pos) {
-  const int64_t off = t.np + t.na - i0;                        // the first token of the b range
+  const int64_t off = (int64_t)t.np + t.na - i0;               // the first token of the b range
   const int64_t at = off - t.b0;                               // bit of position 0
   const uint64_t in_window = low_bits(pos + 1 + at) & ~low_bits(pos - d.window + 1 + at);
   const uint64_t sinks = low_bits((d.sinks < pos + 1 ? d.sinks : pos + 1) + at);
@@ -695,8 +703,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) dense_wide_kernel(const __gri
     if (kFp8) asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftWarps) : "memory");      // row_factor
   }
 
-  const uint32_t all = (uint32_t)((t.total + kStepTokens - 1) / kStepTokens);
-  const int64_t j0 = share_start(all, blockIdx.x, shares);
+  const uint32_t all = t.total / kStepTokens + (t.total % kStepTokens != 0);
+  const uint32_t j0 = share_start(all, blockIdx.x, shares);
   const int steps = (int)(share_start(all, blockIdx.x + 1, shares) - j0);
   bool ok = true;
 
@@ -704,8 +712,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) dense_wide_kernel(const __gri
     // ---- loaders: warp w brings tokens 32 w .. 32 w + 31 of a step, lane = token
     const int w = warp - kRoleLoad;
     const Source src = source_of(p.d, t.u);
-    const int64_t first = j0 * kStepTokens + 32 * w + lane, last = pos0 + nq - 1;
-    auto slot_of = [&](int j) { return j < steps ? slot_at(src, t, first + (int64_t)j * kStepTokens) : -2; };
+    const uint32_t first = j0 * kStepTokens + 32 * w + lane;
+    const int64_t last = pos0 + nq - 1;
+    auto slot_of = [&](int j) { return j < steps ? slot_at(src, t, first + j * kStepTokens) : -2; };
     // FP8 rows are loaded into registers, with no copies in flight: rows two
     // steps ahead are on their way from HBM meanwhile
     auto prefetch = [&](int32_t s) {
@@ -720,7 +729,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) dense_wide_kernel(const __gri
     for (int j = 0; j < steps && ok; ++j) {
       const int st = j % kStages;
       const uint32_t turn = (uint32_t)(j / kStages - 1) & 1u;
-      const int64_t i = first + (int64_t)j * kStepTokens;
+      const uint32_t i = first + j * kStepTokens;
       const uint8_t* row = row_at(b, src, t, i, slot_now);
       const int32_t slot_two = slot_of(j + 2);
       if (j >= kStages) ok = mbar_wait_warp(k_empty(st), turn, err, kKernDenseAttn);
@@ -730,7 +739,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) dense_wide_kernel(const __gri
       StepMeta& m = meta[j % kMetas];
       auto write_meta = [&]() {
         const uint32_t there = __ballot_sync(0xFFFFFFFFu, row != nullptr);
-        const int64_t tok = t.b0 + i - t.np - t.na;          // its position, if it is one of b
+        const int64_t tok = (int64_t)t.b0 + i - t.np - t.na; // its position, if it is one of b
         const bool some = i >= t.np + t.na && (tok > pos0 || (tok >= p.d.sinks && tok <= last - p.d.window));
         const bool special = __any_sync(0xFFFFFFFFu, some || row == nullptr);
         if (lane == 0) {
@@ -905,7 +914,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) dense_wide_kernel(const __gri
       const bool special = (sm.special[0] | sm.special[1] | sm.special[2] | sm.special[3]) != 0;
       uint64_t seen = ~0ull;                         // per token: its row exists and q sees it
       if (special)
-        seen = seen_bits(p.d, t, (j0 + j) * kStepTokens + kSubTokens * c, pos) &
+        seen = seen_bits(p.d, t, (int64_t)(j0 + j) * kStepTokens + kSubTokens * c, pos) &
                ((uint64_t)sm.valid[2 * c] | ((uint64_t)sm.valid[2 * c + 1] << 32));
       // FP8: probabilities times V scales go in as f16, so the reference follows
       // the largest of these products that the row has, not of the probabilities:
@@ -1210,7 +1219,7 @@ int share_steps(const int64_t* steps, int n, int64_t most, int64_t least) {
   return (int)lo;
 }
 
-constexpr int kLeastWide = 2, kLeastFew = 4;          // steps of a share at least
+constexpr int kLeastWide = 2, kLeastFew = 1;          // steps of a share at least
 
 Plan make_plan(const DenseAttn& d, int sms, int32_t* tile0) {
   Plan a;

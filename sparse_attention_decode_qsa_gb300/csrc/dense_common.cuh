@@ -110,8 +110,9 @@ __device__ __forceinline__ void few_keys(uint32_t keys, int k, uint32_t (&ka)[4]
     for (int n = 0; n < 2; ++n) {                    // tokens r, r + 8
       uint32_t w;
       asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(keys + (8 * n + r) * 128 + ((k ^ r) << 4) + 4 * j4));
-      ka[n] = codes2_f16(w & 0xFFFFu);
-      ka[2 + n] = codes2_f16(w >> 16);
+      const uint2 h = codes4_f16(w);
+      ka[n] = h.x;
+      ka[2 + n] = h.y;
     }
   }
 }
