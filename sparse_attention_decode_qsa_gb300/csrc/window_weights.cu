@@ -217,6 +217,56 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
 
 // ------------------------------------------------------------------- wide
 
+// Units of more queries: a CTA takes tiles of 128 kTiles tokens (128 = the tensor
+// core's M) in turn; a turn is 32 queries x 4 heads of a KV head = 128 columns (N)
+// against each 128 tokens, K = 128 dims, both operands in shared memory under the
+// 128-byte swizzle.  K[g] of the tile (two buffers, the next head's or tile's on its
+// way) stays for all of the chunk's queries, Q streams past from L2: with two tiles of
+// 128 it is read half as often, with one there are twice as many tiles to share out.
+// Tensor memory: turns of 128 columns per 128 tokens, 512 in all.  Warps: 16 epilogue
+// (thread = token), 4 load K, 2 or 3 load Q, 1 MMA; all waits bounded.  FP8 codes
+// become bf16, beside which Q stays as it is: f16 would want every row of Q scaled,
+// again in every CTA.
+constexpr int kEpiWarps = 16, kKeyWarps = 4;
+constexpr int kPanel = 128 * 128;                 // 128 rows of 64 16-bit elements
+constexpr int kTurnQueries = 32, kTurnCols = kTurnQueries * kGroup;
+constexpr uint32_t kTmemCols = 512;
+
+template <int kTiles>
+struct Wide {
+  static constexpr int kTokens = 128 * kTiles;
+  static constexpr int kRing = 4 / kTiles;         // turns under way
+  static constexpr int kEpiCols = 32 * kTiles;     // of an epilogue warp and turn
+  // Query warp w of n has the turns w, w + n, ..  At its turn i - n it has waited for
+  // turn i - n - kRing to be done with, so that at turn i it cannot take the phase of
+  // turn i - 2 kRing for that of i - kRing: n <= kRing.  (With the MMA warp six warps
+  // to a scheduler at most: 80 registers.)
+  static constexpr int kQueryWarps = kTiles == 2 ? 2 : 3;
+  static constexpr int kThreads = 32 * (kEpiWarps + kKeyWarps + kQueryWarps + 1);
+  static constexpr int kRoleKeys = kEpiWarps, kRoleQueries = kRoleKeys + kKeyWarps, kRoleMma = kRoleQueries + kQueryWarps;
+  struct __align__(16) Columns {
+    float minus[kTurnCols];        // -lse (log2)
+    float factor[kTurnCols];       // what its rounding leaves
+    int32_t dead, pad[3];          // a column has no weight
+  };
+  // Columns of turn i are written once the products of turn i - kRing are complete,
+  // before which the epilogue of turn i - 2 kRing had left its accumulators.
+  static constexpr int kColumns = 2 * kRing;
+  static constexpr int kKBytes = kTiles * 2 * kPanel, kQPanel = kTurnCols * 128, kQBytes = 2 * kQPanel;
+  static constexpr int kOffQ = 2 * kKBytes, kOffCols = kOffQ + kRing * kQBytes;
+  // of two tiles in turn: K scales float [4][kTokens], column parts' sums float [4][128],
+  // tokens that count uint32 [8]
+  static constexpr int kOffKs = kOffCols + kColumns * (int)sizeof(Columns);
+  static constexpr int kOffSum = kOffKs + 2 * kKvHeads * kTokens * 4;
+  static constexpr int kOffThere = kOffSum + 2 * 4 * 128 * 4;
+  static constexpr int kOffBar = kOffThere + 2 * 32;
+  static constexpr int kNumBars = 4 * kRing + 4;   // full, empty, d_full, d_empty [kRing], k_full, k_empty [2]
+  static constexpr int kOffSlot = kOffBar + 8 * kNumBars;
+  static constexpr int kSmem = kOffSlot + 16 + 1024;
+  static_assert(kSmem <= 227 * 1024 && kOffCols % 16 == 0 && kOffBar % 8 == 0 && kQBytes % 1024 == 0, "shared memory");
+  static_assert(kQueryWarps <= kRing && kThreads <= 24 * 32, "see above");
+};
+
 // Two e4m3 codes (the low 16 bits) as bf16, exactly: their exponent and mantissa at
 // the low end of bf16's make 2^-120 times the value (a subnormal code a subnormal),
 // which the product puts right.  A NaN code (nan_codes) comes out as 480.
@@ -230,88 +280,67 @@ __device__ __forceinline__ uint32_t codes2_bf16(uint32_t two) {
 // Not 0 where one of four codes is a NaN.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
-// Units of more queries: one CTA per 128 kTiles tokens, in tiles of 128 = the tensor
-// core's M; a turn is 32 / kTiles queries x 4 heads of a KV head = 128 / kTiles
-// columns (N), K = 128 dims, both operands in shared memory under the 128-byte
-// swizzle.  K[g] of the tokens (two buffers) stays for all of the chunk's queries,
-// Q streams past in a ring of four turns (from L2: with two tiles every query is
-// read half as often, with one there are twice as many CTAs).  Tensor memory: a ring
-// of four turns of 128 columns.  Warps: 16 epilogue (thread = token, 32 columns a
-// turn: four warps to a scheduler hide each other's waits), 4 load K, 3 load Q, 1
-// MMA; all waits bounded.  Bound by the exponentials:
-// 16 a cycle and SM, 1024 cycles a turn, twice the tensor core's time.
-constexpr int kEpiWarps = 16, kKeyWarps = 4, kQueryWarps = 3;     // 24 with the MMA warp: six to a scheduler, 80 registers
-constexpr int kWideThreads = 32 * (kEpiWarps + kKeyWarps + kQueryWarps + 1);
-constexpr int kRoleKeys = kEpiWarps, kRoleQueries = kRoleKeys + kKeyWarps, kRoleMma = kRoleQueries + kQueryWarps;
-constexpr int kRing = 4;
-constexpr int kPanel = 128 * 128;                 // 128 rows of 64 16-bit elements
-constexpr int kEpiCols = 32;
-constexpr uint32_t kTmemCols = 512;
-
-template <int kTiles>
-struct Wide {
-  static constexpr int kTokens = 128 * kTiles, kQueries = 32 / kTiles, kCols = kQueries * kGroup;
-  struct __align__(16) Columns {
-    float minus[kCols];            // -lse (log2)
-    float factor[kCols];           // what its rounding leaves
-    int32_t dead, pad[3];          // a column has no weight
-  };
-  // Columns of turn i are written once the products of turn i - 4 are complete,
-  // before which the epilogue of turn i - 8 had left its accumulators: eight.
-  static constexpr int kColumns = 2 * kRing;
-  static constexpr int kKBytes = kTiles * 2 * kPanel, kQPanel = kCols * 128, kQBytes = 2 * kQPanel;
-  static constexpr int kOffQ = 2 * kKBytes, kOffCols = kOffQ + kRing * kQBytes;
-  static constexpr int kOffKs = kOffCols + kColumns * (int)sizeof(Columns);     // float [4][kTokens]: K scales
-  static constexpr int kOffSum = kOffKs + kKvHeads * kTokens * 4;               // float [4][128]: sums of the column parts
-  static constexpr int kOffThere = kOffSum + 4 * 128 * 4;                       // uint32 [8]: tokens that count
-  static constexpr int kOffBar = kOffThere + 32;
-  static constexpr int kNumBars = 4 * kRing + 4;   // full, empty, d_full, d_empty [4], k_full, k_empty [2]
-  static constexpr int kOffSlot = kOffBar + 8 * kNumBars;
-  static constexpr int kSmem = kOffSlot + 16 + 1024;
-  static_assert(kSmem <= 227 * 1024 && kOffCols % 16 == 0 && kOffBar % 8 == 0 && kQBytes % 1024 == 0, "shared memory");
-};
-
 template <bool kFp8, int kTiles>
-__global__ void __launch_bounds__(kWideThreads, 1) weight_wide_kernel(const __grid_constant__ WeightParams p) {
+__global__ void __launch_bounds__(Wide<kTiles>::kThreads, 1) weight_wide_kernel(const __grid_constant__ WeightParams p) {
   using W = Wide<kTiles>;
   using Columns = typename W::Columns;
+  constexpr int kRing = W::kRing, kEpiCols = W::kEpiCols;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
   Columns* columns = reinterpret_cast<Columns*>(smem + W::kOffCols);
-  float* key_scale = reinterpret_cast<float*>(smem + W::kOffKs);
-  float* part_sum = reinterpret_cast<float*>(smem + W::kOffSum);
-  uint32_t* there = reinterpret_cast<uint32_t*>(smem + W::kOffThere);
   const uint32_t bars = sb + W::kOffBar;
+  // turns i: buffer i % kRing; heads of K, counted through all tiles: k % 2
   auto full = [&](int i) { return bars + 8u * (uint32_t)(i % kRing); };
   auto empty = [&](int i) { return bars + 8u * (uint32_t)(kRing + i % kRing); };
   auto d_full = [&](int i) { return bars + 8u * (uint32_t)(2 * kRing + i % kRing); };
   auto d_empty = [&](int i) { return bars + 8u * (uint32_t)(3 * kRing + i % kRing); };
-  auto k_full = [&](int g) { return bars + 8u * (uint32_t)(4 * kRing + (g & 1)); };
-  auto k_empty = [&](int g) { return bars + 8u * (uint32_t)(4 * kRing + 2 + (g & 1)); };
+  auto k_full = [&](int k) { return bars + 8u * (uint32_t)(4 * kRing + (k & 1)); };
+  auto k_empty = [&](int k) { return bars + 8u * (uint32_t)(4 * kRing + 2 + (k & 1)); };
   auto turn_of = [](int i) { return (uint32_t)(i / kRing) & 1u; };
+  auto head_of = [](int k) { return (uint32_t)(k >> 1) & 1u; };
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + W::kOffSlot);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const BatchDesc& b = p.d.c.b;
   ErrorWord* err = b.err;
   const int u = blockIdx.y, nq = p.d.c.unit_tokens(u), x0 = p.d.c.row0[u];
-  const int64_t n = b.u[u].n, t0 = (int64_t)blockIdx.x * W::kTokens;
-  if (nq <= kFewQueries || t0 >= n) return;
-  const int64_t pos0 = n - nq, t1 = t0 + W::kTokens < n ? t0 + W::kTokens : n;
+  if (nq <= kFewQueries) return;
+  const int64_t n = b.u[u].n, pos0 = n - nq;
   grid_dependency_wait();
 
-  // ---- the queries that see any of the tokens (positions t0 .. t1 - 1 + window - 1), in whole turns
-  int64_t low = t0 - pos0, high = t0 < p.d.sinks ? nq : t1 - 1 + p.d.window - pos0;
-  if (low < 0) low = 0;
-  if (high > nq) high = nq;
-  const int c0 = (int)(low / W::kQueries), c1 = high > low ? (int)((high + W::kQueries - 1) / W::kQueries) : c0;
-  const int per = c1 - c0, turns = kKvHeads * per;   // turn i: KV head i / per, queries kQueries (c0 + i % per) ..
-  if (turns == 0) {
-    if (!p.accumulate && tid < t1 - t0) store_weight(p, u, t0 + tid, 0.f);
-    return;
-  }
+  // ---- tiles that some query sees: 0 .. front - 1 (sinks) and back .. all - 1
+  const int all = (int)((n + W::kTokens - 1) / W::kTokens);
+  int64_t newest = pos0 - p.d.window;                  // the newest token that no window has
+  if (newest < -1) newest = -1;
+  const int back = (int)((newest + 1) / W::kTokens);
+  int front = (int)((p.d.sinks + W::kTokens - 1) / W::kTokens);
+  if (front > back) front = back;
+  const int seen_tiles = front + all - back;
+  if (!p.accumulate)
+    for (int64_t t = (int64_t)front * W::kTokens + (int64_t)blockIdx.x * W::kThreads + tid; t < (int64_t)back * W::kTokens;
+         t += (int64_t)gridDim.x * W::kThreads)
+      store_weight(p, u, t, 0.f);
+  if ((int)blockIdx.x >= seen_tiles) return;
+  // the v-th of them: its tokens t0 .. t1 - 1, and the queries that see any of these
+  // (positions t0 .. t1 - 1 + window - 1) in whole turns c0 .. c0 + per - 1 (one at
+  // least, which then finds nothing to do)
+  struct Range {
+    int64_t t0, t1;
+    int c0, per;
+  };
+  auto range_of = [&](int v) {
+    Range r;
+    r.t0 = (int64_t)(v < front ? v : back + v - front) * W::kTokens;
+    r.t1 = r.t0 + W::kTokens < n ? r.t0 + W::kTokens : n;
+    int64_t low = r.t0 - pos0, high = r.t0 < p.d.sinks ? nq : r.t1 - 1 + p.d.window - pos0;
+    if (low < 0) low = 0;
+    if (high > nq) high = nq;
+    r.c0 = (int)(low / kTurnQueries);
+    r.per = high > low ? (int)((high + kTurnQueries - 1) / kTurnQueries) - r.c0 : 1;
+    return r;
+  };
 
-  if (warp == kRoleMma) {
+  if (warp == W::kRoleMma) {
     tmem_alloc<kTmemCols>(slot);
     if (lane == 0) {
       for (int i = 0; i < kRing; ++i) {
@@ -333,76 +362,81 @@ __global__ void __launch_bounds__(kWideThreads, 1) weight_wide_kernel(const __gr
   const uint32_t tmem = *slot;
   bool ok = true;
 
-  if (warp >= kRoleKeys && warp < kRoleQueries) {
-    // ---- K: warp w has the tokens 32 kTiles w .. of the CTA's, lane = token of 32
-    const int w = warp - kRoleKeys;
-    const uint8_t* row[kTiles];
-    uint32_t exist[kTiles];
+  if (warp >= W::kRoleKeys && warp < W::kRoleQueries) {
+    // ---- K: warp w has the tokens 32 kTiles w .. of a tile, lane = token of 32.  K of
+    // step k (head k % 4 of tile k / 4) is on its way while K of step k - 1 is handed on
+    const int w = warp - W::kRoleKeys;
+    const int heads = kKvHeads * ((seen_tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1);
+    const uint8_t* row[kTiles] = {};
+    uint32_t exist[kTiles] = {};
+    uint2 scales[2][kTiles] = {};                    // FP8: the tokens' K scales, all heads; this tile's and the last's
+#pragma unroll 1
+    for (int k = 0; k <= heads && ok; ++k) {
+      const int tile = k / kKvHeads, g = k % kKvHeads;
+      if (k < heads) {
+        if (g == 0) {
+          const Range r = range_of(blockIdx.x + tile * gridDim.x);
+          uint32_t* there = reinterpret_cast<uint32_t*>(smem + W::kOffThere) + 8 * (tile & 1);
 #pragma unroll
-    for (int k = 0; k < kTiles; ++k) {
-      const int64_t t = t0 + 32 * (kTiles * w + k) + lane;
-      row[k] = nullptr;
-      if (t < t1 && seen_by_any(p.d, u, t)) {
-        const int32_t s = b.slot_table[b.unit_row(u) + t];
-        if (s >= 0 && (int64_t)s < b.pool_rows) row[k] = b.pool + (int64_t)s * b.row_bytes;
-        else if (s == -1 && b.u[u].host_rows) row[k] = b.u[u].host_rows + t * b.row_bytes;
-        else report_error(err, QSA_ERR_BAD_SLOT, kKernWeights, ((int64_t)u << 40) | (t & 0xFFFFFFFFFFll));
-      }
-      exist[k] = __ballot_sync(0xFFFFFFFFu, row[k] != nullptr);
-      if (lane == 0) there[kTiles * w + k] = exist[k];
-      // the other heads' keys are on their way to L2 meanwhile
-      if (row[k]) {
+          for (int j = 0; j < kTiles; ++j) {
+            const int64_t t = r.t0 + 32 * (kTiles * w + j) + lane;
+            row[j] = nullptr;
+            if (t < r.t1 && seen_by_any(p.d, u, t)) {
+              const int32_t s = b.slot_table[b.unit_row(u) + t];
+              if (s >= 0 && (int64_t)s < b.pool_rows) row[j] = b.pool + (int64_t)s * b.row_bytes;
+              else if (s == -1 && b.u[u].host_rows) row[j] = b.u[u].host_rows + t * b.row_bytes;
+              else report_error(err, QSA_ERR_BAD_SLOT, kKernWeights, ((int64_t)u << 40) | (t & 0xFFFFFFFFFFll));
+            }
+            exist[j] = __ballot_sync(0xFFFFFFFFu, row[j] != nullptr);
+            if (lane == 0) there[kTiles * w + j] = exist[j];
+            scales[1][j] = scales[0][j];
+            scales[0][j] = kFp8 && row[j] ? *reinterpret_cast<const uint2*>(row[j] + 2 * kKvHeads * kHeadDim) : make_uint2(0, 0);
+            // the other heads' keys are on their way to L2 meanwhile
+            if (row[j]) {
 #pragma unroll
-        for (int o = 1; o < kKvHeads; ++o)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(row[k] + o * kHeadDim * (kFp8 ? 1 : 2)));
-      }
-    }
-    // FP8: a token's K scales, all heads
-    uint2 scales[kTiles];
-#pragma unroll
-    for (int k = 0; k < kTiles; ++k)
-      scales[k] = kFp8 && row[k] ? *reinterpret_cast<const uint2*>(row[k] + 2 * kKvHeads * kHeadDim) : make_uint2(0, 0);
-    // K[g] is on its way while K[g - 1] is turned over
-    for (int i = 0; i <= kKvHeads && ok; ++i) {
-      if (i < kKvHeads) {
-        const int g = i;
-        if (g >= 2) ok = mbar_wait_warp(k_empty(g), 0, err, kKernWeights);
+              for (int o = 1; o < kKvHeads; ++o)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(row[j] + o * kHeadDim * (kFp8 ? 1 : 2)));
+            }
+          }
+        }
+        if (k >= 2) ok = mbar_wait_warp(k_empty(k), head_of(k - 2), err, kKernWeights);
         if (!ok) break;
 #pragma unroll
-        for (int k = 0; k < kTiles; ++k) {
-          const int at = 32 * (kTiles * w + k);                  // of the CTA's tokens
-          const uint32_t dst = sb + (g & 1) * W::kKBytes + (at >> 7) * 2 * kPanel + (at & 127) * 128;
-          const uintptr_t from = reinterpret_cast<uintptr_t>(row[k] ? row[k] : b.pool);
+        for (int j = 0; j < kTiles; ++j) {
+          const int at = 32 * (kTiles * w + j);                  // of the tile's tokens
+          const uint32_t dst = sb + (k & 1) * W::kKBytes + (at >> 7) * 2 * kPanel + (at & 127) * 128;
+          const uintptr_t from = reinterpret_cast<uintptr_t>(row[j] ? row[j] : b.pool);
           // BF16: 16 lanes a token, 8 in each panel.  FP8: 8 lanes, the codes as they
           // are in the token's row of the second panel
           constexpr int kLanes = kFp8 ? 8 : 16, kPer = 32 / kLanes;
           const uint32_t c = lane % kLanes;
           const uint32_t to = dst + (kFp8 ? kPanel : (c >> 3) * kPanel);
 #pragma unroll
-          for (int j = 0; j < 32 / kPer; ++j) {
-            const uint32_t t = kPer * j + lane / kLanes;
+          for (int i = 0; i < 32 / kPer; ++i) {
+            const uint32_t t = kPer * i + lane / kLanes;
             const uintptr_t a = __shfl_sync(0xFFFFFFFFu, from, (int)t);
             cp_async16(to + t * 128 + (((c & 7) ^ (t & 7)) << 4),
                        reinterpret_cast<const uint8_t*>(a) + g * (kFp8 ? kHeadDim : 2 * kHeadDim) + c * 16,
-                       (exist[k] >> t) & 1u ? 16u : 0u);
+                       (exist[j] >> t) & 1u ? 16u : 0u);
           }
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
-      if (i == 0) continue;
-      const int g = i - 1;
+      if (k == 0) continue;
+      const int before = k - 1, gb = before % kKvHeads;
       asm volatile("cp.async.wait_group 1;" ::: "memory");
       if (kFp8) {
+        float* key_scale = reinterpret_cast<float*>(smem + W::kOffKs) + ((before / kKvHeads) & 1) * kKvHeads * W::kTokens;
         __syncwarp();
 #pragma unroll
-        for (int k = 0; k < kTiles; ++k) {
-          const int at = 32 * (kTiles * w + k);
-          uint8_t* panel = smem + (g & 1) * W::kKBytes + (at >> 7) * 2 * kPanel + (at & 127) * 128;
+        for (int j = 0; j < kTiles; ++j) {
+          const int at = 32 * (kTiles * w + j);
+          uint8_t* panel = smem + (before & 1) * W::kKBytes + (at >> 7) * 2 * kPanel + (at & 127) * 128;
           const uint32_t c = lane & 7;
           uint32_t bad = 0;                                      // tokens of the 32 with a NaN among their codes
 #pragma unroll 2
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t t = 4 * j + (lane >> 3), sw = t & 7;
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t t = 4 * i + (lane >> 3), sw = t & 7;
             const uint4 v = *reinterpret_cast<const uint4*>(panel + kPanel + t * 128 + ((c ^ sw) << 4));
             uint4 o[2];
             o[0] = make_uint4(codes2_bf16(v.x), codes2_bf16(v.x >> 16), codes2_bf16(v.y), codes2_bf16(v.y >> 16));
@@ -410,198 +444,218 @@ __global__ void __launch_bounds__(kWideThreads, 1) weight_wide_kernel(const __gr
             const uint32_t nan = nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w);
             const uint32_t which = __ballot_sync(0xFFFFFFFFu, nan != 0);       // (and all four rows have been read)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) bad |= (which >> (8 * x)) & 0xFFu ? 1u << (4 * j + x) : 0u;
+            for (int x = 0; x < 4; ++x) bad |= (which >> (8 * x)) & 0xFFu ? 1u << (4 * i + x) : 0u;
             // codes 16 c .. + 15 are the chunks 2 c and 2 c + 1 of the row's 16
             uint8_t* to = panel + (c >> 2) * kPanel + t * 128;
             const uint32_t ch = (2 * c) & 7;
             *reinterpret_cast<uint4*>(to + ((ch ^ sw) << 4)) = o[0];
             *reinterpret_cast<uint4*>(to + (((ch + 1) ^ sw) << 4)) = o[1];
           }
-          const uint32_t two = g < 2 ? scales[k].x : scales[k].y;
-          const float ks = __half2float(__ushort_as_half((uint16_t)(g & 1 ? two >> 16 : two & 0xFFFFu)));
-          key_scale[g * W::kTokens + at + lane] = (bad >> lane) & 1u ? __int_as_float(0x7FC00000) : ks;
+          // (head 0 of a tile has been read by now where head 3 of the one before is handed on)
+          const uint2 sc = gb == kKvHeads - 1 && k < heads ? scales[1][j] : scales[0][j];
+          const uint32_t two = gb < 2 ? sc.x : sc.y;
+          const float ks = __half2float(__ushort_as_half((uint16_t)(gb & 1 ? two >> 16 : two & 0xFFFFu)));
+          key_scale[gb * W::kTokens + at + lane] = (bad >> lane) & 1u ? __int_as_float(0x7FC00000) : ks;
         }
       }
       fence_async_smem();
-      mbar_arrive(k_full(g));
+      mbar_arrive(k_full(before));
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-  } else if (warp >= kRoleQueries && warp < kRoleMma) {
-    // ---- Q: warp w has the turns w, w + 3, ..., so that three are on their way, and
-    // each arrives as soon as it has landed; column query * 4 + head.
-    const int w = warp - kRoleQueries;
-    int g = 0, c = w;                                            // of turn i
-    while (c >= per) c -= per, ++g;
-    for (int i = w; i < turns && ok; i += kQueryWarps) {
-      if (i >= kRing) ok = mbar_wait_warp(empty(i), turn_of(i - kRing), err, kKernWeights);
-      if (!ok) break;
-      const int qa = (c0 + c) * W::kQueries, have = nq - qa < W::kQueries ? nq - qa : W::kQueries;
-      const uint32_t dst = W::kOffQ + (i % kRing) * W::kQBytes + ((lane & 15) >> 3) * W::kQPanel;
-      // two columns at a time, 16 lanes each: heads 2 (k & 1) + (lane >> 4) of query k / 2
-      const uint16_t* from = p.q + ((int64_t)(x0 + qa) * kQHeads + g * kGroup + (lane >> 4)) * kHeadDim + (lane & 15) * 8;
-      auto place = [&](int k) {
-        const int cc = 2 * k + (lane >> 4);
-        return dst + cc * 128 + (((lane & 7) ^ (cc & 7)) << 4);
-      };
+  } else if (warp >= W::kRoleQueries && warp < W::kRoleMma) {
+    // ---- Q: a turn each at a time, so that the next are on their way while one lands;
+    // column query * 4 + head
+    const int w = warp - W::kRoleQueries;
+    int i = 0;
+#pragma unroll 1
+    for (int v = blockIdx.x; v < seen_tiles && ok; v += gridDim.x) {
+      const Range r = range_of(v);
+#pragma unroll 1
+      for (int j = 0; j < kKvHeads * r.per && ok; ++j, ++i) {
+        if (i % W::kQueryWarps != w) continue;
+        const int g = j / r.per, c = r.c0 + j % r.per;
+        if (i >= kRing) ok = mbar_wait_warp(empty(i), turn_of(i - kRing), err, kKernWeights);
+        if (!ok) break;
+        const int qa = c * kTurnQueries, have = nq - qa < kTurnQueries ? nq - qa : kTurnQueries;
+        const uint32_t dst = sb + W::kOffQ + (i % kRing) * W::kQBytes + ((lane & 15) >> 3) * W::kQPanel;
+        // two columns at a time, 16 lanes each: heads 2 (k & 1) + (lane >> 4) of query k / 2
+        const uint16_t* from = p.q + ((int64_t)(x0 + qa) * kQHeads + g * kGroup + (lane >> 4)) * kHeadDim + (lane & 15) * 8;
 #pragma unroll 8
-      for (int k = 0; k < W::kCols / 2; ++k) {
-        const bool there_is = (k >> 1) < have;
-        cp_async16(sb + place(k), there_is ? from + ((k >> 1) * kQHeads + 2 * (k & 1)) * kHeadDim : p.q, there_is ? 16u : 0u);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      Columns& m = columns[i % W::kColumns];
-      bool dead = false;
-#pragma unroll
-      for (int k = 0; k < W::kCols / 32; ++k) {
-        const int col = 32 * k + lane, q = col / kGroup;
-        const float lse = q < have ? p.lse[(int64_t)(x0 + qa + q) * kQHeads + g * kGroup + col % kGroup] : -INFINITY;
-        const float2 y = column_of(lse);
-        m.minus[col] = y.x;
-        m.factor[col] = y.y;
-        dead = dead || lse == -INFINITY;
-      }
-      dead = __any_sync(0xFFFFFFFFu, dead);
-      if (lane == 0) m.dead = dead;
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full(i));
-      for (c += kQueryWarps; c >= per; c -= per) ++g;
-    }
-  } else if (warp == kRoleMma) {
-    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-    for (int i = 0, g = 0, c = 0; i < turns && ok; ++i, ++c) {
-      if (c == per) c = 0, ++g;
-      const int left = (nq - (c0 + c) * W::kQueries) * kGroup;
-      const uint32_t cols = left >= W::kCols ? W::kCols : (uint32_t)((left + 15) / 16 * 16);
-      if (c == 0) ok = mbar_wait_warp(k_full(g), (uint32_t)(g >> 1), err, kKernWeights);
-      if (ok) ok = mbar_wait_warp(full(i), turn_of(i), err, kKernWeights);
-      if (ok && i >= kRing) ok = mbar_wait_warp(d_empty(i), turn_of(i - kRing), err, kKernWeights);
-      if (!ok) break;
-      fence_after();
-      if (elect_one()) {
-        const uint32_t id = idesc_bf16(cols, false);
-        const uint64_t qd = desc_sw128(sb + W::kOffQ + (i % kRing) * W::kQBytes, 16);
-#pragma unroll
-        for (int m = 0; m < kTiles; ++m) {
-          const uint64_t kd = desc_sw128(sb + (g & 1) * W::kKBytes + m * 2 * kPanel, 16);
-#pragma unroll
-          for (int k = 0; k < kHeadDim / 16; ++k)
-            mma_ss(tm + (uint32_t)((i % kRing) * 128 + m * W::kCols), kd + (uint64_t)(((k >> 2) * kPanel + (k & 3) * 32) >> 4),
-                   qd + (uint64_t)(((k >> 2) * W::kQPanel + (k & 3) * 32) >> 4), id, k != 0);
+        for (int k = 0; k < kTurnCols / 2; ++k) {
+          const int cc = 2 * k + (lane >> 4);
+          const bool there_is = (k >> 1) < have;
+          cp_async16(dst + cc * 128 + (((lane & 7) ^ (cc & 7)) << 4),
+                     there_is ? from + ((k >> 1) * kQHeads + 2 * (k & 1)) * kHeadDim : p.q, there_is ? 16u : 0u);
         }
-        mbar_arrive(d_full(i));                      // passes on the loaders' writes of the columns
-        commit(d_full(i));
-        commit(empty(i));
-        if (c == per - 1) commit(k_empty(g));
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        Columns& m = columns[i % W::kColumns];
+        bool dead = false;
+        for (int col = lane; col < kTurnCols; col += 32) {
+          const int q = col / kGroup;
+          const float lse = q < have ? p.lse[(int64_t)(x0 + qa + q) * kQHeads + g * kGroup + col % kGroup] : -INFINITY;
+          const float2 y = column_of(lse);
+          m.minus[col] = y.x;
+          m.factor[col] = y.y;
+          dead = dead || lse == -INFINITY;
+        }
+        dead = __any_sync(0xFFFFFFFFu, dead);
+        if (lane == 0) m.dead = dead;
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full(i));
       }
-      __syncwarp();
+    }
+  } else if (warp == W::kRoleMma) {
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    int i = 0, k = 0;
+#pragma unroll 1
+    for (int v = blockIdx.x; v < seen_tiles && ok; v += gridDim.x) {
+      const Range r = range_of(v);
+#pragma unroll 1
+      for (int j = 0, c = 0; j < kKvHeads * r.per && ok; ++j, ++i, ++c) {
+        if (c == r.per) c = 0, ++k;
+        const int left = (nq - (r.c0 + c) * kTurnQueries) * kGroup;
+        const uint32_t cols = left >= kTurnCols ? kTurnCols : (uint32_t)((left + 15) / 16 * 16);
+        if (c == 0) ok = mbar_wait_warp(k_full(k), head_of(k), err, kKernWeights);
+        if (ok) ok = mbar_wait_warp(full(i), turn_of(i), err, kKernWeights);
+        if (ok && i >= kRing) ok = mbar_wait_warp(d_empty(i), turn_of(i - kRing), err, kKernWeights);
+        if (!ok) break;
+        fence_after();
+        if (elect_one()) {
+          const uint32_t id = idesc_bf16(cols, false);
+          const uint64_t qd = desc_sw128(sb + W::kOffQ + (i % kRing) * W::kQBytes, 16);
+#pragma unroll
+          for (int m = 0; m < kTiles; ++m) {
+            const uint64_t kd = desc_sw128(sb + (k & 1) * W::kKBytes + m * 2 * kPanel, 16);
+#pragma unroll
+            for (int x = 0; x < kHeadDim / 16; ++x)
+              mma_ss(tm + (uint32_t)((i % kRing) * 128 * kTiles + m * kTurnCols), kd + (uint64_t)(((x >> 2) * kPanel + (x & 3) * 32) >> 4),
+                     qd + (uint64_t)(((x >> 2) * W::kQPanel + (x & 3) * 32) >> 4), id, x != 0);
+          }
+          mbar_arrive(d_full(i));                    // passes on the loaders' writes of the columns
+          commit(d_full(i));
+          commit(empty(i));
+          if (c == r.per - 1) commit(k_empty(k));
+        }
+        __syncwarp();
+      }
+      ++k;
     }
     // every product is complete before tensor memory is given back
-    for (int i = turns > kRing ? turns - kRing : 0; i < turns; ++i) mbar_wait_warp(empty(i), turn_of(i), err, kKernWeights);
+    for (int e = i > kRing ? i - kRing : 0; e < i; ++e) mbar_wait_warp(empty(e), turn_of(e), err, kKernWeights);
   } else {
     // ---- epilogue: thread = token; part `part` of four: of the columns, and with
-    // two tiles of these
+    // two tiles of 128 of these
     const int part = warp >> 2, at = (kTiles == 2 ? 128 * (part >> 1) : 0) + 32 * (warp & 3) + lane;
     const int first = kEpiCols * (kTiles == 2 ? part & 1 : part);            // its columns of a turn
-    const int64_t t = t0 + at;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(kEpiCols * part);
-    // queries that see the token
-    int64_t qlo = t - pos0, qhi = t < p.d.sinks ? nq : t + p.d.window - pos0;
-    if (qlo < 0) qlo = 0;
-    if (qhi > nq) qhi = nq;
-    float hi = p.scale_log2, lo = p.scale_rest;
-    uint64_t hi2 = pair(hi, hi), lo2 = pair(lo, lo);
-    float total = 0.f;
-    bool mine = false;
+    int i = 0, odd = 0;                              // odd: the tile's place in what two tiles share
 #pragma unroll 1
-    for (int i = 0, g = 0, c = 0; i < turns; ++i, ++c) {
-      if (c == per) c = 0, ++g;
-      const int qa = (c0 + c) * W::kQueries;
-      ok = mbar_wait_warp(d_full(i), turn_of(i), err, kKernWeights);
-      if (!ok) break;
-      fence_after();
-      if (i == 0) mine = (there[at >> 5] >> (at & 31)) & 1u;
-      if (kFp8 && c == 0) {                          // times the token's K scale, the rounding into the rest
-        const float ks = key_scale[g * W::kTokens + at];
-        hi = p.scale_log2 * ks;
-        lo = fmaf(p.scale_rest, ks, fmaf(p.scale_log2, ks, -hi));
-        hi2 = pair(hi, hi);
-        lo2 = pair(lo, lo);
-      }
-      const Columns& cm = columns[i % W::kColumns];
-      // columns a .. z - 1 count for this token
-      const int a = qlo > qa ? (qlo - qa > W::kQueries ? W::kCols : (int)(qlo - qa) * kGroup) : 0;
-      const int z = qhi < qa ? 0 : (qhi - qa > W::kQueries ? W::kCols : (int)(qhi - qa) * kGroup);
-      const uint32_t d = lane_base + (uint32_t)(i % kRing) * 128u;
-      uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-      // four columns (a query's heads) of a turn
-      auto four = [&](uint32_t* v, int cc, ulonglong2& mi, float (&e)[4]) {
-        mi = *reinterpret_cast<const ulonglong2*>(&cm.minus[cc]);
-        uint64_t x01 = pair(v[0], v[1]), x23 = pair(v[2], v[3]);
-        x01 = fma2(x01, hi2, fma2(x01, lo2, mi.x));
-        x23 = fma2(x23, hi2, fma2(x23, lo2, mi.y));
-        e[0] = exp2_fast(lo_of(x01));
-        e[1] = exp2_fast(hi_of(x01));
-        e[2] = exp2_fast(lo_of(x23));
-        e[3] = exp2_fast(hi_of(x23));
-      };
-      auto add = [&](int cc, const float (&e)[4]) {
-        const ulonglong2 fa = *reinterpret_cast<const ulonglong2*>(&cm.factor[cc]);
-        sum[0] = fma2(pair(e[0], e[1]), fa.x, sum[0]);
-        sum[1] = fma2(pair(e[2], e[3]), fa.y, sum[1]);
-      };
-      const bool some = __any_sync(0xFFFFFFFFu, a < z && z > first && a < first + kEpiCols);
-      const bool plain = __all_sync(0xFFFFFFFFu, a <= first && z >= first + kEpiCols) &&
-                         !cm.dead;
-      if (some) {
-        uint32_t v[kEpiCols];
-        ld32(d, v);
-        wait_ld();
-        reg_fence(v);
-        if (plain) {
+    for (int v = blockIdx.x; v < seen_tiles; v += gridDim.x, odd ^= 1) {     // (all warps meet in every tile, whatever has run out)
+      const Range r = range_of(v);
+      const int64_t t = r.t0 + at;
+      const float* key_scale = reinterpret_cast<const float*>(smem + W::kOffKs) + odd * kKvHeads * W::kTokens;
+      const uint32_t* there = reinterpret_cast<const uint32_t*>(smem + W::kOffThere) + 8 * odd;
+      float* part_sum = reinterpret_cast<float*>(smem + W::kOffSum) + odd * 4 * 128;
+      // queries that see the token, from the first turn's on
+      int64_t low = t - pos0, high = t < p.d.sinks ? nq : t + p.d.window - pos0;
+      if (low < 0) low = 0;
+      if (high > nq) high = nq;
+      const int qlo = (int)low, qhi = (int)(high < 0 ? 0 : high);
+      float hi = p.scale_log2, lo = p.scale_rest;
+      uint64_t hi2 = pair(hi, hi), lo2 = pair(lo, lo);
+      float total = 0.f;
+      bool mine = false;
+#pragma unroll 1
+      for (int j = 0, g = 0, c = 0; j < kKvHeads * r.per; ++j, ++i, ++c) {
+        if (c == r.per) c = 0, ++g;
+        const int qa = (r.c0 + c) * kTurnQueries;
+        if (ok) ok = mbar_wait_warp(d_full(i), turn_of(i), err, kKernWeights);
+        if (!ok) break;
+        fence_after();
+        if (j == 0) mine = (there[at >> 5] >> (at & 31)) & 1u;
+        if (kFp8 && c == 0) {                        // times the token's K scale, the rounding into the rest
+          const float ks = key_scale[g * W::kTokens + at];
+          hi = p.scale_log2 * ks;
+          lo = fmaf(p.scale_rest, ks, fmaf(p.scale_log2, ks, -hi));
+          hi2 = pair(hi, hi);
+          lo2 = pair(lo, lo);
+        }
+        const Columns& cm = columns[i % W::kColumns];
+        // columns a .. z - 1 count for this token
+        int a = (qlo - qa) * kGroup, z = (qhi - qa) * kGroup;
+        a = a < 0 ? 0 : (a > kTurnCols ? kTurnCols : a);
+        z = z < 0 ? 0 : (z > kTurnCols ? kTurnCols : z);
+        const uint32_t d = lane_base + (uint32_t)(i % kRing) * (128u * kTiles);
+        uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        // four columns (a query's heads) of a turn
+        auto four = [&](uint32_t* x, int cc, ulonglong2& mi, float (&e)[4]) {
+          mi = *reinterpret_cast<const ulonglong2*>(&cm.minus[cc]);
+          const uint64_t x01 = pair(x[0], x[1]), x23 = pair(x[2], x[3]);
+          const uint64_t y01 = fma2(x01, hi2, fma2(x01, lo2, mi.x)), y23 = fma2(x23, hi2, fma2(x23, lo2, mi.y));
+          e[0] = exp2_fast(lo_of(y01));
+          e[1] = exp2_fast(hi_of(y01));
+          e[2] = exp2_fast(lo_of(y23));
+          e[3] = exp2_fast(hi_of(y23));
+        };
+        auto add = [&](int cc, const float (&e)[4]) {
+          const ulonglong2 fa = *reinterpret_cast<const ulonglong2*>(&cm.factor[cc]);
+          sum[0] = fma2(pair(e[0], e[1]), fa.x, sum[0]);
+          sum[1] = fma2(pair(e[2], e[3]), fa.y, sum[1]);
+        };
+        const bool some = __any_sync(0xFFFFFFFFu, a < z && z > first && a < first + kEpiCols);
+        const bool plain = __all_sync(0xFFFFFFFFu, a <= first && z >= first + kEpiCols) && !cm.dead;
+#pragma unroll 1
+        for (int x = 0; x < kEpiCols && some; x += 32) {
+          uint32_t s[32];
+          ld32(d + (uint32_t)x, s);
+          wait_ld();
+          reg_fence(s);
+          if (plain) {
 #pragma unroll
-          for (int k = 0; k < kEpiCols; k += 4) {
-            ulonglong2 mi;
-            float e[4];
-            four(&v[k], first + k, mi, e);
-            add(first + k, e);
-          }
-        } else {
+            for (int k = 0; k < 32; k += 4) {
+              ulonglong2 mi;
+              float e[4];
+              four(&s[k], first + x + k, mi, e);
+              add(first + x + k, e);
+            }
+          } else {
 #pragma unroll
-          for (int k = 0; k < kEpiCols; k += 4) {
-            const int cc = first + k;
-            ulonglong2 mi;
-            float e[4];
-            four(&v[k], cc, mi, e);
-            const bool in = cc >= a && cc < z;
-            const float mm[4] = {lo_of(mi.x), hi_of(mi.x), lo_of(mi.y), hi_of(mi.y)};
+            for (int k = 0; k < 32; k += 4) {
+              const int cc = first + x + k;
+              ulonglong2 mi;
+              float e[4];
+              four(&s[k], cc, mi, e);
+              const bool in = cc >= a && cc < z;
+              const float mm[4] = {lo_of(mi.x), hi_of(mi.x), lo_of(mi.y), hi_of(mi.y)};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)              // (columns without weight, and past the queries: minus is infinite)
-              if (!in || fabsf(mm[j]) == INFINITY) e[j] = 0.f;
-            add(cc, e);
+              for (int h = 0; h < 4; ++h)            // (columns without weight, and past the queries: minus is infinite)
+                if (!in || fabsf(mm[h]) == INFINITY) e[h] = 0.f;
+              add(cc, e);
+            }
           }
         }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(d_empty(i));
+        const uint64_t s2 = add2(sum[0], sum[1]);
+        total += lo_of(s2) + hi_of(s2);
       }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(d_empty(i));
-      const uint64_t s2 = add2(sum[0], sum[1]);
-      total += lo_of(s2) + hi_of(s2);
-    }
-    part_sum[part * 128 + 32 * (warp & 3) + lane] = total;
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
-    const float* sums = part_sum + 32 * (warp & 3) + lane;
-    if (kTiles == 2 ? (part & 1) == 0 : part == 0) {
-      total = kTiles == 2 ? sums[part * 128] + sums[part * 128 + 128] : (sums[0] + sums[128]) + (sums[256] + sums[384]);
-      if (ok && t < t1) store_weight(p, u, t, mine ? total : 0.f);
+      part_sum[part * 128 + 32 * (warp & 3) + lane] = total;
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+      const float* sums = part_sum + 32 * (warp & 3) + lane;
+      if (kTiles == 2 ? (part & 1) == 0 : part == 0) {
+        total = kTiles == 2 ? sums[part * 128] + sums[part * 128 + 128] : (sums[0] + sums[128]) + (sums[256] + sums[384]);
+        if (ok && t < r.t1) store_weight(p, u, t, mine ? total : 0.f);
+      }
     }
   }
 
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == kRoleMma) tmem_free<kTmemCols>(tmem);
+  if (warp == W::kRoleMma) tmem_free<kTmemCols>(tmem);
 }
 
 }  // namespace
@@ -638,6 +692,7 @@ cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const f
   p.stride = stride;
   p.accumulate = accumulate;
   int64_t wide = 0, few = 0, few_all = 0;            // the longest contexts; all tokens of few queries
+  int wide_units = 0;
   int rows = 0;                                      // queries of a unit of few, at most
   int64_t seen = 0;                                  // tokens that more than a few queries see
   for (int u = 0; u < d.c.b.n_units; ++u) {
@@ -645,6 +700,7 @@ cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const f
     const int nq = d.c.unit_tokens(u);
     if (nq > kFewQueries) {
       wide = n > wide ? n : wide;
+      ++wide_units;
       const int64_t low = n - nq - d.window + 1;
       seen += low > 0 ? n - low : n;
     } else {
@@ -654,12 +710,15 @@ cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const f
     }
   }
   if (wide > 0) {
-    // two tiles a CTA where that fills the device
+    // tiles of 256 tokens where these fill the device
     const int tiles = seen >= (int64_t)sms * Wide<2>::kTokens ? 2 : 1;
-    const dim3 grid((unsigned)((wide + 128 * tiles - 1) / (128 * tiles)), d.c.b.n_units);
+    // as many CTAs as SMs, shared by the units with more than a few queries
+    int64_t ctas = (wide + 128 * tiles - 1) / (128 * tiles);
+    if (ctas > (sms + wide_units - 1) / wide_units) ctas = (sms + wide_units - 1) / wide_units;
+    const dim3 grid((unsigned)ctas, d.c.b.n_units);
     auto* kernel = fp8 ? (tiles == 2 ? weight_wide_kernel<true, 2> : weight_wide_kernel<true, 1>)
                        : (tiles == 2 ? weight_wide_kernel<false, 2> : weight_wide_kernel<false, 1>);
-    e = launch_kernel(kernel, grid, dim3(kWideThreads), tiles == 2 ? Wide<2>::kSmem : Wide<1>::kSmem, s, 0, dim3(1), p);
+    e = launch_kernel(kernel, grid, dim3(tiles == 2 ? Wide<2>::kThreads : Wide<1>::kThreads), tiles == 2 ? Wide<2>::kSmem : Wide<1>::kSmem, s, 0, dim3(1), p);
   }
   if (e == cudaSuccess && few > 0) {
     // two CTAs on an SM: as many runs of tokens as that, a step of 32 tokens to each warp pair
