@@ -363,75 +363,70 @@ __global__ void __launch_bounds__(Wide<kTiles>::kThreads, 1) weight_wide_kernel(
   bool ok = true;
 
   if (warp >= W::kRoleKeys && warp < W::kRoleQueries) {
-    // ---- K: warp w has the tokens 32 kTiles w .. of a tile, lane = token of 32.  K of
-    // step k (head k % 4 of tile k / 4) is on its way while K of step k - 1 is handed on
+    // ---- K: warp w has the tokens 32 kTiles w .. of a tile, lane = token of 32.  Step k
+    // is head k % 4 of tile k / 4: K of step k + 1 is sent for once step k - 1 has left
+    // its buffer, and handed on when it has landed.
     const int w = warp - W::kRoleKeys;
     const int heads = kKvHeads * ((seen_tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1);
     const uint8_t* row[kTiles] = {};
     uint32_t exist[kTiles] = {};
-    uint2 scales[2][kTiles] = {};                    // FP8: the tokens' K scales, all heads; this tile's and the last's
-#pragma unroll 1
-    for (int k = 0; k <= heads && ok; ++k) {
+    uint2 scales[kTiles] = {};                       // FP8: the tokens' K scales, all heads
+    auto send = [&](int k) {
       const int tile = k / kKvHeads, g = k % kKvHeads;
-      if (k < heads) {
-        if (g == 0) {
-          const Range r = range_of(blockIdx.x + tile * gridDim.x);
-          uint32_t* there = reinterpret_cast<uint32_t*>(smem + W::kOffThere) + 8 * (tile & 1);
-#pragma unroll
-          for (int j = 0; j < kTiles; ++j) {
-            const int64_t t = r.t0 + 32 * (kTiles * w + j) + lane;
-            row[j] = nullptr;
-            if (t < r.t1 && seen_by_any(p.d, u, t)) {
-              const int32_t s = b.slot_table[b.unit_row(u) + t];
-              if (s >= 0 && (int64_t)s < b.pool_rows) row[j] = b.pool + (int64_t)s * b.row_bytes;
-              else if (s == -1 && b.u[u].host_rows) row[j] = b.u[u].host_rows + t * b.row_bytes;
-              else report_error(err, QSA_ERR_BAD_SLOT, kKernWeights, ((int64_t)u << 40) | (t & 0xFFFFFFFFFFll));
-            }
-            exist[j] = __ballot_sync(0xFFFFFFFFu, row[j] != nullptr);
-            if (lane == 0) there[kTiles * w + j] = exist[j];
-            scales[1][j] = scales[0][j];
-            scales[0][j] = kFp8 && row[j] ? *reinterpret_cast<const uint2*>(row[j] + 2 * kKvHeads * kHeadDim) : make_uint2(0, 0);
-            // the other heads' keys are on their way to L2 meanwhile
-            if (row[j]) {
-#pragma unroll
-              for (int o = 1; o < kKvHeads; ++o)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(row[j] + o * kHeadDim * (kFp8 ? 1 : 2)));
-            }
-          }
-        }
-        if (k >= 2) ok = mbar_wait_warp(k_empty(k), head_of(k - 2), err, kKernWeights);
-        if (!ok) break;
+      if (g == 0) {
+        const Range r = range_of(blockIdx.x + tile * gridDim.x);
+        uint32_t* there = reinterpret_cast<uint32_t*>(smem + W::kOffThere) + 8 * (tile & 1);
 #pragma unroll
         for (int j = 0; j < kTiles; ++j) {
-          const int at = 32 * (kTiles * w + j);                  // of the tile's tokens
-          const uint32_t dst = sb + (k & 1) * W::kKBytes + (at >> 7) * 2 * kPanel + (at & 127) * 128;
-          const uintptr_t from = reinterpret_cast<uintptr_t>(row[j] ? row[j] : b.pool);
-          // BF16: 16 lanes a token, 8 in each panel.  FP8: 8 lanes, the codes as they
-          // are in the token's row of the second panel
-          constexpr int kLanes = kFp8 ? 8 : 16, kPer = 32 / kLanes;
-          const uint32_t c = lane % kLanes;
-          const uint32_t to = dst + (kFp8 ? kPanel : (c >> 3) * kPanel);
+          const int64_t t = r.t0 + 32 * (kTiles * w + j) + lane;
+          row[j] = nullptr;
+          if (t < r.t1 && seen_by_any(p.d, u, t)) {
+            const int32_t s = b.slot_table[b.unit_row(u) + t];
+            if (s >= 0 && (int64_t)s < b.pool_rows) row[j] = b.pool + (int64_t)s * b.row_bytes;
+            else if (s == -1 && b.u[u].host_rows) row[j] = b.u[u].host_rows + t * b.row_bytes;
+            else report_error(err, QSA_ERR_BAD_SLOT, kKernWeights, ((int64_t)u << 40) | (t & 0xFFFFFFFFFFll));
+          }
+          exist[j] = __ballot_sync(0xFFFFFFFFu, row[j] != nullptr);
+          if (lane == 0) there[kTiles * w + j] = exist[j];
+          scales[j] = kFp8 && row[j] ? *reinterpret_cast<const uint2*>(row[j] + 2 * kKvHeads * kHeadDim) : make_uint2(0, 0);
+          // the other heads' keys are on their way to L2 meanwhile
+          if (row[j]) {
 #pragma unroll
-          for (int i = 0; i < 32 / kPer; ++i) {
-            const uint32_t t = kPer * i + lane / kLanes;
-            const uintptr_t a = __shfl_sync(0xFFFFFFFFu, from, (int)t);
-            cp_async16(to + t * 128 + (((c & 7) ^ (t & 7)) << 4),
-                       reinterpret_cast<const uint8_t*>(a) + g * (kFp8 ? kHeadDim : 2 * kHeadDim) + c * 16,
-                       (exist[j] >> t) & 1u ? 16u : 0u);
+            for (int o = 1; o < kKvHeads; ++o)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(row[j] + o * kHeadDim * (kFp8 ? 1 : 2)));
           }
         }
       }
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) {
+        const int at = 32 * (kTiles * w + j);                    // of the tile's tokens
+        const uint32_t dst = sb + (k & 1) * W::kKBytes + (at >> 7) * 2 * kPanel + (at & 127) * 128;
+        const uintptr_t from = reinterpret_cast<uintptr_t>(row[j] ? row[j] : b.pool);
+        // BF16: 16 lanes a token, 8 in each panel.  FP8: 8 lanes, the codes as they
+        // are in the token's row of the second panel
+        constexpr int kLanes = kFp8 ? 8 : 16, kPer = 32 / kLanes;
+        const uint32_t c = lane % kLanes;
+        const uint32_t to = dst + (kFp8 ? kPanel : (c >> 3) * kPanel);
+#pragma unroll
+        for (int i = 0; i < 32 / kPer; ++i) {
+          const uint32_t t = kPer * i + lane / kLanes;
+          const uintptr_t a = __shfl_sync(0xFFFFFFFFu, from, (int)t);
+          cp_async16(to + t * 128 + (((c & 7) ^ (t & 7)) << 4),
+                     reinterpret_cast<const uint8_t*>(a) + g * (kFp8 ? kHeadDim : 2 * kHeadDim) + c * 16,
+                     (exist[j] >> t) & 1u ? 16u : 0u);
+        }
+      }
       asm volatile("cp.async.commit_group;" ::: "memory");
-      if (k == 0) continue;
-      const int before = k - 1, gb = before % kKvHeads;
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    };
+    auto hand_on = [&](int k) {                      // (its copies have landed)
+      const int g = k % kKvHeads;
       if (kFp8) {
-        float* key_scale = reinterpret_cast<float*>(smem + W::kOffKs) + ((before / kKvHeads) & 1) * kKvHeads * W::kTokens;
+        float* key_scale = reinterpret_cast<float*>(smem + W::kOffKs) + ((k / kKvHeads) & 1) * kKvHeads * W::kTokens;
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < kTiles; ++j) {
           const int at = 32 * (kTiles * w + j);
-          uint8_t* panel = smem + (before & 1) * W::kKBytes + (at >> 7) * 2 * kPanel + (at & 127) * 128;
+          uint8_t* panel = smem + (k & 1) * W::kKBytes + (at >> 7) * 2 * kPanel + (at & 127) * 128;
           const uint32_t c = lane & 7;
           uint32_t bad = 0;                                      // tokens of the 32 with a NaN among their codes
 #pragma unroll 2
@@ -451,15 +446,26 @@ __global__ void __launch_bounds__(Wide<kTiles>::kThreads, 1) weight_wide_kernel(
             *reinterpret_cast<uint4*>(to + ((ch ^ sw) << 4)) = o[0];
             *reinterpret_cast<uint4*>(to + (((ch + 1) ^ sw) << 4)) = o[1];
           }
-          // (head 0 of a tile has been read by now where head 3 of the one before is handed on)
-          const uint2 sc = gb == kKvHeads - 1 && k < heads ? scales[1][j] : scales[0][j];
-          const uint32_t two = gb < 2 ? sc.x : sc.y;
-          const float ks = __half2float(__ushort_as_half((uint16_t)(gb & 1 ? two >> 16 : two & 0xFFFFu)));
-          key_scale[gb * W::kTokens + at + lane] = (bad >> lane) & 1u ? __int_as_float(0x7FC00000) : ks;
+          const uint32_t two = g < 2 ? scales[j].x : scales[j].y;
+          const float ks = __half2float(__ushort_as_half((uint16_t)(g & 1 ? two >> 16 : two & 0xFFFFu)));
+          key_scale[g * W::kTokens + at + lane] = (bad >> lane) & 1u ? __int_as_float(0x7FC00000) : ks;
         }
       }
       fence_async_smem();
-      mbar_arrive(k_full(before));
+      mbar_arrive(k_full(k));
+    };
+    send(0);
+    send(1);                                         // (a tile has four steps)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    hand_on(0);
+#pragma unroll 1
+    for (int k = 1; k < heads; ++k) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      hand_on(k);
+      if (k + 1 == heads) break;
+      ok = mbar_wait_warp(k_empty(k + 1), head_of(k - 1), err, kKernWeights);
+      if (!ok) break;
+      send(k + 1);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp >= W::kRoleQueries && warp < W::kRoleMma) {
@@ -471,9 +477,10 @@ __global__ void __launch_bounds__(Wide<kTiles>::kThreads, 1) weight_wide_kernel(
     for (int v = blockIdx.x; v < seen_tiles && ok; v += gridDim.x) {
       const Range r = range_of(v);
 #pragma unroll 1
-      for (int j = 0; j < kKvHeads * r.per && ok; ++j, ++i) {
+      for (int j = 0, g = 0, at = 0; j < kKvHeads * r.per && ok; ++j, ++i, ++at) {
+        if (at == r.per) at = 0, ++g;
         if (i % W::kQueryWarps != w) continue;
-        const int g = j / r.per, c = r.c0 + j % r.per;
+        const int c = r.c0 + at;
         if (i >= kRing) ok = mbar_wait_warp(empty(i), turn_of(i - kRing), err, kKernWeights);
         if (!ok) break;
         const int qa = c * kTurnQueries, have = nq - qa < kTurnQueries ? nq - qa : kTurnQueries;
