@@ -457,8 +457,9 @@ qsa_status_t qsa_hot_cache_fetch(qsa_cache* cache, const qsa_batch* batch,
  * zero-copy read would, and writes them into their hot rows as it goes;
  * afterwards the units are in the state qsa_hot_cache_fetch leaves.  Until that attention has run, the misses'
  * hot rows hold stale bytes: no other call may read those units' rows
- * (qsa_gather_rows, attention with `gathered`) but qsa_chunk_sparse_attn and
- * qsa_request_fork, which make the copies first; the pending map is replaced by
+ * (qsa_gather_rows, attention with `gathered`) but qsa_chunk_sparse_attn,
+ * qsa_window_attn, qsa_shared_attn, qsa_window_weights and qsa_request_fork, which
+ * make the copies first; the pending map is replaced by
  * the next plan or fetch of the unit.
  * [RTX4090 port, memory-ledger section: missing blocks moved back on
  * demand; here the move rides on the attention's own read.]

@@ -150,9 +150,9 @@ __device__ __forceinline__ const uint8_t* row_at(const BatchDesc& b, const Sourc
 }
 
 // One warp, one query row x of unit u and head h: online softmax over the row's
-// own tokens, plain fp32.  For rows that the tiles cannot compute: 0 times a value
-// that is not finite is not 0, so that a token which a row does not see may have
-// reached it.
+// own tokens, plain fp32, four at a time.  For rows that the tiles cannot compute: 0
+// times a value that is not finite is not 0, so that a token which a row does not see
+// may have reached it.  Slow, for such values only.
 __device__ __noinline__ void attend_row(const DenseParams& p, int u, int x, int h) {
   const int lane = threadIdx.x & 31, g = h / kGroup;
   const BatchDesc& b = p.d.c.b;
@@ -168,20 +168,43 @@ __device__ __noinline__ void attend_row(const DenseParams& p, int u, int x, int 
   const int64_t pos = p.d.c.position(u, x);
   own_part(p.d, pos, pos, &t);
   const Source src = source_of(p.d, u);
-  for (uint32_t i = 0; i < t.total; ++i) {
-    const uint8_t* row = row_at(b, src, t, i, slot_at(src, t, i));
-    if (!row) continue;
-    const float4 k = row_values(row, g, lane, fp8);
-    float s = fmaf(q[3], k.w, fmaf(q[2], k.z, fmaf(q[1], k.y, q[0] * k.x)));
+  constexpr int kTurn = 4;
+  for (uint32_t i = 0; i < t.total; i += kTurn) {
+    const uint8_t* row[kTurn];
+    float4 k[kTurn], v[kTurn];
+    float s[kTurn];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    const float mn = fmaxf(m, s);
-    const float a = mn == -INFINITY ? 1.f : exp2f(m - mn), e = s == -INFINITY ? 0.f : exp2f(s - mn);
-    const float4 v = row_values(row, kKvHeads + g, lane, fp8);
+    for (int j = 0; j < kTurn; ++j) row[j] = row_at(b, src, t, i + j, slot_at(src, t, i + j));
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) {
+      k[j] = v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!row[j]) continue;
+      k[j] = row_values(row[j], g, lane, fp8);
+      v[j] = row_values(row[j], kKvHeads + g, lane, fp8);
+    }
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) s[j] = fmaf(q[3], k[j].w, fmaf(q[2], k[j].z, fmaf(q[1], k[j].y, q[0] * k[j].x)));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int j = 0; j < kTurn; ++j) s[j] += __shfl_xor_sync(0xFFFFFFFFu, s[j], o);
+    float mn = m;
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) {
+      if (!row[j]) s[j] = -INFINITY;
+      mn = fmaxf(mn, s[j]);
+    }
+    const float a = mn == -INFINITY ? 1.f : exp2f(m - mn);
     m = mn;
-    l = fmaf(l, a, e);
-    acc = make_float4(fmaf(acc.x, a, e * v.x), fmaf(acc.y, a, e * v.y), fmaf(acc.z, a, e * v.z),
-                      fmaf(acc.w, a, e * v.w));
+    l *= a;
+    acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
+#pragma unroll
+    for (int j = 0; j < kTurn; ++j) {
+      if (!row[j]) continue;
+      const float e = s[j] == -INFINITY ? 0.f : exp2f(s[j] - mn);
+      l += e;
+      acc = make_float4(fmaf(e, v[j].x, acc.x), fmaf(e, v[j].y, acc.y), fmaf(e, v[j].z, acc.z), fmaf(e, v[j].w, acc.w));
+    }
   }
   const float r = l == 0.f ? 0.f : 1.f / l;      // no tokens: zeros; NaN stays
   reinterpret_cast<uint2*>(p.out + ((int64_t)x * kQHeads + h) * kHeadDim)[lane] =
