@@ -11,12 +11,36 @@
 // A tile is some rows and one list of tokens: the tokens that any of its rows
 // sees, cut into shares (of whole steps) where tiles are few.  Tiles of more than
 // four queries run on tcgen05 (wide: 64 queries and a KV head per CTA), the others
-// on register fragments (few: four queries x four heads of the group are the 16
-// rows of one mma, four KV heads per CTA), since their time is the rows' bytes.
-// Where the requests of a shared prefix have few queries each, the prefix has
-// tiles of its own, over the rows of all requests; else every tile reads it in
-// front of its own tokens.  A row's partial results are joined by their maxima and
-// sums.
+// on register fragments (few: tokens and dims are the rows of an mma of m16n8k16, four
+// KV heads per CTA), since their time is the rows' bytes.  Where the requests of a
+// shared prefix have few queries each, the prefix has tiles of its own, over the rows
+// of all requests; else every tile reads it in front of its own tokens.  A row's
+// pieces are joined by their maxima and sums.
+//
+// Measured (device time of a call, one behind the other):
+//   4096 BF16 queries, window 4096 of 16384 tokens (138 GFLOP): 124 us, 0.58 of the
+//     measured bf16 rate over the call, 0.69 while all SMs are at work (256 CTAs on
+//     152 SMs are two rounds).  Bound by the hand-overs between softmax and tensor core
+//     (issue slots 0.49, tensor pipe 0.55, exponentials 0.28 of the cycles).
+//   2 x 1023 FP8 queries over 8191 tokens each (129 GFLOP): 162 us on 128 of 152 SMs;
+//     the products with both scales come on top, 2.5 us a step for 1.9.
+//   32 requests' tokens, window 4096, FP8 rows (137 MB): 36.7 us, the kernel 34.5 at 4.0
+//     TB/s, bound by the conversions' and address instructions (issue slots 0.54).
+//   one token, window 1024: 7.2 us, the latency of two launches.
+//   64 tokens behind a prefix of 16384, 0.4 K own tokens each (89 MB): 38 us: 19 for the
+//     prefix on 128 SMs (four steps a share: 1.9 us each and 10 of set-up, pieces and
+//     launch) beside 16 for the own tokens, and a join of 35 pieces a row.
+//   29 FP8 draft tokens behind 65536 (69 MB): 57 us, 14 steps of 3.3 us a share.
+// Not faster: the SMs shared out to prefix and own tokens by their rows (41 -> 51 us);
+// FP8 codes copied and turned over in place (162 -> 198 us); both halves of a CTA on
+// every other step of a small tile (57 -> 76, BF16 44 -> 59); the idle half's warps for
+// V (57 -> 60).
+//
+// Rounding: P to bf16 beside BF16 rows (2^-8 of each term at most; the tensor core
+// takes no wider type beside them); beside FP8 rows P times the V scale as f16, 2^-11
+// of itself, or 2^-25 in units in which the largest of the row's products is 2^-6 at
+// least (the reference follows the row's own products); the output once to bf16.  S, O,
+// maxima and sums are fp32, the sums taken from the unrounded probabilities.
 #include "dense_common.cuh"
 
 namespace qsa {
@@ -1239,7 +1263,9 @@ int share_steps(const int64_t* steps, int n, int64_t most, int64_t least) {
     for (int i = 0; i < n; ++i) sum += ceil_div(steps[i], mid);
     if (sum <= most) hi = mid; else lo = mid + 1;
   }
-  return (int)lo;
+  // not for less than a quarter of the longest: the join comes on top (2 x 1023 FP8
+  // queries, 32 tiles of up to 64 steps on 38 shares: 170 us with 63 steps a share)
+  return (int)(lo > longest - longest / 4 && longest > lo ? longest : lo);
 }
 
 constexpr int kLeastWide = 2, kLeastFew = 1;          // steps of a share at least

@@ -16,6 +16,10 @@
 // at random moves a quarter of the rows (closing the rows up in order would move
 // nearly half, one behind the other).  The request's next tokens find the
 // region's rows from `keep` on free, as qsa_append_token expects.
+//
+// Measured: 12 layers, 32768 -> 16384 BF16 tokens at random: select 23 us (latencies of
+// seven cluster barriers and the passes between them), move 67 us (406 MB, 0.90 of the
+// measured copy rate), close 7 us.  12 layers, 2047 -> 1021 FP8 tokens: 9 + 8 + 4 us.
 #include "qsa_internal.cuh"
 
 namespace qsa {
@@ -91,8 +95,9 @@ __device__ __forceinline__ void cta_offsets(uint32_t a, uint32_t b, uint32_t* s_
 
 // One cluster per layer; each CTA has an eighth of the tokens, and then of the kept
 // ones.  Per digit every CTA counts its own keys and adds up all CTAs' counts from
-// their shared memory: one cluster barrier per digit.  12 layers of 32768 tokens:
-// 50 us with one CTA per layer.
+// their shared memory: one cluster barrier per digit.  12 layers of 32768 tokens: 50
+// us with one CTA per layer, 44 with digits of 11 bits and 1024 threads (the sums over
+// 2048 bins of eight CTAs), 41 where every row's bit was an atomic of its own.
 __global__ void __launch_bounds__(kSelectThreads, 1) __cluster_dims__(kSelectCtas, 1, 1)
 evict_select_kernel(const __grid_constant__ EvictParams p) {
   __shared__ uint32_t hist[4][256], s_warp[kSelectWarps], s_bin[2], s_pair[2][2];
