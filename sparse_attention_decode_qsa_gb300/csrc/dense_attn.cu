@@ -32,7 +32,7 @@
 //     launch) beside 16 for the own tokens, and a join of 35 pieces a row.
 //   29 FP8 draft tokens behind 65536 (69 MB): 57 us, 14 steps of 3.3 us a share.
 // Not faster: the SMs shared out to prefix and own tokens by their rows (41 -> 51 us);
-// FP8 codes copied and turned over in place (162 -> 198 us); both halves of a CTA on
+// FP8 codes copied and turned over in place (170 -> 198 us); both halves of a CTA on
 // every other step of a small tile (57 -> 76, BF16 44 -> 59); the idle half's warps for
 // V (57 -> 60).
 //
