@@ -17,9 +17,9 @@
 // Measured (device time of a call):
 //   8 requests' tokens over 8192 BF16 tokens each (67 MB of keys): 9.2 us, above the
 //     measured copy rate (the keys stay in L2 from call to call; 16.9 from cold caches).
-//   64 queries over 131072 FP8 tokens (134 M exponentials, 34 GFLOP): 79 us.  BF16
-//     rows take 60, 32 queries 62 and 42: codes to bf16 are a part of the bound.  A
-//     further turn of 256 tokens costs 1.7 us up to 128 queries and 2.0 beyond, the
+//   64 queries over 131072 FP8 tokens (134 M exponentials, 34 GFLOP): 72 us.  BF16
+//     rows take 60, 32 queries 56 and 42: codes to bf16 are a part of the bound.  A
+//     further turn of 256 tokens costs 1.8 us up to 128 queries and 2.0 beyond, the
 //     tensor core 0.6 of it (both operands from shared memory, 66 cycles an MMA); the
 //     rest is hand-overs and issue slots (0.51 in use).
 //   1024 BF16 queries, windows of 16384 of 32768 tokens (69 GFLOP): 135 us on 136 of 152
@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
 // again in every CTA.
 constexpr int kEpiWarps = 16, kKeyWarps = 4;
 constexpr int kPanel = 128 * 128;                 // 128 rows of 64 16-bit elements
+constexpr int kAhead = 4;                         // pieces of FP8 codes that a lane reads ahead (2: 76 us for 72)
 constexpr int kTurnQueries = 32, kTurnCols = kTurnQueries * kGroup;
 constexpr uint32_t kTmemCols = 512;
 
@@ -442,23 +443,37 @@ __global__ void __launch_bounds__(Wide<kTiles>::kThreads, 1) weight_wide_kernel(
           const int at = 32 * (kTiles * w + j);
           uint8_t* panel = smem + (k & 1) * W::kKBytes + (at >> 7) * 2 * kPanel + (at & 127) * 128;
           const uint32_t c = lane & 7;
-          uint32_t bad = 0;                                      // tokens of the 32 with a NaN among their codes
-#pragma unroll 2
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t t = 4 * i + (lane >> 3), sw = t & 7;
-            const uint4 v = *reinterpret_cast<const uint4*>(panel + kPanel + t * 128 + ((c ^ sw) << 4));
-            uint4 o[2];
-            o[0] = make_uint4(codes2_bf16(v.x), codes2_bf16(v.x >> 16), codes2_bf16(v.y), codes2_bf16(v.y >> 16));
-            o[1] = make_uint4(codes2_bf16(v.z), codes2_bf16(v.z >> 16), codes2_bf16(v.w), codes2_bf16(v.w >> 16));
-            const uint32_t nan = nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w);
-            const uint32_t which = __ballot_sync(0xFFFFFFFFu, nan != 0);       // (and all four rows have been read)
+          uint32_t nan_of = 0;                                   // bit i: of this lane's 16 codes of token 4 i + lane / 8
+#pragma unroll 1
+          for (int i0 = 0; i0 < 8; i0 += kAhead) {
+            uint4 v[kAhead];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) bad |= (which >> (8 * x)) & 0xFFu ? 1u << (4 * i + x) : 0u;
-            // codes 16 c .. + 15 are the chunks 2 c and 2 c + 1 of the row's 16
-            uint8_t* to = panel + (c >> 2) * kPanel + t * 128;
-            const uint32_t ch = (2 * c) & 7;
-            *reinterpret_cast<uint4*>(to + ((ch ^ sw) << 4)) = o[0];
-            *reinterpret_cast<uint4*>(to + (((ch + 1) ^ sw) << 4)) = o[1];
+            for (int x = 0; x < kAhead; ++x) {
+              const uint32_t t = 4 * (i0 + x) + (lane >> 3);
+              v[x] = *reinterpret_cast<const uint4*>(panel + kPanel + t * 128 + ((c ^ (t & 7)) << 4));
+            }
+            __syncwarp();                                        // (these rows have been read)
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+              const uint32_t t = 4 * (i0 + x) + (lane >> 3), sw = t & 7;
+              if (nan_codes(v[x].x) | nan_codes(v[x].y) | nan_codes(v[x].z) | nan_codes(v[x].w)) nan_of |= 1u << (i0 + x);
+              // codes 16 c .. + 15 are the chunks 2 c and 2 c + 1 of the row's 16
+              uint8_t* to = panel + (c >> 2) * kPanel + t * 128;
+              const uint32_t ch = (2 * c) & 7;
+              *reinterpret_cast<uint4*>(to + ((ch ^ sw) << 4)) =
+                  make_uint4(codes2_bf16(v[x].x), codes2_bf16(v[x].x >> 16), codes2_bf16(v[x].y), codes2_bf16(v[x].y >> 16));
+              *reinterpret_cast<uint4*>(to + (((ch + 1) ^ sw) << 4)) =
+                  make_uint4(codes2_bf16(v[x].z), codes2_bf16(v[x].z >> 16), codes2_bf16(v[x].w), codes2_bf16(v[x].w >> 16));
+            }
+          }
+          uint32_t bad = 0;                                      // tokens of the 32 with a NaN among their codes
+          if (__any_sync(0xFFFFFFFFu, nan_of != 0)) {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t which = __ballot_sync(0xFFFFFFFFu, (nan_of >> i) & 1u);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) bad |= (which >> (8 * x)) & 0xFFu ? 1u << (4 * i + x) : 0u;
+            }
           }
           const uint32_t two = g < 2 ? scales[j].x : scales[j].y;
           const float ks = __half2float(__ushort_as_half((uint16_t)(g & 1 ? two >> 16 : two & 0xFFFFu)));
