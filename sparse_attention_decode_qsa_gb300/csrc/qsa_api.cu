@@ -1123,6 +1123,8 @@ qsa_status_t qsa_request_evict(qsa_cache* c, qsa_handle request, const float* we
     return fail(QSA_ERR_INVALID_ARG, "first %lld and last %lld must be >= 0 and at most keep %lld together",
                 (long long)first, (long long)last, (long long)keep);
   if (!weights || !workspace) return fail(QSA_ERR_INVALID_ARG, "null array");
+  if (weights_out == weights)
+    return fail(QSA_ERR_INVALID_ARG, "weights_out is weights: kept weights would replace others not yet read");
   if (!aligned16(workspace) || !aligned16(kept) || reinterpret_cast<uintptr_t>(weights) % 4 ||
       reinterpret_cast<uintptr_t>(weights_out) % 4)
     return fail(QSA_ERR_INVALID_ARG, "misaligned device buffer");

@@ -304,3 +304,20 @@ def test_refusals_leave_everything_alone():
         _clean(c)
     finally:
         f.close()
+
+
+def test_kept_weights_do_not_replace_the_weights_they_are_read_from():
+    f = Filled([200, 100, 90], [Q.KV_HBM, Q.KV_HBM, Q.KV_HBM], layers=2, seed=3, grow=10)
+    try:
+        c, h = f.c, f.hs[0]
+        models = [Model(c, h, l) for l in range(2)]
+        w = torch.rand(2, 200, device=f.dev)
+        before = w.clone()
+        with pytest.raises(Q.QsaError) as e:
+            c.evict(h, w, 50, weights_out=w)
+        assert e.value.status == Q.ERR_INVALID_ARG
+        assert c.request_info(h).ctx_len == 200 and torch.equal(w, before)
+        for m in models:
+            m.check()
+    finally:
+        f.close()
