@@ -48,8 +48,8 @@
 // warps' instructions and by the hand-overs between them and the tensor core (the
 // schedulers issue in 0.60 of the cycles).  The same with FP8 rows 272 us: the
 // loaders' conversions and the products with both scales are added instructions.
-// 14 FP8 draft queries of 8 requests (30 MB of rows at most) 33 us (plan 8, split
-// 27, join 4 each alone): five steps per CTA, each the latency of rows, conversion
+// 14 FP8 draft queries of 8 requests (30 MB of rows at most) 31 us (33 with two codes
+// a conversion: plan 8, split 27, join 4 each alone): five steps per CTA, each the latency of rows, conversion
 // and softmax one after the other.  Not faster: K and V split over the loader warps (310 us at
 // 2048 FP8 queries), the next step's codes loaded into the registers just stored
 // (321), the idle half's warps on every other 64 tokens of a draft (43 where 39

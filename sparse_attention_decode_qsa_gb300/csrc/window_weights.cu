@@ -21,7 +21,7 @@
 //     rows take 60, 32 queries 56 and 42: codes to bf16 are a part of the bound.  A
 //     further turn of 256 tokens costs 1.8 us up to 128 queries and 2.0 beyond, the
 //     tensor core 0.6 of it (both operands from shared memory, 66 cycles an MMA); the
-//     rest is hand-overs and issue slots (0.51 in use).
+//     rest is hand-overs and issue slots (0.54 in use).
 //   1024 BF16 queries, windows of 16384 of 32768 tokens (69 GFLOP): 135 us on 136 of 152
 //     SMs (128 tokens each; 256 tokens would be 68 CTAs), 1.05 us a turn of 128 x 128.
 // Not faster: turns of 256 columns on 128 tokens (127 -> 165 us: with two turns under
