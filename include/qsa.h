@@ -368,7 +368,9 @@ qsa_status_t qsa_request_advance(qsa_cache* cache, qsa_handle request, int32_t n
  *                     hbm_row_base + l*ring_tokens + t mod ring_tokens;
  *                     slot[t] = that ring row, and the token that held it,
  *                     t - ring_tokens (if >= 0), becomes cold: slot = -1.
- * Both buffers 16-byte aligned.  Every unit needs ctx_len >= 1. */
+ * Both buffers 16-byte aligned.  Every unit needs ctx_len >= 1, and a t that
+ * qsa_request_evict has not kept (kept tokens' rows are in no order: INVALID_ARG,
+ * and nothing is stored for any unit). */
 qsa_status_t qsa_append_token(qsa_cache* cache, const qsa_batch* batch, const float* k_new,
                               const void* kv_new, void* stream);
 
@@ -499,7 +501,9 @@ qsa_status_t qsa_sparse_decode_attn(qsa_cache* cache, const qsa_batch* batch,
  * [rows][2048], quantised and stored under the rules given there.  The slot
  * tables end as n_tokens single appends would leave them: a ring request
  * keeps its newest ring_tokens rows in the ring, every older token of the
- * chunk is cold, and so is every token that lost its ring row.
+ * chunk is cold, and so is every token that lost its ring row.  A chunk may
+ * reach back over tokens that are stored already, but not over those that
+ * qsa_request_evict has kept (INVALID_ARG, nothing is stored).
  * Both buffers 16-byte aligned.
  * Errors: INVALID_ARG, STALE_HANDLE, NO_DEVICE, CUDA. */
 qsa_status_t qsa_append_chunk(qsa_cache* cache, const qsa_chunk* chunk, const float* k_new,
@@ -640,8 +644,10 @@ qsa_status_t qsa_window_weights(qsa_cache* cache, const qsa_chunk* chunk, const 
  * request's region at its layer keeps it; the others in the region, in ascending
  * order, take the free rows there in ascending order.  A row outside the region
  * (qsa_slot_table_set) stays where it is.  Entries of the arrays from `keep` on are
- * left as they were.  Afterwards qsa_request_truncate takes back no kept token (it
- * refuses lengths below keep), since their rows are in no order.
+ * left as they were.  Afterwards the rows of the kept tokens are in no order:
+ * qsa_request_truncate takes back none of them (it refuses lengths below keep), and
+ * qsa_append_token and qsa_append_chunk store none of them again; new tokens, from
+ * position keep on, are advanced over and stored as ever.
  * weights: device fp32, layer l at weights + l * weight_stride (>= ctx_len).
  * kept: device int32 [n_layers][keep] or NULL, the kept tokens' former positions.
  * weights_out: device fp32, layer l at weights_out + l * out_stride (>= keep), or

@@ -340,6 +340,15 @@ cudaError_t complete_units(const BatchDesc& b, cudaStream_t s) {
   return e;
 }
 
+// Tokens from `first` on of a request can be stored: region row t is token t's only
+// behind the tokens that an eviction kept.
+qsa_status_t check_in_order(const Lease& l, int64_t first) {
+  if (first < l.packed)
+    return fail(QSA_ERR_INVALID_ARG, "token %lld is one of the %lld that an eviction has kept: their rows are in no order",
+                (long long)first, (long long)l.packed);
+  return QSA_OK;
+}
+
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 qsa_status_t window_desc(const qsa_cache* c, const qsa_chunk* chunk, int32_t sinks, int32_t window, DenseAttn* d) {
@@ -826,6 +835,7 @@ qsa_status_t qsa_append_token(qsa_cache* c, const qsa_batch* batch, const float*
     const Lease& l = c->leases[d.u[u].req];
     const int64_t t = l.ctx_len - 1;
     const int64_t layer = d.u[u].layer;
+    if (qsa_status_t st = check_in_order(l, t)) return st;
     tg.pool_row[u] = -1;
     tg.evict[u] = -1;
     if (l.placement == QSA_KV_HBM) {
@@ -911,6 +921,8 @@ qsa_status_t qsa_append_chunk(qsa_cache* c, const qsa_chunk* chunk, const float*
   ChunkTargets tg;
   for (int u = 0; u < d.b.n_units; ++u) {
     const Lease& l = c->leases[d.b.u[u].req];
+    if (d.unit_tokens(u) > 0)
+      if (qsa_status_t st = check_in_order(l, l.ctx_len - d.unit_tokens(u))) return st;
     tg.row_base[u] = l.placement == QSA_KV_HOST ? -1 : l.row_base + (int64_t)d.b.u[u].layer * l.layer_rows;
     tg.ring[u] = l.placement == QSA_KV_HOST_RING ? l.layer_rows : 0;
   }

@@ -321,3 +321,62 @@ def test_kept_weights_do_not_replace_the_weights_they_are_read_from():
             m.check()
     finally:
         f.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_kept_tokens_are_not_stored_again(fp8):
+    """The rows of kept tokens are in no order, so that the region's row t may be
+    another token's: storing them again is refused, alone, in a chunk that reaches back
+    over them and in a batch with others, and nothing changes; new tokens are stored."""
+    f = Filled([10, 9], layers=2, fp8=fp8, seed=12, grow=6)
+    try:
+        c, dev, (h, other) = f.c, f.dev, f.hs
+        w = torch.zeros(2, 10)
+        w[:, [0, 3, 4, 7, 9]] = 1.0
+        models = [Model(c, h, l) for l in range(2)] + [Model(c, other, l) for l in range(2)]
+        c.evict(h, w.to(dev), 5)
+        for m in models[:2]:
+            m.evict([0, 3, 4, 7, 9])
+            assert [s - m.base for s in m.slots] == [0, 3, 4, 1, 2]
+        g = torch.Generator().manual_seed(2)
+
+        def new(units):
+            return (torch.randn(units, 64, generator=g).to(dev),
+                    torch.randn(units, 1024, generator=g).bfloat16().view(torch.uint8).to(dev))
+
+        def refused(fn, *a):
+            with pytest.raises(Q.QsaError) as e:
+                fn(*a)
+            assert e.value.status == Q.ERR_INVALID_ARG
+            torch.cuda.synchronize()
+            for m in models:
+                m.check()
+
+        refused(c.append_token, [h], 0, 2, *new(2))
+        refused(c.append_token, [other, h], 0, 2, *new(4))
+        refused(c.append_chunk, [h], [1], 0, 2, *new(2))
+        refused(c.append_chunk, [h, other], [5, 2], 1, 1, *new(7))
+        c.advance(h, 3)
+        models = [Model(c, h, l) for l in range(2)] + models[2:]
+        refused(c.append_chunk, [h], [4], 0, 2, *new(8))
+        # from the first new token on, one by one or together, as often as wanted
+        for _ in range(2):
+            c.append_chunk([h, other], [3, 0], 0, 2, *new(6))
+            k, kv = new(2)
+            c.append_token([h], 0, 2, k, kv)
+            torch.cuda.synchronize()
+            for l, m in enumerate(models[:2]):
+                old = m.slots[:5]
+                now = Model(c, h, l)
+                assert now.slots == old + [m.base + t for t in (5, 6, 7)]
+                assert torch.equal(now.rows[:5], m.rows[:5]) and torch.equal(now.keys[:5], m.keys[:5])
+                assert torch.equal(now.scales[:5], m.scales[:5])
+                if not fp8:
+                    assert torch.equal(now.rows[7], kv[l].cpu())
+            for m in models[2:]:
+                m.check()
+        # a request whose tokens are not stored here does not matter
+        c.append_token([other], 0, 2, *new(2))
+        _clean(c)
+    finally:
+        f.close()
