@@ -1156,6 +1156,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) dense_wide_kernel(const __gri
 
 // kSplit warps per (row, head), each over every kSplit-th piece (eight where there are
 // many: their loads are what the join waits for); lane l holds dims 4 l .. 4 l + 3.
+// No piece is left out, however small its factor is: a sum or an O that is not finite
+// stays one (0 times it is NaN), and the row is computed again.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 template <int kSplit>
 __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_constant__ DenseParams p) {
@@ -1196,7 +1198,6 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_c
 #pragma unroll
     for (int k = 0; k < kTurn; ++k) {
       const float c = ml[k].y != 0.f ? exp2f(ml[k].x - mn) : 0.f;            // 0: nothing there
-      if (c == 0.f) continue;
       l = fmaf(ml[k].y, c, l);
       acc = make_float4(fmaf(o[k].x, c, acc.x), fmaf(o[k].y, c, acc.y), fmaf(o[k].z, c, acc.z), fmaf(o[k].w, c, acc.w));
     }
@@ -1216,7 +1217,6 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_c
       const float2 ml = part_ml[warp + k];
       const float4 o = part_o[warp + k][lane];
       const float c = ml.y != 0.f ? exp2f(ml.x - mn) : 0.f;
-      if (c == 0.f) continue;
       l = fmaf(ml.y, c, l);
       acc = make_float4(fmaf(o.x, c, acc.x), fmaf(o.y, c, acc.y), fmaf(o.z, c, acc.z), fmaf(o.w, c, acc.w));
     }
