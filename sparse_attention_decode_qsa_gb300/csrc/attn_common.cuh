@@ -50,6 +50,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// A K scale as it goes to the logits, NaN if it is infinite: the codes' product with a
+// query has one sign where its terms, each times the scale, have two.
+__device__ __forceinline__ float key_scale_of(uint16_t bits) {
+  const float s = __half2float(__ushort_as_half(bits));
+  return fmaf(s, 0.f, s);
+}
+
 // log2 of a V scale's size.
 __device__ __forceinline__ float log2_size(float s) {
   float y;

@@ -368,9 +368,9 @@ __global__ void __launch_bounds__(kFewThreads, kFp8 && kN == 1 ? 2 : 1) dense_fe
     if (kFp8) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const __half* sc = reinterpret_cast<const __half*>(smem + (st - smem_u32(smem)) + L::kScales + (r + 8 * i) * 16);
-        ks[i] = __half2float(sc[g]);
-        vs[i] = __half2float(sc[kKvHeads + g]);
+        const uint16_t* sc = reinterpret_cast<const uint16_t*>(smem + (st - smem_u32(smem)) + L::kScales + (r + 8 * i) * 16);
+        ks[i] = key_scale_of(sc[g]);
+        vs[i] = __half2float(__ushort_as_half(sc[kKvHeads + g]));
         lv[i] = log2_size(vs[i]);
       }
     }
@@ -845,7 +845,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) dense_wide_kernel(const __gri
           vraw = sc[kKvHeads + g];
         }
         write_meta();
-        const float ks = __half2float(__ushort_as_half(kraw)), vs = __half2float(__ushort_as_half(vraw));
+        const float ks = key_scale_of(kraw), vs = __half2float(__ushort_as_half(vraw));
         scales[j % kMetas].k[32 * w + lane] = ks * p.scale_log2;
         scales[j % kMetas].v[32 * w + lane] = vs;
         scales[j % kMetas].size[32 * w + lane] = log2_size(vs);

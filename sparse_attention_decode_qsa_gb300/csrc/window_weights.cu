@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
       const int c = r + 8 * hi;
       const int64_t t = first + (int64_t)s * kFewStep + c;
       float ks = 1.f;
-      if (kFp8) ks = __half2float(*reinterpret_cast<const __half*>(smem + (st - smem_u32(smem)) + L::kScales + c * 16 + 2 * g));
+      if (kFp8) ks = key_scale_of(*reinterpret_cast<const uint16_t*>(smem + (st - smem_u32(smem)) + L::kScales + c * 16 + 2 * g));
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const bool seen = ((have >> c) & 1u) && sees(p.d, pos[i], t);
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(Wide<kTiles>::kThreads, 1) weight_wide_kernel(
             }
           }
           const uint32_t two = g < 2 ? scales[j].x : scales[j].y;
-          const float ks = __half2float(__ushort_as_half((uint16_t)(g & 1 ? two >> 16 : two & 0xFFFFu)));
+          const float ks = key_scale_of((uint16_t)(g & 1 ? two >> 16 : two & 0xFFFFu));
           key_scale[g * W::kTokens + at + lane] = (bad >> lane) & 1u ? __int_as_float(0x7FC00000) : ks;
         }
       }

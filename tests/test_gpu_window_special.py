@@ -124,3 +124,29 @@ def test_values_that_are_not_finite_behind_logits_far_below(ctx, tokens):
         assert _check(pos, q, out, lse, lambda p: f.values(0, 0, list(range(p + 1)))) == tokens * 16
     finally:
         f.close()
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("ctx,tokens,bad", SHARES + [(20, 1, range(7, 8)), (20, 9, range(2, 3)), (300, 70, range(150, 151))])
+def test_infinite_k_scales(value, ctx, tokens, bad):
+    """Codes of both signs times an infinite scale: logits without a value (for the
+    sum of the codes' products they would have one, and -inf leave the token out)."""
+    f = Filled([ctx], fp8=True, seed=6)
+    try:
+        _poison_keys(f, 0, bad, value)
+        q = _queries(tokens, 7, f.dev)
+        out, lse = _window(f, [tokens], q, 0, FULL)
+        pos = [p for _, p in f.positions([tokens])]
+        assert _check(pos, q, out, lse, lambda p: f.values(0, 0, list(range(p + 1)))) > 0
+        # the weights: NaN for those tokens, the others' as if these were not there
+        lse = torch.full((tokens, 16), 3.0, device=f.dev)
+        w, w0 = torch.zeros(1, ctx, device=f.dev), torch.zeros(1, ctx, device=f.dev)
+        f.c.window_weights(f.hs, [tokens], 0, 1, q, lse, 0, FULL, SCALE, w)
+        _poison_keys(f, 0, bad, 1.0)
+        f.c.window_weights(f.hs, [tokens], 0, 1, q, lse, 0, FULL, SCALE, w0)
+        _clean(f.c)
+        at = torch.zeros(ctx, dtype=torch.bool, device=f.dev)
+        at[list(bad)] = True
+        assert torch.equal(w[0].isnan(), at) and torch.equal(w[0, ~at], w0[0, ~at])
+    finally:
+        f.close()
