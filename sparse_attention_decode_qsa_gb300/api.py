@@ -6,6 +6,7 @@ buffers and supplies the stream.
 from __future__ import annotations
 
 import ctypes as C
+import operator
 
 import torch
 
@@ -51,6 +52,22 @@ def _chunk(handles, n_tokens, layer0: int, n_layers: int):
         raise ValueError("one token count per request")
     # (assigned arrays are kept alive by the structure)
     return N.Chunk(n, layer0, n_layers, 0, (N.Handle * n)(*handles), (C.c_int32 * n)(*n_tokens))
+
+
+_INT32_MAX = (1 << 31) - 1
+
+
+def _reach(v) -> int:
+    """A number of tokens that may be larger than any context; ctypes would cut it
+    to 32 bits.  (Negative ones are the library's to refuse.)"""
+    return max(-1, min(operator.index(v), _INT32_MAX))
+
+
+def _int32(v, what) -> int:
+    v = operator.index(v)
+    if not -_INT32_MAX - 1 <= v <= _INT32_MAX:
+        raise ValueError(f"{what}: {v} does not fit 32 bits")
+    return v
 
 
 class HostMemory:
@@ -400,7 +417,7 @@ class Cache:
     # --------------------------------------- attention without a selection
     def window_attn_workspace_bytes(self, handles, n_tokens, layer0, n_layers, sinks, window) -> int:
         ch = _chunk(handles, n_tokens, layer0, n_layers)
-        return self._bytes(self.L.qsa_window_attn_workspace_bytes(self.h, C.byref(ch), sinks, window),
+        return self._bytes(self.L.qsa_window_attn_workspace_bytes(self.h, C.byref(ch), _reach(sinks), _reach(window)),
                            "qsa_window_attn_workspace_bytes")
 
     def window_attn(self, handles, n_tokens, layer0, n_layers, q, sinks, window, softmax_scale, out, lse=None,
@@ -415,15 +432,17 @@ class Cache:
             workspace = self._scratch(self.window_attn_workspace_bytes(handles, n_tokens, layer0, n_layers, sinks,
                                                                        window), stream)
         check(self.L.qsa_window_attn(
-            self.h, C.byref(ch), self._rows(q, "q", (torch.bfloat16,), heads), sinks, window, float(softmax_scale),
-            self._rows(out, "out", (torch.bfloat16,), heads), self._rows(lse, "lse", (torch.float32,), heads[:2]),
+            self.h, C.byref(ch), self._rows(q, "q", (torch.bfloat16,), heads), _reach(sinks), _reach(window),
+            float(softmax_scale), self._rows(out, "out", (torch.bfloat16,), heads),
+            self._rows(lse, "lse", (torch.float32,), heads[:2]),
             self._rows(workspace, "workspace", (torch.uint8,), (workspace.numel(),)), workspace.numel(),
             self._current(stream)), "qsa_window_attn")
 
     def shared_attn_workspace_bytes(self, handles, n_tokens, layer0, n_layers, prefix, prefix_len, own_first) -> int:
         ch = _chunk(handles, n_tokens, layer0, n_layers)
-        return self._bytes(self.L.qsa_shared_attn_workspace_bytes(self.h, C.byref(ch), prefix, prefix_len, own_first),
-                           "qsa_shared_attn_workspace_bytes")
+        return self._bytes(self.L.qsa_shared_attn_workspace_bytes(
+            self.h, C.byref(ch), prefix, _int32(prefix_len, "prefix_len"), _int32(own_first, "own_first")),
+            "qsa_shared_attn_workspace_bytes")
 
     def shared_attn(self, handles, n_tokens, layer0, n_layers, prefix, prefix_len, own_first, q, softmax_scale, out,
                     lse=None, workspace=None, stream=None):
@@ -437,9 +456,9 @@ class Cache:
             workspace = self._scratch(self.shared_attn_workspace_bytes(handles, n_tokens, layer0, n_layers, prefix,
                                                                        prefix_len, own_first), stream)
         check(self.L.qsa_shared_attn(
-            self.h, C.byref(ch), prefix, prefix_len, own_first, self._rows(q, "q", (torch.bfloat16,), heads),
-            float(softmax_scale), self._rows(out, "out", (torch.bfloat16,), heads),
-            self._rows(lse, "lse", (torch.float32,), heads[:2]),
+            self.h, C.byref(ch), prefix, _int32(prefix_len, "prefix_len"), _int32(own_first, "own_first"),
+            self._rows(q, "q", (torch.bfloat16,), heads), float(softmax_scale),
+            self._rows(out, "out", (torch.bfloat16,), heads), self._rows(lse, "lse", (torch.float32,), heads[:2]),
             self._rows(workspace, "workspace", (torch.uint8,), (workspace.numel(),)), workspace.numel(),
             self._current(stream)), "qsa_shared_attn")
 
@@ -453,7 +472,7 @@ class Cache:
         units = (n_layers * len(handles), weights.shape[-1])
         check(self.L.qsa_window_weights(
             self.h, C.byref(ch), self._rows(q, "q", (torch.bfloat16,), heads),
-            self._rows(lse, "lse", (torch.float32,), heads[:2]), sinks, window, float(softmax_scale),
+            self._rows(lse, "lse", (torch.float32,), heads[:2]), _reach(sinks), _reach(window), float(softmax_scale),
             self._rows(weights, "weights", (torch.float32,), units), units[1], int(bool(accumulate)),
             self._current(stream)), "qsa_window_weights")
 

@@ -67,3 +67,48 @@ def test_the_binding_checks_types_shapes_and_layouts():
     for w in (torch.zeros(3, 99), torch.zeros(2, 100), torch.zeros(3, 100).double(), torch.zeros(100, 3).t()):
         with pytest.raises(ValueError):
             c.evict(h, w, 50, workspace=ws)
+
+
+class _Recorder:
+    def __init__(self):
+        self.calls = {}
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls[name] = args
+            return 0
+        return call
+
+
+def test_numbers_past_32_bits_keep_their_meaning():
+    """A window or a number of sinks past 2^31 is all tokens; a length of a prefix
+    that does not fit is refused, not cut."""
+    c = _cache()
+    h, p = c.request_begin(100), c.request_begin(50)
+    q, out, lse = _heads(3), _heads(3), torch.zeros(3, 16)
+    ws, w = torch.zeros(256, dtype=torch.uint8), torch.zeros(1, 100)
+    lib, c.L = c.L, _Recorder()
+    most = (1 << 31) - 1
+    try:
+        for given, want in ((1 << 32, most), (1 << 31, most), ((1 << 40) + 5, most), (most, most), (7, 7), (0, 0)):
+            c.window_attn([h], [3], 0, 1, q, given, given, 0.1, out, lse, workspace=ws)
+            c.window_attn_workspace_bytes([h], [3], 0, 1, given, given)
+            c.window_weights([h], [3], 0, 1, q, lse, given, given, 0.1, w)
+            assert c.L.calls["qsa_window_attn"][3:5] == (want, want)
+            assert c.L.calls["qsa_window_attn_workspace_bytes"][2:4] == (want, want)
+            assert c.L.calls["qsa_window_weights"][4:6] == (want, want)
+        for given in (-1, -(1 << 32)):
+            c.window_attn([h], [3], 0, 1, q, given, given, 0.1, out, lse, workspace=ws)
+            assert all(x < 0 for x in c.L.calls["qsa_window_attn"][3:5])
+        c.L.calls.clear()
+        for big in ((1 << 32) + 5, 1 << 31, -(1 << 32)):
+            for a in ((big, 0), (5, big)):
+                with pytest.raises(ValueError):
+                    c.shared_attn([h], [3], 0, 1, p, *a, q, 0.1, out, lse, workspace=ws)
+                with pytest.raises(ValueError):
+                    c.shared_attn_workspace_bytes([h], [3], 0, 1, p, *a)
+        assert not c.L.calls
+        c.shared_attn([h], [3], 0, 1, p, 50, 7, q, 0.1, out, lse, workspace=ws)
+        assert c.L.calls["qsa_shared_attn"][3:5] == (50, 7)
+    finally:
+        c.L = lib
