@@ -29,7 +29,7 @@
 //   one token, window 1024: 7.2 us, the latency of two launches.
 //   64 tokens behind a prefix of 16384, 0.4 K own tokens each (89 MB): 38 us: 19 for the
 //     prefix on 128 SMs (four steps a share: 1.9 us each and 10 of set-up, pieces and
-//     launch) beside 16 for the own tokens, and a join of 35 pieces a row.
+//     launch), then 16 for the own tokens, and a join of 35 pieces a row.
 //   29 FP8 draft tokens behind 65536 (69 MB): 57 us, 14 steps of 3.3 us a share.
 // Not faster: the SMs shared out to prefix and own tokens by their rows (41 -> 51 us);
 // FP8 codes copied and turned over in place (170 -> 198 us); both halves of a CTA on
@@ -60,7 +60,6 @@ struct DenseParams {
   int32_t tile0[kMaxUnits + 1];  // prefix sums of the wide tiles per unit
   int32_t grouped;               // 1: the prefix has tiles of its own
   int32_t prefix_pieces;         // of every row, in front of its own ones (0 where not grouped)
-  int32_t overlap;               // 1: the few kernel runs beside the wide one
   int32_t wide_q, few_q;         // steps of a share
   const uint16_t* q;             // [rows][16][128] bf16 bits
   float scale_log2;              // |softmax_scale| * log2(e)
@@ -286,10 +285,8 @@ __global__ void __launch_bounds__(kFewThreads, kFp8 && kN == 1 ? 2 : 1) dense_fe
   }
   const bool some = pre || (t.nq > 0 && p.d.c.unit_tokens(t.u) <= kFewQueries);
   const int shares = some ? shares_of(t, kFewStep, p.few_q, !p.grouped) : 0;
-  // Beside the wide kernel (which lets this one start once its own wait is over, so
-  // that what both read is there) the wait comes at the end: whatever follows this
-  // kernel follows both.
-  if (!p.overlap || (int)blockIdx.x >= shares) grid_dependency_wait();
+  // (before any CTA leaves: where all of them do, what follows still follows the kernel before)
+  grid_dependency_wait();
   if ((int)blockIdx.x >= shares) return;
   const uint32_t all = t.total / kFewStep + (t.total % kFewStep != 0);
   const uint32_t s0 = share_start(all, blockIdx.x, shares);
@@ -495,10 +492,7 @@ __global__ void __launch_bounds__(kFewThreads, kFp8 && kN == 1 ? 2 : 1) dense_fe
     }
   }
   __syncthreads();
-  if (half == 1) {
-    if (p.overlap) grid_dependency_wait();
-    return;
-  }
+  if (half == 1) return;
   float fa[kN][2], fb[kN][2];
 #pragma unroll
   for (int n = 0; n < kN; ++n)
@@ -536,7 +530,6 @@ __global__ void __launch_bounds__(kFewThreads, kFp8 && kN == 1 ? 2 : 1) dense_fe
         make_uint2(pack_bf16(lo.x * inv, lo.y * inv), pack_bf16(hi.x * inv, hi.y * inv));
     if (lane == 0 && p.lse) p.lse[(int64_t)x * kQHeads + h] = (ml.x + log2f(ml.y)) * kLn2;
   }
-  if (p.overlap) grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------- wide
@@ -676,7 +669,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) dense_wide_kernel(const __gri
   const int shares = shares_of(t, kStepTokens, p.wide_q, !p.grouped);
   if ((int)blockIdx.x >= shares) return;
   grid_dependency_wait();
-  if (p.overlap) trigger_dependents();
   const int nq = t.nq, x0 = t.x0;
   const int halves = nq > 32 ? 2 : 1;
   const int64_t pos0 = t.pos0;
@@ -1370,7 +1362,6 @@ cudaError_t launch_dense_attn(const DenseAttn& d, const uint16_t* q, float softm
   p.d = d;
   p.grouped = a.grouped;
   p.prefix_pieces = (int32_t)a.prefix_pieces;
-  p.overlap = a.wide_tiles > 0 && a.few_tiles > 0;
   p.wide_q = a.wide_q;
   p.few_q = a.few_q;
   p.q = q;
