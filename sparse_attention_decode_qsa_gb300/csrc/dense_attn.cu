@@ -58,6 +58,8 @@ constexpr int kMaxShares = 64;                    // of a tile
 struct DenseParams {
   DenseAttn d;
   int32_t tile0[kMaxUnits + 1];  // prefix sums of the wide tiles per unit
+  int32_t part0[kMaxUnits + 1];  // of the own partial rows per unit: its rows times its most pieces, 0 where every row is written at once
+  int32_t join0[kMaxUnits + 1];  // of the rows per unit that have partials
   int32_t grouped;               // 1: the prefix has tiles of its own
   int32_t prefix_pieces;         // of every row, in front of its own ones (0 where not grouped)
   int32_t wide_q, few_q;         // steps of a share
@@ -66,7 +68,7 @@ struct DenseParams {
   float sign;
   uint16_t* out;                 // [rows][16][128] bf16 bits
   float* lse;                    // [rows][16] or nullptr
-  float* part;                   // [pieces][rows][16][kRowFloats]
+  float* part;                   // prefix [pieces][rows], then per unit [pieces][its rows], each [16][kRowFloats]
 };
 
 // Rows x0 .. x0 + nq - 1 (consecutive positions from pos0 on, where they have own
@@ -130,8 +132,12 @@ __device__ __forceinline__ int own_pieces(const DenseParams& p, int u, int x) {
   return shares_of(own_tile(p.d, p.grouped, u, i0), few ? kFewStep : kStepTokens, few ? p.few_q : p.wide_q, !p.grouped);
 }
 
-__device__ __forceinline__ float* piece_ptr(const DenseParams& p, int piece, int x, int h) {
-  return p.part + (((int64_t)piece * p.d.c.rows() + x) * kQHeads + h) * kRowFloats;
+// Row x of unit u and head h in piece i of the prefix, or of its own tokens.
+__device__ __forceinline__ float* piece_ptr(const DenseParams& p, bool prefix, int u, int i, int x, int h) {
+  const int64_t rows = p.d.c.rows();
+  const int64_t row = prefix ? i * rows + x
+                             : p.prefix_pieces * rows + p.part0[u] + (int64_t)i * p.d.c.unit_tokens(u) + x - p.d.c.row0[u];
+  return p.part + (row * kQHeads + h) * kRowFloats;
 }
 
 // Where the tokens of a tile lie: slots and host rows of the prefix and of unit u.
@@ -515,7 +521,7 @@ __global__ void __launch_bounds__(kFewThreads, kFp8 && kN == 1 ? 2 : 1) dense_fe
     const float2 lo = *reinterpret_cast<const float2*>(at + 4 * lane), hi = *reinterpret_cast<const float2*>(at + 4 * lane + 2);
     const float2 ml = *reinterpret_cast<const float2*>(at + kHeadDim);
     if (shares > 1 || p.grouped) {
-      float* to = piece_ptr(p, (pre ? 0 : p.prefix_pieces) + blockIdx.x, x, h);
+      float* to = piece_ptr(p, pre, t.u, blockIdx.x, x, h);
       *reinterpret_cast<float4*>(to + 4 * lane) = make_float4(lo.x, lo.y, hi.x, hi.y);
       if (lane == 0) *reinterpret_cast<float2*>(to + kHeadDim) = ml;
       continue;
@@ -1090,7 +1096,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) dense_wide_kernel(const __gri
               make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
       }
       __syncwarp();
-      float* to = piece_ptr(p, (pre ? 0 : p.prefix_pieces) + blockIdx.x, x0 + 32 * h, head);
+      float* to = piece_ptr(p, pre, t.u, blockIdx.x, x0 + 32 * h, head);
 #pragma unroll 8
       for (int i = 0; i < rows; ++i, to += kQHeads * kRowFloats) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1098,8 +1104,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) dense_wide_kernel(const __gri
         *reinterpret_cast<float4*>(to + 4 * lane) = v;
       }
       if (lane < rows)
-        *reinterpret_cast<float2*>(piece_ptr(p, (pre ? 0 : p.prefix_pieces) + blockIdx.x, x0 + q, head) + kHeadDim) =
-            make_float2(m, l);
+        *reinterpret_cast<float2*>(piece_ptr(p, pre, t.u, blockIdx.x, x0 + q, head) + kHeadDim) = make_float2(m, l);
     } else {
       const float inv = 1.f / l;
       bool good = good_sum(l) && steps > 0;
@@ -1157,15 +1162,26 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_c
   __shared__ float2 part_ml[kSplit > 1 ? kJoinWarps : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s0 = warp % kSplit;
   const int64_t w = (int64_t)blockIdx.x * (kJoinWarps / kSplit) + warp / kSplit;
-  const int x = (int)(w / kQHeads), head = (int)(w % kQHeads);
-  const bool mine = x < p.d.c.rows();                // (with kSplit warps the same for the whole CTA)
-  if (!mine) return;
-  const int u = p.d.c.unit_of_row(x);
+  const int j = (int)(w / kQHeads), head = (int)(w % kQHeads);              // the j-th row that has partials
+  const int units = p.d.c.b.n_units;
+  if (j >= p.join0[units]) return;                   // (with kSplit warps the same for the whole CTA)
+  int u = 0;
+  for (int hi = units - 1; u < hi;) {
+    const int mid = (u + hi + 1) >> 1;
+    if (p.join0[mid] <= j) u = mid; else hi = mid - 1;
+  }
+  const int x = p.d.c.row0[u] + j - p.join0[u];
   const int pieces = p.prefix_pieces + own_pieces(p, u, x);
   grid_dependency_wait();
   if (!p.grouped && pieces == 1) return;             // complete
-  const int64_t stride = (int64_t)kSplit * p.d.c.rows() * kQHeads * kRowFloats;
-  const float* part = piece_ptr(p, s0, x, head);
+  const float* prefix_part = piece_ptr(p, true, u, 0, x, head);
+  const float* own_part = piece_ptr(p, false, u, 0, x, head);
+  const int64_t prefix_stride = (int64_t)p.d.c.rows() * kQHeads * kRowFloats;
+  const int64_t own_stride = (int64_t)p.d.c.unit_tokens(u) * kQHeads * kRowFloats;
+  auto piece = [&](int k) {                          // the k-th of this warp
+    const int i = s0 + k * kSplit;
+    return i < p.prefix_pieces ? prefix_part + i * prefix_stride : own_part + (i - p.prefix_pieces) * own_stride;
+  };
   const int n = pieces > s0 ? (pieces - s0 + kSplit - 1) / kSplit : 0;       // of this warp
   // eight pieces' O, maxima and sums are on their way at a time
   constexpr int kTurn = 8;
@@ -1176,7 +1192,7 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(const __grid_c
     float2 ml[kTurn];
 #pragma unroll
     for (int k = 0; k < kTurn; ++k) {
-      const float* from = part + (k0 + k) * stride;
+      const float* from = piece(k0 + k);
       ml[k] = k0 + k < n ? *reinterpret_cast<const float2*>(from + kHeadDim) : make_float2(-INFINITY, 0.f);
       o[k] = k0 + k < n ? *reinterpret_cast<const float4*>(from + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -1236,6 +1252,7 @@ struct Plan {
   int few_rows = 0;                                  // queries of a tile of the few kernel, at most
   int64_t pieces = 1;                                // of a row, at most
   int64_t prefix_pieces = 0;
+  int join_rows = 0;                                 // rows that have partials
   int64_t bytes = 256;
 };
 
@@ -1262,7 +1279,8 @@ int share_steps(const int64_t* steps, int n, int64_t most, int64_t least) {
 
 constexpr int kLeastWide = 2, kLeastFew = 1;          // steps of a share at least
 
-Plan make_plan(const DenseAttn& d, int sms, int32_t* tile0) {
+// p: receives the prefix sums per unit, or nullptr.
+Plan make_plan(const DenseAttn& d, int sms, DenseParams* p) {
   Plan a;
   const int units = d.c.b.n_units, layers = units / d.n_req, layer_rows = d.c.row0[d.n_req];
   int with_rows = 0;                                 // requests
@@ -1275,13 +1293,13 @@ Plan make_plan(const DenseAttn& d, int sms, int32_t* tile0) {
   int64_t few_steps[kMaxUnits + 1];                  // the layers of a request alike
   for (int u = 0; u < units; ++u) {
     const int n = d.c.unit_tokens(u);
-    if (tile0) tile0[u] = own_tiles;
+    if (p) p->tile0[u] = own_tiles;
     if (n > kFewQueries) own_tiles += (n + kTileQueries - 1) / kTileQueries;
     if (n == 0 || n > kFewQueries) continue;
     a.few_rows = n > a.few_rows ? n : a.few_rows;
     few_steps[few_units++] = ceil_div(own_tile(d, a.grouped, u, 0).total, kFewStep);
   }
-  if (tile0) tile0[units] = own_tiles;
+  if (p) p->tile0[units] = own_tiles;
   const int per_prefix = a.grouped && !few_prefix ? (layer_rows + kTileQueries - 1) / kTileQueries : 0;
   a.wide_tiles = own_tiles + layers * per_prefix;
   int64_t longest_own = 0, longest = 0;              // wide
@@ -1326,11 +1344,31 @@ Plan make_plan(const DenseAttn& d, int sms, int32_t* tile0) {
     a.few_shares = (int)ceil_div(most, a.few_q);
     if (a.few_shares == 0) a.few_shares = 1;
   }
-  int64_t own = a.wide_tiles > 0 ? ceil_div(longest_own, a.wide_q) : 0;
-  if (few_units > 0 && ceil_div(longest_few, a.few_q) > own) own = ceil_div(longest_few, a.few_q);
   if (a.grouped) a.prefix_pieces = few_prefix ? ceil_div(few_prefix_steps, a.few_q) : ceil_div(prefix_steps, a.wide_q);
-  a.pieces = own + a.prefix_pieces;
-  if (a.grouped || a.pieces > 1) a.bytes = a.pieces * d.c.rows() * kQHeads * kRowFloats * 4;
+  // partials for the rows that have several pieces alone: a long context of one token
+  // beside a prompt's rows, each written at once, has 64 and these none
+  int64_t most_own = 0, part_rows = 0;
+  for (int u = 0; u < units; ++u) {
+    const int n = d.c.unit_tokens(u);
+    const bool few = n <= kFewQueries;
+    int64_t own = n > 0 ? 1 : 0;                     // pieces of a row, at most
+    if (n > 0 && (few ? a.few_shares : a.wide_shares) > 1) {
+      for (int i = 0; i < n; i += kTileQueries) {
+        const int64_t k = shares_of(own_tile(d, a.grouped, u, i), few ? kFewStep : kStepTokens, few ? a.few_q : a.wide_q, true);
+        own = k > own ? k : own;
+      }
+    }
+    if (p) p->part0[u] = (int32_t)part_rows;
+    if (p) p->join0[u] = a.join_rows;
+    if (!a.grouped && own <= 1) continue;
+    part_rows += own * n;
+    a.join_rows += n;
+    most_own = own > most_own ? own : most_own;
+  }
+  if (p) p->part0[units] = (int32_t)part_rows;
+  if (p) p->join0[units] = a.join_rows;
+  a.pieces = most_own + a.prefix_pieces;
+  if (a.join_rows > 0) a.bytes = (a.prefix_pieces * d.c.rows() + part_rows) * kQHeads * kRowFloats * 4;
   return a;
 }
 
@@ -1358,7 +1396,7 @@ cudaError_t launch_dense_attn(const DenseAttn& d, const uint16_t* q, float softm
   if (e == cudaSuccess) e = current_sm_count(&sms);
   if (e != cudaSuccess) return e;
   DenseParams p;
-  const Plan a = make_plan(d, sms, p.tile0);
+  const Plan a = make_plan(d, sms, &p);
   p.d = d;
   p.grouped = a.grouped;
   p.prefix_pieces = (int32_t)a.prefix_pieces;
@@ -1383,8 +1421,8 @@ cudaError_t launch_dense_attn(const DenseAttn& d, const uint16_t* q, float softm
                        : (n == 1 ? dense_few_kernel<false, 1> : dense_few_kernel<false, 2>);
     e = launch_kernel(kernel, grid, dim3(kFewThreads), fp8 ? FewLayout<true>::kSmem : FewLayout<false>::kSmem, s, 0, dim3(1), p);
   }
-  if (e != cudaSuccess || (!a.grouped && a.pieces <= 1)) return e;
-  const int64_t rows = (int64_t)d.c.rows() * kQHeads;
+  if (e != cudaSuccess || a.join_rows == 0) return e;
+  const int64_t rows = (int64_t)a.join_rows * kQHeads;
   if (a.pieces > 8)
     return launch_kernel(dense_join_kernel<kJoinWarps>, dim3((unsigned)rows), dim3(kJoinThreads), 0, s, 0, dim3(1), p);
   return launch_kernel(dense_join_kernel<1>, dim3((unsigned)ceil_div(rows, kJoinWarps)), dim3(kJoinThreads), 0, s, 0,
