@@ -1290,7 +1290,9 @@ Plan make_plan(const DenseAttn& d, int sms, DenseParams* p) {
   a.grouped = d.prefix_len > 0 && with_rows > 1 && layer_rows <= with_rows * (kTileQueries / 2);
   const bool few_prefix = a.grouped && layer_rows <= kFewQueries;
   int own_tiles = 0, few_units = 0;
-  int64_t few_steps[kMaxUnits + 1];                  // the layers of a request alike
+  // of every tile of the few kernel: the units, and the prefix at every layer (a few
+  // prefix has two requests at least, so half as many layers as units at most)
+  int64_t few_steps[kMaxUnits + kMaxUnits / 2];
   for (int u = 0; u < units; ++u) {
     const int n = d.c.unit_tokens(u);
     if (p) p->tile0[u] = own_tiles;
@@ -1333,10 +1335,9 @@ Plan make_plan(const DenseAttn& d, int sms, DenseParams* p) {
   if (few_units > 0) {
     a.few_tiles = units + (few_prefix ? layers : 0);
     for (int i = 0; i < few_units; ++i) longest_few = few_steps[i] > longest_few ? few_steps[i] : longest_few;
-    // (at most four rows of a layer: no more than 64 units of a few prefix)
     int n = few_units;
     if (few_prefix)
-      for (int i = 0; i < layers && n <= kMaxUnits; ++i) few_steps[n++] = few_prefix_steps;
+      for (int i = 0; i < layers; ++i) few_steps[n++] = few_prefix_steps;
     if (few_prefix) a.few_rows = layer_rows > a.few_rows ? layer_rows : a.few_rows;
     // (FP8 rows, two queries: two CTAs to an SM)
     a.few_q = share_steps(few_steps, n, a.few_rows <= 2 && d.c.b.row_bytes == kRowBytesFp8 ? 2 * sms : sms, kLeastFew);

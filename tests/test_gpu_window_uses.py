@@ -120,3 +120,19 @@ def test_a_shared_prefix_behind_tokens_and_pieces_of_prompts(fp8, own, n_tokens,
         _check(_rows(f, n_tokens, layers), q, out, lse, values)
     finally:
         f.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("layers", [90, 128])
+def test_a_shared_prefix_at_as_many_layers_as_a_call_takes(layers, fp8):
+    f = Filled([6, 9, 300], layers=layers, fp8=fp8, seed=5)
+    try:
+        q = _queries(2 * layers, 5, f.dev, 1.5)
+        out, lse, _ = _attend_guarded(f, [1, 1], layers, q, (f.hs[2], 300, 0))
+
+        def values(k):
+            a, b = f.values(2, k[0], list(range(300))), f.values(k[1], k[0], list(range(k[2] + 1)))
+            return [np.concatenate(x) for x in zip(a, b)]
+        _check(_rows(f, [1, 1], layers), q, out, lse, values)
+    finally:
+        f.close()
