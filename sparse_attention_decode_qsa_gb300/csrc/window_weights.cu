@@ -16,6 +16,14 @@
 // is weight, and loses nothing (added to the lse first, it would be lost in the lse's
 // last place).  The lse's second part is a factor beside the column.
 //
+// The tensor core cuts partial sums off where fp32 additions round them, so a logit
+// comes out too small in size, by an amount that depends on how its sum grows: no one
+// factor puts that right.  The weights of logits near 10 (their sum, off from float64;
+// a plain fp32 product stays under 5e-7): -2.7e-6 beside BF16 rows and -2.0e-6 beside
+// FP8 rows where all dims add alike, -8e-7 and -2e-7 with random keys, -4.3e-6 and
+// -4.0e-6 where the second half of the dims takes back most of the first, within 2e-7
+// where one dim carries the logit; at 40 three to six times as much.
+//
 // Measured (device time of a call):
 //   8 requests' tokens over 8192 BF16 tokens each (67 MB of keys): 9.2 us, above the
 //     measured copy rate (the keys stay in L2 from call to call; 16.9 from cold caches).
@@ -38,16 +46,6 @@ namespace {
 
 using namespace tc;
 using namespace attn;
-
-// The tensor core cuts partial sums off instead of rounding them: half a unit in the
-// last place of the running sum on average, eight times (K = 16 each) while it grows
-// to a large logit's product.  With a unit 2^-23 / 1.39 of the sum on average and the
-// sum at step i i/8 of the whole, that is 0.5 / 1.39 * (1 + .. + 8) / 8 units = 1.62
-// 2^-23, always towards 0, so that every weight of a large logit x came out 1.9e-7 x
-// too small beside BF16 rows (1.4e-6 of the sums where logits reach 10, 3e-7 with the
-// scale taking it back).  Products of e4m3 codes have their last bits above the sum's:
-// nothing is cut off there.
-constexpr double kCutOff = 1.62 / 8388608;
 
 struct WeightParams {
   DenseAttn d;
@@ -720,7 +718,7 @@ cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const f
   p.q = q;
   p.lse = lse;
   const bool fp8 = d.c.b.row_bytes == kRowBytesFp8;
-  const double f = (double)softmax_scale * 1.4426950408889634 * (fp8 ? 1 : 1 + kCutOff);
+  const double f = (double)softmax_scale * 1.4426950408889634;
   // both parts of one sign, and neither 0: an infinite logit stays one
   p.scale_log2 = (float)f;
   if (fabs((double)p.scale_log2) > fabs(f)) p.scale_log2 = nextafterf(p.scale_log2, 0.f);

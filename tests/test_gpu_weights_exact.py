@@ -54,7 +54,7 @@ def _one_dim(f, value, dim):
 
 @pytest.mark.parametrize("tokens", [1, 3, 40, 300])
 @pytest.mark.parametrize("lse", [10.0, 40.3, 300.7])
-@pytest.mark.parametrize("fp8", [True])
+@pytest.mark.parametrize("fp8", [False, True])
 def test_weights_of_exact_logits(fp8, lse, tokens):
     n = 2000
     f = Filled([n], fp8=fp8, seed=3)
