@@ -666,8 +666,8 @@ __global__ void __launch_bounds__(Wide<kTiles>::kThreads, 1) weight_wide_kernel(
               const bool in = cc >= a && cc < z;
               const float mm[4] = {lo_of(mi.x), hi_of(mi.x), lo_of(mi.y), hi_of(mi.y)};
 #pragma unroll
-              for (int h = 0; h < 4; ++h)            // (columns without weight, and past the queries: minus is infinite)
-                if (!in || fabsf(mm[h]) == INFINITY) e[h] = 0.f;
+              for (int h = 0; h < 4; ++h)            // (columns without weight, and past the queries: minus is +inf)
+                if (!in || mm[h] == INFINITY) e[h] = 0.f;
               add(cc, e);
             }
           }

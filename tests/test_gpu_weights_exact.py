@@ -15,7 +15,7 @@ import pytest
 import torch
 
 import sparse_attention_decode_qsa_gb300 as Q
-from tests.test_gpu_chunk import SCALE, Filled, _clean
+from tests.test_gpu_chunk import SCALE, Filled, _clean, _queries
 from tests.test_gpu_chunk_range import _store
 from tests.test_gpu_window import FULL
 
@@ -101,5 +101,93 @@ def test_infinite_queries(fp8, tokens):
         want = torch.where(held > 0, math.inf, 0.0).float()
         want[seen:] = 0
         assert torch.equal(w[0].cpu(), want)
+    finally:
+        f.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("tokens", [1, 4, 40, 70])
+def test_a_lse_of_infinity(fp8, tokens):
+    """exp(z - inf): nothing for finite logits, no value for an infinite one, whatever
+    other rows of the chunk have no weight at all."""
+    n = 300
+    f = Filled([n], fp8=fp8, seed=3)
+    try:
+        g = torch.Generator().manual_seed(2)
+        held = _one_dim(f, torch.randn(n, generator=g).sign() * (1 + torch.rand(n, generator=g)), 5)
+        q = torch.randn(tokens, 16, 128, generator=g).bfloat16()
+        ls = torch.full((tokens, 16), math.inf)
+        ls[0, 3] = -math.inf
+        w = torch.full((1, n), 7.0, device=f.dev)
+        f.c.window_weights(f.hs, [tokens], 0, 1, q.to(f.dev), ls.to(f.dev), 0, FULL, SCALE, w)
+        assert bool((w == 0).all())
+        q[0, :, 5] = math.inf
+        f.c.window_weights(f.hs, [tokens], 0, 1, q.to(f.dev), ls.to(f.dev), 0, FULL, SCALE, w)
+        _clean(f.c)
+        seen = torch.arange(n) <= n - tokens
+        got = w[0].cpu()
+        assert torch.equal(got.isnan(), (held > 0) & seen) and bool((got[(held < 0) | ~seen] == 0).all())
+    finally:
+        f.close()
+
+
+def _weights(f, n_tokens, q, lse, sinks, window, scale):
+    """In float64, and the tolerance of every entry: a term's logit is off by 2^-17 of
+    |scale| sum |q_d k_d| and by 2^-22 of its distance to the lse, the exponential by
+    2^-21; the sum of up to 2^12 terms by 2^-12 of itself; weights below 2^-126 are 0."""
+    out, tol, x = [], [], 0
+    for r, n in enumerate(n_tokens):
+        K, _ = f.values(r, 0, list(range(f.ctxs[r])))
+        Kh, t = K[:, np.arange(16) // 4], np.arange(f.ctxs[r])
+        w, e_w = np.zeros(f.ctxs[r]), np.zeros(f.ctxs[r])
+        for i in range(n):
+            p = f.ctxs[r] - n + i
+            see = (t <= p) & ((t < sinks) | (t > p - window))
+            qd, ls = q[x].double().cpu().numpy(), lse[x].double().cpu().numpy()
+            x += 1
+            if not see.any():
+                continue
+            d = scale * np.einsum("thd,hd->th", Kh[see], qd) - ls
+            size = abs(scale) * np.einsum("thd,hd->th", np.abs(Kh[see]), np.abs(qd))
+            e = np.exp(d)
+            w[see] += e.sum(1)
+            e_w[see] += (e * np.expm1(2.0 ** -17 * size + 2.0 ** -22 * np.abs(d) + 2.0 ** -21)).sum(1)
+        out.append(w)
+        tol.append(e_w + 2.0 ** -12 * w + 16 * n * 2.0 ** -126)
+    return out, tol
+
+
+def _entry_by_entry(f, n_tokens, sinks, window, scale):
+    q = _queries(sum(n_tokens), 5, f.dev, 1.5)
+    out, lse = torch.zeros_like(q), torch.zeros(sum(n_tokens), 16, device=f.dev)
+    f.c.window_attn(f.hs, n_tokens, 0, 1, q, sinks, window, scale, out, lse)
+    w = torch.full((len(n_tokens), max(f.ctxs)), -3.0, device=f.dev)
+    f.c.window_weights(f.hs, n_tokens, 0, 1, q, lse, sinks, window, scale, w)
+    torch.cuda.synchronize()
+    _clean(f.c)
+    want, tol = _weights(f, n_tokens, q, lse, sinks, window, float(np.float32(scale)))
+    for r, n in enumerate(f.ctxs):
+        got = w[r, :n].double().cpu().numpy()
+        assert np.all(np.abs(got - want[r]) <= tol[r]), (r, np.abs(got - want[r]).max())
+        assert np.all(got[want[r] == 0] == 0) and bool((w[r, n:] == -3).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("scale", [0.0, -SCALE, 6 * SCALE, SCALE / 50])
+@pytest.mark.parametrize("n_tokens", [[2, 1], [4, 40], [300, 33]])
+def test_softmax_scales_of_any_sign_and_size(fp8, scale, n_tokens):
+    f = Filled([700, 650], fp8=fp8, seed=4)
+    try:
+        _entry_by_entry(f, n_tokens, 4, 600, scale)
+    finally:
+        f.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n_tokens", [[1, 2, 3], [40, 3, 70]])
+def test_weights_over_rings_hosts_and_pool(fp8, n_tokens):
+    f = Filled([500, 500, 260], [Q.KV_HOST_RING, Q.KV_HOST, Q.KV_HBM], fp8=fp8, seed=5, ring=64)
+    try:
+        _entry_by_entry(f, n_tokens, 4, 200, SCALE)
     finally:
         f.close()
