@@ -653,7 +653,8 @@ qsa_status_t qsa_window_weights(qsa_cache* cache, const qsa_chunk* chunk, const 
  * weights_out: device fp32, layer l at weights_out + l * out_stride (>= keep), or
  * NULL: the kept tokens' weights.  workspace: device, 16-byte aligned,
  * qsa_evict_workspace_bytes bytes.  Outputs and the workspace overlap no input and
- * not each other (weights_out = weights is refused).  Work on the request that is in flight on other streams must have
+ * not each other (a weights_out any of whose rows meets one of the weights is
+ * refused).  Work on the request that is in flight on other streams must have
  * finished, and later work must be ordered behind `stream`.  Graphs that captured
  * calls on the request must be captured again; a stream that is being captured is
  * refused.

@@ -1087,6 +1087,17 @@ qsa_status_t qsa_window_weights(qsa_cache* c, const qsa_chunk* chunk, const uint
 
 namespace {
 
+// Whether any of `rows` rows of n floats, stride apart, from a on meets one of those
+// of m floats from b on.
+bool rows_meet(const float* a, int64_t a_stride, int64_t n, const float* b, int64_t b_stride, int64_t m, int32_t rows) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  if (a0 >= b0 + 4 * ((rows - 1) * b_stride + m) || b0 >= a0 + 4 * ((rows - 1) * a_stride + n)) return false;
+  for (int32_t i = 0; i < rows; ++i)
+    for (int32_t k = 0; k < rows; ++k)
+      if (a0 + 4 * i * a_stride < b0 + 4 * (k * b_stride + m) && b0 + 4 * k * b_stride < a0 + 4 * (i * a_stride + n)) return true;
+  return false;
+}
+
 qsa_status_t evict_desc(qsa_cache* c, qsa_handle h, int64_t keep, EvictParams* p) {
   if (!c->has_device) return fail(QSA_ERR_NO_DEVICE, "cache has no device storage");
   const Lease* l;
@@ -1135,14 +1146,14 @@ qsa_status_t qsa_request_evict(qsa_cache* c, qsa_handle request, const float* we
     return fail(QSA_ERR_INVALID_ARG, "first %lld and last %lld must be >= 0 and at most keep %lld together",
                 (long long)first, (long long)last, (long long)keep);
   if (!weights || !workspace) return fail(QSA_ERR_INVALID_ARG, "null array");
-  if (weights_out == weights)
-    return fail(QSA_ERR_INVALID_ARG, "weights_out is weights: kept weights would replace others not yet read");
   if (!aligned16(workspace) || !aligned16(kept) || reinterpret_cast<uintptr_t>(weights) % 4 ||
       reinterpret_cast<uintptr_t>(weights_out) % 4)
     return fail(QSA_ERR_INVALID_ARG, "misaligned device buffer");
   if (p.n_layers > 1 && (weight_stride < p.n || (weights_out && out_stride < keep)))
     return fail(QSA_ERR_INVALID_ARG, "weight_stride %lld < %lld tokens, or out_stride %lld < %lld",
                 (long long)weight_stride, (long long)p.n, (long long)out_stride, (long long)keep);
+  if (weights_out && rows_meet(weights, weight_stride, p.n, weights_out, out_stride, keep, p.n_layers))
+    return fail(QSA_ERR_INVALID_ARG, "weights_out lies in weights: kept weights would replace others not yet read");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   cudaError_t e = cudaStreamIsCapturing(s, &cs);

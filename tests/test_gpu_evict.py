@@ -380,3 +380,37 @@ def test_kept_tokens_are_not_stored_again(fp8):
         _clean(c)
     finally:
         f.close()
+
+
+def test_kept_weights_beside_and_inside_the_weights():
+    """weights_out as a view into the tensor of the weights: refused where the two
+    meet, taken where it has columns or rows of its own."""
+    f = Filled([200, 100], layers=2, seed=3)
+    try:
+        c, h = f.c, f.hs[0]
+        models = [Model(c, h, l) for l in range(2)]
+        t = torch.rand(4, 260, device=f.dev)
+        before = t.clone()
+        flat = t.view(-1)
+        for out in (t[:2], t[:2, 10:70], t[:2, 199:], t[1:3], t[1:3, 150:], flat[:400].view(2, 200),
+                    flat[260 + 199:][:100].view(2, 50)):
+            with pytest.raises(Q.QsaError) as e:
+                c.evict(h, t[:2, :200], 50, weights_out=out)
+            assert e.value.status == Q.ERR_INVALID_ARG
+        torch.cuda.synchronize()
+        assert c.request_info(h).ctx_len == 200 and torch.equal(t, before)
+        for m in models:
+            m.check()
+        c.evict(h, t[:2, :200], 60, weights_out=t[:2, 200:])           # columns behind
+        want = [_kept(before[l, :200].cpu().numpy(), 60, 0, 0) for l in range(2)]
+        for l in range(2):
+            models[l].evict(want[l])
+            models[l].check()
+            assert torch.equal(t[l, 200:].cpu(), before[l, want[l]].cpu()) and torch.equal(t[l, :200], before[l, :200])
+        c.evict(h, t[:2, 200:], 30, weights_out=t[2:])                 # rows behind
+        for l in range(2):
+            assert torch.equal(t[2 + l, :30].cpu(), t[l, 200:].cpu()[_kept(t[l, 200:].cpu().numpy(), 30, 0, 0)])
+        assert torch.equal(t[2:, 30:], before[2:, 30:])
+        _clean(c)
+    finally:
+        f.close()
