@@ -17,12 +17,9 @@
 // last place).  The lse's second part is a factor beside the column.
 //
 // The tensor core cuts partial sums off where fp32 additions round them, so a logit
-// comes out too small in size, by an amount that depends on how its sum grows: no one
-// factor puts that right.  The weights of logits near 10 (their sum, off from float64;
-// a plain fp32 product stays under 5e-7): -2.7e-6 beside BF16 rows and -2.0e-6 beside
-// FP8 rows where all dims add alike, -8e-7 and -2e-7 with random keys, -4.3e-6 and
-// -4.0e-6 where the second half of the dims takes back most of the first, within 2e-7
-// where one dim carries the logit; at 40 three to six times as much.
+// comes out too small in size, by an amount that depends on how its sum grows.  For few
+// queries every 16 dims are a product of their own, and the eight are added in fp32.
+// For more the sum stays in tensor memory, and kCutOff makes up for the mean.
 //
 // Measured (device time of a call):
 //   8 requests' tokens over 8192 BF16 tokens each (67 MB of keys): 9.2 us, above the
@@ -46,6 +43,19 @@ namespace {
 
 using namespace tc;
 using namespace attn;
+
+// A mean correction of BF16 logits, relative, in the kernel of many queries: no more
+// than that, since what is cut off depends on the keys, and a logit that loses nothing
+// is then too large by it.  Sums of the weights of logits near 10 (and near 40), off
+// from float64 in units of 1e-7, with the correction and without it; the last number
+// is a plain fp32 product's:
+//   keys at random                                         +2, -8 (-2, -43)      +1
+//   all dims alike                                        -14, -27 (-30, -81)    -1
+//   the second half of the dims takes most back           -31, -43 (-190, -240)  -4
+//   one dim alone                                         +10, -1 (+51, 0)       +1
+// FP8 keys go without: -2, -19, -41, -1 (-11, -29, -58, -1).  The kernel of few queries:
+// -1, -5, +1, -2 beside BF16 and 0, -3, +14, -1 beside FP8 rows (near 10).
+constexpr double kCutOff = 1.1 / 8388608;
 
 struct WeightParams {
   DenseAttn d;
@@ -191,7 +201,12 @@ __global__ void __launch_bounds__(kFewThreads, 2) weight_few_kernel(const __grid
       uint32_t ka[4];
       few_keys<kFp8>(st, k, ka);
 #pragma unroll
-      for (int i = 0; i < kN; ++i) mma16<kFp8>(x[i], ka, qb[i][k][0], qb[i][k][1]);
+      for (int i = 0; i < kN; ++i) {
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16<kFp8>(y, ka, qb[i][k][0], qb[i][k][1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[i][e] += y[e];
+      }
     }
     float w[2] = {0.f, 0.f};
 #pragma unroll
@@ -718,12 +733,14 @@ cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const f
   p.q = q;
   p.lse = lse;
   const bool fp8 = d.c.b.row_bytes == kRowBytesFp8;
-  const double f = (double)softmax_scale * 1.4426950408889634;
   // both parts of one sign, and neither 0: an infinite logit stays one
-  p.scale_log2 = (float)f;
-  if (fabs((double)p.scale_log2) > fabs(f)) p.scale_log2 = nextafterf(p.scale_log2, 0.f);
-  p.scale_rest = (float)(f - (double)p.scale_log2);
-  if (p.scale_rest == 0.f) p.scale_rest = p.scale_log2 * 0x1p-40f;
+  auto set_scale = [&](double f) {
+    p.scale_log2 = (float)f;
+    if (fabs((double)p.scale_log2) > fabs(f)) p.scale_log2 = nextafterf(p.scale_log2, 0.f);
+    p.scale_rest = (float)(f - (double)p.scale_log2);
+    if (p.scale_rest == 0.f) p.scale_rest = p.scale_log2 * 0x1p-40f;
+  };
+  const double f = (double)softmax_scale * 1.4426950408889634;
   p.weights = weights;
   p.stride = stride;
   p.accumulate = accumulate;
@@ -752,6 +769,7 @@ cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const f
     int64_t ctas = (wide + 128 * tiles - 1) / (128 * tiles);
     if (ctas > (sms + wide_units - 1) / wide_units) ctas = (sms + wide_units - 1) / wide_units;
     const dim3 grid((unsigned)ctas, d.c.b.n_units);
+    set_scale(fp8 ? f : f * (1 + kCutOff));
     auto* kernel = fp8 ? (tiles == 2 ? weight_wide_kernel<true, 2> : weight_wide_kernel<true, 1>)
                        : (tiles == 2 ? weight_wide_kernel<false, 2> : weight_wide_kernel<false, 1>);
     e = launch_kernel(kernel, grid, dim3(tiles == 2 ? Wide<2>::kThreads : Wide<1>::kThreads), tiles == 2 ? Wide<2>::kSmem : Wide<1>::kSmem, s, 0, dim3(1), p);
@@ -762,6 +780,7 @@ cudaError_t launch_window_weights(const DenseAttn& d, const uint16_t* q, const f
     run = (run + kFewStep - 1) / kFewStep * kFewStep;
     run = run < 2 * kFewStep ? 2 * kFewStep : (run > kFewMost ? kFewMost : run);
     p.few_tokens = (int32_t)run;
+    set_scale(f);
     auto* kernel = fp8 ? (rows > 2 ? weight_few_kernel<true, 2> : weight_few_kernel<true, 1>)
                        : (rows > 2 ? weight_few_kernel<false, 2> : weight_few_kernel<false, 1>);
     e = launch_kernel(kernel, dim3((unsigned)((few + run - 1) / run), d.c.b.n_units), dim3(kFewThreads),

@@ -75,6 +75,10 @@ def test_weights_of_exact_logits(fp8, lse, tokens):
         want = y.exp()
         want[n - tokens + tokens // 2 + 1:] = 0
         tol = want * (2 * 2.0 ** -22 + 2 * 2.0 ** -24 + 2 * y.abs() * 2.0 ** -24)
+        if tokens > 4 and not fp8:
+            # these logits take a factor of 1 + 1.1 * 2^-23 for what the tensor core cuts
+            # off of other sums: 1.1 * 2^-23 |z| in the exponent
+            tol += want * torch.expm1(1.1 * 2.0 ** -23 * (y + lse).abs())
         err = (w[0].double().cpu() - want).abs()
         assert bool((err <= tol).all()), (err / want).nan_to_num(0).max()
     finally:
