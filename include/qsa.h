@@ -28,7 +28,7 @@
  * takes back tokens (rejected drafts).
  * Attention without a selection, over the same caches: qsa_window_attn (the
  * newest tokens and the context's first ones), qsa_shared_attn (a prefix that a
- * batch has in common, read once for all, and each request's own tokens).
+ * batch has in common, and each request's own tokens).
  * qsa_window_weights adds up the weight that such attention gives each cached
  * token, and qsa_request_evict drops the tokens with the least of it.
  * Pages of the cache: qsa_request_fork starts a request with the first tokens
@@ -601,8 +601,10 @@ int64_t qsa_window_attn_workspace_bytes(qsa_cache* cache, const qsa_chunk* chunk
 /* Attention of a batch that shares a prefix: row x at position p of its request r
  * attends over the tokens 0 .. prefix_len-1 of request `prefix` (0 <= prefix_len <=
  * its ctx_len) and over the tokens own_first .. p of r (none where own_first > p).
- * The prefix's rows are read once per 64 rows of a layer, whichever requests these
- * belong to.  The requests may hold copies of the prefix (qsa_request_fork;
+ * Where the chunk's requests have 32 rows of a layer or fewer on average (those
+ * without rows not counted, two at least), the prefix's rows are read once per 64
+ * rows, whichever requests these belong to; in other batches once per request and 64
+ * of its rows.  The requests may hold copies of the prefix (qsa_request_fork;
  * own_first = prefix_len then), or only their own tokens (own_first = 0);
  * `prefix` may be one of the chunk's requests, and every row sees all of its
  * prefix_len tokens.  Everything else as for qsa_window_attn. */

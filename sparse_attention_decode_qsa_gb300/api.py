@@ -447,7 +447,7 @@ class Cache:
     def shared_attn(self, handles, n_tokens, layer0, n_layers, prefix, prefix_len, own_first, q, softmax_scale, out,
                     lse=None, workspace=None, stream=None):
         """Attention of every query over the first prefix_len tokens of the request
-        `prefix`, read once for the batch, and over its own request's tokens from
+        `prefix`, read once per 64 rows where the requests have few each, and over its own request's tokens from
         own_first (prefix_len for requests that hold a copy of the prefix, 0 for
         those that do not) up to its own.  Arrays as for window_attn."""
         ch = _chunk(handles, n_tokens, layer0, n_layers)

@@ -24,14 +24,14 @@
 //     (issue slots 0.49, tensor pipe 0.55, exponentials 0.28 of the cycles).
 //   2 x 1023 FP8 queries over 8191 tokens each (129 GFLOP): 162 us on 128 of 152 SMs;
 //     the products with both scales come on top, 2.5 us a step for 1.9.
-//   32 requests' tokens, window 4096, FP8 rows (137 MB): 36.7 us, the kernel 34.5 at 4.0
-//     TB/s, bound by the conversions' and address instructions (issue slots 0.54).
+//   32 requests' tokens, window 4096, FP8 rows (137 MB): 36.9 us, the kernel 34.2 at 4.0
+//     TB/s; issue slots 0.51, most of them conversions and addresses, no pipe full.
 //   one token, window 1024: 7.2 us, the latency of two launches.
-//   64 tokens behind a prefix of 16384, 0.4 K own tokens each (89 MB): 38 us: 19 for the
+//   64 tokens behind a prefix of 16384, 0.4 K own tokens each (89 MB): 40 us: 19 for the
 //     prefix on 128 SMs (four steps a share: 1.9 us each and 10 of set-up, pieces and
 //     launch), then 16 for the own tokens, and a join of 35 pieces a row.
-//   29 FP8 draft tokens behind 65536 (69 MB): 57 us, 14 steps of 3.3 us a share.
-// Not faster: the SMs shared out to prefix and own tokens by their rows (41 -> 51 us);
+//   29 FP8 draft tokens behind 65536 (69 MB): 61 us, 14 steps of 3.3 us a share.
+// Not faster: the SMs shared out to prefix and own tokens by their rows (10 us more);
 // FP8 codes copied and turned over in place (170 -> 198 us); both halves of a CTA on
 // every other step of a small tile (57 -> 76, BF16 44 -> 59); the idle half's warps for
 // V (57 -> 60).
@@ -1272,8 +1272,9 @@ int share_steps(const int64_t* steps, int n, int64_t most, int64_t least) {
     for (int i = 0; i < n; ++i) sum += ceil_div(steps[i], mid);
     if (sum <= most) hi = mid; else lo = mid + 1;
   }
-  // not for less than a quarter of the longest: the join comes on top (2 x 1023 FP8
-  // queries, 32 tiles of up to 64 steps on 38 shares: 170 us with 63 steps a share)
+  // not for less than a quarter of the longest: the join comes on top (measured on one
+  // case: 2 x 1023 FP8 queries, 32 tiles of up to 64 steps on 38 shares, 170 us with 63
+  // steps a share, 162 with whole tiles)
   return (int)(lo > longest - longest / 4 && longest > lo ? longest : lo);
 }
 

@@ -22,14 +22,14 @@
 // For more the sum stays in tensor memory, and kCutOff makes up for the mean.
 //
 // Measured (device time of a call):
-//   8 requests' tokens over 8192 BF16 tokens each (67 MB of keys): 9.2 us, above the
-//     measured copy rate (the keys stay in L2 from call to call; 16.9 from cold caches).
+//   8 requests' tokens over 8192 BF16 tokens each (67 MB of keys): 9.4 us, above the
+//     measured copy rate (the keys stay in L2 from call to call; 17.0 from cold caches).
 //   64 queries over 131072 FP8 tokens (134 M exponentials, 34 GFLOP): 72 us.  BF16
 //     rows take 60, 32 queries 56 and 42: codes to bf16 are a part of the bound.  A
 //     further turn of 256 tokens costs 1.8 us up to 128 queries and 2.0 beyond, the
 //     tensor core 0.6 of it (both operands from shared memory, 66 cycles an MMA); the
 //     rest is hand-overs and issue slots (0.54 in use).
-//   1024 BF16 queries, windows of 16384 of 32768 tokens (69 GFLOP): 135 us on 136 of 152
+//   1024 BF16 queries, windows of 16384 of 32768 tokens (69 GFLOP): 134 us on 136 of 152
 //     SMs (128 tokens each; 256 tokens would be 68 CTAs), 1.05 us a turn of 128 x 128.
 // Not faster: turns of 256 columns on 128 tokens (127 -> 165 us: with two turns under
 // way the loads of Q, products and exponentials came one after the other); a scale per
